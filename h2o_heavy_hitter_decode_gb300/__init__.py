@@ -9,6 +9,14 @@ library is missing or the device is not a CUDA device, calls raise.
     O, lse, colsum = cache.prefill(Q, K, V)          # [B,H,L,d] each
     out = cache.step(q_t, k_t, v_t)                  # [B,H,d] each
     outs = cache.steps(q, k, v)                      # [n,B,H,d] each
+
+``H2OBlockCache`` is the cache for batches of different lengths: grouped
+queries, 8-bit codes with one scale per block of entries, eviction in bulk.
+
+    cache = H2OBlockCache(B, H, d, capacity, group=G)
+    cache.append(K, V, lengths, score=colsum)        # the prompt: [B,H,n,d]
+    out = cache.step(q, k, v, lengths)               # q [B,H*G,1,d], k, v [B,H,1,d]
+    lengths = cache.evict(lengths, k_heavy, k_local)
 """
 from __future__ import annotations
 
@@ -18,7 +26,7 @@ import re
 
 import torch
 
-__all__ = ["H2OCache", "H2OError", "lib", "LIB_PATH", "HEADER_PATH", "declared_functions", "kernel_arch", "probe_read_gbs"]
+__all__ = ["H2OCache", "H2OBlockCache", "H2OError", "lib", "LIB_PATH", "HEADER_PATH", "declared_functions", "kernel_arch", "probe_read_gbs"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libh2o.so")
@@ -29,6 +37,11 @@ _STATUS = {0: "H2O_OK", 1: "H2O_EINVAL", 2: "H2O_ESTATE", 3: "H2O_ECUDA", 4: "H2
            5: "H2O_EDEVICE", 6: "H2O_EUNSUPPORTED"}
 
 _lib = None
+
+
+class Rows(C.Structure):
+    """h2o_rows: bf16 rows (b, h, t) at a device pointer, strides in elements."""
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_int64), ("stride_h", C.c_int64), ("stride_t", C.c_int64)]
 
 
 class H2OError(RuntimeError):
@@ -85,12 +98,27 @@ def lib():
         L.h2o_probe_read.restype = i32
         L.h2o_kernel_arch.argtypes = [C.POINTER(i32), C.POINTER(i32)]
         L.h2o_kernel_arch.restype = i32
+        rows, shape = C.POINTER(Rows), [i32, i32, i32, i64, i32, i32, i32]
+        L.h2o_bcache_workspace_bytes.argtypes = shape
+        L.h2o_bcache_workspace_bytes.restype = sz
+        L.h2o_bcache_create.argtypes = shape + [vp, vp, C.POINTER(vp)]
+        L.h2o_bcache_destroy.argtypes = [vp]
+        L.h2o_bcache_set_stream.argtypes = [vp, vp]
+        L.h2o_bcache_arrays.argtypes = [vp] + [C.POINTER(vp)] * 6
+        L.h2o_bcache_append.argtypes = [vp, i32, rows, rows, vp, vp, vp, vp]
+        L.h2o_bcache_attend.argtypes = [vp, i32, rows, vp, vp, i32, i32, rows, vp]
+        L.h2o_bcache_step.argtypes = [vp, i32, rows, rows, rows, vp, vp, vp, i32, rows, vp]
+        L.h2o_bcache_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
+        L.h2o_bcache_get_error.argtypes = [vp, C.POINTER(i32)]
         for f in ("h2o_cache_create", "h2o_cache_destroy", "h2o_set_stream", "h2o_prefill", "h2o_prefill_rows",
                   "h2o_decode_step",
                   "h2o_decode_steps", "h2o_cache_export", "h2o_cache_import", "h2o_cache_info",
                   "h2o_get_error", "h2o_profile_enable", "h2o_profile_read", "h2o_set_decode_form",
                   "h2o_decode_form_used", "h2o_cache_set_policy", "h2o_cache_get_policy",
-                  "h2o_cache_export_scales", "h2o_cache_import_scales"):
+                  "h2o_cache_export_scales", "h2o_cache_import_scales",
+                  "h2o_bcache_create", "h2o_bcache_destroy", "h2o_bcache_set_stream", "h2o_bcache_arrays",
+                  "h2o_bcache_append", "h2o_bcache_attend", "h2o_bcache_step", "h2o_bcache_evict",
+                  "h2o_bcache_get_error"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -354,3 +382,6 @@ class H2OCache:
     def check_device_error(self):
         self._sync_stream()
         _check(lib().h2o_get_error(self._h), "h2o_get_error")
+
+
+from .block_cache import H2OBlockCache  # noqa: E402  (uses the names above)

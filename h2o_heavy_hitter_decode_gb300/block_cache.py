@@ -1,0 +1,199 @@
+"""Block-scaled 8-bit K/V caches with grouped queries and bulk eviction
+(``h2o_bcache_*`` of the C ABI): argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import H2OError, Rows, _check, _ptr, lib
+
+__all__ = ["H2OBlockCache"]
+
+KV = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
+
+
+class H2OBlockCache:
+    """Per (sequence, cached head) up to ``capacity`` entries in the order of
+    their positions; ``group`` query heads share a cached head, and a call
+    takes up to ``max_queries`` query tokens per sequence.
+
+    The entries a sequence holds are the caller's to count: every call takes
+    ``lengths``, an int32 [B] tensor on the device, so one tensor serves the
+    caches of all layers and captured graphs read its current values.
+    ``counts`` (int32 [B], optional) are the real rows of a padded batch.
+
+    K, V [B, H, capacity, d] are the codes (torch.float8_e4m3fn or torch.int8),
+    K_scale, V_scale [B, H, capacity / 32] the scales of blocks of 32 entries
+    (powers of two; an entry is code * scale), pos and score [B, H, capacity]
+    the entries' positions and accumulated attention weights: views of the
+    workspace, one torch uint8 tensor owned by this object.  Calls enqueue on
+    torch's current CUDA stream of the cache's device; calls of one cache must
+    not overlap on the GPU."""
+
+    BLOCK = 32
+
+    def __init__(self, B: int, H: int, d: int, capacity: int, group: int = 1, max_queries: int = 1, kv: str = "e4m3",
+                 device=None):
+        L = lib()
+        if kv not in KV:
+            raise ValueError(f"kv must be one of {sorted(KV)}, got {kv!r}")
+        code, store = KV[kv]
+        self.B, self.H, self.d, self.capacity, self.group, self.max_queries = B, H, d, capacity, group, max_queries
+        self.kv = kv
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError("H2OBlockCache lives on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        shape = (B, H, d, capacity, group, max_queries, code)
+        with torch.cuda.device(self.device):
+            nbytes = L.h2o_bcache_workspace_bytes(*shape)
+            if nbytes == 0:
+                raise H2OError(1, f"h2o_bcache_workspace_bytes{shape}")
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            h = C.c_void_p()
+            _check(L.h2o_bcache_create(*shape, _ptr(self.workspace), C.c_void_p(self._stream()), C.byref(h)),
+                   "h2o_bcache_create")
+        self._h = h
+        at = [C.c_void_p() for _ in range(6)]
+        _check(L.h2o_bcache_arrays(h, *[C.byref(p) for p in at]), "h2o_bcache_arrays")
+        rows, blocks = (B, H, capacity), (B, H, capacity // self.BLOCK)
+        self.K, self.V = self._view(at[0], store, rows + (d,)), self._view(at[1], store, rows + (d,))
+        self.K_scale, self.V_scale = self._view(at[2], torch.float32, blocks), self._view(at[3], torch.float32, blocks)
+        self.pos, self.score = self._view(at[4], torch.int32, rows), self._view(at[5], torch.float32, rows)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None:
+            lib().h2o_bcache_destroy(h)
+            self._h = None
+
+    # -------------------------------------------------------------- helpers
+    def _view(self, p, dtype, shape):
+        at = p.value - self.workspace.data_ptr()
+        n = dtype.itemsize
+        for s in shape:
+            n *= s
+        return self.workspace[at : at + n].view(dtype).view(shape)
+
+    def _stream(self) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _use_stream(self):
+        _check(lib().h2o_bcache_set_stream(self._h, C.c_void_p(self._stream())), "h2o_bcache_set_stream")
+
+    def _dense(self, t, dtype, shape, name):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+        return C.c_void_p(t.data_ptr())
+
+    def _per_sequence(self, t, name, optional=True):
+        if t is None and not optional:
+            raise TypeError(f"{name} must be a tensor")
+        return self._dense(t, torch.int32, (self.B,), name)
+
+    def _rows(self, t, heads, n, name):
+        """h2o_rows of a [B, heads, n, d] bf16 tensor whose rows are contiguous."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dtype != torch.bfloat16 or t.device != self.device or tuple(t.shape) != (self.B, heads, n, self.d):
+            raise ValueError(f"{name}: expected torch.bfloat16 {(self.B, heads, n, self.d)} on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        sb, sh, st, one = t.stride()
+        # a dimension of size 1 is never stepped over: its stride may be anything
+        sb, sh, st = sb if self.B > 1 else 0, sh if heads > 1 else 0, st if n > 1 else 0
+        if one != 1 or sb % 8 or sh % 8 or st % 8 or t.data_ptr() % 16:
+            raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
+                             f"{t.stride()}")
+        return C.byref(Rows(t.data_ptr(), sb, sh, st))
+
+    @staticmethod
+    def _tokens(t, name):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name}: expected a [B, heads, n, d] tensor")
+        return t.shape[2]
+
+    # ---------------------------------------------------------------- calls
+    def append(self, k, v, lengths, counts=None, position=None, score=None):
+        """Quantise rows k, v [B, H, n, d] (bf16) into entries ``lengths[b]``
+        .. of each sequence, with positions from ``position`` (int32 [B],
+        default ``lengths``) and scores ``score`` (fp32 [B, H, n], for example
+        a prompt's column sums; default 0).  See h2o_bcache_append."""
+        n = self._tokens(k, "k")
+        args = (self._rows(k, self.H, n, "k"), self._rows(v, self.H, n, "v"),
+                self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts"),
+                self._per_sequence(position, "position"), self._dense(score, torch.float32, (self.B, self.H, n), "score"))
+        self._use_stream()
+        _check(lib().h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
+
+    def attend(self, q, lengths, counts=None, causal=True, accumulate=True, out=None, lse=None):
+        """Attention of q [B, H * group, n, d] over the ``lengths[b]`` entries
+        each sequence holds; returns out (shaped like q).  ``causal``: the last
+        entries are the queries' own tokens; ``accumulate``: the weights are
+        added to the entries' scores; ``lse`` (fp32 [B, H * group, n]) receives
+        the log-sum-exps.  See h2o_bcache_attend."""
+        n, heads = self._tokens(q, "q"), self.H * self.group
+        qr = self._rows(q, heads, n, "q")
+        lens, cnt = self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts")
+        if out is None:
+            out = self._new_out(q, counts)
+        args = (qr, lens, cnt, int(bool(causal)), int(bool(accumulate)), self._rows(out, heads, n, "out"),
+                self._dense(lse, torch.float32, (self.B, heads, n), "lse"))
+        self._use_stream()
+        _check(lib().h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
+        return out
+
+    def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None):
+        """Append k, v [B, H, n, d] behind ``lengths[b]`` entries, then attend
+        causally with q [B, H * group, n, d]; returns out.  The caller adds the
+        counts (or n) to ``lengths`` afterwards.  See h2o_bcache_step."""
+        n, heads = self._tokens(q, "q"), self.H * self.group
+        rows = (self._rows(q, heads, n, "q"), self._rows(k, self.H, n, "k"), self._rows(v, self.H, n, "v"))
+        lens, cnt = self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts")
+        if out is None:
+            out = self._new_out(q, counts)
+        args = rows + (lens, cnt, self._per_sequence(position, "position"), int(bool(accumulate)),
+                       self._rows(out, heads, n, "out"), self._dense(lse, torch.float32, (self.B, heads, n), "lse"))
+        self._use_stream()
+        _check(lib().h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
+        return out
+
+    def _new_out(self, q, counts):
+        # rows behind a sequence's count are not written
+        make = torch.empty if counts is None else torch.zeros
+        return make(q.shape, dtype=torch.bfloat16, device=self.device)
+
+    def evict(self, lengths, k_heavy: int, k_local: int, n_sink: int = 0, score_mode: int = 0, position=None,
+              new_lengths=None):
+        """Cut every sequence down to ``k_heavy + k_local`` entries: its last
+        ``k_local`` and the ``k_heavy`` others that rank highest (by score, or
+        with ``score_mode`` 1 by score / (position - pos)); entries at positions
+        below ``n_sink`` rank first.  Returns the new lengths (int32 [B]).  See
+        h2o_bcache_evict."""
+        if new_lengths is None:
+            new_lengths = torch.empty(self.B, dtype=torch.int32, device=self.device)
+        args = (self._per_sequence(lengths, "lengths", False), int(k_heavy), int(k_local), int(n_sink), int(score_mode),
+                self._per_sequence(position, "position"), self._per_sequence(new_lengths, "new_lengths"))
+        self._use_stream()
+        _check(lib().h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
+        return new_lengths
+
+    def error_bits(self) -> int:
+        """The sticky error flag (H2O_BERR_* bits; 0 = none); synchronises."""
+        self._use_stream()
+        bits = C.c_int32()
+        rc = lib().h2o_bcache_get_error(self._h, C.byref(bits))
+        if rc not in (0, 5):
+            _check(rc, "h2o_bcache_get_error")
+        return bits.value
+
+    def check_device_error(self):
+        bits = self.error_bits()
+        if bits:
+            raise H2OError(5, f"h2o_bcache_get_error (bits {bits})")

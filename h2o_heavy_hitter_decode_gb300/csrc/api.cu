@@ -27,6 +27,13 @@ cudaError_t launch_prefill_colsum_tc(const CacheView &c, const void *Q, const vo
 
 using namespace h2o;
 
+namespace {
+thread_local int g_last_cuda = 0;
+}
+namespace h2o {
+void note_cuda_error(cudaError_t e) { g_last_cuda = (int)e; }
+}  // namespace h2o
+
 struct h2o_cache {
   int B, H, d, kh, kl, k, nh;
   h2o_dtype dtype;
@@ -54,8 +61,6 @@ struct h2o_cache {
 };
 
 namespace {
-
-thread_local int g_last_cuda = 0;
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxPos = 0x7fffffffLL;  // positions are int32 tags
@@ -102,7 +107,7 @@ Layout layout(int nh, int k, int d, h2o_dtype dt, int nsplit) {
 }
 
 h2o_status cuda_fail(cudaError_t e) {
-  g_last_cuda = (int)e;
+  note_cuda_error(e);
   return H2O_ECUDA;
 }
 

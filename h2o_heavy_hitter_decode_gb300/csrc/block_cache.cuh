@@ -1,0 +1,103 @@
+// block_cache.cuh — what the kernels of the block-scaled 8-bit cache share
+// (h2o_bcache_* in include/h2o.h): its device view, the checked lengths of a
+// sequence, and the code formats with their power-of-two block scales.
+#pragma once
+
+#include "common.cuh"
+
+#include "../../include/h2o.h"
+
+namespace h2o {
+namespace blk {
+
+constexpr int kBlock = H2O_BLOCK;  // entries that share a scale
+constexpr int kMinExp = -100;      // least scale exponent
+
+struct View {
+  int B, H, d, cap, group, max_rows;  // max_rows = group * max_queries
+  int kv;                             // h2o_kv8
+  uint8_t *K, *V;                     // [B*H][cap][d] codes
+  float *Ksc, *Vsc;                   // [B*H][cap / kBlock]
+  int32_t *pos;                       // [B*H][cap]
+  float *score;                       // [B*H][cap]
+  float *logits;                      // [B*H][max_rows][cap] scratch, base-2 logits
+  float *part;                        // scratch, split partials
+  int32_t *kept;                      // [B*H][cap] scratch of an eviction (shares the logits' memory)
+  int *err;                           // [1] sticky H2O_BERR_* bits
+  int sms;
+};
+
+// Rows (b, h, t) of bf16 in memory, strides in elements.
+struct Rows {
+  const __nv_bfloat16 *p;
+  int64_t sb, sh, st;
+  __device__ __forceinline__ const __nv_bfloat16 *at(int b, int h, int t) const {
+    return p + b * sb + h * sh + t * st;
+  }
+};
+
+// The lengths of a call.  appends: the call's rows are entries len ..
+// len + cnt - 1 (before or after they were written).
+struct Lens {
+  const int32_t *lengths, *counts;
+  int n, appends, cap;
+};
+struct Seq {
+  int len, cnt, total;  // entries before the call, real rows, entries to attend over
+  bool ok;              // false: out of range, everything else 0
+};
+__device__ __forceinline__ Seq seq_of(const Lens &l, int b) {
+  Seq s;
+  s.len = l.lengths[b];
+  s.cnt = l.counts ? l.counts[b] : l.n;
+  s.ok = s.len >= 0 && s.cnt >= 0 && s.cnt <= l.n && s.len <= l.cap - (l.appends ? s.cnt : 0);
+  if (!s.ok) s.len = s.cnt = 0;
+  s.total = s.len + (l.appends ? s.cnt : 0);
+  return s;
+}
+
+// ------------------------------------------------------------------ formats
+struct E4M3 {
+  static constexpr float kMax = 448.f;  // 1.75 * 2^8
+  static constexpr int kMaxExp = 8;
+  static constexpr uint32_t kMaxMant = 0x600000u;
+  // x (finite, at most kMax up to rounding) to the nearest code, ties to even.
+  __device__ __forceinline__ static uint32_t code(float x) {
+    return (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+  }
+  // Four codes of a word as floats (exact).
+  __device__ __forceinline__ static void values(uint32_t w, float *x) { e4m3x4_to_f32(w, x); }
+};
+struct I8 {
+  static constexpr float kMax = 127.f;  // 1.984375 * 2^6
+  static constexpr int kMaxExp = 6;
+  static constexpr uint32_t kMaxMant = 0x7e0000u;
+  __device__ __forceinline__ static uint32_t code(float x) { return (uint32_t)__float2int_rn(x) & 0xffu; }
+  __device__ __forceinline__ static void values(uint32_t w, float *x) {
+    x[0] = (float)(int8_t)(w & 0xffu);
+    x[1] = (float)(int8_t)((w >> 8) & 0xffu);
+    x[2] = (float)(int8_t)((w >> 16) & 0xffu);
+    x[3] = (float)(int8_t)(w >> 24);
+  }
+};
+
+// The least power of two 2^e, e >= kMinExp, with amax <= F::kMax * 2^e (amax
+// finite, >= 0).
+template <typename F> __device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - F::kMaxExp + ((u & 0x7fffffu) > F::kMaxMant ? 1 : 0);
+  return __uint_as_float((uint32_t)((e < kMinExp ? kMinExp : e) + 127) << 23);
+}
+// 1 / s of a power of two between 2^kMinExp and 2^126.
+__device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// Launchers (each on the device that is current; arguments checked before).
+cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
+                          const float *score, cudaStream_t st);
+cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
+                          float *lse, cudaStream_t st);
+cudaError_t launch_evict(const View &c, const int32_t *lengths, int k_heavy, int k_local, int n_sink, int score_mode,
+                         const int32_t *position, int32_t *new_lengths, cudaStream_t st);
+
+}  // namespace blk
+}  // namespace h2o

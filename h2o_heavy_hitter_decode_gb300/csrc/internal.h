@@ -73,6 +73,8 @@ cudaError_t launch_prefill_select(const CacheView &c, const void *K, const void 
                                   const float *colsum, int L, cudaStream_t st);
 
 int num_sms_current_device();
+// Keeps e for h2o_last_cuda_error (per thread).
+void note_cuda_error(cudaError_t e);
 
 // cudaFuncGetAttributes of a library kernel on the current device.
 cudaError_t kernel_attributes(cudaFuncAttributes *a);

@@ -263,6 +263,128 @@ h2o_status h2o_decode_step_static(int B, int H, int d, int k_heavy, int k_local,
  * candidate).  The flag is sticky. */
 h2o_status h2o_get_error(h2o_cache_t cache);
 
+/* ---------------------------------------------------------------------------
+ * Block-scaled 8-bit caches: h2o_bcache_*.
+ *
+ * A cache of another shape than h2o_cache_t, for batches whose sequences
+ * differ in length and whose budget is enforced every so many steps instead
+ * of at each: per (sequence b, cached head h) up to `capacity` entries, entry
+ * j at index j, in the order of their positions.  `group` query heads share a
+ * cached head (query head hq reads cached head hq / group), up to
+ * `max_queries` query tokens per sequence and call (a decode step, or draft
+ * tokens to verify).  K and V are held as 8-bit codes with one scale for each
+ * block of H2O_BLOCK consecutive entries of a head; an entry reads back as
+ * code * scale.  Scales are powers of two, at least 2^-100: re-scaling a
+ * block's codes to a larger scale is then exact in e4m3 down to its
+ * subnormals, and all re-scalings of an int8 code together move it by less
+ * than one final step.
+ *
+ *   Quantisation of new rows into a block: a = the largest finite |x| among
+ *   the block's new rows, e(a) = the least e >= -100 with a <= Q * 2^e
+ *   (Q = 448 for e4m3, 127 for int8); the block's scale becomes
+ *   max(2^e(a), its scale before if it holds earlier entries); codes are
+ *   x / scale to nearest even; earlier codes are re-scaled the same way if the
+ *   scale grew.  A NaN is stored as 0 and an infinity as the largest code,
+ *   and both raise bit H2O_BERR_NONFINITE of the error flag.
+ *
+ * The entries a sequence holds are not kept in the cache: every call takes
+ * `lengths`, device int32 [B], so that one array serves the caches of every
+ * layer, a captured graph reads the current values, and draft tokens are
+ * taken back by passing the smaller length.  `counts` (device int32 [B] or
+ * NULL = n for every sequence) says how many of the call's n rows per
+ * sequence are real, 0 <= counts[b] <= n; rows behind them are not read and
+ * their outputs are left as they were.  A sequence whose length or count is
+ * out of range (also: lengths[b] + counts[b] > capacity in a call that
+ * appends) is left alone, outputs included, and raises bit H2O_BERR_RANGE.
+ *
+ * Input and output rows are bf16, given as h2o_rows: element (b, h, t, i) at
+ * data[b * stride_b + h * stride_h + t * stride_t + i], in elements; data
+ * 16-byte aligned, strides non-negative multiples of 8.  Output rows must not
+ * overlap.  The other conventions at the top of this file hold, and:
+ * calls of one cache must not overlap on the GPU (they share its scratch
+ * memory); they may be captured into graphs, and the graphs then share it
+ * too.  Work goes to the cache's device whatever device is current. */
+#define H2O_BLOCK 32
+#define H2O_BLOCK_MAX_ROWS 256 /* group * max_queries is at most this */
+typedef enum { H2O_KV_E4M3 = 0, H2O_KV_INT8 = 1 } h2o_kv8;
+typedef struct h2o_bcache *h2o_bcache_t; /* opaque host-side handle */
+typedef struct {
+  const void *data; /* device, bf16; outputs are written through it */
+  int64_t stride_b, stride_h, stride_t;
+} h2o_rows;
+
+/* Bytes of device workspace (0 for invalid shapes).  B, H >= 1, B * H <=
+ * 2^24; d in {64, 128}; capacity a multiple of H2O_BLOCK, B * H * capacity <
+ * 2^31; group, max_queries >= 1, group * max_queries <= H2O_BLOCK_MAX_ROWS. */
+size_t h2o_bcache_workspace_bytes(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv);
+
+/* Create over caller-owned device memory (256-byte aligned) of the current
+ * device; enqueues its initialisation (codes, scales and scores 0, positions
+ * -1). */
+h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv,
+                             void *workspace, void *cuda_stream, h2o_bcache_t *out);
+h2o_status h2o_bcache_destroy(h2o_bcache_t cache); /* NULL is OK */
+h2o_status h2o_bcache_set_stream(h2o_bcache_t cache, void *cuda_stream);
+
+/* Device pointers of the cache's arrays (any may be NULL): codes K, V
+ * [B][H][capacity][d], scales [B][H][capacity / H2O_BLOCK] fp32, pos
+ * [B][H][capacity] int32, score [B][H][capacity] fp32.  The caller may read
+ * and, between calls, write them; scales must stay powers of two of at least
+ * 2^-100 in blocks that hold entries, and e4m3 codes must not be NaN. */
+h2o_status h2o_bcache_arrays(h2o_bcache_t cache, void **K, void **V, float **K_scale, float **V_scale,
+                             int32_t **pos, float **score);
+
+/* Append n >= 1 rows per sequence: k, v (B, H, n, d) quantised into entries
+ * lengths[b] .. lengths[b] + counts[b] - 1.  Entry lengths[b] + t gets
+ * position position[b] + t (position: device int32 [B], or NULL =
+ * lengths) and score score[b][h][t] (device fp32 [B][H][n], for example the
+ * prompt's column sums of h2o_prefill, or NULL = 0). */
+h2o_status h2o_bcache_append(h2o_bcache_t cache, int n, const h2o_rows *k, const h2o_rows *v,
+                             const int32_t *lengths, const int32_t *counts, const int32_t *position,
+                             const float *score);
+
+/* Attention of n <= max_queries query tokens per sequence over the
+ * lengths[b] entries it holds, scale 1/sqrt(d).  q, out (B, H * group, n, d);
+ * out must not overlap any other argument.  causal: query t sees entries
+ * 0 .. lengths[b] - counts[b] + t (the last counts[b] entries are the
+ * queries' own tokens); else every entry.  accumulate: each entry's
+ * softmax weights, summed over the head's group and the counts[b] queries,
+ * are added to its score.  lse: device fp32 [B][H * group][n], natural-log
+ * log-sum-exp of the scaled logits, or NULL.  A query that sees no entry gets
+ * output 0 and lse -infinity. */
+h2o_status h2o_bcache_attend(h2o_bcache_t cache, int n, const h2o_rows *q, const int32_t *lengths,
+                             const int32_t *counts, int causal, int accumulate, const h2o_rows *out, float *lse);
+
+/* h2o_bcache_append (new scores 0) followed by the causal h2o_bcache_attend
+ * over lengths[b] + counts[b] entries, with the same results.  `lengths` are
+ * those before the call; the caller adds the counts afterwards. */
+h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h2o_rows *k, const h2o_rows *v,
+                           const int32_t *lengths, const int32_t *counts, const int32_t *position,
+                           int accumulate, const h2o_rows *out, float *lse);
+
+/* Evict down to k = k_heavy + k_local >= 1 entries per head.  A sequence with
+ * lengths[b] <= k stays as it is.  Otherwise the last k_local entries stay
+ * plus the k_heavy others that rank highest, by score or (score_mode 1) by
+ * score / (position[b] - pos), both in fp32 with the divisor at least 1;
+ * entries whose pos is below n_sink (0 <= n_sink <= k_heavy) rank above all;
+ * a NaN ranks below all; among equals the lowest index goes first.  The kept
+ * entries move to indices 0 .. k-1 in their order with their positions and
+ * scores, and every block of them is quantised anew from the values its
+ * entries stood for (a fresh block in the sense above).  What lies behind
+ * index k - 1 is left as it was.  position: device int32 [B], the position the
+ * next token takes, or NULL = lengths; read in score_mode 1 only.
+ * new_lengths: device int32 [B], receives min(lengths[b], k) (lengths[b]
+ * itself where it is out of range); must not overlap lengths. */
+h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_heavy, int k_local, int n_sink,
+                            int score_mode, const int32_t *position, int32_t *new_lengths);
+
+/* Synchronises the stream and reads the sticky error flag: H2O_OK, or
+ * H2O_EDEVICE with its bits in *bits (may be NULL). */
+#define H2O_BERR_RANGE 1     /* a length or count out of range: that sequence was left alone */
+#define H2O_BERR_NONFINITE 2 /* a NaN or infinity was appended */
+#define H2O_BERR_INTERNAL 4  /* a kernel gave up a wait, or found a count that does not add up */
+h2o_status h2o_bcache_get_error(h2o_bcache_t cache, int *bits);
+
 /* Human-readable name of a status; the last CUDA error code seen by the
  * library (0 = none). */
 const char *h2o_status_str(h2o_status s);

@@ -1,0 +1,473 @@
+"""GPU tests of H2OBlockCache (append, attend, step, evict) against the plain
+64-bit reference of block_reference.py: codes, scales, positions and kept
+entries exactly, outputs, log-sum-exps and scores within the reference's
+derived tolerances."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from block_reference import BLOCK, RefCache, close, load, same_state
+from h2o_heavy_hitter_decode_gb300 import H2OBlockCache, H2OError
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def rows(g, B, heads, n, d, layout="dense", scale=1.0):
+    """bf16 [B, heads, n, d]: dense, a view of token-first rows, a slice of a wider row, or one head broadcast."""
+    if layout == "tokens":
+        return (torch.randn(B, n, heads, d, generator=g, device=DEV) * scale).bfloat16().transpose(1, 2)
+    if layout == "slice":
+        return (torch.randn(B, n, heads + 3, d + 16, generator=g, device=DEV) * scale).bfloat16()[:, :, 2:-1, 8:-8].transpose(1, 2)
+    if layout == "broadcast":
+        return (torch.randn(B, 1, n, d, generator=g, device=DEV) * scale).bfloat16().expand(B, heads, n, d)
+    return (torch.randn(B, heads, n, d, generator=g, device=DEV) * scale).bfloat16()
+
+
+def filled(seed, B, H, d, cap, lens, group=1, max_queries=1, kv="e4m3", scale=1.0, junk=True):
+    """A cache and its reference with lens entries per sequence; places behind them hold other sequences' rows,
+    e4m3 NaN codes and infinite scales among them."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    c = H2OBlockCache(B, H, d, cap, group=group, max_queries=max_queries, kv=kv)
+    full = rows(g, B, H, cap, d, scale=scale)
+    c.append(full, rows(g, B, H, cap, d, scale=scale), ints([0] * B), score=torch.rand(B, H, cap, generator=g, device=DEV) * 9)
+    if junk:
+        for b, n in enumerate(lens):
+            if kv == "e4m3":
+                c.K.view(torch.uint8)[b, :, n:] = 0x7F
+                c.V.view(torch.uint8)[b, :, n:] = 0xFF
+            first = (n + BLOCK - 1) // BLOCK
+            c.K_scale[b, :, first:] = math.inf
+            c.V_scale[b, :, first:] = math.nan
+            c.score[b, :, n:] = math.nan
+    r = RefCache(B, H, d, cap, group, kv)
+    load(r, c)
+    return c, r, g
+
+
+# ------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("layout", ["dense", "tokens", "slice", "broadcast"])
+@pytest.mark.parametrize("kv,d", [("e4m3", 128), ("e4m3", 64), ("int8", 128), ("int8", 64)])
+def test_append_ragged(kv, d, layout):
+    lens = [0, 1, 31, 32, 33, 95, 60]
+    counts = [70, 0, 1, 33, 31, 5, 64]
+    c, r, g = filled(11, 7, 3, d, 160, lens, kv=kv)
+    k, v = rows(g, 7, 3, 70, d, layout), rows(g, 7, 3, 70, d, layout, scale=3.0)
+    score = torch.rand(7, 3, 70, generator=g, device=DEV)
+    where = [1000 * b for b in range(7)]
+    c.append(k, v, ints(lens), ints(counts), position=ints(where), score=score)
+    r.append(k, v, lens, counts, where, score)
+    same_state(c, r)
+    assert c.error_bits() == 0
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_append_one_at_a_time_scale_grows(kv):
+    g = torch.Generator(DEV).manual_seed(2)
+    c = H2OBlockCache(2, 2, 64, 96, kv=kv)
+    r = RefCache(2, 2, 64, 96, 1, kv)
+    for t in range(75):
+        k = rows(g, 2, 2, 1, 64, scale=2.0 ** ((t * 5) % 13 - 6))
+        v = rows(g, 2, 2, 1, 64, scale=1.1 ** t)
+        c.append(k, v, ints([t, t + 3]))
+        r.append(k, v, [t, t + 3])
+    same_state(c, r)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_append_extreme_values(kv):
+    """Zeros, bf16's least and largest numbers, the borders of the code range, infinities and NaN."""
+    x = torch.zeros(1, 4, 40, 64)
+    x[0, 0, 0, :4] = torch.tensor([448.0, -448.0, 127.0, 0.5])
+    x[0, 0, 33, :2] = torch.tensor([450.0, 127.5])
+    x[0, 1, 5, :3] = torch.tensor([1e-40, -9e-41, 1.2e-38])
+    x[0, 1, 35, 0] = 2.0 ** -101
+    x[0, 2, 7, :3] = torch.tensor([3.0e38, -1.0e38, 1.0])
+    x[0, 3, 9, :4] = torch.tensor([math.inf, -math.inf, math.nan, 2.5])
+    x[0, 3, 39, 0] = math.nan
+    k = x.bfloat16().to(DEV)
+    c = H2OBlockCache(1, 4, 64, 64, kv=kv)
+    r = RefCache(1, 4, 64, 64, 1, kv)
+    c.append(k, -k, ints([0]))
+    r.append(k, -k, [0])
+    same_state(c, r)
+    assert c.error_bits() == 2
+    with pytest.raises(H2OError):
+        c.check_device_error()
+
+
+# ------------------------------------------------------------------- attend
+
+ATTEND = [  # B, H, G, n, d, kv, cap, lens, counts, causal
+    (1, 1, 1, 1, 128, "e4m3", 32, [1], None, True),
+    (1, 1, 1, 1, 64, "int8", 32, [32], None, True),
+    (3, 2, 1, 1, 128, "int8", 96, [33, 0, 96], None, True),
+    (9, 3, 2, 1, 64, "e4m3", 128, [1, 2, 31, 32, 33, 64, 65, 127, 128], None, True),
+    (2, 2, 4, 1, 128, "e4m3", 1024, [1000, 517], None, False),
+    (3, 2, 8, 2, 128, "int8", 512, [500, 2, 77], [2, 1, 0], True),
+    (2, 1, 5, 7, 64, "int8", 256, [256, 3], None, True),        # 35 rows, fewer entries than queries
+    (2, 2, 1, 16, 128, "e4m3", 160, [150, 9], [16, 13], True),
+    (2, 2, 3, 16, 64, "e4m3", 160, [150, 9], [16, 3], False),   # 48 rows
+    (1, 2, 16, 4, 128, "e4m3", 96, [90], None, True),           # 64 rows
+    (2, 1, 71, 1, 64, "int8", 96, [90, 31], None, True),        # one cached head for 71
+    (1, 1, 16, 16, 128, "int8", 96, [70], [11], True),          # 256 rows
+    (40, 2, 1, 1, 64, "e4m3", 64, [(7 * b) % 65 for b in range(40)], None, True),
+    (1, 2, 2, 1, 128, "e4m3", 8192, [8191], None, True),
+]
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: "-".join(str(x) for x in c[:7]))
+@pytest.mark.parametrize("layout", ["dense", "slice"])
+def test_attend(case, layout):
+    B, H, G, n, d, kv, cap, lens, counts, causal = case
+    c, r, g = filled(21, B, H, d, cap, lens, G, n, kv)
+    q = rows(g, B, H * G, n, d, layout, scale=2.0)
+    out = rows(g, B, H * G, n, d, layout)
+    lse = torch.full((B, H * G, n), 7.0, device=DEV)
+    before = out.clone()
+    res = c.attend(q, ints(lens), None if counts is None else ints(counts), causal=causal, out=out, lse=lse)
+    assert res is out
+    want, want_lse, tol, lse_tol = r.attend(q, lens, counts, causal)
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    idle = want_lse.isnan()  # rows behind the counts
+    assert torch.equal(out.cpu()[idle], before.cpu()[idle]) and (lse.cpu()[idle] == 7.0).all()
+    same_state(c, r)
+    assert c.error_bits() == 0
+    # again, without touching the scores
+    out2 = c.attend(q, ints(lens), None if counts is None else ints(counts), causal=causal, accumulate=False)
+    live = ~idle
+    assert torch.equal(out2.cpu()[live], out.cpu()[live])
+    same_state(c, r)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_attend_scales_of_very_different_size(kv):
+    """Blocks whose V scales lie 2^40 apart, a block of zeros, and a block that takes all the weight."""
+    lens = [192, 160]
+    c, r, g = filled(31, 2, 2, 128, 192, lens, 4, 1, kv)
+    for j, e in enumerate([-30, 10, -3, 0, -30, 7]):
+        c.V_scale[:, :, j] = 2.0 ** e
+    c.V.view(torch.uint8)[:, 0, 32:64] = 0
+    c.V_scale[:, 0, 1] = 2.0 ** -100
+    load(r, c)
+    q = rows(g, 2, 8, 1, 128, scale=1.0)
+    key = (c.K[0, 1, 70].float() * c.K_scale[0, 1, 2]).bfloat16()
+    q[0, 5, 0] = key * 3
+    lse = torch.zeros(2, 8, 1, device=DEV)
+    out = c.attend(q, ints(lens), lse=lse)
+    want, want_lse, tol, lse_tol = r.attend(q, lens)
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    same_state(c, r)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** 14, 2.0 ** 60])
+def test_attend_query_sizes(size):
+    """Queries far outside f16's range; with the large ones one entry takes all the weight."""
+    lens = [100]
+    c, r, g = filled(37, 1, 2, 64, 128, lens, 2, 2, "e4m3")
+    q = rows(g, 1, 4, 2, 64, scale=size)
+    lse = torch.zeros(1, 4, 2, device=DEV)
+    out = c.attend(q, ints(lens), lse=lse)
+    want, want_lse, tol, lse_tol = r.attend(q, lens)
+    top = (want_lse.abs().amax() * 2.0 ** -18).item()
+    if size < 2.0 ** 13:
+        close(out, want, tol, "out")
+        same_state(c, r)
+    assert torch.isfinite(out).all()
+    assert ((lse.cpu().double() - want_lse).abs() <= lse_tol + top).all()
+    assert abs(float((c.score[:, :, :100].double().cpu().sum() - r.score[:, :, :100].sum()))) <= 1e-3
+
+
+def test_attend_many_splits_long():
+    """One head long enough that every worker of the device holds a part of it."""
+    n = 70000
+    cap = (n + 31) // 32 * 32
+    c, r, g = filled(41, 1, 1, 64, cap, [n], 3, 2, "int8", junk=True)
+    q = rows(g, 1, 3, 2, 64, scale=4.0)
+    lse = torch.zeros(1, 3, 2, device=DEV)
+    out = c.attend(q, ints([n]), lse=lse)
+    want, want_lse, tol, lse_tol = r.attend(q, [n])
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    same_state(c, r)
+
+
+# --------------------------------------------------------------------- step
+
+@pytest.mark.parametrize("kv,d,G,n", [("e4m3", 128, 1, 1), ("int8", 64, 4, 1), ("e4m3", 64, 3, 5), ("int8", 128, 8, 3)])
+@pytest.mark.parametrize("layout", ["dense", "tokens"])
+def test_step_is_append_then_attend(kv, d, G, n, layout):
+    lens = [0, 1, 30, 32, 63, 200]
+    counts = [n, max(n - 1, 0), n, 0, n, 1]
+    a, r, g = filled(51, 6, 2, d, 224, lens, G, n, kv)
+    z = H2OBlockCache(6, 2, d, 224, group=G, max_queries=n, kv=kv)
+    for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
+        getattr(z, name).copy_(getattr(a, name))
+    q, k, v = rows(g, 6, 2 * G, n, d, layout), rows(g, 6, 2, n, d, layout), rows(g, 6, 2, n, d, layout)
+    where = ints([x + 5 for x in lens])
+    lse = torch.zeros(6, 2 * G, n, device=DEV)
+    out = a.step(q, k, v, ints(lens), ints(counts), position=where, lse=lse)
+    want, want_lse, tol, lse_tol = r.step(q, k, v, lens, counts, [x + 5 for x in lens])
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    same_state(a, r)
+    z.append(k, v, ints(lens), ints(counts), position=where)
+    out2 = z.attend(q, ints([x + y for x, y in zip(lens, counts)]), ints(counts))
+    assert torch.equal(out, out2)
+    for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
+        x, y = getattr(a, name), getattr(z, name)
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+
+
+# -------------------------------------------------------------------- evict
+
+EVICT = [  # lens, k_heavy, k_local, n_sink, mode
+    ([0, 1, 39, 40, 41, 64, 200, 173], 20, 20, 0, 0),
+    ([0, 1, 39, 40, 41, 64, 200, 173], 40, 0, 3, 1),
+    ([0, 1, 39, 40, 41, 64, 200, 173], 0, 40, 0, 0),
+    ([224, 224, 1, 2, 3, 100, 50, 33], 1, 0, 1, 0),
+    ([224, 223, 33, 32, 160, 161, 159, 96], 32, 1, 32, 1),
+    ([224, 223, 33, 32, 160, 161, 159, 96], 7, 190, 0, 1),
+]
+
+
+@pytest.mark.parametrize("kv,d", [("e4m3", 128), ("int8", 64), ("e4m3", 64), ("int8", 128)])
+@pytest.mark.parametrize("case", EVICT, ids=str)
+def test_evict(case, kv, d):
+    lens, kh, kl, sink, mode = case
+    c, r, g = filled(61, 8, 3, d, 224, lens, kv=kv)
+    gaps = torch.randint(1, 4, (8, 3, 224), generator=g, device=DEV)
+    c.pos.copy_(gaps.cumsum(-1) - gaps[..., :1])
+    r.pos.copy_(c.pos.cpu())
+    where = [900 + b for b in range(8)]
+    new = c.evict(ints(lens), kh, kl, n_sink=sink, score_mode=mode, position=ints(where))
+    assert new.tolist() == r.evict(lens, kh, kl, sink, mode, where)
+    same_state(c, r)
+    assert c.error_bits() == 0
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_evict_ties_and_odd_scores(kv):
+    """Equal scores, zeros of both signs, negative ones, infinities, NaN, and positions that repeat below n_sink."""
+    lens = [300, 300, 300, 290]
+    c, r, g = filled(67, 4, 2, 64, 320, lens, kv=kv, junk=False)
+    c.score[0] = 1.0
+    c.score[1] = torch.randint(-2, 3, (2, 320), generator=g, device=DEV).float() * 0.5
+    c.score[1][c.score[1] == 0] = torch.tensor(-0.0, device=DEV)
+    c.score[1, :, ::7] = 0.0
+    c.score[2, :, ::3] = math.inf
+    c.score[2, :, 1::5] = -math.inf
+    c.score[2, :, 2::11] = math.nan
+    c.score[3] = math.nan
+    c.pos[3, :, 100:260] = 1
+    load(r, c)
+    new = c.evict(ints(lens), 90, 37, n_sink=5)
+    assert new.tolist() == r.evict(lens, 90, 37, 5)
+    same_state(c, r)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_evict_rows_of_zeros_and_far_scales(kv):
+    lens = [128]
+    c, r, g = filled(71, 1, 2, 64, 128, lens, kv=kv, junk=False)
+    for j, e in enumerate([100, -90, 3, -100]):
+        c.K_scale[:, :, j] = 2.0 ** e
+        c.V_scale[:, :, j] = 2.0 ** -e if e > -100 else 2.0 ** 60
+    c.K.view(torch.uint8)[:, :, :32] = 0  # zeros under a scale of 2^100
+    load(r, c)
+    assert c.evict(ints(lens), 30, 30).tolist() == r.evict(lens, 30, 30)
+    same_state(c, r)
+
+
+def test_evict_long():
+    n, k = 60000, 9001
+    c, r, g = filled(73, 1, 2, 64, 60000, [n], kv="e4m3", junk=False)
+    new = c.evict(ints([n]), k - 4000, 4000)
+    assert new.tolist() == r.evict([n], k - 4000, 4000)
+    same_state(c, r)
+
+
+# -------------------------------------------------- used together, and where
+
+def test_serving_run():
+    """Prompts of different lengths, decode steps, an eviction, draft tokens of which some are taken back, another
+    eviction: every output and the whole state against the reference throughout."""
+    B, H, G, d, cap, kv = 4, 2, 4, 64, 192, "e4m3"
+    g = torch.Generator(DEV).manual_seed(83)
+    c, r = H2OBlockCache(B, H, d, cap, group=G, max_queries=4, kv=kv), RefCache(B, H, d, cap, G, kv)
+    lens, pos = [0] * B, [0] * B
+
+    def grow(by):
+        for b in range(B):
+            lens[b] += by[b]
+            pos[b] += by[b]
+
+    prompt = [100, 7, 64, 33]
+    k, v, s = rows(g, B, H, 100, d), rows(g, B, H, 100, d), torch.rand(B, H, 100, generator=g, device=DEV)
+    c.append(k, v, ints(lens), ints(prompt), score=s)
+    r.append(k, v, lens, prompt, score=s)
+    grow(prompt)
+    for step in range(24):
+        n = 4 if step % 5 == 4 else 1
+        counts = [n - (b + step) % n for b in range(B)]
+        q, k, v = rows(g, B, H * G, n, d, scale=3.0), rows(g, B, H, n, d), rows(g, B, H, n, d)
+        out = c.step(q, k, v, ints(lens), ints(counts), position=ints(pos))
+        want, _, tol, _ = r.step(q, k, v, lens, counts, pos)
+        close(out, want, tol, f"step {step}")
+        grow([max(1, m - step % 3) if m else 0 for m in counts])  # the last draft tokens taken back
+        if step in (9, 17):
+            load(r, c)  # the scores' roundings must not pick other entries than the kernel's
+            new = c.evict(ints(lens), 24, 16, n_sink=2, score_mode=step % 2, position=ints(pos))
+            lens = r.evict(lens, 24, 16, 2, step % 2, pos)
+            assert new.tolist() == lens
+        same_state(c, r)
+    assert c.error_bits() == 0
+
+
+def test_prefill_then_block_cache():
+    """The prompt through H2OCache.prefill (its column sums are the scores), then the block cache."""
+    from h2o_heavy_hitter_decode_gb300 import H2OCache
+    B, H, d, L = 2, 3, 128, 200
+    g = torch.Generator(DEV).manual_seed(89)
+    Q, K, V = (rows(g, B, H, L, d) for _ in range(3))
+    _, _, colsum = H2OCache(B, H, d, 16, 16).prefill(Q, K, V)
+    c, r = H2OBlockCache(B, H, d, 256), RefCache(B, H, d, 256, 1, "e4m3")
+    c.append(K, V, ints([0, 0]), score=colsum)
+    r.append(K, V, [0, 0], score=colsum)
+    assert c.evict(ints([L, L]), 40, 24).tolist() == r.evict([L, L], 40, 24) == [64, 64]
+    q, k, v = (rows(g, B, H, 1, d) for _ in range(3))
+    out = c.step(q, k, v, ints([64, 64]), position=ints([L, L]))
+    want, _, tol, _ = r.step(q, k, v, [64, 64], position=[L, L])
+    close(out, want, tol, "out")
+    same_state(c, r)
+
+
+def test_captured_step_reads_current_lengths():
+    B, H, G, d = 3, 2, 2, 64
+    lens = [10, 40, 63]
+    c, r, g = filled(97, B, H, d, 128, lens, G, 1, "int8")
+    z, _, _ = filled(97, B, H, d, 128, lens, G, 1, "int8")
+    L = ints(lens)
+    q, k, v = rows(g, B, H * G, 1, d), rows(g, B, H, 1, d), rows(g, B, H, 1, d)
+    out = torch.zeros(B, H * G, 1, d, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.step(q, k, v, L, out=out)  # warm-up outside of the capture, at the same lengths
+    torch.cuda.current_stream().wait_stream(side)
+    for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
+        getattr(c, name).copy_(getattr(z, name))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.step(q, k, v, L, out=out)
+        new = c.evict(L + 1, 30, 20)
+    load(r, z)
+    cur = lens
+    for i in range(3):
+        L.copy_(ints(cur))
+        for x in (q, k, v):
+            x.copy_(rows(g, *x.shape))
+        graph.replay()
+        want, _, tol, _ = r.step(q, k, v, cur)
+        close(out, want, tol, f"replay {i}")
+        cur = r.evict([x + 1 for x in cur], 30, 20)
+        assert new.tolist() == cur
+        same_state(c, r)
+
+
+def test_other_stream():
+    lens = [500, 77]
+    c, r, g = filled(101, 2, 2, 128, 512, lens, 2, 1, "e4m3")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    q, k, v = rows(g, 2, 4, 1, 128), rows(g, 2, 2, 1, 128), rows(g, 2, 2, 1, 128)
+    L = ints(lens)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        out = c.step(q, k, v, L)
+    s.synchronize()
+    want, _, tol, _ = r.step(q, k, v, lens)
+    close(out, want, tol, "out")
+    same_state(c, r)
+
+
+def test_same_call_twice_gives_the_same_bits():
+    lens = [3000, 1234, 17]
+    outs = []
+    for _ in range(2):
+        c, _, g = filled(103, 3, 4, 128, 3008, lens, 4, 2, "e4m3")
+        q = rows(g, 3, 16, 2, 128)
+        lse = torch.zeros(3, 16, 2, device=DEV)
+        out = c.attend(q, ints(lens), lse=lse)
+        outs.append((out, lse, c.score[0, :, :3000].clone(), c.score[1, :, :1234].clone()))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_ranges_out_of_bounds_leave_the_sequence_alone():
+    lens = [64, 64, 64, 64, 64]
+    c, r, g = filled(107, 5, 2, 64, 96, lens, 2, 2, "int8")
+    q, k, v = rows(g, 5, 4, 2, 64), rows(g, 5, 2, 2, 64), rows(g, 5, 2, 2, 64)
+    out = torch.full((5, 4, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((5, 4, 2), 9.0, device=DEV)
+    bad_lens, bad_counts = [64, -1, 95, 64, 64], [2, 1, 2, 3, -1]
+    c.step(q, k, v, ints(bad_lens), ints(bad_counts), out=out, lse=lse)
+    assert c.error_bits() == 1
+    assert (out[1:] == 9).all() and (lse[1:] == 9).all()
+    want, _, tol, _ = r.step(q, k, v, bad_lens[:1] + [0] * 4, bad_counts[:1] + [0] * 4)
+    close(out, want, tol, "out")
+    same_state(c, r)
+    c2, r2, _ = filled(109, 3, 2, 64, 96, [96] * 3)
+    assert c2.evict(ints([97, -5, 96]), 10, 10).tolist() == [97, -5, 20]
+    assert c2.error_bits() == 1
+    r2.evict([0, 0, 96], 10, 10)
+    same_state(c2, r2)
+
+
+def test_arguments_rejected():
+    c = H2OBlockCache(2, 2, 64, 64, group=2, max_queries=2, kv="int8")
+    q, k = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16, device=DEV)
+    L = ints([0, 0])
+    c.step(q, k, k, L)
+    bad = [
+        lambda: c.step(q.float(), k, k, L), lambda: c.step(q, k.half(), k, L), lambda: c.step(q.cpu(), k, k, L),
+        lambda: c.step(q[:1], k, k, L), lambda: c.step(q, k, k[:, :1], L), lambda: c.step(q, k, k, L.long()),
+        lambda: c.step(q, k, k, ints([0])), lambda: c.step(q, k, k, L.cpu()), lambda: c.step(q, k, k, L, counts=L.float()),
+        lambda: c.step(q[..., 0], k, k, L), lambda: c.step(None, k, k, L), lambda: c.step(q, k, k, None),
+        lambda: c.step(q, k, k, L, lse=torch.zeros(2, 4, 2, device=DEV)),
+        lambda: c.step(q, k, k, L, out=torch.zeros(2, 4, 1, 64, device=DEV)),
+        lambda: c.step(q, k, k, L, out=torch.zeros(2, 1, 1, 64, device=DEV, dtype=torch.bfloat16).expand(2, 4, 1, 64)),
+        lambda: c.step(q.transpose(1, 3).contiguous().transpose(1, 3), k, k, L),
+        lambda: c.append(torch.zeros(2 * 2 * 65 + 1, dtype=torch.bfloat16, device=DEV)[1:261].view(2, 2, 65)[..., :64].unsqueeze(2), k, L),
+        lambda: c.append(torch.zeros(2, 2, 65, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 2, 65, 64, dtype=torch.bfloat16, device=DEV), L),
+        lambda: c.append(k, k, L, score=torch.zeros(2, 2, device=DEV)),
+        lambda: c.attend(torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device=DEV), L),
+        lambda: c.evict(L, 0, 0), lambda: c.evict(L, -1, 4), lambda: c.evict(L, 4, -1), lambda: c.evict(L, 4, 4, n_sink=5),
+        lambda: c.evict(L, 4, 4, score_mode=2), lambda: c.evict(L, 4, 4, new_lengths=L), lambda: c.evict(L.float(), 4, 4),
+        lambda: H2OBlockCache(2, 2, 96, 64), lambda: H2OBlockCache(2, 2, 64, 40), lambda: H2OBlockCache(2, 2, 64, 64, group=32, max_queries=9),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((TypeError, ValueError, H2OError)):
+            call()
+            print("not refused:", i)
+    assert c.error_bits() == 0
+
+
+def test_new_cache_is_empty():
+    c = H2OBlockCache(1, 2, 128, 64)
+    assert (c.pos == -1).all() and (c.score == 0).all() and (c.K.float() == 0).all() and (c.V_scale == 0).all()
+    q = torch.ones(1, 2, 1, 128, dtype=torch.bfloat16, device=DEV)
+    assert (c.attend(q, ints([0])) == 0).all()
