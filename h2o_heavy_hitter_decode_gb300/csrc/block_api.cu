@@ -1,5 +1,7 @@
 // block_api.cu — the C ABI of the block-scaled 8-bit caches (h2o_bcache_* in
 // include/h2o.h): argument checks, the workspace carve-up and the launches.
+#include <cudaTypedefs.h>
+
 #include <cstdint>
 #include <new>
 
@@ -9,6 +11,7 @@ using namespace h2o;
 
 struct h2o_bcache {
   blk::View view;
+  CUtensorMap kmap, vmap;
   int max_queries;
   int device;
   cudaStream_t stream;
@@ -52,9 +55,9 @@ bool shape_ok(int B, int H, int d, int64_t capacity, int group, int max_queries,
 bool d_supported(int d) { return d == 64 || d == 128; }
 
 struct Layout {
-  size_t K, V, Ksc, Vsc, pos, score, scratch, err, total;
+  size_t K, V, Ksc, Vsc, pos, score, logits, part, err, total;
 };
-Layout layout(int B, int H, int d, int64_t cap, int rows) {
+Layout layout(int B, int H, int d, int64_t cap, int rows, int sms) {
   const size_t nh = (size_t)B * H, entries = nh * (size_t)cap, scales = entries / H2O_BLOCK * sizeof(float);
   Layout l;
   size_t o = 0;
@@ -64,7 +67,8 @@ Layout layout(int B, int H, int d, int64_t cap, int rows) {
   l.Vsc = o;     o = align_up(o + scales);
   l.pos = o;     o = align_up(o + entries * sizeof(int32_t));
   l.score = o;   o = align_up(o + entries * sizeof(float));
-  l.scratch = o; o = align_up(o + entries * rows * sizeof(float));
+  l.logits = o;  o = align_up(o + entries * rows * sizeof(float));
+  l.part = o;    o = align_up(o + blk::attend_scratch_bytes(B, H, d, rows, sms));
   l.err = o;     o = align_up(o + sizeof(int));
   l.total = o;
   return l;
@@ -101,6 +105,22 @@ blk::Rows rows_of(const h2o_rows *r) {
   return blk::Rows{(const __nv_bfloat16 *)r->data, r->stride_b, r->stride_h, r->stride_t};
 }
 
+// The codes as a matrix of d-byte rows in boxes of one block, with the widest
+// swizzle a row allows.
+bool code_map(CUtensorMap *m, const void *base, int d, int64_t entries) {
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)entries}, strides[1] = {(cuuint64_t)d};
+  const cuuint32_t box[2] = {(cuuint32_t)d, H2O_BLOCK}, step[2] = {1, 1};
+  return ((PFN_cuTensorMapEncodeTiled_v12000)p)(
+             m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool ints_ok(const int32_t *p, bool may_be_null) { return p ? aligned(p, 4) : may_be_null; }
 
 }  // namespace
@@ -109,7 +129,9 @@ extern "C" {
 
 size_t h2o_bcache_workspace_bytes(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv) {
   if (!shape_ok(B, H, d, capacity, group, max_queries, kv) || !d_supported(d)) return 0;
-  return layout(B, H, d, capacity, group * max_queries).total;
+  const int sms = num_sms_current_device();
+  if (sms <= 0) return 0;
+  return layout(B, H, d, capacity, group * max_queries, sms).total;
 }
 
 h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv,
@@ -125,7 +147,7 @@ h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, i
   if (!c) return H2O_ENOMEM;
   c->max_queries = max_queries;
   c->stream = (cudaStream_t)cuda_stream;
-  const Layout l = layout(B, H, d, capacity, group * max_queries);
+  const Layout l = layout(B, H, d, capacity, group * max_queries, sms);
   char *w = (char *)workspace;
   blk::View &v = c->view;
   v.B = B; v.H = H; v.d = d; v.cap = (int)capacity; v.group = group; v.max_rows = group * max_queries;
@@ -133,13 +155,18 @@ h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, i
   v.K = (uint8_t *)w + l.K; v.V = (uint8_t *)w + l.V;
   v.Ksc = (float *)(w + l.Ksc); v.Vsc = (float *)(w + l.Vsc);
   v.pos = (int32_t *)(w + l.pos); v.score = (float *)(w + l.score);
-  v.logits = (float *)(w + l.scratch); v.kept = (int32_t *)(w + l.scratch);
-  v.part = nullptr;
+  v.logits = (float *)(w + l.logits); v.kept = (int32_t *)(w + l.logits);
+  v.part = (float *)(w + l.part);
   v.err = (int *)(w + l.err);
+  const int64_t entries = (int64_t)B * H * capacity;
+  if (!code_map(&c->kmap, v.K, d, entries) || !code_map(&c->vmap, v.V, d, entries)) {
+    delete c;
+    return fail(cudaErrorNotSupported);
+  }
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaMemsetAsync(w + l.K, 0, l.pos - l.K, c->stream);  // codes and scales
   if (e == cudaSuccess) e = cudaMemsetAsync(v.pos, 0xff, l.score - l.pos, c->stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(v.score, 0, l.scratch - l.score, c->stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(v.score, 0, l.logits - l.score, c->stream);
   if (e == cudaSuccess) e = cudaMemsetAsync(v.err, 0, sizeof(int), c->stream);
   if (e != cudaSuccess) {
     delete c;
@@ -193,7 +220,7 @@ h2o_status h2o_bcache_attend(h2o_bcache_t c, int n, const h2o_rows *q, const int
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 0, c->view.cap};
   const cudaError_t e =
-      blk::launch_attend(c->view, l, rows_of(q), causal != 0, accumulate != 0, rows_of(out), lse, c->stream);
+      blk::launch_attend(c->view, l, rows_of(q), causal != 0, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -210,7 +237,7 @@ h2o_status h2o_bcache_step(h2o_bcache_t c, int n, const h2o_rows *q, const h2o_r
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
   cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
   if (e == cudaSuccess)
-    e = blk::launch_attend(c->view, l, rows_of(q), 1, accumulate != 0, rows_of(out), lse, c->stream);
+    e = blk::launch_attend(c->view, l, rows_of(q), 1, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 

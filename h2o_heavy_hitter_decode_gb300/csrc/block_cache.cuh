@@ -3,6 +3,8 @@
 // sequence, and the code formats with their power-of-two block scales.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 #include "../../include/h2o.h"
@@ -94,8 +96,10 @@ __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float(
 // Launchers (each on the device that is current; arguments checked before).
 cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
                           const float *score, cudaStream_t st);
+// kmap, vmap: the codes as rows of d bytes, boxes of kBlock rows (code_map).
 cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
-                          float *lse, cudaStream_t st);
+                          float *lse, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
+size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms);
 cudaError_t launch_evict(const View &c, const int32_t *lengths, int k_heavy, int k_local, int n_sink, int score_mode,
                          const int32_t *position, int32_t *new_lengths, cudaStream_t st);
 
