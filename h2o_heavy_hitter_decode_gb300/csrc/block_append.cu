@@ -6,10 +6,13 @@
 // rounding.  Where the scale grew, the codes already in the block are
 // re-scaled by the power of two s / s' and rounded once more.
 //
-// One warp per (head, block, K or V).  It holds the block's whole row data
+// append_kernel: one warp per (head, block, K or V).  It holds the block's whole row data
 // in registers (32 rows x d bf16 = 8 KB at d = 128: sixteen 16-byte loads per
 // lane, all in flight together), so the input is read once and the codes are
 // written once.
+// append_few_kernel: one warp per (head, K or V) for the rows of a decode
+// step, taken one at a time; the block's earlier codes are read only where its
+// scale grows.
 #include "block_cache.cuh"
 
 namespace h2o {
@@ -17,6 +20,7 @@ namespace blk {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kFew = 8;  // rows a sequence that append_few_kernel takes
 
 template <typename F, int D>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const Lens l, const Rows k, const Rows v,
@@ -127,9 +131,99 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const
   }
 }
 
+// Few rows (they touch two blocks at most): a lane holds D/32 neighbours of a row.
+template <typename F, int D>
+__global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, const Lens l, const Rows k, const Rows v,
+                                                                 const int32_t *__restrict__ position) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const bool is_v = item & 1;
+  const int bh = item >> 1;
+  if (bh >= c.B * c.H) return;
+  const int b = bh / c.H, h = bh - b * c.H;
+  const Seq s = seq_of(l, b);
+  if (!s.ok) {
+    if (lane == 0 && h == 0 && !is_v) atomicOr(c.err, H2O_BERR_RANGE);
+    return;
+  }
+  const Rows &x = is_v ? v : k;
+  uint8_t *codes = (is_v ? c.V : c.K) + (size_t)bh * c.cap * D + lane * E;
+  float *scales = (is_v ? c.Vsc : c.Ksc) + (size_t)bh * (c.cap / kBlock);
+  auto row = [&](int t, uint32_t (&u)[2]) {  // bf16 bits, two to a word
+    const __nv_bfloat16 *p = x.at(b, h, t - s.len) + lane * E;
+    if constexpr (E == 4) {
+      const uint2 w = *(const uint2 *)p;
+      u[0] = w.x, u[1] = w.y;
+    } else {
+      u[0] = *(const uint32_t *)p, u[1] = 0u;
+    }
+  };
+  for (int lo = s.len, end = s.len + s.cnt; lo < end;) {
+    const int blk = lo / kBlock, base = blk * kBlock, hi = min(end, base + kBlock);
+    const float before = base < s.len ? scales[blk] : 0.f;
+    uint32_t top = 0, odd = 0;
+    for (int t = lo; t < hi; ++t) {
+      uint32_t u[2];
+      row(t, u);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t y = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+        if (y < 0x7f80u)
+          top = max(top, y);
+        else
+          odd = 1;
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (odd) atomicOr(c.err, H2O_BERR_NONFINITE);
+    const float after = fmaxf(before, block_scale<F>(__uint_as_float(top << 16)));
+    const float inv = inverse_pow2(after);
+    if (after > before && before > 0.f) {  // earlier entries of the block take the larger scale
+      const float ratio = before * inv;
+      for (int t = base; t < s.len; ++t) {
+        uint32_t u = 0;
+        if constexpr (E == 4)
+          u = *(const uint32_t *)(codes + (size_t)t * D);
+        else
+          u = *(const uint16_t *)(codes + (size_t)t * D);
+        float f[4];
+        F::values(u, f);
+        u = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) u |= F::code(f[e] * ratio) << (8 * e);
+        store_codes<E>(codes + (size_t)t * D, 0, u);
+      }
+    }
+    for (int t = lo; t < hi; ++t) {
+      uint32_t u[2], out = 0;
+      row(t, u);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float y = (e & 1 ? bf16hi(u[e >> 1]) : bf16lo(u[e >> 1])) * inv;
+        y = y != y ? 0.f : fminf(fmaxf(y, -F::kMax), F::kMax);
+        out |= F::code(y) << (8 * e);
+      }
+      store_codes<E>(codes + (size_t)t * D, 0, out);
+    }
+    if (lane == 0) scales[blk] = after;
+    lo = hi;
+  }
+  if (!is_v && lane < s.cnt) {
+    const size_t at = (size_t)bh * c.cap + s.len + lane;
+    c.pos[at] = (position ? position[b] : s.len) + lane;
+    c.score[at] = 0.f;
+  }
+}
+
 template <typename F, int D>
 cudaError_t append_t(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
                      const float *score, cudaStream_t st) {
+  if (l.n <= kFew && !score) {
+    const int64_t warps = (int64_t)c.B * c.H * 2;
+    append_few_kernel<F, D><<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(c, l, k, v, position);
+    return cudaGetLastError();
+  }
   const int blocks = (l.n + kBlock - 1) / kBlock + 1;  // the rows may start inside a block
   const int64_t warps = (int64_t)c.B * c.H * blocks * 2;
   append_kernel<F, D><<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(c, l, k, v, position, score,

@@ -11,14 +11,18 @@
 // attend_kernel: the blocks of all sequences and heads, in one list, are cut
 // into as many equal runs as the device has workers, so a ragged batch, one
 // long sequence and many short ones keep every SM equally busy.  A worker is
-// one warp for each 16 rows (MT warps); it streams its run's K and V blocks
+// a warp for each 8 * NR rows (MT warps); it streams its run's K and V blocks
 // through its own ring of TMA loads (128- or 64-byte swizzle, so the
 // fragment reads below meet no bank conflict), with no barrier shared with
-// other workers.  Per block of 32 entries: codes become f16 in registers
-// (exact), S = Q K^T and P V run on mma.sync m16n8k16 with fp32 sums, softmax
-// is online.  A lane's K words hold four consecutive dimensions of a row and
-// its V words four dimensions of two entries: the matrix instruction sums
-// over any order of k, so the loads stay 16 bytes wide and need no transpose.
+// other workers.  Per block of 32 entries the codes become f16 in registers
+// (exact), once for all of the warp's rows, and are the A operand (16 rows of
+// the matrix instruction) of both products, the query rows the 8 columns of
+// B: S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 with fp32 sums.  A
+// lane's K words hold four consecutive dimensions of an entry and its V words
+// four dimensions of two entries: the instruction sums over any order of k
+// and its rows may be any dimensions, so the loads stay 16 bytes wide and
+// need no transpose.  P^T leaves S^T's accumulator layout for B's by one
+// movmatrix for each 8 x 8.
 // Where a head's blocks lie in more than one run, the partial (m, l, O) go to
 // scratch memory; the runs' and heads' boundaries form a staircase, so
 // (worker + head) numbers the partials without gaps or collisions.
@@ -28,9 +32,9 @@
 // codes have to pass through registers anyway to become f16; tcgen05 would
 // read them back from shared memory, 4 more bytes of its traffic per code.
 //
-// finish_kernel: joins the partials to O and LSE, and turns the logits the
-// first kernel left in scratch memory into weights, once LSE is known:
-// 4 bytes written and read per row and entry, instead of K read again.
+// join_kernel: joins the partials of a row to O and LSE.  score_kernel turns
+// the logits that the first kernel left in scratch memory into weights: 4
+// bytes written and read per row and entry, instead of K read again.
 #include <cuda.h>
 
 #include "block_cache.cuh"
@@ -113,27 +117,48 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------------- formats
-// Two code pairs of a word as f16x2 (exact).
-template <typename F> __device__ __forceinline__ void to_f16(uint32_t w, uint32_t &a, uint32_t &z);
-template <> __device__ __forceinline__ void to_f16<E4M3>(uint32_t w, uint32_t &a, uint32_t &z) {
-  a = e4m3x2_to_f16x2(w);
-  z = e4m3x2_to_f16x2(w >> 16);
-}
-// code + 128 in the low bits of the f16 number 1024, less 1152.
-template <> __device__ __forceinline__ void to_f16<I8>(uint32_t w, uint32_t &a, uint32_t &z) {
-  w ^= 0x80808080u;
-  a = __byte_perm(w, 0x64646464u, 0x4140);
-  z = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const __half2 x = __hsub2(*(const __half2 *)&a, bias), y = __hsub2(*(const __half2 *)&z, bias);
-  a = *(const uint32_t *)&x;
-  z = *(const uint32_t *)&y;
-}
+// A word's four codes c0..c3 as two f16x2 registers (exact), and the byte
+// selections that bring two words' codes x, y to (x0, y0), (x1, y1) and
+// (x2, y2), (x3, y3) through the same conversion.
+template <typename F> struct ToF16;
+template <> struct ToF16<E4M3> {  // (c0, c1), (c2, c3)
+  static constexpr bool kAdjacent = true;
+  static constexpr uint32_t kLow = 0x5140, kHigh = 0x7362;
+  __device__ __forceinline__ static void run(uint32_t w, uint32_t &a, uint32_t &z) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(z)
+        : "r"(w));
+  }
+};
+template <> struct ToF16<I8> {  // (c0, c2), (c1, c3): code + 128 in the low bits of the f16 number 1024, less 1152
+  static constexpr bool kAdjacent = false;
+  static constexpr uint32_t kLow = 0x5410, kHigh = 0x7632;
+  __device__ __forceinline__ static void run(uint32_t w, uint32_t &a, uint32_t &z) {
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u, y = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+    const __half2 p = __hsub2(*(const __half2 *)&x, bias), q = __hsub2(*(const __half2 *)&y, bias);
+    a = *(const uint32_t *)&p;
+    z = *(const uint32_t *)&q;
+  }
+};
 
+// c (+)= A B, 16 x 8 x 16.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Transpose of an 8 x 8 matrix of f16, a lane holding two neighbours of a row.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
@@ -154,19 +179,19 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
 
 constexpr int kTeams = 4;  // workers of a CTA
 
-// MT row tiles of 16 (warps) per worker.  One to two tiles leave a warp 255
-// registers, so its Q stays there; four tiles run 16 warps of 128 registers
-// and keep Q in shared memory.  Ring: about 192 KB per SM for one and two
-// tiles, 128 KB (and 64 KB of Q) for four.
-template <int D, int MT> struct Cfg {
+// A worker's rows: MT warps of NR tiles of 8 rows.  O takes D / 4 registers a
+// tile and Q as many again for half of that: one and two tiles keep Q in
+// registers, four in shared memory.  Ring: 128 to 192 KB per SM.
+template <int D, int NR, int MT> struct Cfg {
   static constexpr int kWarps = kTeams * MT;
-  static constexpr int kCtas = MT == 1 ? 2 : 1;  // per SM
+  static constexpr int kCtas = NR == 1 ? 3 : MT == 1 ? 2 : 1;  // per SM
   static constexpr int kStage = 2 * kBlock * D;
-  static constexpr int kStages = (MT == 1 ? 98304 : MT == 2 ? 196608 : 131072) / (kTeams * kStage);
-  static constexpr bool kQSmem = MT == 4;
-  static constexpr int kQBytes = kQSmem ? kWarps * D * 32 : 0;
+  static constexpr bool kQSmem = NR == 4;
+  static constexpr int kStages = (NR == 1 ? 65536 : NR == 2 ? 98304 : MT == 1 ? 65536 : 131072) / (kTeams * kStage);
+  static constexpr int kQBytes = kQSmem ? kWarps * NR * D * 16 : 0;
   static constexpr int kSmem = 1024 + kTeams * kStages * kStage + kQBytes + kTeams * kStages * 16;
 };
+constexpr int kMaxCtas = 3;
 
 struct Args {
   View c;
@@ -175,16 +200,18 @@ struct Args {
   float *lse;
   float2 *ml;  // [workers + B*H][max_rows]  partial maximum and sum
   float *po;   // [workers + B*H][max_rows][d]  partial output
+  float *lse2;  // [B*H][max_rows]  base-2 log-sum-exp, +infinity where nothing was seen
   int causal, accumulate, workers;
   int rows;  // n * group: rows of a head in this call
 };
 
-template <typename F, int D, int MT>
-__global__ void __launch_bounds__(Cfg<D, MT>::kWarps * 32, Cfg<D, MT>::kCtas)
+template <typename F, int D, int NR, int MT>
+__global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::kCtas)
     attend_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using G = Cfg<D, MT>;
-  constexpr int KS = D / 16;  // k steps of S, words of a lane's K row
-  constexpr int NT = D / 8;   // n tiles of O
+  using G = Cfg<D, NR, MT>;
+  using T = ToF16<F>;
+  constexpr int KS = D / 16;  // k steps of S, words of a lane's share of a K entry
+  constexpr int OT = D / 16;  // 16-row tiles of O^T
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -193,7 +220,7 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kWarps * 32, Cfg<D, MT>::kCtas)
   const int team = warp / MT, tile = warp - team * MT;
   const int g = lane >> 2, t = lane & 3;
   uint8_t *ring = smem + team * S * G::kStage;
-  uint4 *qs = (uint4 *)(smem + kTeams * S * G::kStage) + (G::kQSmem ? warp * KS * 32 : 0);
+  uint4 *qs = (uint4 *)(smem + kTeams * S * G::kStage) + (G::kQSmem ? warp * NR * (KS / 2) * 32 : 0);
   uint64_t *full = (uint64_t *)(smem + kTeams * S * G::kStage + G::kQBytes) + team * 2 * S, *empty = full + S;
   const int worker = team * gridDim.x + blockIdx.x;  // few runs: one for each CTA first
 
@@ -220,63 +247,68 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kWarps * 32, Cfg<D, MT>::kCtas)
   Cursor cur, ld;
   cur.seek(a.l, c.B, c.H, x0);
   ld = cur;
-  auto issue = [&](int i) {  // block i of the run into its stage (leader warp)
+  int issued = 0, put = 0;
+  auto issue = [&]() {  // the run's next block into its stage (leader warp)
     if (lane == 0) {
-      uint8_t *dst = ring + (i % S) * G::kStage;
-      uint64_t *bar = full + i % S;
+      uint8_t *dst = ring + put * G::kStage;
       const int row = (ld.b * c.H + ld.h) * c.cap + ld.blk * kBlock;
-      mbar_expect_tx(bar, G::kStage);
-      tma_load_2d(dst, &kmap, bar, 0, row);
-      tma_load_2d(dst + kBlock * D, &vmap, bar, 0, row);
+      mbar_expect_tx(full + put, G::kStage);
+      tma_load_2d(dst, &kmap, full + put, 0, row);
+      tma_load_2d(dst + kBlock * D, &vmap, full + put, 0, row);
     }
+    ++issued;
+    put = put + 1 == S ? 0 : put + 1;
     ld.next(a.l, c.B, c.H);
   };
-  int issued = 0;
   if (tile == 0)
-    for (; issued < S && issued < count; ++issued) issue(issued);
+    while (issued < S && issued < count) issue();
 
-  const int row0 = (blockIdx.y * MT + tile) * 16 + g;  // rows row0 and row0 + 8 of the head
-  const bool idle = (blockIdx.y * MT + tile) * 16 >= a.rows;
+  const int row0 = (blockIdx.y * MT + tile) * (8 * NR);  // the warp's rows of the head
+  const bool idle = row0 >= a.rows;
   const int nsc = c.cap / kBlock;
-  float o[NT][4], m[2], lsum[2], crow[2];
-  int end[2];
-  bool live[2];
-  uint32_t qr[G::kQSmem ? 1 : KS][4];
-  float *lg[2];
-  int first_blk = 0, min_end = 0;
+  // The lane's rows of tile n: 2 t and 2 t + 1 (columns of S^T and O^T).
+  float o[NR][OT][4], m[NR][2], lsum[NR][2], crow[NR][2];
+  int end[NR][2];
+  uint32_t qr[G::kQSmem ? 1 : NR][KS][2];
+  int first_blk = 0, min_end = 0, live = 0;  // live: bit 2 n + u, the row exists
   bool open = false, lost = false;
-  float ks = 0.f, vs = 0.f;
+  float ks, vs;
   {
     const size_t sc = (size_t)(cur.b * c.H + cur.h) * nsc + cur.blk;
     ks = c.Ksc[sc];
     vs = c.Vsc[sc];
   }
 
+  int st = 0;
+  uint32_t phase = 0;
   for (int i = 0; i < count; ++i) {
     const int bh = cur.b * c.H + cur.h;
     if (!open) {  // a head begins
       open = true;
       first_blk = cur.blk;
       min_end = a.causal ? cur.s.total - cur.s.cnt + 1 : cur.s.total;
+      live = 0;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      uint32_t qh[2][KS * 2];
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = row0 + 8 * u, tok = r / c.group;
-        live[u] = tok < cur.s.cnt;
-        end[u] = live[u] && a.causal ? cur.s.total - cur.s.cnt + tok + 1 : cur.s.total;
-        m[u] = -INFINITY;
-        lsum[u] = 0.f;
-        lg[u] = c.logits + ((size_t)bh * c.max_rows + r) * c.cap + 2 * t;
-        // the lane's D/4 dimensions of the row
-        uint4 w[D / 32];
+        for (int j = 0; j < OT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tok = (row0 + 8 * n + 2 * t + u) / c.group;
+          const bool is = tok < cur.s.cnt;
+          live |= (int)is << (2 * n + u);
+          end[n][u] = is && a.causal ? cur.s.total - cur.s.cnt + tok + 1 : cur.s.total;
+          m[n][u] = -INFINITY;
+          lsum[n][u] = 0.f;
+        }
+        // Q: the lane's D/4 dimensions of row g
+        const int r = row0 + 8 * n + g, tok = r / c.group;
+        const bool is = tok < cur.s.cnt;
         const __nv_bfloat16 *p = a.q.at(cur.b, cur.h * c.group + r % c.group, tok) + t * (D / 4);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) w[e] = live[u] ? ld_nc16(p + e * 8) : make_uint4(0u, 0u, 0u, 0u);
         float f[D / 4], top = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) Unpack<__nv_bfloat16>::run(w[e], f + e * 8);
+        for (int e = 0; e < D / 32; ++e)
+          Unpack<__nv_bfloat16>::run(is ? ld_nc16(p + e * 8) : make_uint4(0u, 0u, 0u, 0u), f + e * 8);
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -286,372 +318,370 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kWarps * 32, Cfg<D, MT>::kCtas)
         int ex = 0;
         frexpf(top, &ex);
         const int sh = top > 0.f && top < INFINITY ? min(14 - ex, 100) : 0;
-        const float up = ldexpf(1.f, sh);
-        crow[u] = ldexpf(rsqrtf((float)D) * kLog2e, -sh);
+        const float up = ldexpf(1.f, sh), back = ldexpf(rsqrtf((float)D) * kLog2e, -sh);
+        crow[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        crow[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        uint32_t qh[KS][2];
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          const __half2 h2 = __floats2half2_rn(f[2 * e] * up, f[2 * e + 1] * up);
-          qh[u][e] = *(const uint32_t *)&h2;
+        for (int k = 0; k < KS; ++k) {  // in the order of the codes' conversion
+          const __half2 x = __floats2half2_rn(f[4 * k] * up, f[4 * k + (T::kAdjacent ? 1 : 2)] * up);
+          const __half2 y = __floats2half2_rn(f[4 * k + (T::kAdjacent ? 2 : 1)] * up, f[4 * k + 3] * up);
+          qh[k][0] = *(const uint32_t *)&x;
+          qh[k][1] = *(const uint32_t *)&y;
         }
-      }
-      if (G::kQSmem) {
-        __syncwarp();
+        if constexpr (G::kQSmem) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          qs[k * 32 + lane] = make_uint4(qh[0][2 * k], qh[1][2 * k], qh[0][2 * k + 1], qh[1][2 * k + 1]);
-        __syncwarp();
-      } else {
+          for (int k = 0; k < KS; k += 2)  // read by this lane only
+            qs[(n * (KS / 2) + k / 2) * 32 + lane] = make_uint4(qh[k][0], qh[k][1], qh[k + 1][0], qh[k + 1][1]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qr[G::kQSmem ? 0 : k][0] = qh[0][2 * k];
-          qr[G::kQSmem ? 0 : k][1] = qh[1][2 * k];
-          qr[G::kQSmem ? 0 : k][2] = qh[0][2 * k + 1];
-          qr[G::kQSmem ? 0 : k][3] = qh[1][2 * k + 1];
+          for (int k = 0; k < KS; ++k) qr[n][k][0] = qh[k][0], qr[n][k][1] = qh[k][1];
         }
       }
     }
     const float ks_now = ks, vs_now = vs;
-    const int blk = cur.blk, total = cur.s.total;
-    const Cursor at = cur;
+    const int blk = cur.blk, rest = cur.s.total - blk * kBlock;
+    const int ab = cur.b, ah = cur.h;
+    const bool last_blk = blk + 1 == cur.nblk;
     cur.next(a.l, c.B, c.H);
-    const bool closes = i + 1 == count || cur.blk == 0;
     if (i + 1 < count) {  // the next block's scales, a block ahead
       const size_t sc = (size_t)(cur.b * c.H + cur.h) * nsc + cur.blk;
       ks = c.Ksc[sc];
       vs = c.Vsc[sc];
     }
-    uint8_t *kt = ring + (i % S) * G::kStage, *vt = kt + kBlock * D;
-    if (!mbar_wait(full + i % S, (i / S) & 1)) {
+    uint8_t *kt = ring + st * G::kStage, *vt = kt + kBlock * D;
+    if (!mbar_wait(full + st, phase)) {
       lost = true;
       break;
     }
     if (MT > 1 && tile == 0 && i > 0 && issued < count) {  // the stage of block i - 1, once every warp has read it
-      if (!mbar_wait(empty + (i - 1) % S, ((i - 1) / S) & 1)) {
+      if (!mbar_wait(empty + put, st == 0 ? phase ^ 1 : phase)) {
         lost = true;
         break;
       }
-      issue(issued++);
+      issue();
     }
     if (!idle) {
-      // S = Q K^T of 16 rows and 32 entries
-      float s[4][4];
+      float s[NR][2][4];  // S^T: entries 16 x + g and + 8, rows 2 t and 2 t + 1
       {
         uint32_t kw[4][KS];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
           for (int e = 0; e < KS / 4; ++e) {
             const uint4 u = *(const uint4 *)(kt + chunk_at<D>(n * 8 + g, t * (KS / 4) + e));
             kw[n][4 * e] = u.x, kw[n][4 * e + 1] = u.y, kw[n][4 * e + 2] = u.z, kw[n][4 * e + 3] = u.w;
           }
-        }
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t qa[4];
-          if (G::kQSmem) {
-            const uint4 u = qs[k * 32 + lane];
-            qa[0] = u.x, qa[1] = u.y, qa[2] = u.z, qa[3] = u.w;
-          } else {
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t q[NR][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qa[e] = qr[G::kQSmem ? 0 : k][e];
+          for (int n = 0; n < NR; ++n) {
+            if constexpr (G::kQSmem) {
+              const uint4 u = qs[(n * (KS / 2) + k / 2) * 32 + lane];
+              q[n][0] = u.x, q[n][1] = u.y, q[n][2] = u.z, q[n][3] = u.w;
+            } else {
+              q[n][0] = qr[n][k][0], q[n][1] = qr[n][k][1], q[n][2] = qr[n][k + 1][0], q[n][3] = qr[n][k + 1][1];
+            }
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t b0, b1;
-            to_f16<F>(kw[n][k], b0, b1);
-            mma16816(s[n], qa, b0, b1);
-          }
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t ka[4];
+              T::run(kw[2 * x][k + e], ka[0], ka[2]);
+              T::run(kw[2 * x + 1][k + e], ka[1], ka[3]);
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
+                if (k + e == 0)
+                  mma16816_new(s[n][x], ka, q[n][0], q[n][1]);
+                else
+                  mma16816(s[n][x], ka, q[n][2 * e], q[n][2 * e + 1]);
+              }
+            }
         }
       }
-      const int j0 = blk * kBlock + 2 * t;
-      const float f0 = crow[0] * ks_now, f1 = crow[1] * ks_now;
+      const int j0 = blk * kBlock + g;
       const bool edge = blk * kBlock + kBlock > min_end;
+      uint32_t p[NR][4];  // P^T as B: entries 8 e + 2 t and + 1 of row g
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        s[n][0] *= f0, s[n][1] *= f0, s[n][2] *= f1, s[n][3] *= f1;
+      for (int n = 0; n < NR; ++n) {
+        const float f0 = crow[n][0] * ks_now, f1 = crow[n][1] * ks_now;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) s[n][x][0] *= f0, s[n][x][1] *= f1, s[n][x][2] *= f0, s[n][x][3] *= f1;
         if (edge) {
-          const int j = j0 + n * 8;
-          if (j >= end[0]) s[n][0] = -INFINITY;
-          if (j + 1 >= end[0]) s[n][1] = -INFINITY;
-          if (j >= end[1]) s[n][2] = -INFINITY;
-          if (j + 1 >= end[1]) s[n][3] = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j0 + 16 * x + 8 * (e >> 1) >= end[n][e & 1]) s[n][x][e] = -INFINITY;
+        }
+        if (a.accumulate) {
+          float *lg = c.logits + ((size_t)bh * c.max_rows + row0 + 8 * n + 2 * t) * c.cap + j0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (live >> (2 * n + u) & 1) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) lg[u * c.cap + 16 * x] = s[n][x][u], lg[u * c.cap + 16 * x + 8] = s[n][x][2 + u];
+            }
         }
       }
-      if (a.accumulate) {
+      float top[NR][2];
+      bool moves = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (live[u]) {
-            float *p = lg[u] + blk * kBlock;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) *(float2 *)(p + n * 8) = make_float2(s[n][2 * u], s[n][2 * u + 1]);
-          }
-      }
-      float top[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        top[u] = fmaxf(fmaxf(fmaxf(s[0][2 * u], s[0][2 * u + 1]), fmaxf(s[1][2 * u], s[1][2 * u + 1])),
-                       fmaxf(fmaxf(s[2][2 * u], s[2][2 * u + 1]), fmaxf(s[3][2 * u], s[3][2 * u + 1])));
-        top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 1));
-        top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 2));
-      }
-      // The running maximum moves only when it is passed by more than 2^8: weights then stay below 2^8, in f16's range
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || m[0] == -INFINITY || m[1] == -INFINITY)) {
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float mn = fmaxf(m[u], top[u]);
-          const float f = m[u] == -INFINITY ? 0.f : ex2(m[u] - mn);
-          m[u] = mn;
-          lsum[u] *= f;
+          float x = fmaxf(fmaxf(s[n][0][u], s[n][0][2 + u]), fmaxf(s[n][1][u], s[n][1][2 + u]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          top[n][u] = x;
+          moves |= x > m[n][u] + 8.f || m[n][u] == -INFINITY;
+        }
+      // The running maximum moves only when it is passed by more than 2^8: weights then stay below 2^8, in f16's range
+      if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) o[j][2 * u] *= f, o[j][2 * u + 1] *= f;
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float mn = fmaxf(m[n][u], top[n][u]);
+            const float f = m[n][u] == -INFINITY ? 0.f : ex2(m[n][u] - mn);
+            m[n][u] = mn;
+            lsum[n][u] *= f;
+#pragma unroll
+            for (int j = 0; j < OT; ++j) o[n][j][u] *= f, o[n][j][2 + u] *= f;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float mu0 = m[n][0] == -INFINITY ? 0.f : m[n][0], mu1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float e0 = ex2(s[n][x][0] - mu0), e1 = ex2(s[n][x][1] - mu1), e2 = ex2(s[n][x][2] - mu0),
+                      e3 = ex2(s[n][x][3] - mu1);
+          lsum[n][0] += e0 + e2;
+          lsum[n][1] += e1 + e3;
+          // 16 bits for the product with V: f16's 2^-11 per weight, an eighth of the output's own rounding
+          const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
+          p[n][2 * x] = transpose8(*(const uint32_t *)&a0);
+          p[n][2 * x + 1] = transpose8(*(const uint32_t *)&a1);
         }
       }
-      const float mu0 = m[0] == -INFINITY ? 0.f : m[0], mu1 = m[1] == -INFINITY ? 0.f : m[1];
-      uint32_t p[2][4];  // P as the A operand of two k steps of 16 entries
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float e0 = ex2(s[n][0] - mu0), e1 = ex2(s[n][1] - mu0), e2 = ex2(s[n][2] - mu1), e3 = ex2(s[n][3] - mu1);
-        lsum[0] += e0 + e1;
-        lsum[1] += e2 + e3;
-        // 16 bits for the product with V: f16's 2^-11 per weight, an eighth of the output's own rounding
-        const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
-        p[n >> 1][(n & 1) * 2] = *(const uint32_t *)&a0;
-        p[n >> 1][(n & 1) * 2 + 1] = *(const uint32_t *)&a1;
-      }
-      const int rest = total - blk * kBlock;
       if (rest < kBlock) {  // codes behind the last entry may be anything, also NaN: weight 0 needs a finite code
         for (int z = rest * D + lane * 16; z < kBlock * D; z += 512) *(uint4 *)(vt + z) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
       }
       // O += vs (P V): a fresh product per block, added in fp32 under the block's scale
-      constexpr int VW = D / 32;  // words of a lane's V row: D/8 dimensions
-      constexpr int HALF = G::kQSmem && VW == 4 ? 2 : VW;  // words at a time (registers)
+      constexpr int VW = D / 32;  // words of the lane's D/8 dimensions of an entry
+      uint32_t vw[8][VW];
 #pragma unroll
-      for (int hw = 0; hw < VW; hw += HALF) {
-        uint32_t vw[8][HALF];
+      for (int e = 0; e < 8; ++e) {
+        const int r = (e >> 1) * 8 + 2 * t + (e & 1);
+        if constexpr (D == 128) {
+          const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
+          vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % VW] = u.z, vw[e][3 % VW] = u.w;
+        } else {
+          const uint2 u = *(const uint2 *)(vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+          vw[e][0] = u.x, vw[e][1] = u.y;
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = (e >> 1) * 8 + 2 * t + (e & 1);
-          if constexpr (HALF == 4) {
-            const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
-            vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % HALF] = u.z, vw[e][3 % HALF] = u.w;
-          } else {
-            const uint8_t *src = D == 128 ? vt + chunk_at<D>(r, g) + hw * 4 : vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
-            const uint2 u = *(const uint2 *)src;
-            vw[e][0] = u.x, vw[e][1] = u.y;
-          }
+      for (int w = 0; w < VW; ++w) {
+        uint32_t va[2][2][4];  // [dimensions 4w, 4w+1 | 4w+2, 4w+3][k step]
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
+          T::run(__byte_perm(x, y, T::kLow), va[0][k][0], va[0][k][1]);
+          T::run(__byte_perm(x, y, T::kHigh), va[1][k][0], va[1][k][1]);
+          T::run(__byte_perm(z, v, T::kLow), va[0][k][2], va[0][k][3]);
+          T::run(__byte_perm(z, v, T::kHigh), va[1][k][2], va[1][k][3]);
         }
 #pragma unroll
-        for (int w = 0; w < HALF; ++w) {
-          float acc[4][4];
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+          for (int y = 0; y < 2; ++y) {
+            float acc[4];
+            mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
+            mma16816(acc, va[y][1], p[n][2], p[n][3]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t b0[4], b1[4];
-            const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
-            to_f16<F>(__byte_perm(x, y, 0x5140), b0[0], b0[1]);
-            to_f16<F>(__byte_perm(x, y, 0x7362), b0[2], b0[3]);
-            to_f16<F>(__byte_perm(z, v, 0x5140), b1[0], b1[1]);
-            to_f16<F>(__byte_perm(z, v, 0x7362), b1[2], b1[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816(acc[j], p[k], b0[j], b1[j]);
+            for (int e = 0; e < 4; ++e) o[n][2 * w + y][e] = fmaf(acc[e], vs_now, o[n][2 * w + y][e]);
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[(hw + w) * 4 + j][e] = fmaf(acc[j][e], vs_now, o[(hw + w) * 4 + j][e]);
-        }
       }
     }
     // this warp has read the stage
     __syncwarp();
     if (MT > 1) {
-      if (lane == 0) mbar_arrive(empty + i % S);
+      if (lane == 0) mbar_arrive(empty + st);
     } else if (issued < count) {
-      issue(issued++);
+      issue();
     }
-    if (!closes) continue;
+    if (++st == S) st = 0, phase ^= 1;
+    if (i + 1 < count && !last_blk) continue;
     open = false;
     if (idle) continue;
-    const int hb = at.b * c.H + at.h;
-    const bool whole = first_blk == 0 && blk + 1 == at.nblk;  // no other worker holds a part of this head
-    const size_t slot = ((size_t)worker + hb) * c.max_rows;
+    const bool whole = first_blk == 0 && last_blk;  // no other worker holds a part of this head
+    const size_t slot = ((size_t)worker + bh) * c.max_rows;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float l = lsum[u];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (!live[u]) continue;
-      const int r = row0 + 8 * u, tok = r / c.group, hq = at.h * c.group + r % c.group;
-      if (t == 0) a.ml[slot + r] = make_float2(m[u], l);
-      if (whole) {
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(at.b, hq, tok)) + t * (D / 4);
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int u = 0; u < 2; ++u) {
+        float l = lsum[n][u];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (!(live >> (2 * n + u) & 1)) continue;
+        const int r = row0 + 8 * n + 2 * t + u;
+        // the lane's D/8 dimensions: g D/8 + 2 j (accumulator u) and + 1 (2 + u)
+        if (whole) {
+          const int tok = r / c.group, hq = ah * c.group + r % c.group;
+          const bool any = l > 0.f || l != l;
+          const float inv = any ? 1.f / l : 0.f;
+          uint32_t *dst = (uint32_t *)(const_cast<__nv_bfloat16 *>(a.out.at(ab, hq, tok)) + g * (D / 8));
+          uint32_t w[OT];
 #pragma unroll
-          for (int j = 0; j < NT; j += 8) {
-            uint4 w;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[j + 2 * y][2 * u + e] * inv, o[j + 2 * y + 1][2 * u + e] * inv);
-              (&w.x)[y] = *(const uint32_t *)&b2;
-            }
-            *(uint4 *)(dst + e * (D / 8) + j) = w;
+          for (int j = 0; j < OT; ++j) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[n][j][u] * inv, o[n][j][2 + u] * inv);
+            w[j] = *(const uint32_t *)&b2;
           }
-        if (a.lse && t == 0)
-          a.lse[((size_t)at.b * c.H * c.group + hq) * a.l.n + tok] = l > 0.f || l != l ? (m[u] + log2f(l)) * kLn2 : -INFINITY;
-      } else {
-        float *dst = a.po + (slot + r) * D + t * (D / 4);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+          for (int j = 0; j < OT; j += 4) *(uint4 *)(dst + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+          if (g == 0) {
+            a.lse2[(size_t)bh * c.max_rows + r] = any ? m[n][u] + log2f(l) : INFINITY;
+            if (a.lse)
+              a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (m[n][u] + log2f(l)) * kLn2 : -INFINITY;
+          }
+        } else {
+          if (g == 0) a.ml[slot + r] = make_float2(m[n][u], l);
+          float *dst = a.po + (slot + r) * D + g * (D / 8);
 #pragma unroll
-          for (int j = 0; j < NT; j += 4)
-            *(float4 *)(dst + e * (D / 8) + j) =
-                make_float4(o[j][2 * u + e], o[j + 1][2 * u + e], o[j + 2][2 * u + e], o[j + 3][2 * u + e]);
+          for (int j = 0; j < OT; j += 2)
+            *(float4 *)(dst + 2 * j) = make_float4(o[n][j][u], o[n][j][2 + u], o[n][j + 1][u], o[n][j + 1][2 + u]);
+        }
       }
-    }
   }
   if (lost) {  // a copy never arrived: report, and let what is in flight land before the memory goes
     if (lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
     if (tile == 0)
-      for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(full + i % S, (i / S) & 1);
+      for (int i = 0; i < S; ++i) mbar_wait(full + i, i >= st ? phase : phase ^ 1);
   }
 }
 
-// ------------------------------------------------------------------- finish
+// --------------------------------------------------------------------- join
 constexpr int kChunk = 256;  // entries of one score item
-constexpr int kFinishWarps = 8;
+constexpr int kItemWarps = 8;  // items (warps) of a CTA
 
-// One item per warp: first D/32 items for each row of a head that lies in
-// several runs (32 output dimensions each: four groups of eight lanes take
-// the partials in turn), then kChunk entries' scores each.
+// 32 dimensions of one row's output per warp, where a head lies in several
+// runs: four groups of eight lanes take the partials in turn.
 template <int D>
-__global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const Args a) {
+__global__ void __launch_bounds__(kItemWarps * 32) join_kernel(const Args a) {
   const View &c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float row_lse[kFinishWarps][H2O_BLOCK_MAX_ROWS];
   const int blocks = c.H * sum_units(a.l, c.B, kBlock);
   const int workers = min(a.workers, blocks);
-  const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
-  const int64_t outs = (int64_t)c.B * c.H * a.rows * (D / 32);
+  const int64_t items = (int64_t)c.B * c.H * a.rows * (D / 32);
   grid_dependency_wait();
-  for (int64_t item = (int64_t)blockIdx.x * kFinishWarps + warp; item < outs + chunks;
-       item += (int64_t)gridDim.x * kFinishWarps) {
-    if (item < outs) {
-      const int part = (int)(item % (D / 32));
-      const int64_t hr = item / (D / 32);
-      const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
-      const Seq s = seq_of(a.l, b);
-      const int tok = r / c.group, hq = h * c.group + r % c.group;
-      if (tok >= s.cnt) continue;
-      __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + part * 32 + (lane & 7) * 4;
-      float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
-      const int nblk = ceil_div(s.total, kBlock);
-      if (nblk == 0) {  // no entry at all
-        if (lane < 8) *(uint2 *)dst = make_uint2(0u, 0u);
-        if (lse && part == 0 && lane == 0) *lse = -INFINITY;
-        continue;
-      }
-      int before = 0;
-      for (int i = lane; i < b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
-      const int x = c.H * __reduce_add_sync(0xffffffffu, before) + h * nblk;
-      const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
-      if (w0 == w1) continue;  // written by its worker
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = w0 + (lane >> 3); w <= w1; w += 4) {
-        const size_t at = ((size_t)w + bh) * c.max_rows + r;
-        const float2 p = a.ml[at];
-        const float4 v = *(const float4 *)(a.po + at * D + part * 32 + (lane & 7) * 4);
-        if (p.x == -INFINITY && p.y == 0.f) continue;  // this run saw nothing of the row
-        const float mn = fmaxf(m, p.x), f = m == -INFINITY ? 0.f : ex2(m - mn), z = ex2(p.x - mn);
-        m = mn;
-        l = l * f + p.y * z;
-        o.x = o.x * f + v.x * z, o.y = o.y * f + v.y * z, o.z = o.z * f + v.z * z, o.w = o.w * f + v.w * z;
-      }
-#pragma unroll
-      for (int off = 8; off < 32; off <<= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, off), ol = __shfl_xor_sync(0xffffffffu, l, off);
-        const float4 oo = make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
-                                      __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off));
-        const float mn = fmaxf(m, om);
-        const float f = m == -INFINITY ? 0.f : ex2(m - mn), z = om == -INFINITY ? 0.f : ex2(om - mn);
-        m = mn;
-        l = l * f + ol * z;
-        o.x = o.x * f + oo.x * z, o.y = o.y * f + oo.y * z, o.z = o.z * f + oo.z * z, o.w = o.w * f + oo.w * z;
-      }
-      const bool any = l > 0.f || l != l;
-      const float inv = any ? 1.f / l : 0.f;
-      if (lane < 8) {
-        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
-      }
-      if (lse && part == 0 && lane == 0) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+  grid_launch_dependents();
+  for (int64_t item = (int64_t)blockIdx.x * kItemWarps + warp; item < items; item += (int64_t)gridDim.x * kItemWarps) {
+    const int part = (int)(item % (D / 32));
+    const int64_t hr = item / (D / 32);
+    const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
+    const Seq s = seq_of(a.l, b);
+    const int tok = r / c.group, hq = h * c.group + r % c.group;
+    if (tok >= s.cnt) continue;
+    __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + part * 32 + (lane & 7) * 4;
+    float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
+    const int nblk = ceil_div(s.total, kBlock);
+    if (nblk == 0) {  // no entry at all
+      if (lane < 8) *(uint2 *)dst = make_uint2(0u, 0u);
+      if (lse && part == 0 && lane == 0) *lse = -INFINITY;
       continue;
     }
-    int x = (int)(item - outs), before;
+    int before = 0;
+    for (int i = lane; i < b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
+    const int x = c.H * __reduce_add_sync(0xffffffffu, before) + h * nblk;
+    const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
+    if (w0 == w1) continue;  // written by its worker
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = w0 + (lane >> 3); w <= w1; w += 4) {
+      const size_t at = ((size_t)w + bh) * c.max_rows + r;
+      const float2 p = a.ml[at];
+      const float4 v = *(const float4 *)(a.po + at * D + part * 32 + (lane & 7) * 4);
+      const bool some = p.x != -INFINITY;  // else this run saw nothing of the row
+      const float mn = fmaxf(m, p.x), f = m == -INFINITY ? 0.f : ex2(m - mn), z = some ? ex2(p.x - mn) : 0.f;
+      m = mn;
+      l = l * f + p.y * z;
+      o.x = o.x * f + v.x * z, o.y = o.y * f + v.y * z, o.z = o.z * f + v.z * z, o.w = o.w * f + v.w * z;
+    }
+#pragma unroll
+    for (int off = 8; off < 32; off <<= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, off), ol = __shfl_xor_sync(0xffffffffu, l, off);
+      const float4 oo = make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
+                                    __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off));
+      const float mn = fmaxf(m, om);
+      const float f = m == -INFINITY ? 0.f : ex2(m - mn), z = om == -INFINITY ? 0.f : ex2(om - mn);
+      m = mn;
+      l = l * f + ol * z;
+      o.x = o.x * f + oo.x * z, o.y = o.y * f + oo.y * z, o.z = o.z * f + oo.z * z, o.w = o.w * f + oo.w * z;
+    }
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? 1.f / l : 0.f;
+    if (lane < 8) {
+      const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
+    }
+    if (part == 0 && lane == 0) {
+      a.lse2[(size_t)bh * c.max_rows + r] = any ? m + log2f(l) : INFINITY;
+      if (lse) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- scores
+// kChunk entries of one head per warp: the weights of every row from its
+// logits and LSE, summed in the rows' order.
+__global__ void __launch_bounds__(kItemWarps * 32) score_kernel(const Args a) {
+  const View &c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = c.H * sum_units(a.l, c.B, kChunk);
+  grid_dependency_wait();
+  for (int item = blockIdx.x * kItemWarps + warp; item < chunks; item += gridDim.x * kItemWarps) {
+    int x = item, before;
     const int b = find_seq(a.l, c.B, c.H, kChunk, x, before);
     const Seq s = seq_of(a.l, b);
-    const int nch = ceil_div(s.total, kChunk), nblk = ceil_div(s.total, kBlock);
-    const int h = x / nch, j0 = (x - h * nch) * kChunk, bh = b * c.H + h;
+    const int nch = ceil_div(s.total, kChunk);
+    const int h = x / nch, j0 = (x - h * nch) * kChunk + lane * 4, bh = b * c.H + h;
     const int rows = s.cnt * c.group;
-    const int start = c.H * before + h * nblk;
-    const int w0 = worker_of(start, blocks, workers), w1 = worker_of(start + nblk - 1, blocks, workers);
-    // log-sum-exp (base 2) of each row; +infinity where nothing was seen, so that its weights are 0
-    if (w1 - w0 < 4) {
-      for (int r = lane; r < rows; r += 32) {
-        float m = -INFINITY, l = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-          const float2 p = a.ml[((size_t)w + bh) * c.max_rows + r];
-          if (p.x == -INFINITY && p.y == 0.f) continue;
-          const float mn = fmaxf(m, p.x);
-          l = (m == -INFINITY ? 0.f : l * ex2(m - mn)) + p.y * ex2(p.x - mn);
-          m = mn;
-        }
-        row_lse[warp][r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;
-      }
-    } else {
-      for (int r = 0; r < rows; ++r) {
-        float m = -INFINITY, l = 0.f;
-        for (int w = w0 + lane; w <= w1; w += 32) {
-          const float2 p = a.ml[((size_t)w + bh) * c.max_rows + r];
-          if (p.x == -INFINITY && p.y == 0.f) continue;
-          const float mn = fmaxf(m, p.x);
-          l = (m == -INFINITY ? 0.f : l * ex2(m - mn)) + p.y * ex2(p.x - mn);
-          m = mn;
-        }
-        const float mn = warp_max(m);
-        l = warp_sum(m == -INFINITY ? (l != l ? l : 0.f) : l * ex2(m - mn));
-        if (lane == 0) row_lse[warp][r] = l > 0.f || l != l ? mn + log2f(l) : INFINITY;
+    const float *lse2 = a.lse2 + (size_t)bh * c.max_rows;
+    const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
+    float *sc = c.score + (size_t)bh * c.cap;
+    float4 w[kChunk / 128];
+#pragma unroll
+    for (int y = 0; y < kChunk / 128; ++y) w[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const float e = lse2[r];
+#pragma unroll
+      for (int y = 0; y < kChunk / 128; ++y) {
+        if (j0 + y * 128 >= s.total) continue;
+        const float4 v = *(const float4 *)(lg + (size_t)r * c.cap + j0 + y * 128);
+        w[y].x += ex2(v.x - e), w[y].y += ex2(v.y - e), w[y].z += ex2(v.z - e), w[y].w += ex2(v.w - e);
       }
     }
-    __syncwarp();
-    const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap + j0 + lane * 4;
-    float *sc = c.score + (size_t)bh * c.cap + j0 + lane * 4;
 #pragma unroll
     for (int y = 0; y < kChunk / 128; ++y) {
-      const int j = j0 + y * 128 + lane * 4;
-      if (j >= s.total) continue;
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const float4 v = *(const float4 *)(lg + (size_t)r * c.cap + y * 128);
-        const float e = row_lse[warp][r];
-        w.x += ex2(v.x - e), w.y += ex2(v.y - e), w.z += ex2(v.z - e), w.w += ex2(v.w - e);
-      }
+      const int j = j0 + y * 128;
       if (j + 4 <= s.total) {
-        float4 v = *(float4 *)(sc + y * 128);
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-        *(float4 *)(sc + y * 128) = v;
+        float4 v = *(float4 *)(sc + j);
+        v.x += w[y].x, v.y += w[y].y, v.z += w[y].z, v.w += w[y].w;
+        *(float4 *)(sc + j) = v;
       } else {  // entries behind the last one keep their score
-        for (int e = 0; j + e < s.total; ++e) sc[y * 128 + e] += (&w.x)[e];
+        for (int e = 0; j + e < s.total; ++e) sc[j + e] += (&w[y].x)[e];
       }
     }
-    __syncwarp();
   }
 }
 
@@ -670,36 +700,46 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename F, int D, int MT>
+template <typename F, int D, int NR, int MT>
 cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-  using G = Cfg<D, MT>;
+  using G = Cfg<D, NR, MT>;
   const int ctas = a.c.sms * G::kCtas;
   a.workers = ctas * kTeams;
-  const int tiles = (a.rows + 15) / 16;
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<F, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+  const dim3 grid(ctas, (a.rows + 8 * NR * MT - 1) / (8 * NR * MT));
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<F, D, NR, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
   if (a.l.appends) {
-    e = launch_after(attend_kernel<F, D, MT>, dim3(ctas, (tiles + MT - 1) / MT), G::kWarps * 32, G::kSmem, st, a, kmap, vmap);
+    e = launch_after(attend_kernel<F, D, NR, MT>, grid, G::kWarps * 32, G::kSmem, st, a, kmap, vmap);
   } else {
-    attend_kernel<F, D, MT><<<dim3(ctas, (tiles + MT - 1) / MT), G::kWarps * 32, G::kSmem, st>>>(a, kmap, vmap);
+    attend_kernel<F, D, NR, MT><<<grid, G::kWarps * 32, G::kSmem, st>>>(a, kmap, vmap);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_after(finish_kernel<D>, dim3(a.c.sms * 8), kFinishWarps * 32, 0, st, a);
+  auto ctas_for = [&](int64_t items) {
+    const int64_t n = (items + kItemWarps - 1) / kItemWarps;
+    return dim3((unsigned)(n < a.c.sms * 8 ? n : a.c.sms * 8));
+  };
+  e = launch_after(join_kernel<D>, ctas_for((int64_t)a.c.B * a.c.H * a.rows * (D / 32)), kItemWarps * 32, 0, st, a);
+  if (e != cudaSuccess || !a.accumulate) return e;
+  return launch_after(score_kernel, ctas_for((int64_t)a.c.B * a.c.H * ((a.c.cap + kChunk - 1) / kChunk)), kItemWarps * 32, 0,
+                      st, a);
 }
 
 template <typename F, int D>
 cudaError_t attend_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-  if (a.rows <= 16) return attend_t<F, D, 1>(a, kmap, vmap, st);
-  if (a.rows <= 32) return attend_t<F, D, 2>(a, kmap, vmap, st);
-  return attend_t<F, D, 4>(a, kmap, vmap, st);
+  if (a.rows <= 8) return attend_t<F, D, 1, 1>(a, kmap, vmap, st);
+  if (a.rows <= 16) return attend_t<F, D, 2, 1>(a, kmap, vmap, st);
+  if (a.rows <= 32) return attend_t<F, D, 4, 1>(a, kmap, vmap, st);
+  return attend_t<F, D, 4, 2>(a, kmap, vmap, st);
 }
+
+size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kTeams + (size_t)B * H; }
 
 }  // namespace
 
 size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms) {
-  const size_t slots = (size_t)sms * Cfg<128, 1>::kCtas * kTeams + (size_t)B * H;
-  return slots * max_rows * (sizeof(float2) + d * sizeof(float));
+  return partial_slots(B, H, sms) * max_rows * (sizeof(float2) + d * sizeof(float)) +
+         (size_t)B * H * max_rows * sizeof(float);
 }
 
 cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
@@ -714,9 +754,10 @@ cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causa
   a.accumulate = accumulate;
   a.workers = 0;
   a.rows = l.n * c.group;
-  const size_t slots = (size_t)c.sms * Cfg<128, 1>::kCtas * kTeams + (size_t)c.B * c.H;
+  const size_t rows = partial_slots(c.B, c.H, c.sms) * c.max_rows;
   a.po = c.part;
-  a.ml = (float2 *)(c.part + slots * c.max_rows * c.d);
+  a.ml = (float2 *)(c.part + rows * c.d);
+  a.lse2 = (float *)(a.ml + rows);
   if (c.kv == H2O_KV_E4M3)
     return c.d == 128 ? attend_d<E4M3, 128>(a, kmap, vmap, st) : attend_d<E4M3, 64>(a, kmap, vmap, st);
   return c.d == 128 ? attend_d<I8, 128>(a, kmap, vmap, st) : attend_d<I8, 64>(a, kmap, vmap, st);
