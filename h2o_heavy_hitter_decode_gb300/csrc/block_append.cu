@@ -90,36 +90,22 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const
     const int r = i * RPI + row0, t = base + r;
     float f[8];
     Unpack<__nv_bfloat16>::run(w[i], f);
-    uint32_t lo4 = 0, hi4 = 0;
+    if (odd) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float y = f[e] * inv;
-      if (odd) y = y != y ? 0.f : fminf(fmaxf(y, -F::kMax), F::kMax);
-      const uint32_t code = F::code(y);
-      if (e < 4)
-        lo4 |= code << (8 * e);
-      else
-        hi4 |= code << (8 * (e - 4));
+      for (int e = 0; e < 8; ++e) f[e] = f[e] != f[e] ? 0.f : fminf(fmaxf(f[e] * inv, -F::kMax), F::kMax);
     }
+    const float by = odd ? 1.f : inv;
+    const uint32_t lo4 = F::codes(f, by), hi4 = F::codes(f + 4, by);
     if (t >= lo && t < hi) *(uint2 *)(codes + (size_t)r * D + sub * 8) = make_uint2(lo4, hi4);
   }
   if (after > before && before > 0.f) {  // earlier entries of the block take the larger scale
-    const float ratio = before * inv;
+    const typename F::Shift shift(exponent(before) - exponent(after));
     for (int i = 0; i < IT; ++i) {
       const int r = i * RPI + row0;
       if (base + r >= s.len) continue;
       uint2 *at = (uint2 *)(codes + (size_t)r * D + sub * 8);
       const uint2 u = *at;
-      float f[8];
-      F::values(u.x, f);
-      F::values(u.y, f + 4);
-      uint32_t lo4 = 0, hi4 = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo4 |= F::code(f[e] * ratio) << (8 * e);
-        hi4 |= F::code(f[e + 4] * ratio) << (8 * e);
-      }
-      *at = make_uint2(lo4, hi4);
+      *at = make_uint2(shift.run(u.x), shift.run(u.y));
     }
   }
   if (lane == 0) *scale = after;
@@ -180,19 +166,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
     const float after = fmaxf(before, block_scale<F>(__uint_as_float(top << 16)));
     const float inv = inverse_pow2(after);
     if (after > before && before > 0.f) {  // earlier entries of the block take the larger scale
-      const float ratio = before * inv;
+      const typename F::Shift shift(exponent(before) - exponent(after));
       for (int t = base; t < s.len; ++t) {
-        uint32_t u = 0;
-        if constexpr (E == 4)
-          u = *(const uint32_t *)(codes + (size_t)t * D);
-        else
-          u = *(const uint16_t *)(codes + (size_t)t * D);
-        float f[4];
-        F::values(u, f);
-        u = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) u |= F::code(f[e] * ratio) << (8 * e);
-        store_codes<E>(codes + (size_t)t * D, 0, u);
+        uint8_t *p = codes + (size_t)t * D;
+        store_codes<E>(p, 0, shift.run(E == 4 ? *(const uint32_t *)p : *(const uint16_t *)p));
       }
     }
     for (int t = lo; t < hi; ++t) {

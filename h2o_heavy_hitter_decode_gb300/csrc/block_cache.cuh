@@ -69,12 +69,62 @@ struct E4M3 {
   }
   // Four codes of a word as floats (exact).
   __device__ __forceinline__ static void values(uint32_t w, float *x) { e4m3x4_to_f32(w, x); }
+  // Codes of x[0..3] * inv (at most kMax up to rounding).
+  __device__ __forceinline__ static uint32_t codes(const float *x, float inv) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t z = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+    return a | z << 16;
+  }
+  // A word's codes times 2^e, rounded to codes (at most kMax up to rounding).
+  // In f16: a code has 4 significant bits, so the two products by 2^(e/2) are
+  // exact wherever the result is 2^-20 or more; below 2^-10 it rounds to 0 in
+  // any case.
+  struct Shift {
+    __half2 a, z;
+    __device__ __forceinline__ explicit Shift(int e) {
+      e = max(-24, min(24, e));  // more than 18: zeros only
+      const int h = e >> 1;
+      a = __half2half2(__ushort_as_half((unsigned short)((h + 15) << 10)));
+      z = __half2half2(__ushort_as_half((unsigned short)((e - h + 15) << 10)));
+    }
+    __device__ __forceinline__ uint32_t run(uint32_t w) const {
+      const uint32_t x = e4m3x2_to_f16x2(w), y = e4m3x2_to_f16x2(w >> 16);
+      const __half2 p = __hmul2(__hmul2(*(const __half2 *)&x, a), z), q = __hmul2(__hmul2(*(const __half2 *)&y, a), z);
+      const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*(const __half2_raw *)&p, __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(*(const __half2_raw *)&q, __NV_SATFINITE, __NV_E4M3);
+      return lo | hi << 16;
+    }
+  };
 };
 struct I8 {
   static constexpr float kMax = 127.f;  // 1.984375 * 2^6
   static constexpr int kMaxExp = 6;
   static constexpr uint32_t kMaxMant = 0x7e0000u;
   __device__ __forceinline__ static uint32_t code(float x) { return (uint32_t)__float2int_rn(x) & 0xffu; }
+  // Added to 1.5 * 2^23 a number rounds to an integer, whose low byte is the
+  // sum's.
+  __device__ __forceinline__ static uint32_t codes(const float *x, float inv) {
+    const float magic = 12582912.f;
+    const uint32_t a = __byte_perm(__float_as_uint(fmaf(x[0], inv, magic)), __float_as_uint(fmaf(x[1], inv, magic)), 0x40);
+    const uint32_t z = __byte_perm(__float_as_uint(fmaf(x[2], inv, magic)), __float_as_uint(fmaf(x[3], inv, magic)), 0x40);
+    return __byte_perm(a, z, 0x5410);
+  }
+  // A word's codes times 2^e, rounded: the same in f16, whose numbers from
+  // 1024 to 2048 are the integers; the fused product has one rounding.
+  struct Shift {
+    __half2 a;
+    __device__ __forceinline__ explicit Shift(int e) {
+      e = max(-15, min(15, e));  // below -8 everything rounds to 0; more than 7: zeros only
+      a = __half2half2(e > -15 ? __ushort_as_half((unsigned short)((e + 15) << 10)) : __ushort_as_half(0));
+    }
+    __device__ __forceinline__ uint32_t run(uint32_t w) const {
+      const __half2 bias = __half2half2(__ushort_as_half(0x6480)), magic = __half2half2(__ushort_as_half(0x6600));
+      const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u, y = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+      const __half2 p = __hfma2(__hsub2(*(const __half2 *)&x, bias), a, magic);
+      const __half2 q = __hfma2(__hsub2(*(const __half2 *)&y, bias), a, magic);
+      return __byte_perm(*(const uint32_t *)&p, *(const uint32_t *)&q, 0x6240);
+    }
+  };
   __device__ __forceinline__ static void values(uint32_t w, float *x) {
     x[0] = (float)(int8_t)(w & 0xffu);
     x[1] = (float)(int8_t)((w >> 8) & 0xffu);
@@ -90,6 +140,8 @@ template <typename F> __device__ __forceinline__ float block_scale(float amax) {
   const int e = (int)(u >> 23) - 127 - F::kMaxExp + ((u & 0x7fffffu) > F::kMaxMant ? 1 : 0);
   return __uint_as_float((uint32_t)((e < kMinExp ? kMinExp : e) + 127) << 23);
 }
+// The exponent of a power of two.
+__device__ __forceinline__ int exponent(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
 // 1 / s of a power of two between 2^kMinExp and 2^126.
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 

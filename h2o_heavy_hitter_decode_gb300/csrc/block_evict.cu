@@ -279,18 +279,11 @@ __global__ void __launch_bounds__(W * 32, 16 / W) move_kernel(const Args a) {
       if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const float inv = inverse_pow2(to[kv]);
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
-            const float ratio = fminf(sc[kv][i] * inv, 3e38f);  // finite for rows of zeros under a large scale
-            if (ratio == 1.f) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x[4];
-              F::values((&w[kv][i].x)[e], x);
-              (&w[kv][i].x)[e] = F::code(x[0] * ratio) | F::code(x[1] * ratio) << 8 | F::code(x[2] * ratio) << 16 |
-                                 F::code(x[3] * ratio) << 24;
-            }
+            if (sc[kv][i] == to[kv]) continue;
+            const typename F::Shift shift(exponent(sc[kv][i]) - exponent(to[kv]));
+            w[kv][i] = make_uint4(shift.run(w[kv][i].x), shift.run(w[kv][i].y), shift.run(w[kv][i].z), shift.run(w[kv][i].w));
           }
         }
       }

@@ -105,6 +105,19 @@ def test_append_extreme_values(kv):
         c.check_device_error()
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_append_infinity_next_to_the_largest_number(kv, n):
+    """An infinity takes the largest code also where largest code * scale is beyond fp32."""
+    x = torch.zeros(1, 1, n, 64)
+    x[0, 0, n - 1, :3] = torch.tensor([3.38e38, math.inf, -math.inf])
+    k = x.bfloat16().to(DEV)
+    c, r = H2OBlockCache(1, 1, 64, 64, kv=kv), RefCache(1, 1, 64, 64, 1, kv)
+    c.append(k, -k, ints([0]))
+    r.append(k, -k, [0])
+    same_state(c, r)
+
+
 # ------------------------------------------------------------------- attend
 
 ATTEND = [  # B, H, G, n, d, kv, cap, lens, counts, causal
