@@ -1,22 +1,25 @@
 // block_evict.cu — a block-scaled 8-bit cache cut down to its k_heavy
 // highest-ranking entries and its k_local last ones.
 //
-// select_kernel: keys mapped to unsigned integers that order like them; a
+// One launch; a CTA, or a cluster of up to 16 where there are few heads, takes
+// a head through both phases, so that on a busy device one head's selection
+// (arithmetic) runs under its neighbours' move (memory).
+//
+// Selection: keys mapped to unsigned integers that order like them; a
 // four-pass radix select (8-bit digits) finds the threshold and how many of
 // the entries equal to it stay (the ones with the highest indices); one scan
-// then gives the kept indices in order.  A head's candidates are shared out
-// over a cluster of up to 8 CTAs where there are few heads; each CTA reads its
-// share once and keeps the keys in shared memory, and the digits' counts meet
-// over distributed shared memory.
+// then gives the kept indices in order.  A CTA reads its share of the
+// candidates once and keeps the keys in shared memory; the digits' counts of a
+// cluster meet over distributed shared memory.
 //
-// move_kernel: entry i of the result comes from index src(i) >= i, so a round
-// of consecutive destination blocks, each read into registers by a warp, may
-// be written once every warp of the round has read: later rounds read only
-// behind what was written.  That makes the move in place with one barrier a
-// round (the CTA's, or the cluster's where few heads share the device) and no
-// copy of the cache.  Every destination block gets a fresh scale from the
-// values it receives; where that equals its sources' scale, as mostly, the
-// codes go over unchanged.
+// Move: entry i of the result comes from index src(i) >= i, so a round of
+// consecutive destination blocks, each held by a warp, may be written once
+// every warp of the round has read: later rounds read only behind what was
+// written.  That makes the move in place with one barrier a round and no copy
+// of the cache.  A warp's item is a block of K or of V; the rows of its next
+// two items are on their way to shared memory (cp.async, each lane its own 16
+// bytes) while it works on one.  Every destination block gets a fresh scale
+// from the values it receives; rows whose scale it shares go over unchanged.
 #include <cooperative_groups.h>
 
 #include "block_cache.cuh"
@@ -39,150 +42,8 @@ struct Args {
   const int32_t *lengths, *position;
   int32_t *new_lengths;
   int kh, kl, n_sink, mode;
-  int held;  // keys a CTA of select_kernel has room for
+  int held;  // keys a CTA has room for
 };
-
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kHists = 4;  // histograms of a CTA (each for a quarter of its warps)
-
-template <int P>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ unsigned hist[kHists][256];
-  __shared__ unsigned sums[2][256];  // this CTA's counts, by pass parity
-  __shared__ unsigned total[256];
-  __shared__ unsigned s_digit, s_want, s_eq;
-  __shared__ int s_warp[2][kSelWarps];
-  __shared__ int s_count[2];  // this CTA's entries above and at the threshold
-  cg::cluster_group cluster = cg::this_cluster();
-  const View &c = a.c;
-  const int rank = P > 1 ? (int)cluster.block_rank() : 0;
-  const int bh = blockIdx.x / P, b = bh / c.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int len = a.lengths[b], k = a.kh + a.kl;
-  const bool ok = len >= 0 && len <= c.cap;
-  if (bh == b * c.H && rank == 0 && tid == 0) {
-    a.new_lengths[b] = ok ? min(len, k) : len;
-    if (!ok) atomicOr(c.err, H2O_BERR_RANGE);
-  }
-  if (!ok || len <= k || a.kh == 0) return;  // the whole cluster
-  const int nc = len - a.kl;  // candidates 0 .. nc-1, this CTA's lo .. hi-1
-  const int share = (nc + P - 1) / P, lo = min(nc, rank * share), hi = min(nc, lo + share), n = hi - lo;
-  const int32_t *pos = c.pos + (size_t)bh * c.cap + lo;
-  const float *score = c.score + (size_t)bh * c.cap + lo;
-  int32_t *kept = c.kept + (size_t)bh * c.cap;
-  const int p = a.position ? a.position[b] : len;
-  auto read_key = [&](int j) -> uint32_t {
-    float v = score[j];
-    if (a.n_sink > 0 || a.mode) {
-      const int pj = pos[j];
-      if (pj < a.n_sink) return 0xffffffffu;
-      if (a.mode) {
-        const int seen = p - pj;
-        v = __fdiv_rn(v, (float)(seen > 1 ? seen : 1));
-      }
-    }
-    return order_bits(v);
-  };
-  for (int j = tid; j < min(n, a.held); j += kSelThreads) keys[j] = read_key(j);
-  auto key_of = [&](int j) -> uint32_t { return j < a.held ? keys[j] : read_key(j); };
-
-  uint32_t prefix = 0, pmask = 0;
-  unsigned want = (unsigned)a.kh, eq_total = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < kHists * 256; i += kSelThreads) (&hist[0][0])[i] = 0u;
-    __syncthreads();
-    unsigned *mine = hist[warp & (kHists - 1)];
-    for (int j = tid; j < n; j += kSelThreads) {
-      const uint32_t key = key_of(j);
-      if ((key & pmask) == prefix) atomicAdd(&mine[(key >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid < 256) {
-      unsigned t = 0;
-#pragma unroll
-      for (int i = 0; i < kHists; ++i) t += hist[i][tid];
-      sums[pass & 1][tid] = t;
-      if (P == 1) total[tid] = t;
-    }
-    if (P > 1) {
-      cluster.sync();
-      if (tid < 256) {
-        unsigned t = 0;
-#pragma unroll
-        for (int i = 0; i < P; ++i) t += *cluster.map_shared_rank(&sums[pass & 1][tid], i);
-        total[tid] = t;
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {  // the digit d with count(> d) < want <= count(>= d); lane 0 has the highest digits
-      unsigned own = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) own += total[255 - lane * 8 - i];
-      unsigned run = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += x;
-      }
-      const unsigned above = run - own;
-      if (above < want && want <= run) {
-        unsigned cum = above;
-        int d = 255 - lane * 8;
-        while (cum + total[d] < want) cum += total[d--];
-        s_digit = (unsigned)d;
-        s_want = want - cum;
-        s_eq = total[d];
-      }
-    }
-    __syncthreads();
-    prefix |= s_digit << shift;
-    pmask |= 255u << shift;
-    want = s_want;
-    eq_total = s_eq;
-    __syncthreads();
-  }
-
-  // Each thread scans a run of consecutive candidates (of odd length: no bank conflicts).
-  const int run = (n + kSelThreads - 1) / kSelThreads | 1;
-  const int j0 = min(n, tid * run), j1 = min(n, j0 + run);
-  int above = 0, equal = 0;
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t key = key_of(j);
-    above += key > prefix;
-    equal += key == prefix;
-  }
-  int ia = above, ie = equal;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ie, o);
-    if (lane >= o) ia += x, ie += y;
-  }
-  if (lane == 31) s_warp[0][warp] = ia, s_warp[1][warp] = ie;
-  __syncthreads();
-  int before_a = ia - above, before_e = ie - equal;
-  for (int w = 0; w < warp; ++w) before_a += s_warp[0][w], before_e += s_warp[1][w];
-  if (P > 1) {
-    if (tid == kSelThreads - 1) s_count[0] = before_a + above, s_count[1] = before_e + equal;
-    cluster.sync();
-    for (int i = 0; i < rank; ++i) {
-      before_a += *cluster.map_shared_rank(&s_count[0], i);
-      before_e += *cluster.map_shared_rank(&s_count[1], i);
-    }
-  }
-  const int drop = (int)(eq_total - want);  // the first of the equal ones go
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t key = key_of(j);
-    bool keep = key > prefix;
-    const int slot = before_a + max(0, before_e - drop);
-    if (keep) ++before_a;
-    if (key == prefix) keep = before_e++ >= drop;
-    if (keep && slot < a.kh) kept[slot] = lo + j;
-  }
-  if (P > 1) cluster.sync();  // no CTA leaves while its counts are read
-}
 
 // The largest magnitude among codes, kept as code numbers.
 template <typename F> struct TopCode;
@@ -212,138 +73,305 @@ template <> struct TopCode<I8> {  // codes + 128, largest and least
   }
 };
 
+template <int P> __device__ __forceinline__ void head_sync(cg::cluster_group &cluster) {
+  if constexpr (P > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+}
+
+// 16 bytes global -> shared, zeros where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 template <typename F, int D, int P, int W>
-__global__ void __launch_bounds__(W * 32, 16 / W) move_kernel(const Args a) {
-  constexpr int LPR = D / 16;       // lanes per row, 16 codes each
-  constexpr int RPI = 32 / LPR;     // rows per load of the warp
-  constexpr int IT = kBlock / RPI;  // loads
+__global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Args a) {
+  constexpr int kThreads = W * 32;
+  constexpr int kHists = W / 2;  // histograms of a CTA, one for each two warps
+  extern __shared__ __align__(16) uint32_t dyn[];  // the keys, then the warps' row buffers
+  __shared__ unsigned hist[kHists][256];
+  __shared__ unsigned sums[2][256];  // this CTA's counts, by pass parity
+  __shared__ unsigned total[256];
+  __shared__ unsigned s_digit, s_want, s_eq;
+  __shared__ int s_warp[2][W];
+  __shared__ int s_count[2];  // this CTA's entries above and at the threshold
   cg::cluster_group cluster = cg::this_cluster();
   const View &c = a.c;
   const int rank = P > 1 ? (int)cluster.block_rank() : 0;
-  const int bh = blockIdx.x / P, b = bh / c.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int len = a.lengths[b], kh = a.kh, k = kh + a.kl;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept indices
-  if (len < 0 || len > c.cap || len <= k) return;     // the whole cluster
-  const int nc = len - a.kl;
+  const int bh = blockIdx.x / P, b = bh / c.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = a.lengths[b], kh = a.kh, k = a.kh + a.kl;
+  const bool ok = len >= 0 && len <= c.cap;
+  if (bh == b * c.H && rank == 0 && tid == 0) {
+    a.new_lengths[b] = ok ? min(len, k) : len;
+    if (!ok) atomicOr(c.err, H2O_BERR_RANGE);
+  }
+  if (!ok || len <= k) return;  // the whole cluster
+  const int nc = len - a.kl;    // candidates 0 .. nc-1
   int32_t *pos = c.pos + (size_t)bh * c.cap;
   float *score = c.score + (size_t)bh * c.cap;
-  const int32_t *kept = c.kept + (size_t)bh * c.cap;
+  int32_t *kept = c.kept + (size_t)bh * c.cap;
+
+  if (kh > 0) {
+    // this CTA's candidates lo .. lo + n - 1
+    const int share = ((nc + P - 1) / P + 3) & ~3, lo = min(nc, rank * share), n = min(nc, lo + share) - lo;
+    const int p = a.position ? a.position[b] : len;
+    auto to_key = [&](float v, int j) -> uint32_t {
+      if (a.n_sink > 0 || a.mode) {
+        const int pj = pos[lo + j];
+        if (pj < a.n_sink) return 0xffffffffu;
+        if (a.mode) {
+          const int seen = p - pj;
+          v = __fdiv_rn(v, (float)(seen > 1 ? seen : 1));
+        }
+      }
+      return order_bits(v);
+    };
+    auto key_of = [&](int j) -> uint32_t { return j < a.held ? dyn[j] : to_key(score[lo + j], j); };
+
+    uint32_t prefix = 0, pmask = 0;
+    unsigned want = (unsigned)kh, eq_total = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      for (int i = tid; i < kHists * 256; i += kThreads) (&hist[0][0])[i] = 0u;
+      __syncthreads();
+      unsigned *mine = hist[warp >> 1];
+      auto count = [&](uint32_t key) {
+        if ((key & pmask) == prefix) atomicAdd(&mine[(key >> shift) & 255u], 1u);
+      };
+      if (pass == 0) {
+        const int whole = min(n, a.held) & ~3;
+#pragma unroll 2
+        for (int j = tid * 4; j < whole; j += kThreads * 4) {
+          const float4 v = *(const float4 *)(score + lo + j);
+          const uint4 u = make_uint4(to_key(v.x, j), to_key(v.y, j + 1), to_key(v.z, j + 2), to_key(v.w, j + 3));
+          *(uint4 *)(dyn + j) = u;
+          count(u.x), count(u.y), count(u.z), count(u.w);
+        }
+        for (int j = whole + tid; j < n; j += kThreads) {
+          const uint32_t u = to_key(score[lo + j], j);
+          if (j < a.held) dyn[j] = u;
+          count(u);
+        }
+      } else {
+        const int whole = min(n, a.held) & ~3;
+#pragma unroll 2
+        for (int j = tid * 4; j < whole; j += kThreads * 4) {
+          const uint4 u = *(const uint4 *)(dyn + j);
+          count(u.x), count(u.y), count(u.z), count(u.w);
+        }
+        for (int j = whole + tid; j < n; j += kThreads) count(key_of(j));
+      }
+      __syncthreads();
+      if (tid < 256) {
+        unsigned t = 0;
+#pragma unroll
+        for (int i = 0; i < kHists; ++i) t += hist[i][tid];
+        sums[pass & 1][tid] = t;
+        if (P == 1) total[tid] = t;
+      }
+      if (P > 1) {
+        cluster.sync();
+        if (tid < 256) {
+          unsigned t = 0;
+#pragma unroll
+          for (int i = 0; i < P; ++i) t += *cluster.map_shared_rank(&sums[pass & 1][tid], i);
+          total[tid] = t;
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {  // the digit d with count(> d) < want <= count(>= d); lane 0 has the highest digits
+        unsigned own = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) own += total[255 - lane * 8 - i];
+        unsigned run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += x;
+        }
+        const unsigned above = run - own;
+        if (above < want && want <= run) {
+          unsigned cum = above;
+          int d = 255 - lane * 8;
+          while (cum + total[d] < want) cum += total[d--];
+          s_digit = (unsigned)d;
+          s_want = want - cum;
+          s_eq = total[d];
+        }
+      }
+      __syncthreads();
+      prefix |= s_digit << shift;
+      pmask |= 255u << shift;
+      want = s_want;
+      eq_total = s_eq;
+    }
+
+    // Each thread scans a run of consecutive candidates (of odd length: no bank conflicts).
+    const int run = (n + kThreads - 1) / kThreads | 1;
+    const int j0 = min(n, tid * run), j1 = min(n, j0 + run);
+    int above = 0, equal = 0;
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t key = key_of(j);
+      above += key > prefix;
+      equal += key == prefix;
+    }
+    int ia = above, ie = equal;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ie, o);
+      if (lane >= o) ia += x, ie += y;
+    }
+    if (lane == 31) s_warp[0][warp] = ia, s_warp[1][warp] = ie;
+    __syncthreads();
+    int before_a = ia - above, before_e = ie - equal;
+    for (int w = 0; w < warp; ++w) before_a += s_warp[0][w], before_e += s_warp[1][w];
+    if (P > 1) {
+      if (tid == kThreads - 1) s_count[0] = before_a + above, s_count[1] = before_e + equal;
+      cluster.sync();
+      for (int i = 0; i < rank; ++i) {
+        before_a += *cluster.map_shared_rank(&s_count[0], i);
+        before_e += *cluster.map_shared_rank(&s_count[1], i);
+      }
+    }
+    const int drop = (int)(eq_total - want);  // the first of the equal ones go
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t key = key_of(j);
+      bool keep = key > prefix;
+      const int slot = before_a + max(0, before_e - drop);
+      if (keep) ++before_a;
+      if (key == prefix) keep = before_e++ >= drop;
+      if (keep && slot < kh) kept[slot] = lo + j;
+    }
+    head_sync<P>(cluster);  // every index written, every key and count read
+  }
+
+  constexpr int LPR = D / 16;          // lanes per row, 16 codes each
+  constexpr int RPI = 32 / LPR;        // rows per copy of the warp
+  constexpr int IT = kBlock / RPI;     // copies
+  constexpr int kItem = kBlock * D;    // bytes
   const size_t scales = (size_t)bh * (c.cap / kBlock);
   const int sub = lane % LPR, row0 = lane / LPR;
-  const int blocks = (k + kBlock - 1) / kBlock;
-  // Source of the lane's entry of a block; 0 behind the last one.
-  auto source = [&](int i) { return i < kh ? min(max(kept[i], 0), len - 1) : i < k ? i - kh + nc : 0; };
-  int blk = rank * W + warp;
-  int src_next = source(min(blk * kBlock + lane, k));
-  for (int round = 0; round < blocks; round += P * W, blk += P * W) {
-    const int base = blk * kBlock;
-    const bool work = blk < blocks;
-    const int own = base + lane;
-    const int src_own = src_next;
-    src_next = blk + P * W < blocks ? source(own + P * W * kBlock) : 0;
-    uint4 w[2][IT];
-    float sc[2][IT], to[2];
-    int pos_own = 0;
-    float score_own = 0.f;
-    bool same = true;
-    if (work) {
+  const int items = (k + kBlock - 1) / kBlock * 2;  // K and V of every block
+  const uint32_t buf = (uint32_t)__cvta_generic_to_shared(dyn) + warp * 2 * kItem + lane * 16;
+  const uint4 *held = (const uint4 *)((const uint8_t *)dyn + warp * 2 * kItem) + lane;
+  // The lane's entry of an item, and what travels with it.
+  struct Entry {
+    int src, pos;
+    float scale, score;
+  };
+  auto source = [&](int q) {  // 0 behind the last entry
+    const int i = (q >> 1) * kBlock + lane;
+    return q >= items || i >= k ? 0 : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
+  };
+  auto fetch = [&](int q, int slot, int src) {  // an item's rows into one of the warp's two buffers
+    Entry x{src, 0, 0.f, 0.f};
+    if (q < items) {
+      const bool is_v = q & 1;
+      const int base = (q >> 1) * kBlock;
+      const uint8_t *codes = (is_v ? c.V : c.K) + (size_t)bh * c.cap * D + sub * 16;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t *codes = (kv ? c.V : c.K) + (size_t)bh * c.cap * D + sub * 16;
-        const float *scale = (kv ? c.Vsc : c.Ksc) + scales;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int src = __shfl_sync(0xffffffffu, src_own, i * RPI + row0);
-          const bool in = base + i * RPI + row0 < k;
-          w[kv][i] = in ? *(const uint4 *)(codes + (size_t)src * D) : make_uint4(0u, 0u, 0u, 0u);
-          sc[kv][i] = in ? scale[src / kBlock] : 0.f;
-        }
+      for (int i = 0; i < IT; ++i) {
+        const int from = __shfl_sync(0xffffffffu, src, i * RPI + row0);
+        copy16(buf + slot * kItem + i * 512, codes + (size_t)from * D, base + i * RPI + row0 < k);
       }
-      if (own < k) {
-        pos_own = pos[src_own];
-        score_own = score[src_own];
-      }
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          TopCode<F> top;
-          top.add(w[kv][i].x), top.add(w[kv][i].y), top.add(w[kv][i].z), top.add(w[kv][i].w);
-          amax = fmaxf(amax, top.value() * sc[kv][i]);
-        }
-        to[kv] = block_scale<F>(warp_max(amax));
-#pragma unroll
-        for (int i = 0; i < IT; ++i) same = same && (sc[kv][i] == to[kv] || sc[kv][i] == 0.f);
-      }
-      if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            if (sc[kv][i] == to[kv]) continue;
-            const typename F::Shift shift(exponent(sc[kv][i]) - exponent(to[kv]));
-            w[kv][i] = make_uint4(shift.run(w[kv][i].x), shift.run(w[kv][i].y), shift.run(w[kv][i].z), shift.run(w[kv][i].w));
-          }
+      if (base + lane < k) {
+        x.scale = ((is_v ? c.Vsc : c.Ksc) + scales)[src / kBlock];
+        if (!is_v) {
+          x.pos = pos[src];
+          x.score = score[src];
         }
       }
     }
-    if (P > 1)
-      cluster.sync();
-    else
-      __syncthreads();  // every warp of the round has read its sources
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return x;
+  };
+  const int stride = P * W;
+  int q = rank * W + warp;
+  const int s0 = source(q), s1 = source(q + stride);
+  int src2 = source(q + 2 * stride);
+  Entry x0 = fetch(q, 0, s0), x1 = fetch(q + stride, 1, s1);
+  for (int round = 0, slot = 0; round < items; round += stride, q += stride, slot ^= 1) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this item; each lane reads back what it copied
+    uint4 w[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) w[i] = held[slot * (kItem / 16) + i * 32];
+    const Entry x = x0;
+    x0 = x1;
+    x1 = fetch(q + 2 * stride, slot, src2);
+    src2 = source(q + 3 * stride);
+    const bool work = q < items;
+    const int base = (q >> 1) * kBlock;
+    float to = 0.f;
     if (work) {
+      float amax = 0.f, sc[IT];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint8_t *codes = (kv ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
-#pragma unroll
-        for (int i = 0; i < IT; ++i)
-          if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[kv][i];
-        if (lane == 0) ((kv ? c.Vsc : c.Ksc) + scales)[blk] = to[kv];
+      for (int i = 0; i < IT; ++i) {
+        TopCode<F> top;
+        top.add(w[i].x), top.add(w[i].y), top.add(w[i].z), top.add(w[i].w);
+        sc[i] = __shfl_sync(0xffffffffu, x.scale, i * RPI + row0);
+        amax = fmaxf(amax, top.value() * sc[i]);
       }
-      if (own < k) {
-        pos[own] = pos_own;
-        score[own] = score_own;
+      to = block_scale<F>(warp_max(amax));
+      if (__any_sync(0xffffffffu, x.scale != to)) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          if (sc[i] == to) continue;
+          const typename F::Shift shift(exponent(sc[i]) - exponent(to));
+          w[i] = make_uint4(shift.run(w[i].x), shift.run(w[i].y), shift.run(w[i].z), shift.run(w[i].w));
+        }
+      }
+    }
+    head_sync<P>(cluster);  // every warp of the round has read its sources
+    if (work) {
+      const bool is_v = q & 1;
+      uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+        if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[i];
+      if (lane == 0) ((is_v ? c.Vsc : c.Ksc) + scales)[q >> 1] = to;
+      if (!is_v && base + lane < k) {
+        pos[base + lane] = x.pos;
+        score[base + lane] = x.score;
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <typename K>
-cudaError_t launch_cluster(K *kernel, int ctas, int cluster, int threads, int smem, bool after, cudaStream_t st,
-                           const Args &a) {
+template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStream_t st) {
+  constexpr int kRing = W * 2 * kBlock * D;
+  const int share = ((a.c.cap + P - 1) / P + 3) & ~3, most = 110 * 1024 / 4;  // keys: two CTAs still fit an SM
+  const int keys = share < most ? share : most;
+  const int smem = keys * 4 > kRing ? keys * 4 : kRing;
+  a.held = smem / 4;
+  cudaError_t e = cudaFuncSetAttribute(evict_kernel<F, D, P, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && P > 8)
+    e = cudaFuncSetAttribute(evict_kernel<F, D, P, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3(a.c.B * a.c.H * P);
+  cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim = {(unsigned)cluster, 1, 1};
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim = {(unsigned)P, 1, 1};
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W>, a);
 }
 
-template <int P> cudaError_t select_p(Args a, cudaStream_t st) {
-  constexpr int kRoom = 49152;  // keys, 192 KB
-  const int share = (a.c.cap + P - 1) / P;
-  a.held = share < kRoom ? share : kRoom;
-  const int smem = a.held * 4;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_cluster(select_kernel<P>, a.c.B * a.c.H * P, P, kSelThreads, smem, false, st, a);
-}
-
-template <typename F, int D> cudaError_t move_t(const Args &a, cudaStream_t st) {
-  // Few heads: a cluster of 8 wide CTAs for each, so that a round covers 128 blocks; many: one CTA of 8 warps, two
-  // to an SM, whose barriers then overlap.
+template <typename F, int D> cudaError_t evict_t(const Args &a, cudaStream_t st) {
+  // Up to 16 CTAs share a head while that fills empty SMs and leaves each a thousand entries.
   const int heads = a.c.B * a.c.H;
-  if (heads * 8 <= a.c.sms) return launch_cluster(move_kernel<F, D, 8, 16>, heads * 8, 8, 512, 0, true, st, a);
-  if (heads * 2 <= a.c.sms) return launch_cluster(move_kernel<F, D, 4, 8>, heads * 4, 4, 256, 0, true, st, a);
-  return launch_cluster(move_kernel<F, D, 1, 8>, heads, 1, 256, 0, true, st, a);
+  auto shared = [&](int p, int per_sm) { return heads * p <= a.c.sms * per_sm && a.c.cap / p >= 1024; };
+  if (shared(16, 1)) return evict_p<F, D, 16, 16>(a, st);
+  if (shared(8, 3)) return evict_p<F, D, 8, 8>(a, st);
+  if (shared(4, 3)) return evict_p<F, D, 4, 8>(a, st);
+  if (shared(2, 3)) return evict_p<F, D, 2, 8>(a, st);
+  return evict_p<F, D, 1, 8>(a, st);
 }
 
 }  // namespace
@@ -351,13 +379,8 @@ template <typename F, int D> cudaError_t move_t(const Args &a, cudaStream_t st) 
 cudaError_t launch_evict(const View &c, const int32_t *lengths, int kh, int kl, int n_sink, int mode,
                          const int32_t *position, int32_t *new_lengths, cudaStream_t st) {
   const Args a{c, lengths, position, new_lengths, kh, kl, n_sink, mode, 0};
-  // Up to 8 CTAs share a head while that fills empty SMs and leaves each some thousand candidates.
-  int p = 1;
-  while (p < 8 && c.B * c.H * p * 2 <= 2 * c.sms && c.cap / p > 4096) p *= 2;
-  cudaError_t e = p == 8 ? select_p<8>(a, st) : p == 4 ? select_p<4>(a, st) : p == 2 ? select_p<2>(a, st) : select_p<1>(a, st);
-  if (e != cudaSuccess) return e;
-  if (c.kv == H2O_KV_E4M3) return c.d == 128 ? move_t<E4M3, 128>(a, st) : move_t<E4M3, 64>(a, st);
-  return c.d == 128 ? move_t<I8, 128>(a, st) : move_t<I8, 64>(a, st);
+  if (c.kv == H2O_KV_E4M3) return c.d == 128 ? evict_t<E4M3, 128>(a, st) : evict_t<E4M3, 64>(a, st);
+  return c.d == 128 ? evict_t<I8, 128>(a, st) : evict_t<I8, 64>(a, st);
 }
 
 }  // namespace blk

@@ -311,6 +311,41 @@ def test_evict_long():
     same_state(c, r)
 
 
+@pytest.mark.parametrize("B,H,cap,lens,kv", [(2, 10, 8192, [8192, 5001], "e4m3"), (6, 10, 4096, [4001, 4096, 600, 599, 3333, 2048], "int8"),
+                                             (12, 10, 2048, [2048 - 31 * b for b in range(12)], "e4m3"),
+                                             (1, 240, 30016, [30011], "int8")], ids=str)
+@pytest.mark.parametrize("mode", [0, 1])
+def test_evict_shared_heads(B, H, cap, lens, kv, mode):
+    """Heads taken by clusters of 8, 4 and 2 CTAs, and by one CTA with more candidates than it keeps in shared memory;
+    the positions of all heads by a stable sort, the whole state of some."""
+    d, kh, kl = 64, 401, 198
+    g = torch.Generator(DEV).manual_seed(79)
+    c = H2OBlockCache(B, H, d, cap, kv=kv)
+    c.append(rows(g, B, H, cap, d), rows(g, B, H, cap, d), ints([0] * B), score=torch.rand(B, H, cap, generator=g, device=DEV).mul_(200).round_())
+    refs = {}
+    for b, h in [(0, 0), (B - 1, H - 1), (B // 2, H // 3)]:
+        r = refs[b, h] = RefCache(1, 1, d, cap, 1, kv)
+        for n in ("K", "V", "K_scale", "V_scale", "score"):
+            getattr(r, n).copy_(getattr(c, n)[b : b + 1, h : h + 1].cpu().double())
+        r.pos.copy_(c.pos[b : b + 1, h : h + 1].cpu().long())
+    i = torch.arange(cap, device=DEV)
+    n = ints(lens)[:, None, None].long()
+    key = c.score / (cap - c.pos).clamp(min=1).float() if mode else c.score
+    key = torch.where((i >= n - kl) | (c.pos < 3), math.inf, key)
+    gone = torch.zeros_like(key, dtype=torch.bool).scatter_(2, key.sort(dim=-1, stable=True).indices, (i < n - (kh + kl)).expand(B, H, cap))
+    kept = ~gone & (i < n)
+    new = c.evict(ints(lens), kh, kl, n_sink=3, score_mode=mode, position=ints([cap] * B))
+    assert new.tolist() == [min(x, kh + kl) for x in lens]
+    for b in range(B):
+        want = i.expand(H, cap)[kept[b]].view(H, -1)
+        assert torch.equal(c.pos[b, :, : want.shape[1]].long(), want), b
+    for (b, h), r in refs.items():
+        r.evict([lens[b]], kh, kl, 3, mode, [cap])
+        for name in ("K", "V", "K_scale", "V_scale", "score", "pos"):
+            assert torch.equal(getattr(c, name)[b, h].cpu().double(), getattr(r, name)[0, 0].double()), (name, b, h)
+    assert c.error_bits() == 0
+
+
 # -------------------------------------------------- used together, and where
 
 def test_serving_run():
