@@ -6,11 +6,13 @@
 // (arithmetic) runs under its neighbours' move (memory).
 //
 // Selection: keys mapped to unsigned integers that order like them; a
-// four-pass radix select (8-bit digits) finds the threshold and how many of
-// the entries equal to it stay (the ones with the highest indices); one scan
-// then gives the kept indices in order.  A CTA reads its share of the
-// candidates once and keeps the keys in shared memory; the digits' counts of a
-// cluster meet over distributed shared memory.
+// three-pass radix select (digits of 11, 11 and 10 bits: the first one spreads
+// scores of a few octaves over four digits an octave, where atomics on 8-bit
+// digits queued up) finds the threshold and how many of the entries equal to
+// it stay (the ones with the highest indices); one scan then gives the kept
+// indices in order.  A CTA reads its share of the candidates once and keeps
+// the keys in shared memory; the digits' counts of a cluster meet over
+// distributed shared memory.
 //
 // Move: entry i of the result comes from index src(i) >= i, so a round of
 // consecutive destination blocks, each held by a warp, may be written once
@@ -79,6 +81,18 @@ template <int P> __device__ __forceinline__ void head_sync(cg::cluster_group &cl
   else
     __syncthreads();
 }
+// Between the reads and the writes of a round.  What was read is in registers
+// when a warp arrives, so the warps only have to meet: a releasing arrival
+// would make each round wait for the stores of the one before to reach L2.
+template <int P> __device__ __forceinline__ void round_arrive() {
+  if constexpr (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+template <int P> __device__ __forceinline__ void round_wait() {
+  if constexpr (P > 1)
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  else
+    __syncthreads();
+}
 
 // 16 bytes global -> shared, zeros where `in` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
@@ -88,13 +102,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
 template <typename F, int D, int P, int W>
 __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Args a) {
   constexpr int kThreads = W * 32;
-  constexpr int kHists = W / 2;  // histograms of a CTA, one for each two warps
+  constexpr int kDigits = 2048, kOwn = kDigits / kThreads;
   extern __shared__ __align__(16) uint32_t dyn[];  // the keys, then the warps' row buffers
-  __shared__ unsigned hist[kHists][256];
-  __shared__ unsigned sums[2][256];  // this CTA's counts, by pass parity
-  __shared__ unsigned total[256];
+  __shared__ __align__(16) unsigned hist[P > 1 ? 2 : 1][kDigits];  // this CTA's counts, in a cluster by pass parity
+  __shared__ __align__(16) unsigned totals[P > 1 ? 2 : 1][P > 1 ? kDigits / P : 4];  // the cluster's counts of a slice
   __shared__ unsigned s_digit, s_want, s_eq;
   __shared__ int s_warp[2][W];
+  __shared__ unsigned s_sum[W];
   __shared__ int s_count[2];  // this CTA's entries above and at the threshold
   cg::cluster_group cluster = cg::this_cluster();
   const View &c = a.c;
@@ -132,17 +146,18 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     uint32_t prefix = 0, pmask = 0;
     unsigned want = (unsigned)kh, eq_total = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      for (int i = tid; i < kHists * 256; i += kThreads) (&hist[0][0])[i] = 0u;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t dmask = pass == 2 ? 1023u : 2047u;
+      unsigned *mine = hist[P > 1 ? pass & 1 : 0];
+      for (int i = tid * 4; i < kDigits; i += kThreads * 4) *(uint4 *)(mine + i) = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
-      unsigned *mine = hist[warp >> 1];
       auto count = [&](uint32_t key) {
-        if ((key & pmask) == prefix) atomicAdd(&mine[(key >> shift) & 255u], 1u);
+        if ((key & pmask) == prefix) atomicAdd(&mine[(key >> shift) & dmask], 1u);
       };
+      const int whole = min(n, a.held) & ~3;
       if (pass == 0) {
-        const int whole = min(n, a.held) & ~3;
-#pragma unroll 2
+#pragma unroll 4
         for (int j = tid * 4; j < whole; j += kThreads * 4) {
           const float4 v = *(const float4 *)(score + lo + j);
           const uint4 u = make_uint4(to_key(v.x, j), to_key(v.y, j + 1), to_key(v.z, j + 2), to_key(v.w, j + 3));
@@ -155,67 +170,82 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
           count(u);
         }
       } else {
-        const int whole = min(n, a.held) & ~3;
-#pragma unroll 2
+#pragma unroll 4
         for (int j = tid * 4; j < whole; j += kThreads * 4) {
           const uint4 u = *(const uint4 *)(dyn + j);
           count(u.x), count(u.y), count(u.z), count(u.w);
         }
         for (int j = whole + tid; j < n; j += kThreads) count(key_of(j));
       }
-      __syncthreads();
-      if (tid < 256) {
-        unsigned t = 0;
-#pragma unroll
-        for (int i = 0; i < kHists; ++i) t += hist[i][tid];
-        sums[pass & 1][tid] = t;
-        if (P == 1) total[tid] = t;
-      }
-      if (P > 1) {
-        cluster.sync();
-        if (tid < 256) {
+      head_sync<P>(cluster);
+      if constexpr (P > 1) {
+        // Each CTA adds up its slice of the digits over the cluster, and every CTA then
+        // reads all the slices.
+        constexpr int kSlice = kDigits / P;
+        for (int d = tid; d < kSlice; d += kThreads) {
           unsigned t = 0;
 #pragma unroll
-          for (int i = 0; i < P; ++i) t += *cluster.map_shared_rank(&sums[pass & 1][tid], i);
-          total[tid] = t;
+          for (int i = 0; i < P; ++i) t += *cluster.map_shared_rank(mine + rank * kSlice + d, i);
+          totals[pass & 1][d] = t;
         }
+        cluster.sync();
       }
-      __syncthreads();
-      if (warp == 0) {  // the digit d with count(> d) < want <= count(>= d); lane 0 has the highest digits
-        unsigned own = 0;
+      // The digit d with count(> d) < want <= count(>= d): thread i sums its digits, the highest ones first.
+      unsigned own[kOwn], sum = 0;
+      const int top = kDigits - kOwn * (tid + 1);  // its lowest digit
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own += total[255 - lane * 8 - i];
-        unsigned run = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += x;
+      for (int e = 0; e < kOwn; e += 4) {
+        uint4 t;
+        if constexpr (P > 1) {
+          constexpr int kSlice = kDigits / P;
+          t = *(const uint4 *)(cluster.map_shared_rank(totals[pass & 1], (top + e) / kSlice) + (top + e) % kSlice);
+        } else {
+          t = *(const uint4 *)(mine + top + e);
         }
-        const unsigned above = run - own;
-        if (above < want && want <= run) {
-          unsigned cum = above;
-          int d = 255 - lane * 8;
-          while (cum + total[d] < want) cum += total[d--];
-          s_digit = (unsigned)d;
-          s_want = want - cum;
-          s_eq = total[d];
+        own[e] = t.x, own[e + 1] = t.y, own[e + 2] = t.z, own[e + 3] = t.w;
+        sum += t.x + t.y + t.z + t.w;
+      }
+      unsigned run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += x;
+      }
+      if (lane == 31) s_sum[warp] = run;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) run += s_sum[w];
+      unsigned cum = run - sum;
+      if (cum < want && want <= run) {
+#pragma unroll
+        for (int e = kOwn - 1; e >= 0; --e) {
+          if (cum < want && want <= cum + own[e]) {
+            s_digit = (unsigned)(top + e);
+            s_want = want - cum;
+            s_eq = own[e];
+          }
+          cum += own[e];
         }
       }
       __syncthreads();
       prefix |= s_digit << shift;
-      pmask |= 255u << shift;
+      pmask |= dmask << shift;
       want = s_want;
       eq_total = s_eq;
     }
 
-    // Each thread scans a run of consecutive candidates (of odd length: no bank conflicts).
-    const int run = (n + kThreads - 1) / kThreads | 1;
+    // Each thread scans a run of consecutive candidates, four at a time (an odd number of fours: no bank conflicts).
+    const int run = ((n + kThreads * 4 - 1) / (kThreads * 4) | 1) * 4;
     const int j0 = min(n, tid * run), j1 = min(n, j0 + run);
+    auto four = [&](int j) -> uint4 {  // 0, below every threshold that is kept, behind the last one
+      if (j + 4 <= min(n, a.held)) return *(const uint4 *)(dyn + j);
+      return make_uint4(key_of(j), j + 1 < j1 ? key_of(j + 1) : 0u, j + 2 < j1 ? key_of(j + 2) : 0u,
+                        j + 3 < j1 ? key_of(j + 3) : 0u);
+    };
     int above = 0, equal = 0;
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t key = key_of(j);
-      above += key > prefix;
-      equal += key == prefix;
+    for (int j = j0; j < j1; j += 4) {
+      const uint4 u = four(j);
+      above += (u.x > prefix) + (u.y > prefix) + (u.z > prefix) + (u.w > prefix);
+      equal += (u.x == prefix) + (u.y == prefix) + (u.z == prefix) + (u.w == prefix);
     }
     int ia = above, ie = equal;
 #pragma unroll
@@ -236,13 +266,17 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
       }
     }
     const int drop = (int)(eq_total - want);  // the first of the equal ones go
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t key = key_of(j);
-      bool keep = key > prefix;
-      const int slot = before_a + max(0, before_e - drop);
-      if (keep) ++before_a;
-      if (key == prefix) keep = before_e++ >= drop;
-      if (keep && slot < kh) kept[slot] = lo + j;
+    for (int j = j0; j < j1; j += 4) {
+      const uint4 u = four(j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t key = (&u.x)[e];
+        bool keep = key > prefix;
+        const int slot = before_a + max(0, before_e - drop);
+        if (keep) ++before_a;
+        if (key == prefix) keep = before_e++ >= drop;
+        if (keep && slot < kh) kept[slot] = lo + j + e;
+      }
     }
     head_sync<P>(cluster);  // every index written, every key and count read
   }
@@ -258,7 +292,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
   const uint4 *held = (const uint4 *)((const uint8_t *)dyn + warp * 2 * kItem) + lane;
   // The lane's entry of an item, and what travels with it.
   struct Entry {
-    int src, pos;
+    int pos;
     float scale, score;
   };
   auto source = [&](int q) {  // 0 behind the last entry
@@ -266,7 +300,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     return q >= items || i >= k ? 0 : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
   };
   auto fetch = [&](int q, int slot, int src) {  // an item's rows into one of the warp's two buffers
-    Entry x{src, 0, 0.f, 0.f};
+    Entry x{0, 0.f, 0.f};
     if (q < items) {
       const bool is_v = q & 1;
       const int base = (q >> 1) * kBlock;
@@ -297,7 +331,10 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     uint4 w[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) w[i] = held[slot * (kItem / 16) + i * 32];
-    const Entry x = x0;
+    const float scale_own = __shfl_sync(0xffffffffu, x0.scale, lane);  // the loads have come back
+    const int pos_own = __shfl_sync(0xffffffffu, x0.pos, lane);
+    const float score_own = __shfl_sync(0xffffffffu, x0.score, lane);
+    round_arrive<P>();
     x0 = x1;
     x1 = fetch(q + 2 * stride, slot, src2);
     src2 = source(q + 3 * stride);
@@ -310,11 +347,11 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
       for (int i = 0; i < IT; ++i) {
         TopCode<F> top;
         top.add(w[i].x), top.add(w[i].y), top.add(w[i].z), top.add(w[i].w);
-        sc[i] = __shfl_sync(0xffffffffu, x.scale, i * RPI + row0);
+        sc[i] = __shfl_sync(0xffffffffu, scale_own, i * RPI + row0);
         amax = fmaxf(amax, top.value() * sc[i]);
       }
       to = block_scale<F>(warp_max(amax));
-      if (__any_sync(0xffffffffu, x.scale != to)) {
+      if (__any_sync(0xffffffffu, scale_own != to)) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           if (sc[i] == to) continue;
@@ -323,7 +360,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
         }
       }
     }
-    head_sync<P>(cluster);  // every warp of the round has read its sources
+    round_wait<P>();  // every warp of the round has read its sources
     if (work) {
       const bool is_v = q & 1;
       uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
@@ -332,8 +369,8 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
         if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[i];
       if (lane == 0) ((is_v ? c.Vsc : c.Ksc) + scales)[q >> 1] = to;
       if (!is_v && base + lane < k) {
-        pos[base + lane] = x.pos;
-        score[base + lane] = x.score;
+        pos[base + lane] = pos_own;
+        score[base + lane] = score_own;
       }
     }
   }
@@ -364,13 +401,15 @@ template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStrea
 }
 
 template <typename F, int D> cudaError_t evict_t(const Args &a, cudaStream_t st) {
-  // Up to 16 CTAs share a head while that fills empty SMs and leaves each a thousand entries.
+  // Up to 16 CTAs share a head while the clusters all fit the device (two CTAs an SM; of 16, whose CTAs have to find
+  // room in one GPC, 14 clusters fit) and each has a thousand entries.  8 heads of 131,072 entries: 58 us with 16, 76
+  // with 8, 150 with 4.
   const int heads = a.c.B * a.c.H;
-  auto shared = [&](int p, int per_sm) { return heads * p <= a.c.sms * per_sm && a.c.cap / p >= 1024; };
-  if (shared(16, 1)) return evict_p<F, D, 16, 16>(a, st);
-  if (shared(8, 3)) return evict_p<F, D, 8, 8>(a, st);
-  if (shared(4, 3)) return evict_p<F, D, 4, 8>(a, st);
-  if (shared(2, 3)) return evict_p<F, D, 2, 8>(a, st);
+  auto shared = [&](int p) { return heads * p <= a.c.sms * 15 / 8 && a.c.cap / p >= 1024; };
+  if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8>(a, st);
+  if (shared(8)) return evict_p<F, D, 8, 8>(a, st);
+  if (shared(4)) return evict_p<F, D, 4, 8>(a, st);
+  if (shared(2)) return evict_p<F, D, 2, 8>(a, st);
   return evict_p<F, D, 1, 8>(a, st);
 }
 
