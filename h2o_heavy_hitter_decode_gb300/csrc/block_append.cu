@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const
   constexpr int RPI = 32 / LPR;     // rows per load of the warp
   constexpr int IT = kBlock / RPI;  // loads
   const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const bool is_v = item & 1;
   const int64_t bj = item >> 1;  // (b, h, j): j-th block the sequence's rows may touch
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
                                                                  const int32_t *__restrict__ position) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
   const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const bool is_v = item & 1;
   const int bh = item >> 1;

@@ -32,9 +32,9 @@
 // codes have to pass through registers anyway to become f16; tcgen05 would
 // read them back from shared memory, 4 more bytes of its traffic per code.
 //
-// join_kernel: joins the partials of a row to O and LSE.  score_kernel turns
-// the logits that the first kernel left in scratch memory into weights: 4
-// bytes written and read per row and entry, instead of K read again.
+// finish_kernel: joins the partials of a row to O and LSE, and turns the
+// logits that the first kernel left in scratch memory into weights: 4 bytes
+// written and read per row and entry, instead of K read again.
 #include <cuda.h>
 
 #include "block_cache.cuh"
@@ -169,9 +169,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
-
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block.
 template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
   return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
@@ -179,15 +176,16 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
 
 constexpr int kTeams = 4;  // workers of a CTA
 
-// A worker's rows: MT warps of NR tiles of 8 rows.  O takes D / 4 registers a
-// tile and Q as many again for half of that: one and two tiles keep Q in
-// registers, four in shared memory.  Ring: 128 to 192 KB per SM.
+// A worker's rows: MT warps of NR tiles of 8 rows.  Up to 8 rows one warp has
+// one tile (D / 4 registers of O); more rows are tiles of 16, on up to four
+// warps that share the worker's ring.  8 to 16 warps and 128 to 192 KB of
+// ring to an SM; Q is in registers where a worker is one warp.
 template <int D, int NR, int MT> struct Cfg {
   static constexpr int kWarps = kTeams * MT;
-  static constexpr int kCtas = NR == 1 ? 3 : MT == 1 ? 2 : 1;  // per SM
+  static constexpr int kCtas = NR == 1 ? 3 : MT <= 2 ? 2 : 1;  // per SM
   static constexpr int kStage = 2 * kBlock * D;
-  static constexpr bool kQSmem = NR == 4;
-  static constexpr int kStages = (NR == 1 ? 65536 : NR == 2 ? 98304 : MT == 1 ? 65536 : 131072) / (kTeams * kStage);
+  static constexpr bool kQSmem = MT > 1;
+  static constexpr int kStages = (NR == 2 && MT == 1 ? 98304 : MT <= 2 ? 65536 : 131072) / (kTeams * kStage);
   static constexpr int kQBytes = kQSmem ? kWarps * NR * D * 16 : 0;
   static constexpr int kSmem = 1024 + kTeams * kStages * kStage + kQBytes + kTeams * kStages * 16;
 };
@@ -200,7 +198,6 @@ struct Args {
   float *lse;
   float2 *ml;  // [workers + B*H][max_rows]  partial maximum and sum
   float *po;   // [workers + B*H][max_rows][d]  partial output
-  float *lse2;  // [B*H][max_rows]  base-2 log-sum-exp, +infinity where nothing was seen
   int causal, accumulate, workers;
   int rows;  // n * group: rows of a head in this call
 };
@@ -240,9 +237,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   if (worker == 0 && tile == 0 && blockIdx.y == 0)  // refused sequences are reported once
     for (int b = lane; b < c.B; b += 32)
       if (!seq_of(a.l, b).ok) atomicOr(c.err, H2O_BERR_RANGE);
-  grid_dependency_wait();  // the append before this launch
-  grid_launch_dependents();
-  if (count == 0) return;
+  if (count == 0) {
+    grid_dependency_wait();
+    return;
+  }
 
   Cursor cur, ld;
   cur.seek(a.l, c.B, c.H, x0);
@@ -260,6 +258,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     put = put + 1 == S ? 0 : put + 1;
     ld.next(a.l, c.B, c.H);
   };
+  // Blocks that the append before this launch does not change are on their way while it still runs.
+  if (tile == 0)
+    while (issued < S && issued < count && (ld.blk + 1) * kBlock <= ld.s.len) issue();
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (tile == 0)
     while (issued < S && issued < count) issue();
 
@@ -363,25 +366,25 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     }
     if (!idle) {
       float s[NR][2][4];  // S^T: entries 16 x + g and + 8, rows 2 t and 2 t + 1
-      {
-        uint32_t kw[4][KS];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+      for (int part = 0; part < KS / 4; ++part) {  // 16 bytes of each K row at a time
+        uint32_t kw[4][4];
 #pragma unroll
-          for (int e = 0; e < KS / 4; ++e) {
-            const uint4 u = *(const uint4 *)(kt + chunk_at<D>(n * 8 + g, t * (KS / 4) + e));
-            kw[n][4 * e] = u.x, kw[n][4 * e + 1] = u.y, kw[n][4 * e + 2] = u.z, kw[n][4 * e + 3] = u.w;
-          }
+        for (int n = 0; n < 4; ++n) {
+          const uint4 u = *(const uint4 *)(kt + chunk_at<D>(n * 8 + g, t * (KS / 4) + part));
+          kw[n][0] = u.x, kw[n][1] = u.y, kw[n][2] = u.z, kw[n][3] = u.w;
+        }
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
+        for (int k = 0; k < 4; k += 2) {
           uint32_t q[NR][4];
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
             if constexpr (G::kQSmem) {
-              const uint4 u = qs[(n * (KS / 2) + k / 2) * 32 + lane];
+              const uint4 u = qs[(n * (KS / 2) + part * 2 + k / 2) * 32 + lane];
               q[n][0] = u.x, q[n][1] = u.y, q[n][2] = u.z, q[n][3] = u.w;
             } else {
-              q[n][0] = qr[n][k][0], q[n][1] = qr[n][k][1], q[n][2] = qr[n][k + 1][0], q[n][3] = qr[n][k + 1][1];
+              q[n][0] = qr[n][part * 4 + k][0], q[n][1] = qr[n][part * 4 + k][1];
+              q[n][2] = qr[n][part * 4 + k + 1][0], q[n][3] = qr[n][part * 4 + k + 1][1];
             }
           }
 #pragma unroll
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
               T::run(kw[2 * x + 1][k + e], ka[1], ka[3]);
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
-                if (k + e == 0)
+                if (part == 0 && k + e == 0)
                   mma16816_new(s[n][x], ka, q[n][0], q[n][1]);
                 else
                   mma16816(s[n][x], ka, q[n][2 * e], q[n][2 * e + 1]);
@@ -474,40 +477,45 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
         __syncwarp();
       }
       // O += vs (P V): a fresh product per block, added in fp32 under the block's scale
-      constexpr int VW = D / 32;  // words of the lane's D/8 dimensions of an entry
-      uint32_t vw[8][VW];
+      constexpr int VW = D == 128 && NR == 1 ? 4 : 2;  // words of the lane's D/8 dimensions of an entry at a time
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = (e >> 1) * 8 + 2 * t + (e & 1);
-        if constexpr (D == 128) {
-          const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
-          vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % VW] = u.z, vw[e][3 % VW] = u.w;
-        } else {
-          const uint2 u = *(const uint2 *)(vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
-          vw[e][0] = u.x, vw[e][1] = u.y;
-        }
-      }
+      for (int part = 0; part < D / 32 / VW; ++part) {
+        uint32_t vw[8][VW];
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        uint32_t va[2][2][4];  // [dimensions 4w, 4w+1 | 4w+2, 4w+3][k step]
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
-          T::run(__byte_perm(x, y, T::kLow), va[0][k][0], va[0][k][1]);
-          T::run(__byte_perm(x, y, T::kHigh), va[1][k][0], va[1][k][1]);
-          T::run(__byte_perm(z, v, T::kLow), va[0][k][2], va[0][k][3]);
-          T::run(__byte_perm(z, v, T::kHigh), va[1][k][2], va[1][k][3]);
-        }
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float acc[4];
-            mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
-            mma16816(acc, va[y][1], p[n][2], p[n][3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][2 * w + y][e] = fmaf(acc[e], vs_now, o[n][2 * w + y][e]);
+        for (int e = 0; e < 8; ++e) {
+          const int r = (e >> 1) * 8 + 2 * t + (e & 1);
+          if constexpr (VW == 4) {
+            const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
+            vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % VW] = u.z, vw[e][3 % VW] = u.w;
+          } else {
+            const uint8_t *from = D == 128 ? vt + chunk_at<D>(r, g) + part * 8 : vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
+            const uint2 u = *(const uint2 *)from;
+            vw[e][0] = u.x, vw[e][1] = u.y;
           }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t va[2][2][4];  // [dimensions 4w, 4w+1 | 4w+2, 4w+3][k step]
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
+            T::run(__byte_perm(x, y, T::kLow), va[0][k][0], va[0][k][1]);
+            T::run(__byte_perm(x, y, T::kHigh), va[1][k][0], va[1][k][1]);
+            T::run(__byte_perm(z, v, T::kLow), va[0][k][2], va[0][k][3]);
+            T::run(__byte_perm(z, v, T::kHigh), va[1][k][2], va[1][k][3]);
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int j = (part * VW + w) * 2 + y;
+              float acc[4];
+              mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
+              mma16816(acc, va[y][1], p[n][2], p[n][3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][j][e] = fmaf(acc[e], vs_now, o[n][j][e]);
+            }
+        }
       }
     }
     // this warp has read the stage
@@ -533,6 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (!(live >> (2 * n + u) & 1)) continue;
         const int r = row0 + 8 * n + 2 * t + u;
+        if (g == 0) a.ml[slot + r] = make_float2(m[n][u], l);
         // the lane's D/8 dimensions: g D/8 + 2 j (accumulator u) and + 1 (2 + u)
         if (whole) {
           const int tok = r / c.group, hq = ah * c.group + r % c.group;
@@ -547,13 +556,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
           }
 #pragma unroll
           for (int j = 0; j < OT; j += 4) *(uint4 *)(dst + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-          if (g == 0) {
-            a.lse2[(size_t)bh * c.max_rows + r] = any ? m[n][u] + log2f(l) : INFINITY;
-            if (a.lse)
-              a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (m[n][u] + log2f(l)) * kLn2 : -INFINITY;
-          }
+          if (a.lse && g == 0)
+            a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (m[n][u] + log2f(l)) * kLn2 : -INFINITY;
         } else {
-          if (g == 0) a.ml[slot + r] = make_float2(m[n][u], l);
           float *dst = a.po + (slot + r) * D + g * (D / 8);
 #pragma unroll
           for (int j = 0; j < OT; j += 2)
@@ -568,118 +573,143 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   }
 }
 
-// --------------------------------------------------------------------- join
-constexpr int kChunk = 256;  // entries of one score item
-constexpr int kItemWarps = 8;  // items (warps) of a CTA
+// ------------------------------------------------------------------- finish
+constexpr int kFinWarps = 8;
+constexpr int kChunk = 256 * kFinWarps;  // entries of a CTA's score item
 
-// 32 dimensions of one row's output per warp, where a head lies in several
-// runs: four groups of eight lanes take the partials in turn.
+// (m, l) of two parts of a row, base 2.
+__device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
+  const float mn = fmaxf(m, om);
+  l = (m == -INFINITY ? l : l * ex2(m - mn)) + (om == -INFINITY ? ol : ol * ex2(om - mn));
+  m = mn;
+}
+
+// First eight items to a CTA (one a warp) of 32 dimensions of one row's
+// output, where a head lies in several runs: all lanes gather the row's LSE,
+// then four groups of eight lanes take the partials in turn.  Then kChunk
+// entries of one head to a CTA: the warps gather the rows' LSE, then each
+// thread adds the rows' weights of its entries, in the rows' order.
 template <int D>
-__global__ void __launch_bounds__(kItemWarps * 32) join_kernel(const Args a) {
+__global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
   const View &c = a.c;
+  __shared__ float2 part_ml[kFinWarps][H2O_BLOCK_MAX_ROWS];
+  __shared__ float row_lse[H2O_BLOCK_MAX_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks = c.H * sum_units(a.l, c.B, kBlock);
   const int workers = min(a.workers, blocks);
-  const int64_t items = (int64_t)c.B * c.H * a.rows * (D / 32);
+  const int64_t outs = (int64_t)c.B * c.H * a.rows * (D / 32);
+  const int out_ctas = (int)((outs + kFinWarps - 1) / kFinWarps);
+  const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
   grid_dependency_wait();
-  grid_launch_dependents();
-  for (int64_t item = (int64_t)blockIdx.x * kItemWarps + warp; item < items; item += (int64_t)gridDim.x * kItemWarps) {
-    const int part = (int)(item % (D / 32));
-    const int64_t hr = item / (D / 32);
-    const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
-    const Seq s = seq_of(a.l, b);
-    const int tok = r / c.group, hq = h * c.group + r % c.group;
-    if (tok >= s.cnt) continue;
-    __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + part * 32 + (lane & 7) * 4;
-    float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
-    const int nblk = ceil_div(s.total, kBlock);
-    if (nblk == 0) {  // no entry at all
-      if (lane < 8) *(uint2 *)dst = make_uint2(0u, 0u);
-      if (lse && part == 0 && lane == 0) *lse = -INFINITY;
+  for (int cta = blockIdx.x; cta < out_ctas + chunks; cta += gridDim.x) {
+    if (cta < out_ctas) {
+      const int64_t item = (int64_t)cta * kFinWarps + warp;
+      if (item >= outs) continue;
+      const int part = (int)(item % (D / 32));
+      const int64_t hr = item / (D / 32);
+      const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
+      const Seq s = seq_of(a.l, b);
+      const int tok = r / c.group, hq = h * c.group + r % c.group;
+      if (tok >= s.cnt) continue;
+      __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + part * 32 + (lane & 7) * 4;
+      float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
+      const int nblk = ceil_div(s.total, kBlock);
+      if (nblk == 0) {  // no entry at all
+        if (lane < 8) *(uint2 *)dst = make_uint2(0u, 0u);
+        if (lse && part == 0 && lane == 0) *lse = -INFINITY;
+        continue;
+      }
+      int before = 0;
+      for (int i = lane; i < b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
+      const int x = c.H * __reduce_add_sync(0xffffffffu, before) + h * nblk;
+      const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
+      if (w0 == w1) continue;  // written by its worker
+      const float2 *ml = a.ml + (size_t)bh * c.max_rows + r;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+      for (int w = w0 + lane; w <= w1; w += 32) {
+        const float2 p = ml[(size_t)w * c.max_rows];
+        join(m, l, p.x, p.y);
+      }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1)
+        join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
+      const bool any = l > 0.f || l != l;
+      const float e = any ? m + log2f(l) : INFINITY;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int w = w0 + (lane >> 3); w <= w1; w += 4) {
+        const float z = ex2(ml[(size_t)w * c.max_rows].x - e);
+        const float4 v = *(const float4 *)(a.po + (((size_t)w + bh) * c.max_rows + r) * D + part * 32 + (lane & 7) * 4);
+        o.x = fmaf(v.x, z, o.x), o.y = fmaf(v.y, z, o.y), o.z = fmaf(v.z, z, o.z), o.w = fmaf(v.w, z, o.w);
+      }
+#pragma unroll
+      for (int off = 8; off < 32; off <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, off), o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, off), o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+      }
+      if (lane < 8) {
+        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x, o.y), p1 = __floats2bfloat162_rn(o.z, o.w);
+        *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
+      }
+      if (lse && part == 0 && lane == 0) *lse = any ? e * kLn2 : -INFINITY;
       continue;
     }
-    int before = 0;
-    for (int i = lane; i < b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
-    const int x = c.H * __reduce_add_sync(0xffffffffu, before) + h * nblk;
-    const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
-    if (w0 == w1) continue;  // written by its worker
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = w0 + (lane >> 3); w <= w1; w += 4) {
-      const size_t at = ((size_t)w + bh) * c.max_rows + r;
-      const float2 p = a.ml[at];
-      const float4 v = *(const float4 *)(a.po + at * D + part * 32 + (lane & 7) * 4);
-      const bool some = p.x != -INFINITY;  // else this run saw nothing of the row
-      const float mn = fmaxf(m, p.x), f = m == -INFINITY ? 0.f : ex2(m - mn), z = some ? ex2(p.x - mn) : 0.f;
-      m = mn;
-      l = l * f + p.y * z;
-      o.x = o.x * f + v.x * z, o.y = o.y * f + v.y * z, o.z = o.z * f + v.z * z, o.w = o.w * f + v.w * z;
-    }
-#pragma unroll
-    for (int off = 8; off < 32; off <<= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, m, off), ol = __shfl_xor_sync(0xffffffffu, l, off);
-      const float4 oo = make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
-                                    __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off));
-      const float mn = fmaxf(m, om);
-      const float f = m == -INFINITY ? 0.f : ex2(m - mn), z = om == -INFINITY ? 0.f : ex2(om - mn);
-      m = mn;
-      l = l * f + ol * z;
-      o.x = o.x * f + oo.x * z, o.y = o.y * f + oo.y * z, o.z = o.z * f + oo.z * z, o.w = o.w * f + oo.w * z;
-    }
-    const bool any = l > 0.f || l != l;
-    const float inv = any ? 1.f / l : 0.f;
-    if (lane < 8) {
-      const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
-    }
-    if (part == 0 && lane == 0) {
-      a.lse2[(size_t)bh * c.max_rows + r] = any ? m + log2f(l) : INFINITY;
-      if (lse) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
-    }
-  }
-}
-
-// ------------------------------------------------------------------- scores
-// kChunk entries of one head per warp: the weights of every row from its
-// logits and LSE, summed in the rows' order.
-__global__ void __launch_bounds__(kItemWarps * 32) score_kernel(const Args a) {
-  const View &c = a.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunks = c.H * sum_units(a.l, c.B, kChunk);
-  grid_dependency_wait();
-  for (int item = blockIdx.x * kItemWarps + warp; item < chunks; item += gridDim.x * kItemWarps) {
-    int x = item, before;
+    int x = cta - out_ctas, before;
     const int b = find_seq(a.l, c.B, c.H, kChunk, x, before);
     const Seq s = seq_of(a.l, b);
-    const int nch = ceil_div(s.total, kChunk);
-    const int h = x / nch, j0 = (x - h * nch) * kChunk + lane * 4, bh = b * c.H + h;
+    const int nch = ceil_div(s.total, kChunk), nblk = ceil_div(s.total, kBlock);
+    const int h = x / nch, j0 = (x - h * nch) * kChunk + threadIdx.x * 4, bh = b * c.H + h;
     const int rows = s.cnt * c.group;
-    const float *lse2 = a.lse2 + (size_t)bh * c.max_rows;
+    const int start = c.H * before + h * nblk;
+    const int w0 = worker_of(start, blocks, workers), w1 = worker_of(start + nblk - 1, blocks, workers);
+    // A warp takes every eighth part, four of them at once by groups of eight lanes (one a row).
+    const float2 *ml = a.ml + (size_t)bh * c.max_rows;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      const int r = r0 + (lane & 7);
+      float m = -INFINITY, l = 0.f;
+      if (r < rows)
+#pragma unroll 4
+        for (int w = w0 + warp * 4 + (lane >> 3); w <= w1; w += kFinWarps * 4) {
+          const float2 p = ml[(size_t)w * c.max_rows + r];
+          join(m, l, p.x, p.y);
+        }
+#pragma unroll
+      for (int off = 8; off < 32; off <<= 1)
+        join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
+      if (lane < 8 && r < rows) part_ml[warp][r] = make_float2(m, l);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < rows; r += kFinWarps * 32) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFinWarps; ++w) join(m, l, part_ml[w][r].x, part_ml[w][r].y);
+      row_lse[r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;  // nothing seen: every weight 0
+    }
+    __syncthreads();
     const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
     float *sc = c.score + (size_t)bh * c.cap;
-    float4 w[kChunk / 128];
-#pragma unroll
-    for (int y = 0; y < kChunk / 128; ++y) w[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 w[2];
+    w[0] = w[1] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
-      const float e = lse2[r];
+      const float e = row_lse[r];
 #pragma unroll
-      for (int y = 0; y < kChunk / 128; ++y) {
-        if (j0 + y * 128 >= s.total) continue;
-        const float4 v = *(const float4 *)(lg + (size_t)r * c.cap + j0 + y * 128);
+      for (int y = 0; y < 2; ++y) {
+        if (j0 + y * (kChunk / 2) >= s.total) continue;
+        const float4 v = *(const float4 *)(lg + (size_t)r * c.cap + j0 + y * (kChunk / 2));
         w[y].x += ex2(v.x - e), w[y].y += ex2(v.y - e), w[y].z += ex2(v.z - e), w[y].w += ex2(v.w - e);
       }
     }
 #pragma unroll
-    for (int y = 0; y < kChunk / 128; ++y) {
-      const int j = j0 + y * 128;
+    for (int y = 0; y < 2; ++y) {
+      const int j = j0 + y * (kChunk / 2);
       if (j + 4 <= s.total) {
         float4 v = *(float4 *)(sc + j);
         v.x += w[y].x, v.y += w[y].y, v.z += w[y].z, v.w += w[y].w;
         *(float4 *)(sc + j) = v;
       } else {  // entries behind the last one keep their score
-        for (int e = 0; j + e < s.total; ++e) sc[j + e] += (&w[y].x)[e];
+        for (int e = 0; j + e < s.total; ++e) sc[j + e] += e == 0 ? w[y].x : e == 1 ? w[y].y : w[y].z;
       }
     }
   }
@@ -715,22 +745,19 @@ cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  auto ctas_for = [&](int64_t items) {
-    const int64_t n = (items + kItemWarps - 1) / kItemWarps;
-    return dim3((unsigned)(n < a.c.sms * 8 ? n : a.c.sms * 8));
-  };
-  e = launch_after(join_kernel<D>, ctas_for((int64_t)a.c.B * a.c.H * a.rows * (D / 32)), kItemWarps * 32, 0, st, a);
-  if (e != cudaSuccess || !a.accumulate) return e;
-  return launch_after(score_kernel, ctas_for((int64_t)a.c.B * a.c.H * ((a.c.cap + kChunk - 1) / kChunk)), kItemWarps * 32, 0,
-                      st, a);
+  const int64_t heads = (int64_t)a.c.B * a.c.H;
+  const int64_t items = (heads * a.rows * (D / 32) + kFinWarps - 1) / kFinWarps +
+                        (a.accumulate ? heads * ((a.c.cap + kChunk - 1) / kChunk) : 0);
+  return launch_after(finish_kernel<D>, dim3((unsigned)(items < a.c.sms * 8 ? items : a.c.sms * 8)), kFinWarps * 32, 0, st, a);
 }
 
 template <typename F, int D>
 cudaError_t attend_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   if (a.rows <= 8) return attend_t<F, D, 1, 1>(a, kmap, vmap, st);
   if (a.rows <= 16) return attend_t<F, D, 2, 1>(a, kmap, vmap, st);
-  if (a.rows <= 32) return attend_t<F, D, 4, 1>(a, kmap, vmap, st);
-  return attend_t<F, D, 4, 2>(a, kmap, vmap, st);
+  if (a.rows <= 32) return attend_t<F, D, 2, 2>(a, kmap, vmap, st);
+  if (a.rows <= 48) return attend_t<F, D, 2, 3>(a, kmap, vmap, st);
+  return attend_t<F, D, 2, 4>(a, kmap, vmap, st);
 }
 
 size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kTeams + (size_t)B * H; }
@@ -738,8 +765,7 @@ size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kT
 }  // namespace
 
 size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms) {
-  return partial_slots(B, H, sms) * max_rows * (sizeof(float2) + d * sizeof(float)) +
-         (size_t)B * H * max_rows * sizeof(float);
+  return partial_slots(B, H, sms) * max_rows * (sizeof(float2) + d * sizeof(float));
 }
 
 cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
@@ -757,7 +783,6 @@ cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causa
   const size_t rows = partial_slots(c.B, c.H, c.sms) * c.max_rows;
   a.po = c.part;
   a.ml = (float2 *)(c.part + rows * c.d);
-  a.lse2 = (float *)(a.ml + rows);
   if (c.kv == H2O_KV_E4M3)
     return c.d == 128 ? attend_d<E4M3, 128>(a, kmap, vmap, st) : attend_d<E4M3, 64>(a, kmap, vmap, st);
   return c.d == 128 ? attend_d<I8, 128>(a, kmap, vmap, st) : attend_d<I8, 64>(a, kmap, vmap, st);

@@ -145,6 +145,11 @@ __device__ __forceinline__ int exponent(float s) { return (int)(__float_as_uint(
 // 1 / s of a power of two between 2^kMinExp and 2^126.
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// A kernel launched behind this one with programmatic serialisation may start;
+// what it reads of this one's results it reads after its own wait.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Launchers (each on the device that is current; arguments checked before).
 cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
                           const float *score, cudaStream_t st);
