@@ -98,7 +98,7 @@ def lib():
         L.h2o_probe_read.restype = i32
         L.h2o_kernel_arch.argtypes = [C.POINTER(i32), C.POINTER(i32)]
         L.h2o_kernel_arch.restype = i32
-        rows, shape = C.POINTER(Rows), [i32, i32, i32, i64, i32, i32, i32]
+        rows, shape = vp, [i32, i32, i32, i64, i32, i32, i32]  # rows: address of an h2o_rows
         L.h2o_bcache_workspace_bytes.argtypes = shape
         L.h2o_bcache_workspace_bytes.restype = sz
         L.h2o_bcache_create.argtypes = shape + [vp, vp, C.POINTER(vp)]

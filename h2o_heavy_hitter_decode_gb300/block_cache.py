@@ -6,7 +6,7 @@ import ctypes as C
 
 import torch
 
-from . import H2OError, Rows, _check, _ptr, lib
+from . import H2OError, _check, _ptr, lib
 
 __all__ = ["H2OBlockCache"]
 
@@ -35,7 +35,7 @@ class H2OBlockCache:
 
     def __init__(self, B: int, H: int, d: int, capacity: int, group: int = 1, max_queries: int = 1, kv: str = "e4m3",
                  device=None):
-        L = lib()
+        L = self._lib = lib()
         if kv not in KV:
             raise ValueError(f"kv must be one of {sorted(KV)}, got {kv!r}")
         code, store = KV[kv]
@@ -55,7 +55,11 @@ class H2OBlockCache:
             h = C.c_void_p()
             _check(L.h2o_bcache_create(*shape, _ptr(self.workspace), C.c_void_p(self._stream()), C.byref(h)),
                    "h2o_bcache_create")
-        self._h = h
+        self._h, self._set_stream = h, None
+        self._heads, self._per_seq = H * group, (B,)
+        # h2o_rows of q, k, v and out, filled in by each call
+        self._slots = [(C.c_int64 * 4)() for _ in range(4)]
+        self._slot_at = [C.addressof(s) for s in self._slots]
         at = [C.c_void_p() for _ in range(6)]
         _check(L.h2o_bcache_arrays(h, *[C.byref(p) for p in at]), "h2o_bcache_arrays")
         rows, blocks = (B, H, capacity), (B, H, capacity // self.BLOCK)
@@ -66,7 +70,7 @@ class H2OBlockCache:
     def __del__(self):
         h = getattr(self, "_h", None)
         if h is not None:
-            lib().h2o_bcache_destroy(h)
+            self._lib.h2o_bcache_destroy(h)
             self._h = None
 
     # -------------------------------------------------------------- helpers
@@ -78,46 +82,57 @@ class H2OBlockCache:
         return self.workspace[at : at + n].view(dtype).view(shape)
 
     def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def _use_stream(self):
-        _check(lib().h2o_bcache_set_stream(self._h, C.c_void_p(self._stream())), "h2o_bcache_set_stream")
+        s = self._stream()
+        if s != self._set_stream:
+            _check(self._lib.h2o_bcache_set_stream(self._h, C.c_void_p(s)), "h2o_bcache_set_stream")
+            self._set_stream = s
 
     def _dense(self, t, dtype, shape, name):
+        """Address of a contiguous tensor, None for None."""
         if t is None:
             return None
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
-        return C.c_void_p(t.data_ptr())
+        return t.data_ptr()
 
-    def _per_sequence(self, t, name, optional=True):
-        if t is None and not optional:
+    def _lengths(self, t, name):
+        if t is None:
             raise TypeError(f"{name} must be a tensor")
-        return self._dense(t, torch.int32, (self.B,), name)
+        return self._dense(t, torch.int32, self._per_seq, name)
 
-    def _rows(self, t, heads, n, name):
-        """h2o_rows of a [B, heads, n, d] bf16 tensor whose rows are contiguous."""
+    def _rows(self, slot, t, shape, name):
+        """Address of the h2o_rows of a bf16 tensor [B, heads, n, d] whose rows are contiguous."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.dtype != torch.bfloat16 or t.device != self.device or tuple(t.shape) != (self.B, heads, n, self.d):
-            raise ValueError(f"{name}: expected torch.bfloat16 {(self.B, heads, n, self.d)} on {self.device}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != self.device:
+            raise ValueError(f"{name}: expected torch.bfloat16 {shape} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
         sb, sh, st, one = t.stride()
-        # a dimension of size 1 is never stepped over: its stride may be anything
-        sb, sh, st = sb if self.B > 1 else 0, sh if heads > 1 else 0, st if n > 1 else 0
-        if one != 1 or sb % 8 or sh % 8 or st % 8 or t.data_ptr() % 16:
-            raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
-                             f"{t.stride()}")
-        return C.byref(Rows(t.data_ptr(), sb, sh, st))
+        p = t.data_ptr()
+        if one != 1 or (sb | sh | st) & 7 or p & 15:
+            # a dimension of size 1 is never stepped over: its stride may be anything
+            sb, sh, st = (s if n > 1 else 0 for s, n in zip((sb, sh, st), shape))
+            if one != 1 or (sb | sh | st) & 7 or p & 15:
+                raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
+                                 f"{t.stride()} at address {p:#x}")
+        r = self._slots[slot]
+        r[0], r[1], r[2], r[3] = p, sb, sh, st
+        return self._slot_at[slot]
 
     @staticmethod
     def _tokens(t, name):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name}: expected a [B, heads, n, d] tensor")
         return t.shape[2]
+
+    def _shape(self, heads, n):
+        return (self.B, heads, n, self.d)
 
     # ---------------------------------------------------------------- calls
     def append(self, k, v, lengths, counts=None, position=None, score=None):
@@ -126,11 +141,13 @@ class H2OBlockCache:
         default ``lengths``) and scores ``score`` (fp32 [B, H, n], for example
         a prompt's column sums; default 0).  See h2o_bcache_append."""
         n = self._tokens(k, "k")
-        args = (self._rows(k, self.H, n, "k"), self._rows(v, self.H, n, "v"),
-                self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts"),
-                self._per_sequence(position, "position"), self._dense(score, torch.float32, (self.B, self.H, n), "score"))
+        shape = self._shape(self.H, n)
+        args = (self._rows(1, k, shape, "k"), self._rows(2, v, shape, "v"), self._lengths(lengths, "lengths"),
+                self._dense(counts, torch.int32, self._per_seq, "counts"),
+                self._dense(position, torch.int32, self._per_seq, "position"),
+                self._dense(score, torch.float32, shape[:3], "score"))
         self._use_stream()
-        _check(lib().h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
+        _check(self._lib.h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
 
     def attend(self, q, lengths, counts=None, causal=True, accumulate=True, out=None, lse=None):
         """Attention of q [B, H * group, n, d] over the ``lengths[b]`` entries
@@ -138,36 +155,38 @@ class H2OBlockCache:
         entries are the queries' own tokens; ``accumulate``: the weights are
         added to the entries' scores; ``lse`` (fp32 [B, H * group, n]) receives
         the log-sum-exps.  See h2o_bcache_attend."""
-        n, heads = self._tokens(q, "q"), self.H * self.group
-        qr = self._rows(q, heads, n, "q")
-        lens, cnt = self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts")
+        n = self._tokens(q, "q")
+        shape = self._shape(self._heads, n)
+        qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
+        cnt = self._dense(counts, torch.int32, self._per_seq, "counts")
         if out is None:
-            out = self._new_out(q, counts)
-        args = (qr, lens, cnt, int(bool(causal)), int(bool(accumulate)), self._rows(out, heads, n, "out"),
-                self._dense(lse, torch.float32, (self.B, heads, n), "lse"))
+            out = self._new_out(shape, counts)
+        args = (qr, lens, cnt, 1 if causal else 0, 1 if accumulate else 0, self._rows(3, out, shape, "out"),
+                self._dense(lse, torch.float32, shape[:3], "lse"))
         self._use_stream()
-        _check(lib().h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
+        _check(self._lib.h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
         return out
 
     def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None):
         """Append k, v [B, H, n, d] behind ``lengths[b]`` entries, then attend
         causally with q [B, H * group, n, d]; returns out.  The caller adds the
         counts (or n) to ``lengths`` afterwards.  See h2o_bcache_step."""
-        n, heads = self._tokens(q, "q"), self.H * self.group
-        rows = (self._rows(q, heads, n, "q"), self._rows(k, self.H, n, "k"), self._rows(v, self.H, n, "v"))
-        lens, cnt = self._per_sequence(lengths, "lengths", False), self._per_sequence(counts, "counts")
+        n = self._tokens(q, "q")
+        shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
+        rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
+        lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, torch.int32, self._per_seq, "counts")
         if out is None:
-            out = self._new_out(q, counts)
-        args = rows + (lens, cnt, self._per_sequence(position, "position"), int(bool(accumulate)),
-                       self._rows(out, heads, n, "out"), self._dense(lse, torch.float32, (self.B, heads, n), "lse"))
+            out = self._new_out(shape, counts)
+        args = rows + (lens, cnt, self._dense(position, torch.int32, self._per_seq, "position"), 1 if accumulate else 0,
+                       self._rows(3, out, shape, "out"), self._dense(lse, torch.float32, shape[:3], "lse"))
         self._use_stream()
-        _check(lib().h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
+        _check(self._lib.h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
         return out
 
-    def _new_out(self, q, counts):
+    def _new_out(self, shape, counts):
         # rows behind a sequence's count are not written
         make = torch.empty if counts is None else torch.zeros
-        return make(q.shape, dtype=torch.bfloat16, device=self.device)
+        return make(shape, dtype=torch.bfloat16, device=self.device)
 
     def evict(self, lengths, k_heavy: int, k_local: int, n_sink: int = 0, score_mode: int = 0, position=None,
               new_lengths=None):
@@ -178,17 +197,17 @@ class H2OBlockCache:
         h2o_bcache_evict."""
         if new_lengths is None:
             new_lengths = torch.empty(self.B, dtype=torch.int32, device=self.device)
-        args = (self._per_sequence(lengths, "lengths", False), int(k_heavy), int(k_local), int(n_sink), int(score_mode),
-                self._per_sequence(position, "position"), self._per_sequence(new_lengths, "new_lengths"))
+        args = (self._lengths(lengths, "lengths"), int(k_heavy), int(k_local), int(n_sink), int(score_mode),
+                self._dense(position, torch.int32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
         self._use_stream()
-        _check(lib().h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
+        _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
         return new_lengths
 
     def error_bits(self) -> int:
         """The sticky error flag (H2O_BERR_* bits; 0 = none); synchronises."""
         self._use_stream()
         bits = C.c_int32()
-        rc = lib().h2o_bcache_get_error(self._h, C.byref(bits))
+        rc = self._lib.h2o_bcache_get_error(self._h, C.byref(bits))
         if rc not in (0, 5):
             _check(rc, "h2o_bcache_get_error")
         return bits.value

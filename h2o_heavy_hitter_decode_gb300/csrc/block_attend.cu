@@ -575,7 +575,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
 
 // ------------------------------------------------------------------- finish
 constexpr int kFinWarps = 8;
-constexpr int kChunk = 256 * kFinWarps;  // entries of a CTA's score item
 
 // (m, l) of two parts of a row, base 2.
 __device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
@@ -584,38 +583,46 @@ __device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
   m = mn;
 }
 
-// First eight items to a CTA (one a warp) of 32 dimensions of one row's
-// output, where a head lies in several runs: all lanes gather the row's LSE,
-// then four groups of eight lanes take the partials in turn.  Then kChunk
-// entries of one head to a CTA: the warps gather the rows' LSE, then each
-// thread adds the rows' weights of its entries, in the rows' order.
-template <int D>
+// Items of a CTA: first eight (one a warp) of a row's output, where its head
+// lies in several runs: all lanes gather the row's LSE, then take its partials.
+// Then scores: W warps gather the LSE of a head's rows, and each lane adds the
+// rows' weights of V fours of entries, in the rows' order.
+// W = 8 where the parts and rows to gather are many, so that they are gathered
+// once for 1024 V entries and a row's output is four (d = 128) or two items;
+// else W = 1, eight items of 128 V entries to a CTA, which need no barrier.
+template <int D, int W, int V>
 __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
+  constexpr int kChunk = 128 * W * V;              // entries of a score item
+  constexpr int kPer = kFinWarps / W;              // score items of a CTA
+  constexpr int kLanes = W == 1 ? D / 4 : 8;       // lanes of an output item, 4 dimensions each
+  constexpr int kGroups = 32 / kLanes;             // groups that take the partials in turn
+  constexpr int kSlices = D / (4 * kLanes);        // output items of a row
   const View &c = a.c;
-  __shared__ float2 part_ml[kFinWarps][H2O_BLOCK_MAX_ROWS];
-  __shared__ float row_lse[H2O_BLOCK_MAX_ROWS];
+  __shared__ float2 part_ml[W == 1 ? 1 : W][W == 1 ? 1 : H2O_BLOCK_MAX_ROWS];
+  __shared__ float row_lse[kPer][H2O_BLOCK_MAX_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks = c.H * sum_units(a.l, c.B, kBlock);
   const int workers = min(a.workers, blocks);
-  const int64_t outs = (int64_t)c.B * c.H * a.rows * (D / 32);
+  const int64_t outs = (int64_t)c.B * c.H * a.rows * kSlices;
   const int out_ctas = (int)((outs + kFinWarps - 1) / kFinWarps);
   const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
   grid_dependency_wait();
-  for (int cta = blockIdx.x; cta < out_ctas + chunks; cta += gridDim.x) {
+  for (int cta = blockIdx.x; cta < out_ctas + (chunks + kPer - 1) / kPer; cta += gridDim.x) {
     if (cta < out_ctas) {
       const int64_t item = (int64_t)cta * kFinWarps + warp;
       if (item >= outs) continue;
-      const int part = (int)(item % (D / 32));
-      const int64_t hr = item / (D / 32);
+      const int part = (int)(item % kSlices);
+      const int64_t hr = item / kSlices;
       const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
       const Seq s = seq_of(a.l, b);
       const int tok = r / c.group, hq = h * c.group + r % c.group;
       if (tok >= s.cnt) continue;
-      __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + part * 32 + (lane & 7) * 4;
+      const int d0 = (part * kLanes + lane % kLanes) * 4;
+      __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0;
       float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
       const int nblk = ceil_div(s.total, kBlock);
       if (nblk == 0) {  // no entry at all
-        if (lane < 8) *(uint2 *)dst = make_uint2(0u, 0u);
+        if (lane < kLanes) *(uint2 *)dst = make_uint2(0u, 0u);
         if (lse && part == 0 && lane == 0) *lse = -INFINITY;
         continue;
       }
@@ -626,7 +633,6 @@ __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
       if (w0 == w1) continue;  // written by its worker
       const float2 *ml = a.ml + (size_t)bh * c.max_rows + r;
       float m = -INFINITY, l = 0.f;
-#pragma unroll 4
       for (int w = w0 + lane; w <= w1; w += 32) {
         const float2 p = ml[(size_t)w * c.max_rows];
         join(m, l, p.x, p.y);
@@ -637,81 +643,120 @@ __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
       const bool any = l > 0.f || l != l;
       const float e = any ? m + log2f(l) : INFINITY;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int w = w0 + (lane >> 3); w <= w1; w += 4) {
-        const float z = ex2(ml[(size_t)w * c.max_rows].x - e);
-        const float4 v = *(const float4 *)(a.po + (((size_t)w + bh) * c.max_rows + r) * D + part * 32 + (lane & 7) * 4);
-        o.x = fmaf(v.x, z, o.x), o.y = fmaf(v.y, z, o.y), o.z = fmaf(v.z, z, o.z), o.w = fmaf(v.w, z, o.w);
+      constexpr int kBatch = W == 1 ? 4 : 8;  // partials on their way at once
+      for (int wb = w0 + lane / kLanes; wb <= w1; wb += kGroups * kBatch) {
+        float4 v[kBatch];
+        float z[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int w = min(wb + i * kGroups, w1);  // the last one again, with weight 0
+          z[i] = ml[(size_t)w * c.max_rows].x;
+          v[i] = *(const float4 *)(a.po + (((size_t)w + bh) * c.max_rows + r) * D + d0);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float f = wb + i * kGroups <= w1 ? ex2(z[i] - e) : 0.f;
+          o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+        }
       }
 #pragma unroll
-      for (int off = 8; off < 32; off <<= 1) {
+      for (int off = kLanes; off < 32; off <<= 1) {
         o.x += __shfl_xor_sync(0xffffffffu, o.x, off), o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
         o.z += __shfl_xor_sync(0xffffffffu, o.z, off), o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
       }
-      if (lane < 8) {
+      if (lane < kLanes) {
         const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x, o.y), p1 = __floats2bfloat162_rn(o.z, o.w);
         *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
       }
       if (lse && part == 0 && lane == 0) *lse = any ? e * kLn2 : -INFINITY;
       continue;
     }
-    int x = cta - out_ctas, before;
+    int x = (cta - out_ctas) * kPer + warp / W, before;
+    if (x >= chunks) continue;  // W = 8 has no such item
     const int b = find_seq(a.l, c.B, c.H, kChunk, x, before);
     const Seq s = seq_of(a.l, b);
     const int nch = ceil_div(s.total, kChunk), nblk = ceil_div(s.total, kBlock);
-    const int h = x / nch, j0 = (x - h * nch) * kChunk + threadIdx.x * 4, bh = b * c.H + h;
+    const int h = x / nch, j0 = (x - h * nch) * kChunk + warp % W * (128 * V) + lane * 4, bh = b * c.H + h;
     const int rows = s.cnt * c.group;
     const int start = c.H * before + h * nblk;
     const int w0 = worker_of(start, blocks, workers), w1 = worker_of(start + nblk - 1, blocks, workers);
-    // A warp takes every eighth part, four of them at once by groups of eight lanes (one a row).
+    // Eight rows to a warp, a lane of each group of eight for one; the four groups, and the warps that have the same
+    // rows, take the parts in turn.
     const float2 *ml = a.ml + (size_t)bh * c.max_rows;
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      const int r = r0 + (lane & 7);
+    const int tiles = (rows + 7) / 8, sharing = W == 1 || tiles >= W ? 1 : W / max(tiles, 1);
+    for (int tile = warp % W; tile < tiles * sharing; tile += W) {
+      const int r = tile % tiles * 8 + (lane & 7), turn = tile / tiles;
       float m = -INFINITY, l = 0.f;
       if (r < rows)
-#pragma unroll 4
-        for (int w = w0 + warp * 4 + (lane >> 3); w <= w1; w += kFinWarps * 4) {
-          const float2 p = ml[(size_t)w * c.max_rows + r];
-          join(m, l, p.x, p.y);
+        for (int wb = w0 + turn * 4 + (lane >> 3); wb <= w1; wb += sharing * 16) {
+          float2 p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = ml[(size_t)min(wb + i * sharing * 4, w1) * c.max_rows + r];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (wb + i * sharing * 4 <= w1) join(m, l, p[i].x, p[i].y);
         }
 #pragma unroll
       for (int off = 8; off < 32; off <<= 1)
         join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
-      if (lane < 8 && r < rows) part_ml[warp][r] = make_float2(m, l);
+      if (lane < 8 && r < rows) {
+        if constexpr (W == 1)
+          row_lse[warp][r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;  // nothing seen: every weight 0
+        else
+          part_ml[turn][r] = make_float2(m, l);
+      }
     }
-    __syncthreads();
-    for (int r = threadIdx.x; r < rows; r += kFinWarps * 32) {
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kFinWarps; ++w) join(m, l, part_ml[w][r].x, part_ml[w][r].y);
-      row_lse[r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;  // nothing seen: every weight 0
+    if constexpr (W > 1) {
+      __syncthreads();
+      for (int r = threadIdx.x; r < rows; r += kFinWarps * 32) {
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < sharing; ++i) join(m, l, part_ml[i][r].x, part_ml[i][r].y);
+        row_lse[0][r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;
+      }
+      __syncthreads();
+    } else {
+      __syncwarp();
     }
-    __syncthreads();
     const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
     float *sc = c.score + (size_t)bh * c.cap;
-    float4 w[2];
-    w[0] = w[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const float e = row_lse[r];
+    constexpr int kRows = 8 / V;  // rows whose logits are on their way at once
+    const int j_last = max(0, s.total - 1) & ~3;
+    float4 w[V], old[V];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if (j0 + y * (kChunk / 2) >= s.total) continue;
-        const float4 v = *(const float4 *)(lg + (size_t)r * c.cap + j0 + y * (kChunk / 2));
-        w[y].x += ex2(v.x - e), w[y].y += ex2(v.y - e), w[y].z += ex2(v.z - e), w[y].w += ex2(v.w - e);
+    for (int y = 0; y < V; ++y) {
+      w[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      old[y] = *(const float4 *)(sc + min(j0 + y * 128, j_last));
+    }
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
+      float4 v[kRows][V];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int y = 0; y < V; ++y)
+          v[i][y] = *(const float4 *)(lg + (size_t)min(r0 + i, rows - 1) * c.cap + min(j0 + y * 128, j_last));
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (r0 + i >= rows) break;
+        const float e = row_lse[warp / W][r0 + i];
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+          w[y].x += ex2(v[i][y].x - e), w[y].y += ex2(v[i][y].y - e);
+          w[y].z += ex2(v[i][y].z - e), w[y].w += ex2(v[i][y].w - e);
+        }
       }
     }
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int j = j0 + y * (kChunk / 2);
+    for (int y = 0; y < V; ++y) {
+      const int j = j0 + y * 128;
       if (j + 4 <= s.total) {
-        float4 v = *(float4 *)(sc + j);
-        v.x += w[y].x, v.y += w[y].y, v.z += w[y].z, v.w += w[y].w;
-        *(float4 *)(sc + j) = v;
+        *(float4 *)(sc + j) = make_float4(old[y].x + w[y].x, old[y].y + w[y].y, old[y].z + w[y].z, old[y].w + w[y].w);
       } else {  // entries behind the last one keep their score
-        for (int e = 0; j + e < s.total; ++e) sc[j + e] += e == 0 ? w[y].x : e == 1 ? w[y].y : w[y].z;
+        if (j < s.total) sc[j] = old[y].x + w[y].x;
+        if (j + 1 < s.total) sc[j + 1] = old[y].y + w[y].y;
+        if (j + 2 < s.total) sc[j + 2] = old[y].z + w[y].z;
       }
     }
+    __syncwarp();  // before the next item's row_lse (W = 8: the barriers above keep it back)
   }
 }
 
@@ -736,7 +781,8 @@ cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
   const int ctas = a.c.sms * G::kCtas;
   a.workers = ctas * kTeams;
   const dim3 grid(ctas, (a.rows + 8 * NR * MT - 1) / (8 * NR * MT));
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<F, D, NR, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise((const void *)attend_kernel<F, D, NR, MT>, G::kSmem);
   if (e != cudaSuccess) return e;
   if (a.l.appends) {
     e = launch_after(attend_kernel<F, D, NR, MT>, grid, G::kWarps * 32, G::kSmem, st, a, kmap, vmap);
@@ -745,10 +791,17 @@ cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
+  // Parts to gather for a head's rows, about: a warp reads a few at once.
   const int64_t heads = (int64_t)a.c.B * a.c.H;
-  const int64_t items = (heads * a.rows * (D / 32) + kFinWarps - 1) / kFinWarps +
-                        (a.accumulate ? heads * ((a.c.cap + kChunk - 1) / kChunk) : 0);
-  return launch_after(finish_kernel<D>, dim3((unsigned)(items < a.c.sms * 8 ? items : a.c.sms * 8)), kFinWarps * 32, 0, st, a);
+  const bool many = (a.workers / heads + 1) * a.rows > 64;
+  const bool wide = !many || heads * ((a.c.cap + 4095) / 4096) >= 2 * a.c.sms;  // enough items of four fours a lane
+  const int chunk = (many ? 1024 : 128) * (wide ? 4 : 1), per = many ? 1 : 8, slices = many ? D / 32 : 1;
+  const int64_t items = (heads * a.rows * slices + kFinWarps - 1) / kFinWarps +
+                        (a.accumulate ? (heads * ((a.c.cap + chunk - 1) / chunk) + per - 1) / per : 0);
+  const dim3 fin((unsigned)(items < a.c.sms * 8 ? items : a.c.sms * 8));
+  return !many  ? launch_after(finish_kernel<D, 1, 4>, fin, kFinWarps * 32, 0, st, a)
+         : wide ? launch_after(finish_kernel<D, 8, 4>, fin, kFinWarps * 32, 0, st, a)
+                : launch_after(finish_kernel<D, 8, 1>, fin, kFinWarps * 32, 0, st, a);
 }
 
 template <typename F, int D>

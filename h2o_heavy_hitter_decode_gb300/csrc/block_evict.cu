@@ -383,9 +383,10 @@ template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStrea
   const int keys = share < most ? share : most;
   const int smem = keys * 4 > kRing ? keys * 4 : kRing;
   a.held = smem / 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel<F, D, P, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && P > 8)
-    e = cudaFuncSetAttribute(evict_kernel<F, D, P, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static SmemLimit limit;
+  const void *kernel = (const void *)evict_kernel<F, D, P, W>;
+  cudaError_t e = limit.raise(kernel, smem);
+  if (e == cudaSuccess && P > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.c.B * a.c.H * P);
