@@ -164,6 +164,7 @@ h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, i
     return fail(cudaErrorNotSupported);
   }
   cudaError_t e = cudaGetDevice(&c->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&v.l2_bytes, cudaDevAttrL2CacheSize, c->device);
   if (e == cudaSuccess) e = cudaMemsetAsync(w + l.K, 0, l.pos - l.K, c->stream);  // codes and scales
   if (e == cudaSuccess) e = cudaMemsetAsync(v.pos, 0xff, l.score - l.pos, c->stream);
   if (e == cudaSuccess) e = cudaMemsetAsync(v.score, 0, l.logits - l.score, c->stream);

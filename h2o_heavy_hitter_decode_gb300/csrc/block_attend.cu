@@ -161,12 +161,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1) {
+// 2-D tiled TMA load with an L2 eviction policy.
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
+                                            uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], "
+      "[%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy(bool evict_first) {
+  uint64_t p;
+  if (evict_first)
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a swizzled block.
@@ -200,6 +210,7 @@ struct Args {
   float *po;   // [workers + B*H][max_rows][d]  partial output
   int causal, accumulate, workers;
   int rows;  // n * group: rows of a head in this call
+  int streams;  // the codes pass through L2 once: they make way first
 };
 
 template <typename F, int D, int NR, int MT>
@@ -246,13 +257,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   cur.seek(a.l, c.B, c.H, x0);
   ld = cur;
   int issued = 0, put = 0;
+  const uint64_t policy = l2_policy(a.streams);
   auto issue = [&]() {  // the run's next block into its stage (leader warp)
     if (lane == 0) {
       uint8_t *dst = ring + put * G::kStage;
       const int row = (ld.b * c.H + ld.h) * c.cap + ld.blk * kBlock;
       mbar_expect_tx(full + put, G::kStage);
-      tma_load_2d(dst, &kmap, full + put, 0, row);
-      tma_load_2d(dst + kBlock * D, &vmap, full + put, 0, row);
+      tma_load_2d(dst, &kmap, full + put, 0, row, policy);
+      tma_load_2d(dst + kBlock * D, &vmap, full + put, 0, row, policy);
     }
     ++issued;
     put = put + 1 == S ? 0 : put + 1;
@@ -588,42 +600,42 @@ __device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
 // Then scores: W warps gather the LSE of a head's rows, and each lane adds the
 // rows' weights of V fours of entries, in the rows' order.
 // W = 8 where the parts and rows to gather are many, so that they are gathered
-// once for 1024 V entries and a row's output is four (d = 128) or two items;
-// else W = 1, eight items of 128 V entries to a CTA, which need no barrier.
-template <int D, int W, int V>
+// once for 1024 V entries; else W = 1, eight items of 128 V entries to a CTA,
+// which need no barrier.  Deep: few heads in many runs, whose rows' outputs
+// then take a CTA each, its warps in turn for the partials.
+template <int D, int W, int V, bool Deep>
 __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
   constexpr int kChunk = 128 * W * V;              // entries of a score item
   constexpr int kPer = kFinWarps / W;              // score items of a CTA
-  constexpr int kLanes = W == 1 ? D / 4 : 8;       // lanes of an output item, 4 dimensions each
-  constexpr int kGroups = 32 / kLanes;             // groups that take the partials in turn
-  constexpr int kSlices = D / (4 * kLanes);        // output items of a row
+  constexpr int kLanes = D / 4;                                     // lanes of an output row, 4 dimensions each
+  constexpr int kGroups = (Deep ? kFinWarps : 1) * (32 / kLanes);   // groups of lanes that take the partials in turn
   const View &c = a.c;
   __shared__ float2 part_ml[W == 1 ? 1 : W][W == 1 ? 1 : H2O_BLOCK_MAX_ROWS];
+  __shared__ float4 part_o[Deep ? kFinWarps : 1][kLanes];
   __shared__ float row_lse[kPer][H2O_BLOCK_MAX_ROWS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blocks = c.H * sum_units(a.l, c.B, kBlock);
   const int workers = min(a.workers, blocks);
-  const int64_t outs = (int64_t)c.B * c.H * a.rows * kSlices;
-  const int out_ctas = (int)((outs + kFinWarps - 1) / kFinWarps);
+  const int64_t outs = (int64_t)c.B * c.H * a.rows;
+  const int out_ctas = (int)(Deep ? outs : (outs + kFinWarps - 1) / kFinWarps);
   const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
   grid_dependency_wait();
   for (int cta = blockIdx.x; cta < out_ctas + (chunks + kPer - 1) / kPer; cta += gridDim.x) {
     if (cta < out_ctas) {
-      const int64_t item = (int64_t)cta * kFinWarps + warp;
+      const int64_t item = Deep ? cta : (int64_t)cta * kFinWarps + warp;
       if (item >= outs) continue;
-      const int part = (int)(item % kSlices);
-      const int64_t hr = item / kSlices;
-      const int r = (int)(hr % a.rows), bh = (int)(hr / a.rows), b = bh / c.H, h = bh - b * c.H;
+      const int r = (int)(item % a.rows), bh = (int)(item / a.rows), b = bh / c.H, h = bh - b * c.H;
       const Seq s = seq_of(a.l, b);
       const int tok = r / c.group, hq = h * c.group + r % c.group;
       if (tok >= s.cnt) continue;
-      const int d0 = (part * kLanes + lane % kLanes) * 4;
+      const int d0 = lane % kLanes * 4;
+      const bool writes = lane < kLanes && (!Deep || warp == 0);
       __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0;
       float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
       const int nblk = ceil_div(s.total, kBlock);
       if (nblk == 0) {  // no entry at all
-        if (lane < kLanes) *(uint2 *)dst = make_uint2(0u, 0u);
-        if (lse && part == 0 && lane == 0) *lse = -INFINITY;
+        if (writes) *(uint2 *)dst = make_uint2(0u, 0u);
+        if (lse && writes && lane == 0) *lse = -INFINITY;
         continue;
       }
       int before = 0;
@@ -632,43 +644,64 @@ __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
       const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
       if (w0 == w1) continue;  // written by its worker
       const float2 *ml = a.ml + (size_t)bh * c.max_rows + r;
+      const float *po = a.po + ((size_t)bh * c.max_rows + r) * D + d0;
+      // Each group weighs its partials by its own maximum, then the groups meet.
+      constexpr int kBatch = Deep ? 8 : 4;  // partials on their way at once
       float m = -INFINITY, l = 0.f;
-      for (int w = w0 + lane; w <= w1; w += 32) {
-        const float2 p = ml[(size_t)w * c.max_rows];
-        join(m, l, p.x, p.y);
-      }
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1)
-        join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
-      const bool any = l > 0.f || l != l;
-      const float e = any ? m + log2f(l) : INFINITY;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kBatch = W == 1 ? 4 : 8;  // partials on their way at once
-      for (int wb = w0 + lane / kLanes; wb <= w1; wb += kGroups * kBatch) {
+      for (int wb = w0 + (Deep ? warp * (32 / kLanes) : 0) + lane / kLanes; wb <= w1; wb += kGroups * kBatch) {
         float4 v[kBatch];
-        float z[kBatch];
+        float2 p[kBatch];
+        float mn = m;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int w = min(wb + i * kGroups, w1);  // the last one again, with weight 0
-          z[i] = ml[(size_t)w * c.max_rows].x;
-          v[i] = *(const float4 *)(a.po + (((size_t)w + bh) * c.max_rows + r) * D + d0);
+          const size_t w = min(wb + i * kGroups, w1);  // the last one again counts as unseen
+          p[i] = ml[w * c.max_rows];
+          v[i] = *(const float4 *)(po + w * c.max_rows * D);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const float f = wb + i * kGroups <= w1 ? ex2(z[i] - e) : 0.f;
-          o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+          if (wb + i * kGroups > w1) p[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          mn = fmaxf(mn, p[i].x);
+        }
+        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float z = p[i].x == -INFINITY ? 0.f : ex2(p[i].x - m);
+          l += p[i].x == -INFINITY ? p[i].y : p[i].y * z;
+          o.x = fmaf(v[i].x, z, o.x), o.y = fmaf(v[i].y, z, o.y), o.z = fmaf(v[i].z, z, o.z), o.w = fmaf(v[i].w, z, o.w);
         }
       }
+      auto meet = [&](float om, float ol, float4 oo) {
+        const float mn = fmaxf(m, om), f = m == -INFINITY ? 0.f : ex2(m - mn), z = om == -INFINITY ? 0.f : ex2(om - mn);
+        l = (m == -INFINITY ? l : l * f) + (om == -INFINITY ? ol : ol * z);
+        o.x = o.x * f + oo.x * z, o.y = o.y * f + oo.y * z, o.z = o.z * f + oo.z * z, o.w = o.w * f + oo.w * z;
+        m = mn;
+      };
 #pragma unroll
-      for (int off = kLanes; off < 32; off <<= 1) {
-        o.x += __shfl_xor_sync(0xffffffffu, o.x, off), o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
-        o.z += __shfl_xor_sync(0xffffffffu, o.z, off), o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+      for (int off = kLanes; off < 32; off <<= 1)
+        meet(__shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off),
+             make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
+                         __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off)));
+      if constexpr (Deep) {  // every warp of the CTA is here: the item is the CTA's
+        if (lane < kLanes) {
+          part_o[warp][lane] = o;
+          if (lane == 0) part_ml[warp][0] = make_float2(m, l);
+        }
+        __syncthreads();
+        if (warp == 0)
+          for (int i = 1; i < kFinWarps; ++i) meet(part_ml[i][0].x, part_ml[i][0].y, part_o[i][lane % kLanes]);
+        __syncthreads();
       }
-      if (lane < kLanes) {
-        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x, o.y), p1 = __floats2bfloat162_rn(o.z, o.w);
+      const bool any = l > 0.f || l != l;
+      const float inv = any ? 1.f / l : 0.f;
+      if (writes) {
+        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
         *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
+        if (lse && lane == 0) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
-      if (lse && part == 0 && lane == 0) *lse = any ? e * kLn2 : -INFINITY;
       continue;
     }
     int x = (cta - out_ctas) * kPer + warp / W, before;
@@ -791,17 +824,18 @@ cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  // Parts to gather for a head's rows, about: a warp reads a few at once.
-  const int64_t heads = (int64_t)a.c.B * a.c.H;
-  const bool many = (a.workers / heads + 1) * a.rows > 64;
+  // Parts of a head, about, and what a warp can gather at once of them and its rows.
+  const int64_t heads = (int64_t)a.c.B * a.c.H, parts = a.workers / heads + 1;
+  const bool deep = parts > 48, many = deep || parts * a.rows > 64;
   const bool wide = !many || heads * ((a.c.cap + 4095) / 4096) >= 2 * a.c.sms;  // enough items of four fours a lane
-  const int chunk = (many ? 1024 : 128) * (wide ? 4 : 1), per = many ? 1 : 8, slices = many ? D / 32 : 1;
-  const int64_t items = (heads * a.rows * slices + kFinWarps - 1) / kFinWarps +
+  const int chunk = (many ? 1024 : 128) * (wide ? 4 : 1), per = many ? 1 : 8;
+  const int64_t items = (deep ? heads * a.rows : (heads * a.rows + kFinWarps - 1) / kFinWarps) +
                         (a.accumulate ? (heads * ((a.c.cap + chunk - 1) / chunk) + per - 1) / per : 0);
   const dim3 fin((unsigned)(items < a.c.sms * 8 ? items : a.c.sms * 8));
-  return !many  ? launch_after(finish_kernel<D, 1, 4>, fin, kFinWarps * 32, 0, st, a)
-         : wide ? launch_after(finish_kernel<D, 8, 4>, fin, kFinWarps * 32, 0, st, a)
-                : launch_after(finish_kernel<D, 8, 1>, fin, kFinWarps * 32, 0, st, a);
+  const auto kernel = !many  ? finish_kernel<D, 1, 4, false>
+                      : deep ? (wide ? finish_kernel<D, 8, 4, true> : finish_kernel<D, 8, 1, true>)
+                             : (wide ? finish_kernel<D, 8, 4, false> : finish_kernel<D, 8, 1, false>);
+  return launch_after(kernel, fin, kFinWarps * 32, 0, st, a);
 }
 
 template <typename F, int D>
@@ -833,6 +867,9 @@ cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causa
   a.accumulate = accumulate;
   a.workers = 0;
   a.rows = l.n * c.group;
+  // Codes of more than L2's size evict each other before the next call reads them; the logits, which are read again
+  // in this one, then stay.  56 heads, 1.3 GB of codes: 239 us without the hint.
+  a.streams = 2 * (int64_t)c.B * c.H * c.cap * c.d > (int64_t)c.l2_bytes;
   const size_t rows = partial_slots(c.B, c.H, c.sms) * c.max_rows;
   a.po = c.part;
   a.ml = (float2 *)(c.part + rows * c.d);

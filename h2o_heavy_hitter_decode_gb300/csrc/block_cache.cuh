@@ -28,7 +28,7 @@ struct View {
   float *part;                        // scratch, split partials
   int32_t *kept;                      // [B*H][cap] scratch of an eviction (shares the logits' memory)
   int *err;                           // [1] sticky H2O_BERR_* bits
-  int sms;
+  int sms, l2_bytes;
 };
 
 // Rows (b, h, t) of bf16 in memory, strides in elements.
