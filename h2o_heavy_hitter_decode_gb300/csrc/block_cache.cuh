@@ -77,24 +77,26 @@ struct E4M3 {
     const uint32_t z = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
     return a | z << 16;
   }
-  // A word's codes times 2^e, rounded to codes (at most kMax up to rounding).
-  // In f16: a code has 4 significant bits, so the two products by 2^(e/2) are
-  // exact wherever the result is 2^-20 or more; below 2^-10 it rounds to 0 in
-  // any case.
+  // A word's codes times 2^e, e <= 15, rounded to codes (at most kMax up to
+  // rounding).  In f16: a code has 4 significant bits, so the product is exact
+  // wherever it is 2^-20 or more; below 2^-10 it rounds to 0 in any case.
   struct Shift {
-    __half2 a, z;
+    __half2 a;
     __device__ __forceinline__ explicit Shift(int e) {
-      e = max(-24, min(24, e));  // more than 18: zeros only
-      const int h = e >> 1;
-      a = __half2half2(__ushort_as_half((unsigned short)((h + 15) << 10)));
-      z = __half2half2(__ushort_as_half((unsigned short)((e - h + 15) << 10)));
+      a = __half2half2(__ushort_as_half((unsigned short)(e > -15 ? (e + 15) << 10 : e >= -24 ? 1 << (e + 24) : 0)));
     }
     __device__ __forceinline__ uint32_t run(uint32_t w) const {
-      const uint32_t x = e4m3x2_to_f16x2(w), y = e4m3x2_to_f16x2(w >> 16);
-      const __half2 p = __hmul2(__hmul2(*(const __half2 *)&x, a), z), q = __hmul2(__hmul2(*(const __half2 *)&y, a), z);
-      const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(*(const __half2_raw *)&p, __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(*(const __half2_raw *)&q, __NV_SATFINITE, __NV_E4M3);
-      return lo | hi << 16;
+      uint32_t x, y;
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+          : "=r"(x), "=r"(y)
+          : "r"(w));
+      const __half2 p = __hmul2(*(const __half2 *)&x, a), q = __hmul2(*(const __half2 *)&y, a);
+      asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\t"
+          "mov.b32 %0, {lo, hi};\n\t}"
+          : "=r"(w)
+          : "r"(*(const uint32_t *)&p), "r"(*(const uint32_t *)&q));
+      return w;
     }
   };
 };
@@ -111,13 +113,12 @@ struct I8 {
     const uint32_t z = __byte_perm(__float_as_uint(fmaf(x[2], inv, magic)), __float_as_uint(fmaf(x[3], inv, magic)), 0x40);
     return __byte_perm(a, z, 0x5410);
   }
-  // A word's codes times 2^e, rounded: the same in f16, whose numbers from
+  // A word's codes times 2^e, e <= 15, rounded: the same in f16, whose numbers from
   // 1024 to 2048 are the integers; the fused product has one rounding.
   struct Shift {
     __half2 a;
     __device__ __forceinline__ explicit Shift(int e) {
-      e = max(-15, min(15, e));  // below -8 everything rounds to 0; more than 7: zeros only
-      a = __half2half2(e > -15 ? __ushort_as_half((unsigned short)((e + 15) << 10)) : __ushort_as_half(0));
+      a = __half2half2(__ushort_as_half((unsigned short)(e > -15 ? (e + 15) << 10 : 0)));  // below -8 all is 0
     }
     __device__ __forceinline__ uint32_t run(uint32_t w) const {
       const __half2 bias = __half2half2(__ushort_as_half(0x6480)), magic = __half2half2(__ushort_as_half(0x6600));

@@ -17,14 +17,17 @@
 // Move: entry i of the result comes from index src(i) >= i, so a round of
 // consecutive destination blocks, each held by a warp, may be written once
 // every warp of the round has read: later rounds read only behind what was
-// written.  That makes the move in place with one barrier a round and no copy
-// of the cache.  A warp's item is a block of K or of V; the rows of its next
+// written.  That makes the move in place, with no copy of the cache.  A warp
+// arrives at a round's barrier when it has read; it waits for that barrier
+// before it writes only where this round's sources begin inside the round's
+// own destination, else (once some entries are gone) for the round before.  A warp's item is a block of K or of V; the rows of its next
 // two items are on their way to shared memory (cp.async, each lane its own 16
 // bytes) while it works on one.  Every destination block gets a fresh scale
 // from the values it receives; rows whose scale it shares go over unchanged.
 #include <cooperative_groups.h>
 
 #include "block_cache.cuh"
+#include "sm100.cuh"
 
 namespace h2o {
 namespace blk {
@@ -52,8 +55,7 @@ template <typename F> struct TopCode;
 template <> struct TopCode<E4M3> {  // a code's low 7 bits order like its magnitude
   uint32_t m = 0;
   __device__ __forceinline__ void add(uint32_t w) {
-    m = __vmaxu2(m, w & 0x007f007fu);
-    m = __vmaxu2(m, (w >> 8) & 0x007f007fu);
+    m = __vmaxu2(m, __vmaxu2(w & 0x007f007fu, (w >> 8) & 0x007f007fu));
   }
   __device__ __forceinline__ float value() const {
     float x[4];
@@ -81,18 +83,34 @@ template <int P> __device__ __forceinline__ void head_sync(cg::cluster_group &cl
   else
     __syncthreads();
 }
-// Between the reads and the writes of a round.  What was read is in registers
-// when a warp arrives, so the warps only have to meet: a releasing arrival
-// would make each round wait for the stores of the one before to reach L2.
-template <int P> __device__ __forceinline__ void round_arrive() {
-  if constexpr (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-template <int P> __device__ __forceinline__ void round_wait() {
-  if constexpr (P > 1)
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  else
-    __syncthreads();
-}
+// The barrier between the reads and the writes of rounds.  What was read is in
+// registers when a warp arrives, so the warps only have to meet: a releasing
+// arrival would make each round wait for the stores of the one before to reach
+// L2.  One CTA: an mbarrier with an arrival for each warp.
+template <int P> struct Rounds {
+  uint64_t *bar;
+  uint32_t phase = 0;
+  bool pending = false, ok = true;
+  __device__ __forceinline__ void arrive(int lane) {
+    if constexpr (P > 1) {
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    } else {
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(bar);
+    }
+    pending = true;
+  }
+  __device__ __forceinline__ void wait() {
+    if (!pending) return;
+    if constexpr (P > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+      ok = sm100::mbar_wait(bar, phase) && ok;
+      phase ^= 1;
+    }
+    pending = false;
+  }
+};
 
 // 16 bytes global -> shared, zeros where `in` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
@@ -109,6 +127,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
   __shared__ unsigned s_digit, s_want, s_eq;
   __shared__ int s_warp[2][W];
   __shared__ unsigned s_sum[W];
+  __shared__ __align__(8) uint64_t s_bar;
   __shared__ int s_count[2];  // this CTA's entries above and at the threshold
   cg::cluster_group cluster = cg::this_cluster();
   const View &c = a.c;
@@ -157,12 +176,19 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
       };
       const int whole = min(n, a.held) & ~3;
       if (pass == 0) {
-#pragma unroll 4
-        for (int j = tid * 4; j < whole; j += kThreads * 4) {
-          const float4 v = *(const float4 *)(score + lo + j);
-          const uint4 u = make_uint4(to_key(v.x, j), to_key(v.y, j + 1), to_key(v.z, j + 2), to_key(v.w, j + 3));
-          *(uint4 *)(dyn + j) = u;
-          count(u.x), count(u.y), count(u.z), count(u.w);
+        constexpr int kBatch = 8;  // fours of scores on their way at once
+        for (int jb = tid * 4; jb < whole; jb += kThreads * 4 * kBatch) {
+          float4 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) v[i] = *(const float4 *)(score + lo + min(jb + i * kThreads * 4, whole - 4));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int j = jb + i * kThreads * 4;
+            if (j >= whole) break;
+            const uint4 u = make_uint4(to_key(v[i].x, j), to_key(v[i].y, j + 1), to_key(v[i].z, j + 2), to_key(v[i].w, j + 3));
+            *(uint4 *)(dyn + j) = u;
+            count(u.x), count(u.y), count(u.z), count(u.w);
+          }
         }
         for (int j = whole + tid; j < n; j += kThreads) {
           const uint32_t u = to_key(score[lo + j], j);
@@ -281,6 +307,14 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     head_sync<P>(cluster);  // every index written, every key and count read
   }
 
+  if constexpr (P == 1) {
+    if (tid == 0) {
+      sm100::mbar_init(&s_bar, W);
+      sm100::fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  Rounds<P> rounds{&s_bar};
   constexpr int LPR = D / 16;          // lanes per row, 16 codes each
   constexpr int RPI = 32 / LPR;        // rows per copy of the warp
   constexpr int IT = kBlock / RPI;     // copies
@@ -326,7 +360,15 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
   const int s0 = source(q), s1 = source(q + stride);
   int src2 = source(q + 2 * stride);
   Entry x0 = fetch(q, 0, s0), x1 = fetch(q + stride, 1, s1);
+  // Where the round's first entry comes from; its destination ends 16 * stride entries behind 16 * round.
+  auto first_source = [&](int round) {
+    const int i = round * (kBlock / 2);
+    return i >= k ? len : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
+  };
+  int from = first_source(0);
   for (int round = 0, slot = 0; round < items; round += stride, q += stride, slot ^= 1) {
+    const bool inside = from < (round + stride) * (kBlock / 2);
+    from = first_source(round + stride);
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // this item; each lane reads back what it copied
     uint4 w[IT];
 #pragma unroll
@@ -334,7 +376,8 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     const float scale_own = __shfl_sync(0xffffffffu, x0.scale, lane);  // the loads have come back
     const int pos_own = __shfl_sync(0xffffffffu, x0.pos, lane);
     const float score_own = __shfl_sync(0xffffffffu, x0.score, lane);
-    round_arrive<P>();
+    rounds.wait();  // everyone has read the round before
+    rounds.arrive(lane);
     x0 = x1;
     x1 = fetch(q + 2 * stride, slot, src2);
     src2 = source(q + 3 * stride);
@@ -342,25 +385,30 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
     const int base = (q >> 1) * kBlock;
     float to = 0.f;
     if (work) {
-      float amax = 0.f, sc[IT];
+      float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         TopCode<F> top;
         top.add(w[i].x), top.add(w[i].y), top.add(w[i].z), top.add(w[i].w);
-        sc[i] = __shfl_sync(0xffffffffu, scale_own, i * RPI + row0);
-        amax = fmaxf(amax, top.value() * sc[i]);
+        amax = fmaxf(amax, top.value() * __shfl_sync(0xffffffffu, scale_own, i * RPI + row0));
       }
       to = block_scale<F>(warp_max(amax));
-      if (__any_sync(0xffffffffu, scale_own != to)) {
+      // Times 2^(exponent of its scale - the new one's).  More than 15 is rare (small codes of a far larger scale) and
+      // takes two steps, the first of them exact; more than 30 is a row of zeros.
+      int left = min(exponent(scale_own) - exponent(to), 30);
+      while (__any_sync(0xffffffffu, left != 0)) {
+        const int step = min(left, 15);
+        left = max(left - 15, 0);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          if (sc[i] == to) continue;
-          const typename F::Shift shift(exponent(sc[i]) - exponent(to));
-          w[i] = make_uint4(shift.run(w[i].x), shift.run(w[i].y), shift.run(w[i].z), shift.run(w[i].w));
+          const int e = __shfl_sync(0xffffffffu, step, i * RPI + row0);
+          if (e == 0) continue;
+          const typename F::Shift by(e);
+          w[i] = make_uint4(by.run(w[i].x), by.run(w[i].y), by.run(w[i].z), by.run(w[i].w));
         }
       }
     }
-    round_wait<P>();  // every warp of the round has read its sources
+    if (inside) rounds.wait();  // this round's sources lie in what it writes: everyone has to have read them
     if (work) {
       const bool is_v = q & 1;
       uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
@@ -374,7 +422,9 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
       }
     }
   }
+  rounds.wait();
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!rounds.ok && lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
 }
 
 template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStream_t st) {

@@ -346,6 +346,30 @@ def test_evict_shared_heads(B, H, cap, lens, kv, mode):
     assert c.error_bits() == 0
 
 
+@pytest.mark.parametrize("H,cap", [(3, 20480), (240, 4096)])
+@pytest.mark.parametrize("every", [8, 16, 20, 40, 80])
+def test_evict_scores_with_a_period(H, cap, every):
+    """Scores whose largest (or least) values lie at regular distances, so that a regular sample of them misleads."""
+    g = torch.Generator(DEV).manual_seed(113)
+    c = H2OBlockCache(1, H, 64, cap, kv="int8")
+    c.append(rows(g, 1, H, cap, 64), rows(g, 1, H, cap, 64), ints([0]))
+    c.score.copy_(torch.rand(1, H, cap, generator=g, device=DEV))
+    c.score[:, ::2, ::every] += 100
+    c.score[:, 1::2, ::every] -= 100
+    for kh in (cap // 7, 1, cap - 200):
+        i = torch.arange(cap, device=DEV)
+        score, pos = c.score.clone(), c.pos.clone()
+        K, V, Ks, Vs = c.K.clone(), c.V.clone(), c.K_scale.clone(), c.V_scale.clone()
+        key = torch.where(i >= cap - 100, math.inf, score)
+        gone = torch.zeros_like(key, dtype=torch.bool).scatter_(2, key.sort(dim=-1, stable=True).indices, (i < cap - kh - 100).expand(1, H, cap))
+        c.evict(ints([cap]), kh, 100)
+        want = i.expand(1, H, cap)[~gone].view(1, H, -1)
+        assert torch.equal(c.pos[:, :, : kh + 100].long(), want)
+        assert torch.equal(c.score[:, :, : kh + 100], score.gather(2, want))
+        for name, x in dict(score=score, pos=pos, K=K, V=V, K_scale=Ks, V_scale=Vs).items():
+            getattr(c, name).copy_(x)
+
+
 # -------------------------------------------------- used together, and where
 
 def test_serving_run():
