@@ -23,7 +23,7 @@ constexpr int kWarps = 4;
 constexpr int kFew = 8;  // rows a sequence that append_few_kernel takes
 
 template <typename F, int D>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const Lens l, const Rows k, const Rows v,
+__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const View c, const Lens l, const Rows k, const Rows v,
                                                              const int32_t *__restrict__ position,
                                                              const float *__restrict__ score, int blocks) {
   constexpr int LPR = D / 8;        // lanes per row, 8 elements (16 bytes) each
@@ -61,15 +61,12 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const View c, const
   const float before = base < s.len ? *scale : 0.f;
   auto words = [&](int i) -> uint32_t * { return &w[i].x; };
   // Absolute values of bf16 order like their bits.
-  uint32_t top = 0;
+  uint32_t top2 = 0;
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t u = words(i)[e];
-      top = max(top, max(u & 0x7fffu, (u >> 16) & 0x7fffu));
-    }
-  top = __reduce_max_sync(0xffffffffu, top);
+    for (int e = 0; e < 4; ++e) top2 = __vmaxu2(top2, words(i)[e] & 0x7fff7fffu);
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
   const bool odd = top >= 0x7f80u;  // an infinity or NaN among them
   if (odd) {
     top = 0;

@@ -604,7 +604,7 @@ __device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
 // which need no barrier.  Deep: few heads in many runs, whose rows' outputs
 // then take a CTA each, its warps in turn for the partials.
 template <int D, int W, int V, bool Deep>
-__global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
+__global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a) {
   constexpr int kChunk = 128 * W * V;              // entries of a score item
   constexpr int kPer = kFinWarps / W;              // score items of a CTA
   constexpr int kLanes = D / 4;                                     // lanes of an output row, 4 dimensions each
@@ -619,29 +619,60 @@ __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
   const int64_t outs = (int64_t)c.B * c.H * a.rows;
   const int out_ctas = (int)(Deep ? outs : (outs + kFinWarps - 1) / kFinWarps);
   const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
-  grid_dependency_wait();
-  for (int cta = blockIdx.x; cta < out_ctas + (chunks + kPer - 1) / kPer; cta += gridDim.x) {
+  const int ctas = out_ctas + (chunks + kPer - 1) / kPer;
+  // Where an item lies follows from the lengths alone; the first one is found while the launch before still runs.
+  struct Item {
+    int b, h, bh, r, j0, w0, w1, nblk;  // r: row of an output; j0: first entry of the item's scores; w0 .. w1: parts
+    Seq s;
+    bool some;
+  };
+  auto find = [&](int cta) {
+    Item it;
+    it.some = false;
+    if (cta >= ctas) return it;
+    int before = 0;
     if (cta < out_ctas) {
       const int64_t item = Deep ? cta : (int64_t)cta * kFinWarps + warp;
-      if (item >= outs) continue;
-      const int r = (int)(item % a.rows), bh = (int)(item / a.rows), b = bh / c.H, h = bh - b * c.H;
-      const Seq s = seq_of(a.l, b);
-      const int tok = r / c.group, hq = h * c.group + r % c.group;
-      if (tok >= s.cnt) continue;
+      if (item >= outs) return it;
+      it.r = (int)(item % a.rows), it.bh = (int)(item / a.rows), it.b = it.bh / c.H, it.h = it.bh - it.b * c.H;
+      it.s = seq_of(a.l, it.b);
+      for (int i = lane; i < it.b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
+      before = __reduce_add_sync(0xffffffffu, before);
+      it.some = it.r / c.group < it.s.cnt;
+    } else {
+      int x = (cta - out_ctas) * kPer + warp / W;
+      if (x >= chunks) return it;  // W = 8 has no such item
+      it.b = find_seq(a.l, c.B, c.H, kChunk, x, before);
+      it.s = seq_of(a.l, it.b);
+      const int nch = ceil_div(it.s.total, kChunk);
+      it.h = x / nch, it.bh = it.b * c.H + it.h, it.j0 = (x - it.h * nch) * kChunk;
+      it.some = true;
+    }
+    it.nblk = ceil_div(it.s.total, kBlock);
+    if (it.nblk > 0) {
+      const int start = c.H * before + it.h * it.nblk;
+      it.w0 = worker_of(start, blocks, workers), it.w1 = worker_of(start + it.nblk - 1, blocks, workers);
+    }
+    return it;
+  };
+  Item it = find(blockIdx.x);
+  grid_dependency_wait();
+  for (int cta = blockIdx.x; cta < ctas; cta += gridDim.x) {
+    if (cta != blockIdx.x) it = find(cta);
+    if (!it.some) continue;
+    const int b = it.b, h = it.h, bh = it.bh, w0 = it.w0, w1 = it.w1;
+    const Seq s = it.s;
+    if (cta < out_ctas) {
+      const int r = it.r, tok = r / c.group, hq = h * c.group + r % c.group;
       const int d0 = lane % kLanes * 4;
       const bool writes = lane < kLanes && (!Deep || warp == 0);
       __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0;
       float *lse = a.lse ? a.lse + ((size_t)b * c.H * c.group + hq) * a.l.n + tok : nullptr;
-      const int nblk = ceil_div(s.total, kBlock);
-      if (nblk == 0) {  // no entry at all
+      if (it.nblk == 0) {  // no entry at all
         if (writes) *(uint2 *)dst = make_uint2(0u, 0u);
         if (lse && writes && lane == 0) *lse = -INFINITY;
         continue;
       }
-      int before = 0;
-      for (int i = lane; i < b; i += 32) before += ceil_div(seq_of(a.l, i).total, kBlock);
-      const int x = c.H * __reduce_add_sync(0xffffffffu, before) + h * nblk;
-      const int w0 = worker_of(x, blocks, workers), w1 = worker_of(x + nblk - 1, blocks, workers);
       if (w0 == w1) continue;  // written by its worker
       const float2 *ml = a.ml + (size_t)bh * c.max_rows + r;
       const float *po = a.po + ((size_t)bh * c.max_rows + r) * D + d0;
@@ -704,15 +735,7 @@ __global__ void __launch_bounds__(kFinWarps * 32) finish_kernel(const Args a) {
       }
       continue;
     }
-    int x = (cta - out_ctas) * kPer + warp / W, before;
-    if (x >= chunks) continue;  // W = 8 has no such item
-    const int b = find_seq(a.l, c.B, c.H, kChunk, x, before);
-    const Seq s = seq_of(a.l, b);
-    const int nch = ceil_div(s.total, kChunk), nblk = ceil_div(s.total, kBlock);
-    const int h = x / nch, j0 = (x - h * nch) * kChunk + warp % W * (128 * V) + lane * 4, bh = b * c.H + h;
-    const int rows = s.cnt * c.group;
-    const int start = c.H * before + h * nblk;
-    const int w0 = worker_of(start, blocks, workers), w1 = worker_of(start + nblk - 1, blocks, workers);
+    const int j0 = it.j0 + warp % W * (128 * V) + lane * 4, rows = s.cnt * c.group;
     // Eight rows to a warp, a lane of each group of eight for one; the four groups, and the warps that have the same
     // rows, take the parts in turn.
     const float2 *ml = a.ml + (size_t)bh * c.max_rows;
