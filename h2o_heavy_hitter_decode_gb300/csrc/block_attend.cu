@@ -595,10 +595,10 @@ __device__ __forceinline__ void join(float &m, float &l, float om, float ol) {
   m = mn;
 }
 
-// Items of a CTA: first eight (one a warp) of a row's output, where its head
-// lies in several runs: all lanes gather the row's LSE, then take its partials.
-// Then scores: W warps gather the LSE of a head's rows, and each lane adds the
-// rows' weights of V fours of entries, in the rows' order.
+// Items of a CTA, the longer ones first.  Scores: W warps gather the LSE of a
+// head's rows, and each lane adds the rows' weights of V fours of entries, in
+// the rows' order.  Then a row's output to each warp, where its head lies in
+// several runs: the lanes take its partials in turn.
 // W = 8 where the parts and rows to gather are many, so that they are gathered
 // once for 1024 V entries; else W = 1, eight items of 128 V entries to a CTA,
 // which need no barrier.  Deep: few heads in many runs, whose rows' outputs
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
   const int64_t outs = (int64_t)c.B * c.H * a.rows;
   const int out_ctas = (int)(Deep ? outs : (outs + kFinWarps - 1) / kFinWarps);
   const int chunks = a.accumulate ? c.H * sum_units(a.l, c.B, kChunk) : 0;
-  const int ctas = out_ctas + (chunks + kPer - 1) / kPer;
+  const int score_ctas = (chunks + kPer - 1) / kPer, ctas = score_ctas + out_ctas;
   // Where an item lies follows from the lengths alone; the first one is found while the launch before still runs.
   struct Item {
     int b, h, bh, r, j0, w0, w1, nblk;  // r: row of an output; j0: first entry of the item's scores; w0 .. w1: parts
@@ -631,8 +631,8 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
     it.some = false;
     if (cta >= ctas) return it;
     int before = 0;
-    if (cta < out_ctas) {
-      const int64_t item = Deep ? cta : (int64_t)cta * kFinWarps + warp;
+    if (cta >= score_ctas) {
+      const int64_t item = Deep ? cta - score_ctas : (int64_t)(cta - score_ctas) * kFinWarps + warp;
       if (item >= outs) return it;
       it.r = (int)(item % a.rows), it.bh = (int)(item / a.rows), it.b = it.bh / c.H, it.h = it.bh - it.b * c.H;
       it.s = seq_of(a.l, it.b);
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       before = __reduce_add_sync(0xffffffffu, before);
       it.some = it.r / c.group < it.s.cnt;
     } else {
-      int x = (cta - out_ctas) * kPer + warp / W;
+      int x = cta * kPer + warp / W;
       if (x >= chunks) return it;  // W = 8 has no such item
       it.b = find_seq(a.l, c.B, c.H, kChunk, x, before);
       it.s = seq_of(a.l, it.b);
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
     if (!it.some) continue;
     const int b = it.b, h = it.h, bh = it.bh, w0 = it.w0, w1 = it.w1;
     const Seq s = it.s;
-    if (cta < out_ctas) {
+    if (cta >= score_ctas) {
       const int r = it.r, tok = r / c.group, hq = h * c.group + r % c.group;
       const int d0 = lane % kLanes * 4;
       const bool writes = lane < kLanes && (!Deep || warp == 0);
