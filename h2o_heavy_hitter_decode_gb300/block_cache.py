@@ -10,7 +10,11 @@ from . import H2OError, _check, _ptr, lib
 
 __all__ = ["H2OBlockCache"]
 
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 KV = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(device).cuda_stream without its objects
 
 
 class H2OBlockCache:
@@ -46,6 +50,7 @@ class H2OBlockCache:
             raise ValueError("H2OBlockCache lives on a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         shape = (B, H, d, capacity, group, max_queries, code)
         with torch.cuda.device(self.device):
             nbytes = L.h2o_bcache_workspace_bytes(*shape)
@@ -82,7 +87,7 @@ class H2OBlockCache:
         return self.workspace[at : at + n].view(dtype).view(shape)
 
     def _stream(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return _raw_stream(self._index)
 
     def _use_stream(self):
         s = self._stream()
@@ -96,7 +101,7 @@ class H2OBlockCache:
             return None
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
         return t.data_ptr()
@@ -104,13 +109,13 @@ class H2OBlockCache:
     def _lengths(self, t, name):
         if t is None:
             raise TypeError(f"{name} must be a tensor")
-        return self._dense(t, torch.int32, self._per_seq, name)
+        return self._dense(t, I32, self._per_seq, name)
 
     def _rows(self, slot, t, shape, name):
         """Address of the h2o_rows of a bf16 tensor [B, heads, n, d] whose rows are contiguous."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != self.device:
+        if t.dtype is not BF16 or t.shape != shape or t.get_device() != self._index:
             raise ValueError(f"{name}: expected torch.bfloat16 {shape} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         sb, sh, st, one = t.stride()
@@ -143,9 +148,9 @@ class H2OBlockCache:
         n = self._tokens(k, "k")
         shape = self._shape(self.H, n)
         args = (self._rows(1, k, shape, "k"), self._rows(2, v, shape, "v"), self._lengths(lengths, "lengths"),
-                self._dense(counts, torch.int32, self._per_seq, "counts"),
-                self._dense(position, torch.int32, self._per_seq, "position"),
-                self._dense(score, torch.float32, shape[:3], "score"))
+                self._dense(counts, I32, self._per_seq, "counts"),
+                self._dense(position, I32, self._per_seq, "position"),
+                self._dense(score, F32, shape[:3], "score"))
         self._use_stream()
         _check(self._lib.h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
 
@@ -158,11 +163,11 @@ class H2OBlockCache:
         n = self._tokens(q, "q")
         shape = self._shape(self._heads, n)
         qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
-        cnt = self._dense(counts, torch.int32, self._per_seq, "counts")
+        cnt = self._dense(counts, I32, self._per_seq, "counts")
         if out is None:
             out = self._new_out(shape, counts)
         args = (qr, lens, cnt, 1 if causal else 0, 1 if accumulate else 0, self._rows(3, out, shape, "out"),
-                self._dense(lse, torch.float32, shape[:3], "lse"))
+                self._dense(lse, F32, shape[:3], "lse"))
         self._use_stream()
         _check(self._lib.h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
         return out
@@ -174,11 +179,11 @@ class H2OBlockCache:
         n = self._tokens(q, "q")
         shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
         rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
-        lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, torch.int32, self._per_seq, "counts")
+        lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
         if out is None:
             out = self._new_out(shape, counts)
-        args = rows + (lens, cnt, self._dense(position, torch.int32, self._per_seq, "position"), 1 if accumulate else 0,
-                       self._rows(3, out, shape, "out"), self._dense(lse, torch.float32, shape[:3], "lse"))
+        args = rows + (lens, cnt, self._dense(position, I32, self._per_seq, "position"), 1 if accumulate else 0,
+                       self._rows(3, out, shape, "out"), self._dense(lse, F32, shape[:3], "lse"))
         self._use_stream()
         _check(self._lib.h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
         return out
@@ -198,7 +203,7 @@ class H2OBlockCache:
         if new_lengths is None:
             new_lengths = torch.empty(self.B, dtype=torch.int32, device=self.device)
         args = (self._lengths(lengths, "lengths"), int(k_heavy), int(k_local), int(n_sink), int(score_mode),
-                self._dense(position, torch.int32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
+                self._dense(position, I32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
         self._use_stream()
         _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
         return new_lengths

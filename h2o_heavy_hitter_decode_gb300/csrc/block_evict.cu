@@ -447,7 +447,7 @@ template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStrea
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim = {(unsigned)P, 1, 1};
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = P > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W>, a);
 }
 
