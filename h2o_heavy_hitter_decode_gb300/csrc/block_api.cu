@@ -46,7 +46,7 @@ struct OnDevice {
 
 bool shape_ok(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv) {
   if (B < 1 || H < 1 || (int64_t)B * H > (1LL << 24) || d < 1) return false;
-  if (capacity < H2O_BLOCK || capacity % H2O_BLOCK || capacity > 0x7fffffffLL) return false;
+  if (capacity < H2O_BLOCK || capacity % H2O_BLOCK || capacity > (1LL << 30)) return false;
   if ((int64_t)B * H * capacity > 0x7fffffffLL) return false;
   if (group < 1 || max_queries < 1 || group > H2O_BLOCK_MAX_ROWS || max_queries > H2O_BLOCK_MAX_ROWS) return false;
   if (group * max_queries > H2O_BLOCK_MAX_ROWS) return false;
@@ -122,6 +122,11 @@ bool code_map(CUtensorMap *m, const void *base, int d, int64_t entries) {
 }
 
 bool ints_ok(const int32_t *p, bool may_be_null) { return p ? aligned(p, 4) : may_be_null; }
+
+bool overlap(const int32_t *x, const int32_t *y, int n) {
+  const uintptr_t a = (uintptr_t)x, z = (uintptr_t)y, bytes = (uintptr_t)n * sizeof(int32_t);
+  return a < z + bytes && z < a + bytes;
+}
 
 }  // namespace
 
@@ -248,8 +253,9 @@ h2o_status h2o_bcache_evict(h2o_bcache_t c, const int32_t *lengths, int k_heavy,
     return H2O_EINVAL;
   if (n_sink < 0 || n_sink > k_heavy || (score_mode != 0 && score_mode != 1)) return H2O_EINVAL;
   if (!ints_ok(lengths, false) || !ints_ok(new_lengths, false) || !ints_ok(position, true)) return H2O_EINVAL;
-  const uintptr_t a = (uintptr_t)lengths, z = (uintptr_t)new_lengths, bytes = (uintptr_t)c->view.B * sizeof(int32_t);
-  if (a < z + bytes && z < a + bytes) return H2O_EINVAL;
+  // heads still read the lengths and positions when the first ones write the new lengths
+  if (overlap(lengths, new_lengths, c->view.B) || (position && overlap(position, new_lengths, c->view.B)))
+    return H2O_EINVAL;
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const cudaError_t e = blk::launch_evict(c->view, lengths, k_heavy, k_local, n_sink, score_mode, position,

@@ -206,7 +206,7 @@ struct Args {
   Lens l;
   Rows q, out;
   float *lse;
-  float2 *ml;  // [workers + B*H][max_rows]  partial maximum and sum
+  float2 *ml;  // [workers + B*H][max_rows]  partial reference and sum
   float *po;   // [workers + B*H][max_rows][d]  partial output
   int causal, accumulate, workers;
   int rows;  // n * group: rows of a head in this call
@@ -452,15 +452,17 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           top[n][u] = x;
-          moves |= x > m[n][u] + 8.f || m[n][u] == -INFINITY;
+          moves |= x > m[n][u] + 15.f || m[n][u] == -INFINITY;
         }
-      // The running maximum moves only when it is passed by more than 2^8: weights then stay below 2^8, in f16's range
+      // The weights' reference lies 2^7 below the maximum when it is set, and moves only when it is passed by more than
+      // 2^15.  Weights then stay below 2^15, in f16's range, and one 2^21 times smaller than the largest is still a
+      // normal number of it: a long tail of small weights next to a large one is not lost.
       if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float mn = fmaxf(m[n][u], top[n][u]);
+            const float mn = fmaxf(m[n][u], top[n][u] - 7.f);
             const float f = m[n][u] == -INFINITY ? 0.f : ex2(m[n][u] - mn);
             m[n][u] = mn;
             lsum[n][u] *= f;

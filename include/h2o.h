@@ -313,9 +313,12 @@ typedef struct {
   int64_t stride_b, stride_h, stride_t;
 } h2o_rows;
 
-/* Bytes of device workspace (0 for invalid shapes).  B, H >= 1, B * H <=
- * 2^24; d in {64, 128}; capacity a multiple of H2O_BLOCK, B * H * capacity <
- * 2^31; group, max_queries >= 1, group * max_queries <= H2O_BLOCK_MAX_ROWS. */
+/* Bytes of device workspace (0 for invalid shapes, or without a device).
+ * B, H >= 1, B * H <= 2^24; d in {64, 128}; capacity a multiple of H2O_BLOCK,
+ * at most 2^30, B * H * capacity < 2^31; group, max_queries >= 1, group *
+ * max_queries <= H2O_BLOCK_MAX_ROWS.  Besides the cache's arrays (2 d + 8 bytes
+ * an entry and the scales) the workspace holds 4 * group * max_queries bytes of
+ * scratch an entry and the partial results of attention. */
 size_t h2o_bcache_workspace_bytes(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv);
 
 /* Create over caller-owned device memory (256-byte aligned) of the current
@@ -370,11 +373,11 @@ h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h
  * a NaN ranks below all; among equals the lowest index goes first.  The kept
  * entries move to indices 0 .. k-1 in their order with their positions and
  * scores, and every block of them is quantised anew from the values its
- * entries stood for (a fresh block in the sense above).  What lies behind
- * index k - 1 is left as it was.  position: device int32 [B], the position the
+ * entries stood for (a fresh block in the sense above).  Codes, positions and
+ * scores behind index k - 1 are left as they were.  position: device int32 [B], the position the
  * next token takes, or NULL = lengths; read in score_mode 1 only.
  * new_lengths: device int32 [B], receives min(lengths[b], k) (lengths[b]
- * itself where it is out of range); must not overlap lengths. */
+ * itself where it is out of range); must not overlap lengths or position. */
 h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_heavy, int k_local, int n_sink,
                             int score_mode, const int32_t *position, int32_t *new_lengths);
 

@@ -18,7 +18,7 @@ def L():
 
 
 BAD = [(0, 3, 64, 64, 2, 4, 0), (2, 0, 64, 64, 2, 4, 0), (2, 3, 0, 64, 2, 4, 0), (2, 3, 64, 0, 2, 4, 0),
-       (2, 3, 64, 63, 2, 4, 0), (2, 3, 64, 2 ** 40, 2, 4, 0), (2, 3, 64, 64, 0, 4, 0), (2, 3, 64, 64, 2, 0, 0),
+       (2, 3, 64, 63, 2, 4, 0), (2, 3, 64, 2 ** 40, 2, 4, 0), (1, 1, 64, 2 ** 30 + 32, 1, 1, 0), (2, 3, 64, 64, 0, 4, 0), (2, 3, 64, 64, 2, 0, 0),
        (2, 3, 64, 64, 32, 9, 0), (2, 3, 64, 64, 257, 1, 0), (2, 3, 64, 64, 2, 4, 2), (2, 3, 64, 64, 2, 4, -1),
        (1 << 13, 1 << 12, 64, 64, 1, 1, 0), (1 << 12, 1 << 12, 64, 128, 1, 1, 0)]
 

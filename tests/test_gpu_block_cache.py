@@ -216,6 +216,67 @@ def test_attend_many_splits_long():
     same_state(c, r)
 
 
+def test_attend_small_weights_next_to_a_large_one():
+    """One entry holds nearly all the weight and 60,000 others 2^-25 of it each, with equal values: their share of the
+    output (0.2 %) is not lost to the weights' rounding."""
+    n = 60000
+    c = H2OBlockCache(1, 1, 64, 60000 // 32 * 32 + 32, kv="int8")
+    k = torch.zeros(1, 1, n, 64, device=DEV)
+    k[0, 0, 77, 0] = 64.0
+    v = torch.full((1, 1, n, 64), 100.0, device=DEV)
+    v[0, 0, 77] = 1.0
+    c.append(k.bfloat16(), v.bfloat16(), ints([0]))
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 25 * math.log(2) * 8 / 64
+    out = c.attend(q, ints([n]))
+    w = math.exp(-float(q[0, 0, 0, 0]) * 64 / 8)
+    want = (1 + (n - 1) * w * 100) / (1 + (n - 1) * w)
+    # the tail's weights: f16 half steps 2^-11 (2^-12 for a power of two's neighbours) of their share; bf16 2^-8 of the sum
+    assert abs(float(out[0, 0, 0, 5]) - want) <= 2.0 ** -8 * want + 2.0 ** -11 * want
+
+
+def test_attend_many_sequences():
+    """More sequences than a warp looks over at once, most of them short, some empty."""
+    B = 700
+    lens = [(17 * b) % 33 for b in range(B)]
+    c, r, g = filled(43, B, 1, 64, 32, lens, 2, 1, "int8")
+    q = rows(g, B, 2, 1, 64)
+    lse = torch.zeros(B, 2, 1, device=DEV)
+    out = c.attend(q, ints(lens), lse=lse)
+    want, want_lse, tol, lse_tol = r.attend(q, lens)
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    same_state(c, r)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_offsets_past_32_bits(kv):
+    """4.6 GB of codes for K alone: the last head's append, attention, scores and eviction against those of a cache of
+    that head's own."""
+    H, cap, d, n = 512, 70016, 128, 69990
+    g = torch.Generator(DEV).manual_seed(47)
+    big, one = H2OBlockCache(1, H, d, cap, group=2, kv=kv), H2OBlockCache(1, 1, d, cap, group=2, kv=kv)
+    for j in range(0, n, 23330):
+        k, v = rows(g, 1, 1, 23330, d), rows(g, 1, 1, 23330, d)
+        one.append(k, v, ints([j]))
+        big.append(k.expand(1, H, 23330, d), v.expand(1, H, 23330, d), ints([j]))
+    q = rows(g, 1, 2, 1, d, scale=2.0)
+    a = big.attend(q.repeat(1, H, 1, 1), ints([n]))
+    z = one.attend(q, ints([n]))
+    for h in (0, 1, 300, H - 1):
+        # the heads' blocks are shared out to workers differently: sums in another order
+        assert torch.allclose(a[:, 2 * h : 2 * h + 2].float(), z.float(), atol=2e-3, rtol=2.0 ** -7), h
+        assert torch.allclose(big.score[:, h, :n], one.score[:, 0, :n], rtol=1e-4, atol=1e-9), h
+        assert torch.equal(big.K[:, h].view(torch.uint8), one.K[:, 0].view(torch.uint8))
+    big.score.copy_(one.score.expand(1, H, cap))
+    assert big.evict(ints([n]), 5000, 1000).tolist() == one.evict(ints([n]), 5000, 1000).tolist() == [6000]
+    for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
+        x, y = getattr(big, name), getattr(one, name)
+        for h in (0, 257, H - 1):
+            assert torch.equal(x[:, h].contiguous().view(torch.uint8), y[:, 0].contiguous().view(torch.uint8)), (name, h)
+    assert big.error_bits() == one.error_bits() == 0
+
+
 # --------------------------------------------------------------------- step
 
 @pytest.mark.parametrize("kv,d,G,n", [("e4m3", 128, 1, 1), ("int8", 64, 4, 1), ("e4m3", 64, 3, 5), ("int8", 128, 8, 3)])
@@ -300,6 +361,14 @@ def test_evict_rows_of_zeros_and_far_scales(kv):
     c.K.view(torch.uint8)[:, :, :32] = 0  # zeros under a scale of 2^100
     load(r, c)
     assert c.evict(ints(lens), 30, 30).tolist() == r.evict(lens, 30, 30)
+    same_state(c, r)
+
+
+def test_evict_mean_weight_without_positions():
+    """score_mode 1 without positions: the lengths are the next positions."""
+    lens = [200, 130]
+    c, r, g = filled(77, 2, 2, 64, 224, lens, kv="int8")
+    assert c.evict(ints(lens), 50, 40, score_mode=1).tolist() == r.evict(lens, 50, 40, 0, 1)
     same_state(c, r)
 
 
@@ -512,7 +581,7 @@ def test_ranges_out_of_bounds_leave_the_sequence_alone():
 def test_arguments_rejected():
     c = H2OBlockCache(2, 2, 64, 64, group=2, max_queries=2, kv="int8")
     q, k = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 2, 1, 64, dtype=torch.bfloat16, device=DEV)
-    L = ints([0, 0])
+    L, P = ints([0, 0]), ints([5, 5])
     c.step(q, k, k, L)
     bad = [
         lambda: c.step(q.float(), k, k, L), lambda: c.step(q, k.half(), k, L), lambda: c.step(q.cpu(), k, k, L),
@@ -528,7 +597,7 @@ def test_arguments_rejected():
         lambda: c.append(k, k, L, score=torch.zeros(2, 2, device=DEV)),
         lambda: c.attend(torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device=DEV), L),
         lambda: c.evict(L, 0, 0), lambda: c.evict(L, -1, 4), lambda: c.evict(L, 4, -1), lambda: c.evict(L, 4, 4, n_sink=5),
-        lambda: c.evict(L, 4, 4, score_mode=2), lambda: c.evict(L, 4, 4, new_lengths=L), lambda: c.evict(L.float(), 4, 4),
+        lambda: c.evict(L, 4, 4, score_mode=2), lambda: c.evict(L, 4, 4, new_lengths=L), lambda: c.evict(L, 4, 4, position=P, new_lengths=P), lambda: c.evict(L.float(), 4, 4),
         lambda: H2OBlockCache(2, 2, 96, 64), lambda: H2OBlockCache(2, 2, 64, 40), lambda: H2OBlockCache(2, 2, 64, 64, group=32, max_queries=9),
     ]
     for i, call in enumerate(bad):
