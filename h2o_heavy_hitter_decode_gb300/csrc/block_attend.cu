@@ -192,14 +192,14 @@ constexpr int kTeams = 4;  // workers of a CTA
 // ring to an SM; Q is in registers where a worker is one warp.
 template <int D, int NR, int MT> struct Cfg {
   static constexpr int kWarps = kTeams * MT;
-  static constexpr int kCtas = NR == 1 ? 3 : MT <= 2 ? 2 : 1;  // per SM
+  static constexpr int kCtas = NR == 1 ? (D == 64 ? 4 : 3) : MT <= 2 ? 2 : 1;  // per SM
   static constexpr int kStage = 2 * kBlock * D;
   static constexpr bool kQSmem = MT > 1;
-  static constexpr int kStages = (NR == 2 && MT == 1 ? 98304 : MT <= 2 ? 65536 : 131072) / (kTeams * kStage);
+  static constexpr int kStages = (NR == 2 && MT == 1 ? 98304 : kCtas == 4 ? 49152 : MT <= 2 ? 65536 : 131072) / (kTeams * kStage);
   static constexpr int kQBytes = kQSmem ? kWarps * NR * D * 16 : 0;
   static constexpr int kSmem = 1024 + kTeams * kStages * kStage + kQBytes + kTeams * kStages * 16;
 };
-constexpr int kMaxCtas = 3;
+constexpr int kMaxCtas = 4;
 
 struct Args {
   View c;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   constexpr int OT = D / 16;  // 16-row tiles of O^T
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
   const View &c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / MT, tile = warp - team * MT;
