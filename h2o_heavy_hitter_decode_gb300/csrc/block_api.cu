@@ -226,7 +226,11 @@ h2o_status h2o_bcache_attend(h2o_bcache_t c, int n, const h2o_rows *q, const int
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 0, c->view.cap};
   const cudaError_t e =
-      blk::launch_attend(c->view, l, rows_of(q), causal != 0, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);
+      blk::head_fits(c->view, n)
+          ? blk::launch_head(c->view, l, rows_of(q), nullptr, nullptr, nullptr, causal != 0, accumulate != 0, rows_of(out),
+                             lse, c->kmap, c->vmap, c->stream)
+          : blk::launch_attend(c->view, l, rows_of(q), causal != 0, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap,
+                               c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -241,6 +245,12 @@ h2o_status h2o_bcache_step(h2o_bcache_t c, int n, const h2o_rows *q, const h2o_r
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
+  if (blk::head_fits(c->view, n)) {
+    const blk::Rows kr = rows_of(k), vr = rows_of(v);
+    const cudaError_t e = blk::launch_head(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, rows_of(out),
+                                           lse, c->kmap, c->vmap, c->stream);
+    return e == cudaSuccess ? H2O_OK : fail(e);
+  }
   cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
   if (e == cudaSuccess)
     e = blk::launch_attend(c->view, l, rows_of(q), 1, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);

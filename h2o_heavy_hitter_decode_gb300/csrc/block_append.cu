@@ -20,7 +20,6 @@ namespace blk {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kFew = 8;  // rows a sequence that append_few_kernel takes
 
 template <typename F, int D>
 __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const View c, const Lens l, const Rows k, const Rows v,
@@ -115,11 +114,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const View c, co
   }
 }
 
-// Few rows (they touch two blocks at most): a lane holds D/32 neighbours of a row.
+// Few rows: a warp per (head, K or V).
 template <typename F, int D>
 __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, const Lens l, const Rows k, const Rows v,
                                                                  const int32_t *__restrict__ position) {
-  constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   grid_launch_dependents();
   const int item = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -132,57 +130,9 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
     if (lane == 0 && h == 0 && !is_v) atomicOr(c.err, H2O_BERR_RANGE);
     return;
   }
-  const Rows &x = is_v ? v : k;
-  uint8_t *codes = (is_v ? c.V : c.K) + (size_t)bh * c.cap * D + lane * E;
-  float *scales = (is_v ? c.Vsc : c.Ksc) + (size_t)bh * (c.cap / kBlock);
-  auto row = [&](int t, uint32_t (&u)[2]) {  // bf16 bits, two to a word
-    const __nv_bfloat16 *p = x.at(b, h, t - s.len) + lane * E;
-    if constexpr (E == 4) {
-      const uint2 w = *(const uint2 *)p;
-      u[0] = w.x, u[1] = w.y;
-    } else {
-      u[0] = *(const uint32_t *)p, u[1] = 0u;
-    }
-  };
   for (int lo = s.len, end = s.len + s.cnt; lo < end;) {
-    const int blk = lo / kBlock, base = blk * kBlock, hi = min(end, base + kBlock);
-    const float before = base < s.len ? scales[blk] : 0.f;
-    uint32_t top = 0, odd = 0;
-    for (int t = lo; t < hi; ++t) {
-      uint32_t u[2];
-      row(t, u);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t y = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
-        if (y < 0x7f80u)
-          top = max(top, y);
-        else
-          odd = 1;
-      }
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (odd) atomicOr(c.err, H2O_BERR_NONFINITE);
-    const float after = fmaxf(before, block_scale<F>(__uint_as_float(top << 16)));
-    const float inv = inverse_pow2(after);
-    if (after > before && before > 0.f) {  // earlier entries of the block take the larger scale
-      const typename F::Shift shift(exponent(before) - exponent(after));
-      for (int t = base; t < s.len; ++t) {
-        uint8_t *p = codes + (size_t)t * D;
-        store_codes<E>(p, 0, shift.run(E == 4 ? *(const uint32_t *)p : *(const uint16_t *)p));
-      }
-    }
-    for (int t = lo; t < hi; ++t) {
-      uint32_t u[2], out = 0;
-      row(t, u);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float y = (e & 1 ? bf16hi(u[e >> 1]) : bf16lo(u[e >> 1])) * inv;
-        y = y != y ? 0.f : fminf(fmaxf(y, -F::kMax), F::kMax);
-        out |= F::code(y) << (8 * e);
-      }
-      store_codes<E>(codes + (size_t)t * D, 0, out);
-    }
-    if (lane == 0) scales[blk] = after;
+    const int hi = min(end, (lo / kBlock + 1) * kBlock);
+    append_rows<F, D>(c, is_v, is_v ? v : k, b, h, s.len, lo, hi);
     lo = hi;
   }
   if (!is_v && lane < s.cnt) {
@@ -195,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
 template <typename F, int D>
 cudaError_t append_t(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
                      const float *score, cudaStream_t st) {
-  if (l.n <= kFew && !score) {
+  if (l.n <= kFewRows && !score) {
     const int64_t warps = (int64_t)c.B * c.H * 2;
     append_few_kernel<F, D><<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(c, l, k, v, position);
     return cudaGetLastError();

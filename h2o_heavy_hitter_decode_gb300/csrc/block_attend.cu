@@ -213,13 +213,246 @@ struct Args {
   int streams;  // the codes pass through L2 once: they make way first
 };
 
+// What a warp holds of a head while it attends: Q, and for its NR tiles of 8
+// rows the output, the reference and the sum of the weights so far.
+template <typename F, int D, int NR, bool QSmem> struct Tile {
+  using T = ToF16<F>;
+  static constexpr int KS = D / 16;  // k steps of S, words of a lane's share of a K entry
+  static constexpr int OT = D / 16;  // 16-row tiles of O^T
+  // The lane's rows of tile n: 2 t and 2 t + 1 (columns of S^T and O^T).
+  float o[NR][OT][4], m[NR][2], lsum[NR][2], crow[NR][2];
+  int end[NR][2];
+  uint32_t qr[QSmem ? 1 : NR][KS][2];
+  int min_end, live;  // live: bit 2 n + u, the row exists
+
+  // Rows row0 .. of head h of sequence b; qs: this warp's share of shared memory for Q.
+  __device__ __forceinline__ void begin(const Args &a, const Seq &s, int b, int h, int row0, uint4 *qs) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    min_end = a.causal ? s.total - s.cnt + 1 : s.total;
+    live = 0;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int j = 0; j < OT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tok = (row0 + 8 * n + 2 * t + u) / a.c.group;
+        const bool is = tok < s.cnt;
+        live |= (int)is << (2 * n + u);
+        end[n][u] = is && a.causal ? s.total - s.cnt + tok + 1 : s.total;
+        m[n][u] = -INFINITY;
+        lsum[n][u] = 0.f;
+      }
+      // Q: the lane's D/4 dimensions of row g
+      const int r = row0 + 8 * n + g, tok = r / a.c.group;
+      const bool is = tok < s.cnt;
+      const __nv_bfloat16 *p = a.q.at(b, h * a.c.group + r % a.c.group, tok) + t * (D / 4);
+      float f[D / 4], top = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        Unpack<__nv_bfloat16>::run(is ? ld_nc16(p + e * 8) : make_uint4(0u, 0u, 0u, 0u), f + e * 8);
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // q to f16: a power of two brings the row's largest element to 2^13 .. 2^14; bf16's 8 bits then fit, and
+      // only elements 2^-27 of the largest and below lose bits
+      int ex = 0;
+      frexpf(top, &ex);
+      const int sh = top > 0.f && top < INFINITY ? min(14 - ex, 100) : 0;
+      const float up = ldexpf(1.f, sh), back = ldexpf(rsqrtf((float)D) * kLog2e, -sh);
+      crow[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      crow[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      uint32_t qh[KS][2];
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {  // in the order of the codes' conversion
+        const __half2 x = __floats2half2_rn(f[4 * k] * up, f[4 * k + (T::kAdjacent ? 1 : 2)] * up);
+        const __half2 y = __floats2half2_rn(f[4 * k + (T::kAdjacent ? 2 : 1)] * up, f[4 * k + 3] * up);
+        qh[k][0] = *(const uint32_t *)&x;
+        qh[k][1] = *(const uint32_t *)&y;
+      }
+      if constexpr (QSmem) {
+#pragma unroll
+        for (int k = 0; k < KS; k += 2)  // read by this lane only
+          qs[(n * (KS / 2) + k / 2) * 32 + lane] = make_uint4(qh[k][0], qh[k][1], qh[k + 1][0], qh[k + 1][1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qr[n][k][0] = qh[k][0], qr[n][k][1] = qh[k][1];
+      }
+    }
+  }
+
+  // The block's K and V codes (swizzled) under their scales; `rest` entries are left of the head; keep(r, j, ...)
+  // receives the base-2 logits of row row0 + r and entries j, j + 8, j + 16 and j + 24.
+  template <typename Keep>
+  __device__ __forceinline__ void block(const uint8_t *kt, uint8_t *vt, float ks, float vs, int blk, int rest,
+                                        const uint4 *qs, Keep keep) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float s[NR][2][4];  // S^T: entries 16 x + g and + 8, rows 2 t and 2 t + 1
+#pragma unroll
+    for (int part = 0; part < KS / 4; ++part) {  // 16 bytes of each K row at a time
+      uint32_t kw[4][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint4 u = *(const uint4 *)(kt + chunk_at<D>(n * 8 + g, t * (KS / 4) + part));
+        kw[n][0] = u.x, kw[n][1] = u.y, kw[n][2] = u.z, kw[n][3] = u.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        uint32_t q[NR][4];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          if constexpr (QSmem) {
+            const uint4 u = qs[(n * (KS / 2) + part * 2 + k / 2) * 32 + lane];
+            q[n][0] = u.x, q[n][1] = u.y, q[n][2] = u.z, q[n][3] = u.w;
+          } else {
+            q[n][0] = qr[n][part * 4 + k][0], q[n][1] = qr[n][part * 4 + k][1];
+            q[n][2] = qr[n][part * 4 + k + 1][0], q[n][3] = qr[n][part * 4 + k + 1][1];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t ka[4];
+            T::run(kw[2 * x][k + e], ka[0], ka[2]);
+            T::run(kw[2 * x + 1][k + e], ka[1], ka[3]);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              if (part == 0 && k + e == 0)
+                mma16816_new(s[n][x], ka, q[n][0], q[n][1]);
+              else
+                mma16816(s[n][x], ka, q[n][2 * e], q[n][2 * e + 1]);
+            }
+          }
+      }
+    }
+    const int j0 = blk * kBlock + g;
+    const bool edge = blk * kBlock + kBlock > min_end;
+    uint32_t p[NR][4];  // P^T as B: entries 8 e + 2 t and + 1 of row g
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float f0 = crow[n][0] * ks, f1 = crow[n][1] * ks;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) s[n][x][0] *= f0, s[n][x][1] *= f1, s[n][x][2] *= f0, s[n][x][3] *= f1;
+      if (edge) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j0 + 16 * x + 8 * (e >> 1) >= end[n][e & 1]) s[n][x][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (live >> (2 * n + u) & 1) keep(8 * n + 2 * t + u, j0, s[n][0][u], s[n][0][2 + u], s[n][1][u], s[n][1][2 + u]);
+    }
+    float top[NR][2];
+    bool moves = false;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x = fmaxf(fmaxf(s[n][0][u], s[n][0][2 + u]), fmaxf(s[n][1][u], s[n][1][2 + u]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        top[n][u] = x;
+        moves |= x > m[n][u] + 15.f || m[n][u] == -INFINITY;
+      }
+    // The weights' reference lies 2^7 below the maximum when it is set, and moves only when it is passed by more than
+    // 2^15.  Weights then stay below 2^15, in f16's range, and one 2^21 times smaller than the largest is still a
+    // normal number of it: a long tail of small weights next to a large one is not lost.
+    if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float mn = fmaxf(m[n][u], top[n][u] - 7.f);
+          const float f = m[n][u] == -INFINITY ? 0.f : ex2(m[n][u] - mn);
+          m[n][u] = mn;
+          lsum[n][u] *= f;
+#pragma unroll
+          for (int j = 0; j < OT; ++j) o[n][j][u] *= f, o[n][j][2 + u] *= f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float mu0 = m[n][0] == -INFINITY ? 0.f : m[n][0], mu1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float e0 = ex2(s[n][x][0] - mu0), e1 = ex2(s[n][x][1] - mu1), e2 = ex2(s[n][x][2] - mu0),
+                    e3 = ex2(s[n][x][3] - mu1);
+        lsum[n][0] += e0 + e2;
+        lsum[n][1] += e1 + e3;
+        // 16 bits for the product with V: f16's 2^-11 per weight, an eighth of the output's own rounding
+        const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
+        p[n][2 * x] = transpose8(*(const uint32_t *)&a0);
+        p[n][2 * x + 1] = transpose8(*(const uint32_t *)&a1);
+      }
+    }
+    if (rest < kBlock) {  // codes behind the last entry may be anything, also NaN: weight 0 needs a finite code
+      for (int z = rest * D + lane * 16; z < kBlock * D; z += 512) *(uint4 *)(vt + z) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    // O += vs (P V): a fresh product per block, added in fp32 under the block's scale
+    constexpr int VW = D == 128 && NR == 1 ? 4 : 2;  // words of the lane's D/8 dimensions of an entry at a time
+#pragma unroll
+    for (int part = 0; part < D / 32 / VW; ++part) {
+      uint32_t vw[8][VW];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = (e >> 1) * 8 + 2 * t + (e & 1);
+        if constexpr (VW == 4) {
+          const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
+          vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % VW] = u.z, vw[e][3 % VW] = u.w;
+        } else {
+          const uint8_t *from = D == 128 ? vt + chunk_at<D>(r, g) + part * 8 : vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
+          const uint2 u = *(const uint2 *)from;
+          vw[e][0] = u.x, vw[e][1] = u.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        uint32_t va[2][2][4];  // [dimensions 4w, 4w+1 | 4w+2, 4w+3][k step]
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
+          T::run(__byte_perm(x, y, T::kLow), va[0][k][0], va[0][k][1]);
+          T::run(__byte_perm(x, y, T::kHigh), va[1][k][0], va[1][k][1]);
+          T::run(__byte_perm(z, v, T::kLow), va[0][k][2], va[0][k][3]);
+          T::run(__byte_perm(z, v, T::kHigh), va[1][k][2], va[1][k][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int j = (part * VW + w) * 2 + y;
+            float acc[4];
+            mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
+            mma16816(acc, va[y][1], p[n][2], p[n][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][j][e] = fmaf(acc[e], vs, o[n][j][e]);
+          }
+      }
+    }
+  }
+
+  // Sum of the lane's row over the warp.
+  __device__ __forceinline__ float sum(int n, int u) const {
+    float l = lsum[n][u];
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    return l;
+  }
+};
+
 template <typename F, int D, int NR, int MT>
 __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::kCtas)
     attend_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using G = Cfg<D, NR, MT>;
-  using T = ToF16<F>;
-  constexpr int KS = D / 16;  // k steps of S, words of a lane's share of a K entry
-  constexpr int OT = D / 16;  // 16-row tiles of O^T
+  constexpr int KS = D / 16, OT = D / 16;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
@@ -281,11 +514,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   const int row0 = (blockIdx.y * MT + tile) * (8 * NR);  // the warp's rows of the head
   const bool idle = row0 >= a.rows;
   const int nsc = c.cap / kBlock;
-  // The lane's rows of tile n: 2 t and 2 t + 1 (columns of S^T and O^T).
-  float o[NR][OT][4], m[NR][2], lsum[NR][2], crow[NR][2];
-  int end[NR][2];
-  uint32_t qr[G::kQSmem ? 1 : NR][KS][2];
-  int first_blk = 0, min_end = 0, live = 0;  // live: bit 2 n + u, the row exists
+  Tile<F, D, NR, G::kQSmem> tl;
+  int first_blk = 0;
   bool open = false, lost = false;
   float ks, vs;
   {
@@ -301,58 +531,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     if (!open) {  // a head begins
       open = true;
       first_blk = cur.blk;
-      min_end = a.causal ? cur.s.total - cur.s.cnt + 1 : cur.s.total;
-      live = 0;
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-#pragma unroll
-        for (int j = 0; j < OT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int tok = (row0 + 8 * n + 2 * t + u) / c.group;
-          const bool is = tok < cur.s.cnt;
-          live |= (int)is << (2 * n + u);
-          end[n][u] = is && a.causal ? cur.s.total - cur.s.cnt + tok + 1 : cur.s.total;
-          m[n][u] = -INFINITY;
-          lsum[n][u] = 0.f;
-        }
-        // Q: the lane's D/4 dimensions of row g
-        const int r = row0 + 8 * n + g, tok = r / c.group;
-        const bool is = tok < cur.s.cnt;
-        const __nv_bfloat16 *p = a.q.at(cur.b, cur.h * c.group + r % c.group, tok) + t * (D / 4);
-        float f[D / 4], top = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          Unpack<__nv_bfloat16>::run(is ? ld_nc16(p + e * 8) : make_uint4(0u, 0u, 0u, 0u), f + e * 8);
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(f[e]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // q to f16: a power of two brings the row's largest element to 2^13 .. 2^14; bf16's 8 bits then fit, and
-        // only elements 2^-27 of the largest and below lose bits
-        int ex = 0;
-        frexpf(top, &ex);
-        const int sh = top > 0.f && top < INFINITY ? min(14 - ex, 100) : 0;
-        const float up = ldexpf(1.f, sh), back = ldexpf(rsqrtf((float)D) * kLog2e, -sh);
-        crow[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-        crow[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
-        uint32_t qh[KS][2];
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {  // in the order of the codes' conversion
-          const __half2 x = __floats2half2_rn(f[4 * k] * up, f[4 * k + (T::kAdjacent ? 1 : 2)] * up);
-          const __half2 y = __floats2half2_rn(f[4 * k + (T::kAdjacent ? 2 : 1)] * up, f[4 * k + 3] * up);
-          qh[k][0] = *(const uint32_t *)&x;
-          qh[k][1] = *(const uint32_t *)&y;
-        }
-        if constexpr (G::kQSmem) {
-#pragma unroll
-          for (int k = 0; k < KS; k += 2)  // read by this lane only
-            qs[(n * (KS / 2) + k / 2) * 32 + lane] = make_uint4(qh[k][0], qh[k][1], qh[k + 1][0], qh[k + 1][1]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) qr[n][k][0] = qh[k][0], qr[n][k][1] = qh[k][1];
-        }
-      }
+      tl.begin(a, cur.s, cur.b, cur.h, row0, qs);
     }
     const float ks_now = ks, vs_now = vs;
     const int blk = cur.blk, rest = cur.s.total - blk * kBlock;
@@ -376,162 +555,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
       }
       issue();
     }
-    if (!idle) {
-      float s[NR][2][4];  // S^T: entries 16 x + g and + 8, rows 2 t and 2 t + 1
-#pragma unroll
-      for (int part = 0; part < KS / 4; ++part) {  // 16 bytes of each K row at a time
-        uint32_t kw[4][4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 u = *(const uint4 *)(kt + chunk_at<D>(n * 8 + g, t * (KS / 4) + part));
-          kw[n][0] = u.x, kw[n][1] = u.y, kw[n][2] = u.z, kw[n][3] = u.w;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          uint32_t q[NR][4];
-#pragma unroll
-          for (int n = 0; n < NR; ++n) {
-            if constexpr (G::kQSmem) {
-              const uint4 u = qs[(n * (KS / 2) + part * 2 + k / 2) * 32 + lane];
-              q[n][0] = u.x, q[n][1] = u.y, q[n][2] = u.z, q[n][3] = u.w;
-            } else {
-              q[n][0] = qr[n][part * 4 + k][0], q[n][1] = qr[n][part * 4 + k][1];
-              q[n][2] = qr[n][part * 4 + k + 1][0], q[n][3] = qr[n][part * 4 + k + 1][1];
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t ka[4];
-              T::run(kw[2 * x][k + e], ka[0], ka[2]);
-              T::run(kw[2 * x + 1][k + e], ka[1], ka[3]);
-#pragma unroll
-              for (int n = 0; n < NR; ++n) {
-                if (part == 0 && k + e == 0)
-                  mma16816_new(s[n][x], ka, q[n][0], q[n][1]);
-                else
-                  mma16816(s[n][x], ka, q[n][2 * e], q[n][2 * e + 1]);
-              }
-            }
-        }
-      }
-      const int j0 = blk * kBlock + g;
-      const bool edge = blk * kBlock + kBlock > min_end;
-      uint32_t p[NR][4];  // P^T as B: entries 8 e + 2 t and + 1 of row g
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const float f0 = crow[n][0] * ks_now, f1 = crow[n][1] * ks_now;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) s[n][x][0] *= f0, s[n][x][1] *= f1, s[n][x][2] *= f0, s[n][x][3] *= f1;
-        if (edge) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j0 + 16 * x + 8 * (e >> 1) >= end[n][e & 1]) s[n][x][e] = -INFINITY;
-        }
-        if (a.accumulate) {
-          float *lg = c.logits + ((size_t)bh * c.max_rows + row0 + 8 * n + 2 * t) * c.cap + j0;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (live >> (2 * n + u) & 1) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) lg[u * c.cap + 16 * x] = s[n][x][u], lg[u * c.cap + 16 * x + 8] = s[n][x][2 + u];
-            }
-        }
-      }
-      float top[NR][2];
-      bool moves = false;
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float x = fmaxf(fmaxf(s[n][0][u], s[n][0][2 + u]), fmaxf(s[n][1][u], s[n][1][2 + u]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          top[n][u] = x;
-          moves |= x > m[n][u] + 15.f || m[n][u] == -INFINITY;
-        }
-      // The weights' reference lies 2^7 below the maximum when it is set, and moves only when it is passed by more than
-      // 2^15.  Weights then stay below 2^15, in f16's range, and one 2^21 times smaller than the largest is still a
-      // normal number of it: a long tail of small weights next to a large one is not lost.
-      if (__any_sync(0xffffffffu, moves)) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float mn = fmaxf(m[n][u], top[n][u] - 7.f);
-            const float f = m[n][u] == -INFINITY ? 0.f : ex2(m[n][u] - mn);
-            m[n][u] = mn;
-            lsum[n][u] *= f;
-#pragma unroll
-            for (int j = 0; j < OT; ++j) o[n][j][u] *= f, o[n][j][2 + u] *= f;
-          }
-      }
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const float mu0 = m[n][0] == -INFINITY ? 0.f : m[n][0], mu1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float e0 = ex2(s[n][x][0] - mu0), e1 = ex2(s[n][x][1] - mu1), e2 = ex2(s[n][x][2] - mu0),
-                      e3 = ex2(s[n][x][3] - mu1);
-          lsum[n][0] += e0 + e2;
-          lsum[n][1] += e1 + e3;
-          // 16 bits for the product with V: f16's 2^-11 per weight, an eighth of the output's own rounding
-          const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
-          p[n][2 * x] = transpose8(*(const uint32_t *)&a0);
-          p[n][2 * x + 1] = transpose8(*(const uint32_t *)&a1);
-        }
-      }
-      if (rest < kBlock) {  // codes behind the last entry may be anything, also NaN: weight 0 needs a finite code
-        for (int z = rest * D + lane * 16; z < kBlock * D; z += 512) *(uint4 *)(vt + z) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      // O += vs (P V): a fresh product per block, added in fp32 under the block's scale
-      constexpr int VW = D == 128 && NR == 1 ? 4 : 2;  // words of the lane's D/8 dimensions of an entry at a time
-#pragma unroll
-      for (int part = 0; part < D / 32 / VW; ++part) {
-        uint32_t vw[8][VW];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = (e >> 1) * 8 + 2 * t + (e & 1);
-          if constexpr (VW == 4) {
-            const uint4 u = *(const uint4 *)(vt + chunk_at<D>(r, g));
-            vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2 % VW] = u.z, vw[e][3 % VW] = u.w;
-          } else {
-            const uint8_t *from = D == 128 ? vt + chunk_at<D>(r, g) + part * 8 : vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
-            const uint2 u = *(const uint2 *)from;
-            vw[e][0] = u.x, vw[e][1] = u.y;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t va[2][2][4];  // [dimensions 4w, 4w+1 | 4w+2, 4w+3][k step]
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t x = vw[4 * k][w], y = vw[4 * k + 1][w], z = vw[4 * k + 2][w], v = vw[4 * k + 3][w];
-            T::run(__byte_perm(x, y, T::kLow), va[0][k][0], va[0][k][1]);
-            T::run(__byte_perm(x, y, T::kHigh), va[1][k][0], va[1][k][1]);
-            T::run(__byte_perm(z, v, T::kLow), va[0][k][2], va[0][k][3]);
-            T::run(__byte_perm(z, v, T::kHigh), va[1][k][2], va[1][k][3]);
-          }
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int j = (part * VW + w) * 2 + y;
-              float acc[4];
-              mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
-              mma16816(acc, va[y][1], p[n][2], p[n][3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[n][j][e] = fmaf(acc[e], vs_now, o[n][j][e]);
-            }
-        }
-      }
-    }
+    if (!idle)
+      tl.block(kt, vt, ks_now, vs_now, blk, rest, qs, [&](int r, int j, float s0, float s1, float s2, float s3) {
+        if (!a.accumulate) return;
+        float *lg = c.logits + ((size_t)bh * c.max_rows + row0 + r) * c.cap + j;
+        lg[0] = s0, lg[8] = s1, lg[16] = s2, lg[24] = s3;
+      });
     // this warp has read the stage
     __syncwarp();
     if (MT > 1) {
@@ -549,13 +578,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        float l = lsum[n][u];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (!(live >> (2 * n + u) & 1)) continue;
+        const float l = tl.sum(n, u);
+        if (!(tl.live >> (2 * n + u) & 1)) continue;
         const int r = row0 + 8 * n + 2 * t + u;
-        if (g == 0) a.ml[slot + r] = make_float2(m[n][u], l);
+        if (g == 0) a.ml[slot + r] = make_float2(tl.m[n][u], l);
         // the lane's D/8 dimensions: g D/8 + 2 j (accumulator u) and + 1 (2 + u)
         if (whole) {
           const int tok = r / c.group, hq = ah * c.group + r % c.group;
@@ -565,18 +591,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
           uint32_t w[OT];
 #pragma unroll
           for (int j = 0; j < OT; ++j) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[n][j][u] * inv, o[n][j][2 + u] * inv);
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(tl.o[n][j][u] * inv, tl.o[n][j][2 + u] * inv);
             w[j] = *(const uint32_t *)&b2;
           }
 #pragma unroll
           for (int j = 0; j < OT; j += 4) *(uint4 *)(dst + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
           if (a.lse && g == 0)
-            a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (m[n][u] + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (tl.m[n][u] + log2f(l)) * kLn2 : -INFINITY;
         } else {
           float *dst = a.po + (slot + r) * D + g * (D / 8);
 #pragma unroll
           for (int j = 0; j < OT; j += 2)
-            *(float4 *)(dst + 2 * j) = make_float4(o[n][j][u], o[n][j][2 + u], o[n][j + 1][u], o[n][j + 1][2 + u]);
+            *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u], tl.o[n][j][2 + u], tl.o[n][j + 1][u], tl.o[n][j + 1][2 + u]);
         }
       }
   }
@@ -584,6 +610,144 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     if (lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
     if (tile == 0)
       for (int i = 0; i < S; ++i) mbar_wait(full + i, i >= st ? phase : phase ^ 1);
+  }
+}
+
+// --------------------------------------------------------- one CTA per head
+constexpr int kHeadCap = 512;  // entries
+
+// A head of at most kHeadCap entries and 8 rows in one CTA, and with it the
+// append of a step, where the heads fit the device at once: one launch instead
+// of three that depend on each other.  Measured, us a step as a graph, this
+// form / the other: 32 heads of 256 entries 6.4 / 7.9, of 512 8.1 / 8.9, of
+// 1024 11.7 / 9.2; 128 cached heads x 4, 300 entries 8.5 / 12.1; 256 heads of
+// 512 12.8 / 14.1; 1024 heads of 512 47.7 / 35.1.  Each warp takes every W-th block through two stages of its
+// own; the warp of a block that receives new rows quantises them first.  The
+// logits stay in shared memory; when every warp is done the CTA joins the
+// rows' outputs and adds the weights to the scores.
+template <typename F, int D, int W>
+__global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
+    head_kernel(const Args a, const Rows k, const Rows v, const int32_t *__restrict__ position,
+                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr int S = 2, OT = D / 16, kStage = 2 * kBlock * D;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
+  float *logits = (float *)(smem + W * S * kStage);          // [rows][cap]
+  __shared__ uint64_t full[W][S];
+  __shared__ float2 part_ml[W][8];
+  __shared__ float row_lse[8];
+  const View &c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int bh = blockIdx.x, b = bh / c.H, h = bh - b * c.H;
+  const Seq s = seq_of(a.l, b);
+  if (!s.ok && h == 0 && threadIdx.x == 0) atomicOr(c.err, H2O_BERR_RANGE);
+  if (s.cnt == 0) return;  // neither rows nor queries
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int nblk = ceil_div(s.total, kBlock);
+  uint8_t *ring = smem + warp * S * kStage;
+  const uint64_t policy = l2_policy(a.streams);
+  auto fetch = [&](int i) {  // the warp's i-th block into its stage
+    const int blk = warp + i * W, base = blk * kBlock;
+    if (blk >= nblk) return;
+    if (a.l.appends && base + kBlock > s.len) {
+      const int lo = max(s.len, base), hi = min(s.total, base + kBlock);
+      append_rows<F, D>(c, false, k, b, h, s.len, lo, hi);
+      append_rows<F, D>(c, true, v, b, h, s.len, lo, hi);
+      const int j = base + lane;
+      if (j >= lo && j < hi) {
+        c.pos[(size_t)bh * c.cap + j] = (position ? position[b] : s.len) + (j - s.len);
+        c.score[(size_t)bh * c.cap + j] = 0.f;
+      }
+      // the codes are read back by the copy below
+      __threadfence();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+    }
+    if (lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      uint8_t *dst = ring + i % S * kStage;
+      uint64_t *bar = &full[warp][i % S];
+      mbar_expect_tx(bar, kStage);
+      tma_load_2d(dst, &kmap, bar, 0, bh * c.cap + base, policy);
+      tma_load_2d(dst + kBlock * D, &vmap, bar, 0, bh * c.cap + base, policy);
+    }
+  };
+  for (int i = 0; i < S; ++i) fetch(i);
+
+  Tile<F, D, 1, false> tl;
+  tl.begin(a, s, b, h, 0, nullptr);
+  const size_t scales = (size_t)bh * (c.cap / kBlock);
+  bool lost = false;
+  for (int i = 0; warp + i * W < nblk; ++i) {
+    const int blk = warp + i * W;
+    const float ks = c.Ksc[scales + blk], vs = c.Vsc[scales + blk];
+    if (!mbar_wait(&full[warp][i % S], i / S & 1)) {
+      lost = true;
+      break;
+    }
+    uint8_t *kt = ring + i % S * kStage;
+    tl.block(kt, kt + kBlock * D, ks, vs, blk, s.total - blk * kBlock, nullptr,
+             [&](int r, int j, float s0, float s1, float s2, float s3) {
+               float *lg = logits + r * c.cap + j;
+               lg[0] = s0, lg[8] = s1, lg[16] = s2, lg[24] = s3;
+             });
+    __syncwarp();  // this warp has read the stage
+    fetch(i + S);
+  }
+  if (lost) {  // a copy never arrived: report, and wait for the other one before the memory goes
+    if (lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
+    for (int i = 0; i < S; ++i) mbar_wait(&full[warp][i], 0), mbar_wait(&full[warp][i], 1);
+  }
+  __syncthreads();  // every warp is done with its ring: the partial outputs go there
+  float *po = (float *)smem;  // [W][8][D]
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float l = tl.sum(0, u);
+    const int r = 2 * t + u;
+    if (g == 0) part_ml[warp][r] = make_float2(tl.m[0][u], l);
+    float *dst = po + (warp * 8 + r) * D + g * (D / 8);
+#pragma unroll
+    for (int j = 0; j < OT; j += 2)
+      *(float4 *)(dst + 2 * j) = make_float4(tl.o[0][j][u], tl.o[0][j][2 + u], tl.o[0][j + 1][u], tl.o[0][j + 1][2 + u]);
+  }
+  __syncthreads();
+  const int rows = s.cnt * c.group;
+  for (int x = threadIdx.x; x < rows * (D / 4); x += W * 32) {
+    const int r = x / (D / 4), d0 = x % (D / 4) * 4, tok = r / c.group, hq = h * c.group + r % c.group;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, part_ml[w][r].x);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 p = part_ml[w][r];
+      const float z = p.x == -INFINITY ? 0.f : ex2(p.x - m);
+      l += p.x == -INFINITY ? p.y : p.y * z;
+      const float4 e = *(const float4 *)(po + (w * 8 + r) * D + d0);
+      o.x = fmaf(e.x, z, o.x), o.y = fmaf(e.y, z, o.y), o.z = fmaf(e.z, z, o.z), o.w = fmaf(e.w, z, o.w);
+    }
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? 1.f / l : 0.f;
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *(uint2 *)(const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0) =
+        make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
+    if (d0 == 0) {
+      const float e = m + log2f(l);
+      row_lse[r] = any ? e : INFINITY;
+      if (a.lse) a.lse[((size_t)b * c.H * c.group + hq) * a.l.n + tok] = any ? e * kLn2 : -INFINITY;
+    }
+  }
+  if (!a.accumulate) return;
+  __syncthreads();
+  float *sc = c.score + (size_t)bh * c.cap;
+  for (int j = threadIdx.x; j < s.total; j += W * 32) {
+    float w = 0.f;
+    for (int r = 0; r < rows; ++r) w += ex2(logits[r * c.cap + j] - row_lse[r]);
+    sc[j] += w;
   }
 }
 
@@ -872,16 +1036,25 @@ cudaError_t attend_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &
   return attend_t<F, D, 2, 4>(a, kmap, vmap, st);
 }
 
-size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kTeams + (size_t)B * H; }
-
-}  // namespace
-
-size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms) {
-  return partial_slots(B, H, sms) * max_rows * (sizeof(float2) + d * sizeof(float));
+template <typename F, int D, int W>
+cudaError_t head_t(const Args &a, const Rows &k, const Rows &v, const int32_t *position, const CUtensorMap &kmap,
+                   const CUtensorMap &vmap, cudaStream_t st) {
+  const int smem = 1024 + W * 2 * 2 * kBlock * D + a.rows * a.c.cap * 4;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise((const void *)head_kernel<F, D, W>, smem);
+  if (e != cudaSuccess) return e;
+  head_kernel<F, D, W><<<a.c.B * a.c.H, W * 32, smem, st>>>(a, k, v, position, kmap, vmap);
+  return cudaGetLastError();
 }
 
-cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
-                          float *lse, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+template <typename F, int D>
+cudaError_t head_d(const Args &a, const Rows &k, const Rows &v, const int32_t *position, const CUtensorMap &kmap,
+                   const CUtensorMap &vmap, cudaStream_t st) {
+  return a.c.B * a.c.H <= a.c.sms ? head_t<F, D, 8>(a, k, v, position, kmap, vmap, st)
+                                  : head_t<F, D, 4>(a, k, v, position, kmap, vmap, st);
+}
+
+Args args_of(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out, float *lse) {
   Args a;
   a.c = c;
   a.l = l;
@@ -895,12 +1068,44 @@ cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causa
   // Codes of more than L2's size evict each other before the next call reads them; the logits, which are read again
   // in this one, then stay.  56 heads, 1.3 GB of codes: 239 us without the hint.
   a.streams = 2 * (int64_t)c.B * c.H * c.cap * c.d > (int64_t)c.l2_bytes;
+  a.po = nullptr;
+  a.ml = nullptr;
+  return a;
+}
+
+size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kTeams + (size_t)B * H; }
+
+}  // namespace
+
+size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms) {
+  return partial_slots(B, H, sms) * max_rows * (sizeof(float2) + d * sizeof(float));
+}
+
+cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
+                          float *lse, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+  Args a = args_of(c, l, q, causal, accumulate, out, lse);
   const size_t rows = partial_slots(c.B, c.H, c.sms) * c.max_rows;
   a.po = c.part;
   a.ml = (float2 *)(c.part + rows * c.d);
   if (c.kv == H2O_KV_E4M3)
     return c.d == 128 ? attend_d<E4M3, 128>(a, kmap, vmap, st) : attend_d<E4M3, 64>(a, kmap, vmap, st);
   return c.d == 128 ? attend_d<I8, 128>(a, kmap, vmap, st) : attend_d<I8, 64>(a, kmap, vmap, st);
+}
+
+bool head_fits(const View &c, int n) {
+  return n * c.group <= 8 && c.cap <= kHeadCap && (int64_t)c.B * c.H <= 2 * c.sms;
+}
+
+cudaError_t launch_head(const View &c, const Lens &l, const Rows &q, const Rows *k, const Rows *v,
+                        const int32_t *position, int causal, int accumulate, const Rows &out, float *lse,
+                        const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+  const Args a = args_of(c, l, q, causal, accumulate, out, lse);
+  const Rows none{};
+  if (c.kv == H2O_KV_E4M3)
+    return c.d == 128 ? head_d<E4M3, 128>(a, k ? *k : none, v ? *v : none, position, kmap, vmap, st)
+                      : head_d<E4M3, 64>(a, k ? *k : none, v ? *v : none, position, kmap, vmap, st);
+  return c.d == 128 ? head_d<I8, 128>(a, k ? *k : none, v ? *v : none, position, kmap, vmap, st)
+                    : head_d<I8, 64>(a, k ? *k : none, v ? *v : none, position, kmap, vmap, st);
 }
 
 }  // namespace blk

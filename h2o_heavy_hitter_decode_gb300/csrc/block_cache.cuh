@@ -148,6 +148,67 @@ __device__ __forceinline__ int exponent(float s) { return (int)(__float_as_uint(
 // 1 / s of a power of two between 2^kMinExp and 2^126.
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// ------------------------------------------------------------ few new rows
+constexpr int kFewRows = 8;  // rows of a sequence that are appended one at a time
+
+// Rows lo .. hi-1 of head (b, h), all in one block, appended behind `len`
+// entries by one warp, a lane taking D/32 neighbours of a row.  The block's
+// earlier codes are read only where its scale grows.
+template <typename F, int D>
+__device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows &x, int b, int h, int len, int lo,
+                                            int hi) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, bh = b * c.H + h, blk = lo / kBlock, base = blk * kBlock;
+  uint8_t *codes = (is_v ? c.V : c.K) + (size_t)bh * c.cap * D + lane * E;
+  float *scale = (is_v ? c.Vsc : c.Ksc) + (size_t)bh * (c.cap / kBlock) + blk;
+  auto row = [&](int t, uint32_t (&u)[2]) {  // bf16 bits, two to a word
+    const __nv_bfloat16 *p = x.at(b, h, t - len) + lane * E;
+    if constexpr (E == 4) {
+      const uint2 w = *(const uint2 *)p;
+      u[0] = w.x, u[1] = w.y;
+    } else {
+      u[0] = *(const uint32_t *)p, u[1] = 0u;
+    }
+  };
+  const float before = base < len ? *scale : 0.f;
+  uint32_t top = 0, odd = 0;
+  for (int t = lo; t < hi; ++t) {
+    uint32_t u[2];
+    row(t, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t y = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+      if (y < 0x7f80u)
+        top = max(top, y);
+      else
+        odd = 1;
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (odd) atomicOr(c.err, H2O_BERR_NONFINITE);
+  const float after = fmaxf(before, block_scale<F>(__uint_as_float(top << 16)));
+  const float inv = inverse_pow2(after);
+  if (after > before && before > 0.f) {  // earlier entries of the block take the larger scale
+    const typename F::Shift shift(exponent(before) - exponent(after));
+    for (int t = base; t < len; ++t) {
+      uint8_t *p = codes + (size_t)t * D;
+      store_codes<E>(p, 0, shift.run(E == 4 ? *(const uint32_t *)p : *(const uint16_t *)p));
+    }
+  }
+  for (int t = lo; t < hi; ++t) {
+    uint32_t u[2], out = 0;
+    row(t, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float y = (e & 1 ? bf16hi(u[e >> 1]) : bf16lo(u[e >> 1])) * inv;
+      y = y != y ? 0.f : fminf(fmaxf(y, -F::kMax), F::kMax);
+      out |= F::code(y) << (8 * e);
+    }
+    store_codes<E>(codes + (size_t)t * D, 0, out);
+  }
+  if (lane == 0) *scale = after;
+}
+
 // A kernel launched behind this one with programmatic serialisation may start;
 // what it reads of this one's results it reads after its own wait.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
@@ -175,6 +236,13 @@ cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Row
 // kmap, vmap: the codes as rows of d bytes, boxes of kBlock rows (code_map).
 cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, const Rows &out,
                           float *lse, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
+// Append and causal attention (k, v, position as in launch_append, no scores),
+// or attention alone (k, v null), in one launch where a CTA can hold a head:
+// head_fits says whether.
+bool head_fits(const View &c, int n);
+cudaError_t launch_head(const View &c, const Lens &l, const Rows &q, const Rows *k, const Rows *v,
+                        const int32_t *position, int causal, int accumulate, const Rows &out, float *lse,
+                        const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st);
 size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms);
 cudaError_t launch_evict(const View &c, const int32_t *lengths, int k_heavy, int k_local, int n_sink, int score_mode,
                          const int32_t *position, int32_t *new_lengths, cudaStream_t st);

@@ -135,6 +135,13 @@ ATTEND = [  # B, H, G, n, d, kv, cap, lens, counts, causal
     (1, 1, 16, 16, 128, "int8", 96, [70], [11], True),          # 256 rows
     (40, 2, 1, 1, 64, "e4m3", 64, [(7 * b) % 65 for b in range(40)], None, True),
     (1, 2, 2, 1, 128, "e4m3", 8192, [8191], None, True),
+    # shapes at the border of what one CTA takes whole: capacity, rows, heads
+    (9, 3, 2, 1, 64, "e4m3", 544, [1, 2, 31, 32, 33, 64, 65, 127, 544], None, True),
+    (3, 2, 4, 2, 128, "int8", 544, [500, 2, 77], [2, 1, 0], True),
+    (3, 2, 4, 2, 128, "e4m3", 512, [512, 2, 77], [2, 1, 0], True),
+    (4, 2, 3, 3, 64, "int8", 512, [512, 0, 77, 300], None, False),
+    (70, 3, 1, 2, 128, "int8", 96, [(13 * b) % 97 for b in range(70)], None, True),
+    (103, 3, 1, 1, 64, "e4m3", 64, [(13 * b) % 65 for b in range(103)], None, True),
 ]
 
 
@@ -279,13 +286,14 @@ def test_offsets_past_32_bits(kv):
 
 # --------------------------------------------------------------------- step
 
-@pytest.mark.parametrize("kv,d,G,n", [("e4m3", 128, 1, 1), ("int8", 64, 4, 1), ("e4m3", 64, 3, 5), ("int8", 128, 8, 3)])
+@pytest.mark.parametrize("kv,d,G,n", [("e4m3", 128, 1, 1), ("int8", 64, 4, 1), ("e4m3", 64, 3, 5), ("int8", 128, 8, 3), ("int8", 128, 1, 8)])
 @pytest.mark.parametrize("layout", ["dense", "tokens"])
-def test_step_is_append_then_attend(kv, d, G, n, layout):
+@pytest.mark.parametrize("cap", [224, 544])
+def test_step_is_append_then_attend(kv, d, G, n, layout, cap):
     lens = [0, 1, 30, 32, 63, 200]
     counts = [n, max(n - 1, 0), n, 0, n, 1]
-    a, r, g = filled(51, 6, 2, d, 224, lens, G, n, kv)
-    z = H2OBlockCache(6, 2, d, 224, group=G, max_queries=n, kv=kv)
+    a, r, g = filled(51, 6, 2, d, cap, lens, G, n, kv)
+    z = H2OBlockCache(6, 2, d, cap, group=G, max_queries=n, kv=kv)
     for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
         getattr(z, name).copy_(getattr(a, name))
     q, k, v = rows(g, 6, 2 * G, n, d, layout), rows(g, 6, 2, n, d, layout), rows(g, 6, 2, n, d, layout)
