@@ -512,11 +512,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     while (issued < S && issued < count) issue();
 
   const int row0 = (blockIdx.y * MT + tile) * (8 * NR);  // the warp's rows of the head
-  const bool idle = row0 >= a.rows;
   const int nsc = c.cap / kBlock;
   Tile<F, D, NR, G::kQSmem> tl;
   int first_blk = 0;
-  bool open = false, lost = false;
+  bool open = false, busy = true, lost = false;
   float ks, vs;
   {
     const size_t sc = (size_t)(cur.b * c.H + cur.h) * nsc + cur.blk;
@@ -531,7 +530,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     if (!open) {  // a head begins
       open = true;
       first_blk = cur.blk;
-      tl.begin(a, cur.s, cur.b, cur.h, row0, qs);
+      if (MT > 1) busy = row0 < cur.s.cnt * c.group;  // else the warp has no row of this head
+      if (busy) tl.begin(a, cur.s, cur.b, cur.h, row0, qs);
     }
     const float ks_now = ks, vs_now = vs;
     const int blk = cur.blk, rest = cur.s.total - blk * kBlock;
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
       }
       issue();
     }
-    if (!idle)
+    if (busy)
       tl.block(kt, vt, ks_now, vs_now, blk, rest, qs, [&](int r, int j, float s0, float s1, float s2, float s3) {
         if (!a.accumulate) return;
         float *lg = c.logits + ((size_t)bh * c.max_rows + row0 + r) * c.cap + j;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     if (++st == S) st = 0, phase ^= 1;
     if (i + 1 < count && !last_blk) continue;
     open = false;
-    if (idle) continue;
+    if (!busy) continue;
     const bool whole = first_blk == 0 && last_blk;  // no other worker holds a part of this head
     const size_t slot = ((size_t)worker + bh) * c.max_rows;
 #pragma unroll
@@ -902,6 +902,29 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       continue;
     }
     const int j0 = it.j0 + warp % W * (128 * V) + lane * 4, rows = s.cnt * c.group;
+    constexpr int kRows = 8 / V;  // rows whose logits are on their way at once
+    const int j_last = max(0, s.total - 1) & ~3;
+    const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
+    float *sc = c.score + (size_t)bh * c.cap;
+    float4 w[V], old[V], v[kRows][V];
+    auto load = [&](int r0) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int y = 0; y < V; ++y)
+          v[i][y] = *(const float4 *)(lg + (size_t)min(r0 + i, rows - 1) * c.cap + min(j0 + y * 128, j_last));
+    };
+    auto first = [&]() {
+#pragma unroll
+      for (int y = 0; y < V; ++y) {
+        w[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        old[y] = *(const float4 *)(sc + min(j0 + y * 128, j_last));
+      }
+      if (V == 1) load(0);
+    };
+    // One four a lane (many rows): its first loads are on their way while the LSE is gathered (draft tokens 47 -> 39 us
+    // a step); four of them would not fit the registers beside that (long text 122 -> 128 us).
+    if (V == 1) first();
     // Eight rows to a warp, a lane of each group of eight for one; the four groups, and the warps that have the same
     // rows, take the parts in turn.
     const float2 *ml = a.ml + (size_t)bh * c.max_rows;
@@ -939,23 +962,9 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
     } else {
       __syncwarp();
     }
-    const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
-    float *sc = c.score + (size_t)bh * c.cap;
-    constexpr int kRows = 8 / V;  // rows whose logits are on their way at once
-    const int j_last = max(0, s.total - 1) & ~3;
-    float4 w[V], old[V];
-#pragma unroll
-    for (int y = 0; y < V; ++y) {
-      w[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-      old[y] = *(const float4 *)(sc + min(j0 + y * 128, j_last));
-    }
+    if (V > 1) first();
     for (int r0 = 0; r0 < rows; r0 += kRows) {
-      float4 v[kRows][V];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-#pragma unroll
-        for (int y = 0; y < V; ++y)
-          v[i][y] = *(const float4 *)(lg + (size_t)min(r0 + i, rows - 1) * c.cap + min(j0 + y * 128, j_last));
+      if (V > 1 || r0 > 0) load(r0);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         if (r0 + i >= rows) break;

@@ -47,7 +47,7 @@ struct Lens {
   int n, appends, cap;
 };
 struct Seq {
-  int len, cnt, total;  // entries before the call, real rows, entries to attend over
+  int len, cnt, total;  // entries before the call, real rows, entries to attend over (none without a query)
   bool ok;              // false: out of range, everything else 0
 };
 __device__ __forceinline__ Seq seq_of(const Lens &l, int b) {
@@ -56,7 +56,7 @@ __device__ __forceinline__ Seq seq_of(const Lens &l, int b) {
   s.cnt = l.counts ? l.counts[b] : l.n;
   s.ok = s.len >= 0 && s.cnt >= 0 && s.cnt <= l.n && s.len <= l.cap - (l.appends ? s.cnt : 0);
   if (!s.ok) s.len = s.cnt = 0;
-  s.total = s.len + (l.appends ? s.cnt : 0);
+  s.total = s.cnt == 0 ? 0 : s.len + (l.appends ? s.cnt : 0);
   return s;
 }
 
