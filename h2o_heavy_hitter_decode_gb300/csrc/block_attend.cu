@@ -184,22 +184,25 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
   return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-constexpr int kTeams = 4;  // workers of a CTA
-
 // A worker's rows: MT warps of NR tiles of 8 rows.  Up to 8 rows one warp has
 // one tile (D / 4 registers of O); more rows are tiles of 16, on up to four
-// warps that share the worker's ring.  8 to 16 warps and 128 to 192 KB of
-// ring to an SM; Q is in registers where a worker is one warp.
+// warps that share the worker's ring.  8 to 16 warps and 96 to 192 KB of ring
+// to an SM; Q is in registers where a worker is one warp.  At d = 128 twelve
+// warps of 168 registers, at d = 64 also sixteen of 128, measured faster than
+// the other: 32 heads of 16,384 entries, d = 128, 32 rows 64 / 80 us, 64 rows
+// 101 / 121 us; d = 64, 64 rows 62 / 60 us.
 template <int D, int NR, int MT> struct Cfg {
+  static constexpr int kTeams = MT == 2 ? 6 : MT == 4 && D == 128 ? 3 : 4;  // workers of a CTA, mostly of 12 warps in all
   static constexpr int kWarps = kTeams * MT;
-  static constexpr int kCtas = NR == 1 ? (D == 64 ? 4 : 3) : MT <= 2 ? 2 : 1;  // per SM
+  static constexpr int kCtas = NR == 1 ? (D == 64 ? 4 : 3) : MT == 1 ? 2 : 1;  // per SM
   static constexpr int kStage = 2 * kBlock * D;
   static constexpr bool kQSmem = MT > 1;
-  static constexpr int kStages = (NR == 2 && MT == 1 ? 98304 : kCtas == 4 ? 49152 : MT <= 2 ? 65536 : 131072) / (kTeams * kStage);
+  static constexpr int kRing = MT == 4 && D == 64 ? 131072 : MT > 1 ? 147456 : NR == 2 ? 98304 : kCtas == 4 ? 49152 : 65536;
+  static constexpr int kStages = kRing / (kTeams * kStage);
   static constexpr int kQBytes = kQSmem ? kWarps * NR * D * 16 : 0;
   static constexpr int kSmem = 1024 + kTeams * kStages * kStage + kQBytes + kTeams * kStages * 16;
 };
-constexpr int kMaxCtas = 4;
+constexpr int kMaxWorkers = 16;  // of an SM
 
 struct Args {
   View c;
@@ -461,8 +464,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
   const int team = warp / MT, tile = warp - team * MT;
   const int g = lane >> 2, t = lane & 3;
   uint8_t *ring = smem + team * S * G::kStage;
-  uint4 *qs = (uint4 *)(smem + kTeams * S * G::kStage) + (G::kQSmem ? warp * NR * (KS / 2) * 32 : 0);
-  uint64_t *full = (uint64_t *)(smem + kTeams * S * G::kStage + G::kQBytes) + team * 2 * S, *empty = full + S;
+  uint4 *qs = (uint4 *)(smem + G::kTeams * S * G::kStage) + (G::kQSmem ? warp * NR * (KS / 2) * 32 : 0);
+  uint64_t *full = (uint64_t *)(smem + G::kTeams * S * G::kStage + G::kQBytes) + team * 2 * S, *empty = full + S;
   const int worker = team * gridDim.x + blockIdx.x;  // few runs: one for each CTA first
 
   if (tile == 0 && lane == 0) {
@@ -1010,7 +1013,7 @@ template <typename F, int D, int NR, int MT>
 cudaError_t attend_t(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   using G = Cfg<D, NR, MT>;
   const int ctas = a.c.sms * G::kCtas;
-  a.workers = ctas * kTeams;
+  a.workers = ctas * G::kTeams;
   const dim3 grid(ctas, (a.rows + 8 * NR * MT - 1) / (8 * NR * MT));
   static SmemLimit limit;
   cudaError_t e = limit.raise((const void *)attend_kernel<F, D, NR, MT>, G::kSmem);
@@ -1082,7 +1085,7 @@ Args args_of(const View &c, const Lens &l, const Rows &q, int causal, int accumu
   return a;
 }
 
-size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxCtas * kTeams + (size_t)B * H; }
+size_t partial_slots(int B, int H, int sms) { return (size_t)sms * kMaxWorkers + (size_t)B * H; }
 
 }  // namespace
 
