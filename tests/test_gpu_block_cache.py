@@ -142,6 +142,11 @@ ATTEND = [  # B, H, G, n, d, kv, cap, lens, counts, causal
     (4, 2, 3, 3, 64, "int8", 512, [512, 0, 77, 300], None, False),
     (70, 3, 1, 2, 128, "int8", 96, [(13 * b) % 97 for b in range(70)], None, True),
     (103, 3, 1, 1, 64, "e4m3", 64, [(13 * b) % 65 for b in range(103)], None, True),
+    # 17 to 64 rows: two to four warps a worker, some without a row of the sequence
+    (3, 2, 8, 4, 128, "e4m3", 320, [300, 31, 129], [4, 1, 3], True),
+    (3, 2, 4, 6, 64, "int8", 320, [300, 31, 129], [6, 2, 0], False),
+    (3, 2, 3, 11, 128, "int8", 320, [300, 31, 129], [11, 1, 5], True),
+    (3, 2, 5, 12, 128, "e4m3", 320, [300, 31, 129], [12, 3, 7], True),
 ]
 
 
@@ -240,6 +245,30 @@ def test_attend_small_weights_next_to_a_large_one():
     want = (1 + (n - 1) * w * 100) / (1 + (n - 1) * w)
     # the tail's weights: f16 half steps 2^-11 (2^-12 for a power of two's neighbours) of their share; bf16 2^-8 of the sum
     assert abs(float(out[0, 0, 0, 5]) - want) <= 2.0 ** -8 * want + 2.0 ** -11 * want
+
+
+@pytest.mark.parametrize("H,G,n,cap,kv", [(20, 1, 1, 65536, "e4m3"), (48, 8, 2, 28672, "int8"), (10, 8, 5, 5120, "e4m3")])
+def test_attend_forms_of_the_finishing_launch(H, G, n, cap, kv):
+    """Few heads in many runs each, many rows over many entries, and many rows over few: some heads against the
+    reference."""
+    d, lens = 64, [cap - 77]
+    g = torch.Generator(DEV).manual_seed(45)
+    c = H2OBlockCache(1, H, d, cap, group=G, max_queries=n, kv=kv)
+    c.append(rows(g, 1, H, cap, d), rows(g, 1, H, cap, d), ints([0]), score=torch.rand(1, H, cap, generator=g, device=DEV))
+    refs = {}
+    for h in (0, H // 3, H - 1):
+        r = refs[h] = RefCache(1, 1, d, cap, G, kv)
+        for name in ("K", "V", "K_scale", "V_scale", "score"):
+            getattr(r, name).copy_(getattr(c, name)[:, h : h + 1].cpu().double())
+    q = rows(g, 1, H * G, n, d, scale=2.0)
+    lse = torch.zeros(1, H * G, n, device=DEV)
+    out = c.attend(q, ints(lens), lse=lse)
+    for h, r in refs.items():
+        want, want_lse, tol, lse_tol = r.attend(q[:, h * G : h * G + G], lens)
+        close(out[:, h * G : h * G + G], want, tol, f"out {h}")
+        close(lse[:, h * G : h * G + G], want_lse, lse_tol, f"lse {h}")
+        close(c.score[:, h : h + 1], r.score, r.score_tol, f"score {h}")
+    assert c.error_bits() == 0
 
 
 def test_attend_many_sequences():
@@ -502,11 +531,12 @@ def test_prefill_then_block_cache():
     same_state(c, r)
 
 
-def test_captured_step_reads_current_lengths():
+@pytest.mark.parametrize("cap", [128, 640])
+def test_captured_step_reads_current_lengths(cap):
     B, H, G, d = 3, 2, 2, 64
     lens = [10, 40, 63]
-    c, r, g = filled(97, B, H, d, 128, lens, G, 1, "int8")
-    z, _, _ = filled(97, B, H, d, 128, lens, G, 1, "int8")
+    c, r, g = filled(97, B, H, d, cap, lens, G, 1, "int8")
+    z, _, _ = filled(97, B, H, d, cap, lens, G, 1, "int8")
     L = ints(lens)
     q, k, v = rows(g, B, H * G, 1, d), rows(g, B, H, 1, d), rows(g, B, H, 1, d)
     out = torch.zeros(B, H * G, 1, d, dtype=torch.bfloat16, device=DEV)
@@ -535,9 +565,10 @@ def test_captured_step_reads_current_lengths():
         same_state(c, r)
 
 
-def test_other_stream():
+@pytest.mark.parametrize("cap", [512, 1024])
+def test_other_stream(cap):
     lens = [500, 77]
-    c, r, g = filled(101, 2, 2, 128, 512, lens, 2, 1, "e4m3")
+    c, r, g = filled(101, 2, 2, 128, cap, lens, 2, 1, "e4m3")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     q, k, v = rows(g, 2, 4, 1, 128), rows(g, 2, 2, 1, 128), rows(g, 2, 2, 1, 128)
