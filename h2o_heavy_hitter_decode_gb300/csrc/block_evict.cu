@@ -21,7 +21,7 @@
 // arrives at a round's barrier when it has read; it waits for that barrier
 // before it writes only where this round's sources begin inside the round's
 // own destination, else (once some entries are gone) for the round before.  A warp's item is a block of K or of V; the rows of its next
-// two items are on their way to shared memory (cp.async, each lane its own 16
+// items are on their way to shared memory (cp.async, each lane its own 16
 // bytes) while it works on one.  Every destination block gets a fresh scale
 // from the values it receives; rows whose scale it shares go over unchanged.
 #include <cooperative_groups.h>
@@ -117,8 +117,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-template <typename F, int D, int P, int W>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Args a) {
+template <typename F, int D, int P, int W, int NI>
+__global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Args a) {
   constexpr int kThreads = W * 32;
   constexpr int kDigits = 2048, kOwn = kDigits / kThreads;
   extern __shared__ __align__(16) uint32_t dyn[];  // the keys, then the warps' row buffers
@@ -352,71 +352,91 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
         }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     return x;
   };
-  const int stride = P * W;
-  int q = rank * W + warp;
-  const int s0 = source(q), s1 = source(q + stride);
-  int src2 = source(q + 2 * stride);
-  Entry x0 = fetch(q, 0, s0), x1 = fetch(q + stride, 1, s1);
+  // A round has NI items for each warp; the warp's two buffers hold one item of each of the next two rounds (NI = 1),
+  // or both items, K and V of a block, of the next round.
+  constexpr int kAhead = 2 / NI;
+  const int stride = P * W * NI;
+  int q = (rank * W + warp) * NI;
+  Entry next[kAhead][NI];
+  auto fetch_round = [&](Entry (&x)[NI], int q, int slot, int src) {
+#pragma unroll
+    for (int u = 0; u < NI; ++u) x[u] = fetch(q + u, slot + u, src);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch_round(next[i], q + i * stride, i, source(q + i * stride));
+  int src = source(q + kAhead * stride);
   // Where the round's first entry comes from; its destination ends 16 * stride entries behind 16 * round.
   auto first_source = [&](int round) {
     const int i = round * (kBlock / 2);
     return i >= k ? len : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
   };
   int from = first_source(0);
-  for (int round = 0, slot = 0; round < items; round += stride, q += stride, slot ^= 1) {
+  for (int round = 0, slot = 0; round < items; round += stride, q += stride, slot ^= kAhead - 1) {
     const bool inside = from < (round + stride) * (kBlock / 2);
     from = first_source(round + stride);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");  // this item; each lane reads back what it copied
-    uint4 w[IT];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");  // each lane reads back what it copied
+    uint4 w[NI][IT];
+    float scale_own[NI], to[NI];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) w[i] = held[slot * (kItem / 16) + i * 32];
-    const float scale_own = __shfl_sync(0xffffffffu, x0.scale, lane);  // the loads have come back
-    const int pos_own = __shfl_sync(0xffffffffu, x0.pos, lane);
-    const float score_own = __shfl_sync(0xffffffffu, x0.score, lane);
+    for (int u = 0; u < NI; ++u) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) w[u][i] = held[(slot + u) * (kItem / 16) + i * 32];
+      scale_own[u] = __shfl_sync(0xffffffffu, next[0][u].scale, lane);  // the loads have come back
+    }
+    const int pos_own = __shfl_sync(0xffffffffu, next[0][0].pos, lane);
+    const float score_own = __shfl_sync(0xffffffffu, next[0][0].score, lane);
     rounds.wait();  // everyone has read the round before
     rounds.arrive(lane);
-    x0 = x1;
-    x1 = fetch(q + 2 * stride, slot, src2);
-    src2 = source(q + 3 * stride);
+    if constexpr (kAhead == 2) next[0][0] = next[1][0];
+    fetch_round(next[kAhead - 1], q + kAhead * stride, slot, src);
+    src = source(q + (kAhead + 1) * stride);
     const bool work = q < items;
     const int base = (q >> 1) * kBlock;
-    float to = 0.f;
     if (work) {
-      float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        TopCode<F> top;
-        top.add(w[i].x), top.add(w[i].y), top.add(w[i].z), top.add(w[i].w);
-        amax = fmaxf(amax, top.value() * __shfl_sync(0xffffffffu, scale_own, i * RPI + row0));
-      }
-      to = block_scale<F>(warp_max(amax));
-      // Times 2^(exponent of its scale - the new one's).  More than 15 is rare (small codes of a far larger scale) and
-      // takes two steps, the first of them exact; more than 30 is a row of zeros.
-      int left = min(exponent(scale_own) - exponent(to), 30);
-      while (__any_sync(0xffffffffu, left != 0)) {
-        const int step = min(left, 15);
-        left = max(left - 15, 0);
+      for (int u = 0; u < NI; ++u) {
+        float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-          const int e = __shfl_sync(0xffffffffu, step, i * RPI + row0);
-          if (e == 0) continue;
-          const typename F::Shift by(e);
-          w[i] = make_uint4(by.run(w[i].x), by.run(w[i].y), by.run(w[i].z), by.run(w[i].w));
+          TopCode<F> top;
+          top.add(w[u][i].x), top.add(w[u][i].y), top.add(w[u][i].z), top.add(w[u][i].w);
+          amax = fmaxf(amax, top.value() * __shfl_sync(0xffffffffu, scale_own[u], i * RPI + row0));
+        }
+        to[u] = block_scale<F>(warp_max(amax));
+      }
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        // Times 2^(exponent of its scale - the new one's).  More than 15 is rare (small codes of a far larger scale)
+        // and takes two steps, the first of them exact; more than 30 is a row of zeros.
+        int left = min(exponent(scale_own[u]) - exponent(to[u]), 30);
+        while (__any_sync(0xffffffffu, left != 0)) {
+          const int step = min(left, 15);
+          left = max(left - 15, 0);
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const int e = __shfl_sync(0xffffffffu, step, i * RPI + row0);
+            if (e == 0) continue;
+            const typename F::Shift by(e);
+            w[u][i] = make_uint4(by.run(w[u][i].x), by.run(w[u][i].y), by.run(w[u][i].z), by.run(w[u][i].w));
+          }
         }
       }
     }
     if (inside) rounds.wait();  // this round's sources lie in what it writes: everyone has to have read them
     if (work) {
-      const bool is_v = q & 1;
-      uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
 #pragma unroll
-      for (int i = 0; i < IT; ++i)
-        if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[i];
-      if (lane == 0) ((is_v ? c.Vsc : c.Ksc) + scales)[q >> 1] = to;
-      if (!is_v && base + lane < k) {
+      for (int u = 0; u < NI; ++u) {
+        const bool is_v = (q + u) & 1;
+        uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+          if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[u][i];
+        if (lane == 0) ((is_v ? c.Vsc : c.Ksc) + scales)[q >> 1] = to[u];
+      }
+      if (!(q & 1) && base + lane < k) {
         pos[base + lane] = pos_own;
         score[base + lane] = score_own;
       }
@@ -427,14 +447,14 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 3 : 1) evict_kernel(const Arg
   if (!rounds.ok && lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
 }
 
-template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStream_t st) {
+template <typename F, int D, int P, int W, int NI> cudaError_t evict_p(Args a, cudaStream_t st) {
   constexpr int kRing = W * 2 * kBlock * D;
   const int share = ((a.c.cap + P - 1) / P + 3) & ~3, most = 110 * 1024 / 4;  // keys: two CTAs still fit an SM
   const int keys = share < most ? share : most;
   const int smem = keys * 4 > kRing ? keys * 4 : kRing;
   a.held = smem / 4;
   static SmemLimit limit;
-  const void *kernel = (const void *)evict_kernel<F, D, P, W>;
+  const void *kernel = (const void *)evict_kernel<F, D, P, W, NI>;
   cudaError_t e = limit.raise(kernel, smem);
   if (e == cudaSuccess && P > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -448,20 +468,22 @@ template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStrea
   at.val.clusterDim = {(unsigned)P, 1, 1};
   cfg.attrs = &at;
   cfg.numAttrs = P > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W>, a);
+  return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W, NI>, a);
 }
 
 template <typename F, int D> cudaError_t evict_t(const Args &a, cudaStream_t st) {
   // Up to 16 CTAs share a head while the clusters all fit the device (two CTAs an SM; of 16, whose CTAs have to find
   // room in one GPC, 14 clusters fit) and each has a thousand entries.  8 heads of 131,072 entries: 58 us with 16, 76
-  // with 8, 150 with 4.
+  // with 8, 150 with 4, all with one item a round.  Large clusters then take both items of a block a round: half the
+  // barriers and two independent chains a warp, 53 us; a CTA of its own would lose a third of its warps to the
+  // registers that takes.
   const int heads = a.c.B * a.c.H;
   auto shared = [&](int p) { return heads * p <= a.c.sms * 15 / 8 && a.c.cap / p >= 1024; };
-  if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8>(a, st);
-  if (shared(8)) return evict_p<F, D, 8, 8>(a, st);
-  if (shared(4)) return evict_p<F, D, 4, 8>(a, st);
-  if (shared(2)) return evict_p<F, D, 2, 8>(a, st);
-  return evict_p<F, D, 1, 8>(a, st);
+  if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8, 2>(a, st);
+  if (shared(8)) return evict_p<F, D, 8, 8, 2>(a, st);
+  if (shared(4)) return evict_p<F, D, 4, 8, 1>(a, st);
+  if (shared(2)) return evict_p<F, D, 2, 8, 1>(a, st);
+  return evict_p<F, D, 1, 8, 1>(a, st);
 }
 
 }  // namespace
