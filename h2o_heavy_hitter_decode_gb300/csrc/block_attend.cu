@@ -35,6 +35,14 @@
 // finish_kernel: joins the partials of a row to O and LSE, and turns the
 // logits that the first kernel left in scratch memory into weights: 4 bytes
 // written and read per row and entry, instead of K read again.
+//
+// head_kernel: few and short heads, a CTA each, in one launch.
+//
+// Bound by memory up to about 16 rows: 8 heads of 262,000 entries, 537 MB of
+// codes, 86 us without scores, 92 % of the copy rate; with the logits of 8 rows
+// 107 us, and 17 us of the finishing launch.  Above, by the products'
+// instructions: 32 heads of 16,384 entries, d = 128, 256 rows 379 us, 181
+// TFLOP/s.
 #include <cuda.h>
 
 #include "block_cache.cuh"
