@@ -21,15 +21,15 @@
 // arrives at a round's barrier when it has read; it waits for that barrier
 // before it writes only where this round's sources begin inside the round's
 // own destination, else (once some entries are gone) for the round before.  A
-// warp's item is a block of K or of V; the rows of its next items are on their
-// way to shared memory (cp.async, each lane its own 16 bytes) while it works on
-// one.  Every destination block gets a fresh scale from the values it receives;
-// rows whose scale it shares go over unchanged.
+// warp's items of a round are a block's K and V; those of its next block are on
+// their way to shared memory (cp.async, each lane its own 16 bytes) meanwhile.
+// Every destination block gets a fresh scale from the values it receives; rows
+// whose scale it shares go over unchanged.
 //
-// Bound by memory in the move (1024 heads, 8,448 -> 1,690 entries: 155 us, 85 %
-// of the copy rate) and by the first digit's atomics in the selection (45 us);
-// on few heads by latency (8 heads, 131,072 -> 26,214: 53 us, of it 22 us
-// selection).
+// Bound by memory in the move (1024 heads, 8,448 -> 1,690 entries: 142 us, 92 %
+// of the copy rate) and by the first digit's atomics in the selection (60 us
+// alone, part of it under other heads' moves: 185 us in all); on few heads by
+// latency (8 heads, 131,072 -> 26,214: 53 us, of it 22 us selection).
 #include <cooperative_groups.h>
 
 #include "block_cache.cuh"
@@ -123,8 +123,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-template <typename F, int D, int P, int W, int NI>
-__global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Args a) {
+template <typename F, int D, int P, int W>
+__global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
   constexpr int kThreads = W * 32;
   constexpr int kDigits = 2048, kOwn = kDigits / kThreads;
   extern __shared__ __align__(16) uint32_t dyn[];  // the keys, then the warps' row buffers
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Ar
     const int i = (q >> 1) * kBlock + lane;
     return q >= items || i >= k ? 0 : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
   };
-  auto fetch = [&](int q, int slot, int src) {  // an item's rows into one of the warp's two buffers
+  auto fetch = [&](int q, int slot, int src) {  // an item's rows into its buffer
     Entry x{0, 0.f, 0.f};
     if (q < items) {
       const bool is_v = q & 1;
@@ -360,50 +360,47 @@ __global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Ar
     }
     return x;
   };
-  // A round has NI items for each warp; the warp's two buffers hold one item of each of the next two rounds (NI = 1),
-  // or both items, K and V of a block, of the next round.
-  constexpr int kAhead = 2 / NI;
-  const int stride = P * W * NI;
-  int q = (rank * W + warp) * NI;
-  Entry next[kAhead][NI];
-  auto fetch_round = [&](Entry (&x)[NI], int q, int slot, int src) {
+  // A round has two items, K and V of a block, for each warp: two independent chains of work, and half the barriers of
+  // one (1024 heads 189 -> 185 us, 8 long ones 60 -> 53 us).  The next round's are on their way meanwhile.
+  const int stride = P * W * 2;
+  int q = (rank * W + warp) * 2;
+  Entry next[2];
+  auto fetch_round = [&](int q, int src) {
 #pragma unroll
-    for (int u = 0; u < NI; ++u) x[u] = fetch(q + u, slot + u, src);
+    for (int u = 0; u < 2; ++u) next[u] = fetch(q + u, u, src);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch_round(next[i], q + i * stride, i, source(q + i * stride));
-  int src = source(q + kAhead * stride);
+  fetch_round(q, source(q));
+  int src = source(q + stride);
   // Where the round's first entry comes from; its destination ends 16 * stride entries behind 16 * round.
   auto first_source = [&](int round) {
     const int i = round * (kBlock / 2);
     return i >= k ? len : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
   };
   int from = first_source(0);
-  for (int round = 0, slot = 0; round < items; round += stride, q += stride, slot ^= kAhead - 1) {
+  for (int round = 0; round < items; round += stride, q += stride) {
     const bool inside = from < (round + stride) * (kBlock / 2);
     from = first_source(round + stride);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");  // each lane reads back what it copied
-    uint4 w[NI][IT];
-    float scale_own[NI], to[NI];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // each lane reads back what it copied
+    uint4 w[2][IT];
+    float scale_own[2], to[2];
 #pragma unroll
-    for (int u = 0; u < NI; ++u) {
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int i = 0; i < IT; ++i) w[u][i] = held[(slot + u) * (kItem / 16) + i * 32];
-      scale_own[u] = __shfl_sync(0xffffffffu, next[0][u].scale, lane);  // the loads have come back
+      for (int i = 0; i < IT; ++i) w[u][i] = held[u * (kItem / 16) + i * 32];
+      scale_own[u] = __shfl_sync(0xffffffffu, next[u].scale, lane);  // the loads have come back
     }
-    const int pos_own = __shfl_sync(0xffffffffu, next[0][0].pos, lane);
-    const float score_own = __shfl_sync(0xffffffffu, next[0][0].score, lane);
+    const int pos_own = __shfl_sync(0xffffffffu, next[0].pos, lane);
+    const float score_own = __shfl_sync(0xffffffffu, next[0].score, lane);
     rounds.wait();  // everyone has read the round before
     rounds.arrive(lane);
-    if constexpr (kAhead == 2) next[0][0] = next[1][0];
-    fetch_round(next[kAhead - 1], q + kAhead * stride, slot, src);
-    src = source(q + (kAhead + 1) * stride);
+    fetch_round(q + stride, src);
+    src = source(q + 2 * stride);
     const bool work = q < items;
     const int base = (q >> 1) * kBlock;
     if (work) {
 #pragma unroll
-      for (int u = 0; u < NI; ++u) {
+      for (int u = 0; u < 2; ++u) {
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -414,7 +411,7 @@ __global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Ar
         to[u] = block_scale<F>(warp_max(amax));
       }
 #pragma unroll
-      for (int u = 0; u < NI; ++u) {
+      for (int u = 0; u < 2; ++u) {
         // Times 2^(exponent of its scale - the new one's).  More than 15 is rare (small codes of a far larger scale)
         // and takes two steps, the first of them exact; more than 30 is a row of zeros.
         int left = min(exponent(scale_own[u]) - exponent(to[u]), 30);
@@ -434,15 +431,15 @@ __global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Ar
     if (inside) rounds.wait();  // this round's sources lie in what it writes: everyone has to have read them
     if (work) {
 #pragma unroll
-      for (int u = 0; u < NI; ++u) {
-        const bool is_v = (q + u) & 1;
+      for (int u = 0; u < 2; ++u) {
+        const bool is_v = u;
         uint8_t *codes = (is_v ? c.V : c.K) + ((size_t)bh * c.cap + base) * D + sub * 16;
 #pragma unroll
         for (int i = 0; i < IT; ++i)
           if (base + i * RPI + row0 < k) *(uint4 *)(codes + (size_t)(i * RPI + row0) * D) = w[u][i];
         if (lane == 0) ((is_v ? c.Vsc : c.Ksc) + scales)[q >> 1] = to[u];
       }
-      if (!(q & 1) && base + lane < k) {
+      if (base + lane < k) {
         pos[base + lane] = pos_own;
         score[base + lane] = score_own;
       }
@@ -453,14 +450,14 @@ __global__ void __launch_bounds__(W * 32, NI == 1 ? 3 : 2) evict_kernel(const Ar
   if (!rounds.ok && lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
 }
 
-template <typename F, int D, int P, int W, int NI> cudaError_t evict_p(Args a, cudaStream_t st) {
+template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStream_t st) {
   constexpr int kRing = W * 2 * kBlock * D;
   const int share = ((a.c.cap + P - 1) / P + 3) & ~3, most = 110 * 1024 / 4;  // keys: two CTAs still fit an SM
   const int keys = share < most ? share : most;
   const int smem = keys * 4 > kRing ? keys * 4 : kRing;
   a.held = smem / 4;
   static SmemLimit limit;
-  const void *kernel = (const void *)evict_kernel<F, D, P, W, NI>;
+  const void *kernel = (const void *)evict_kernel<F, D, P, W>;
   cudaError_t e = limit.raise(kernel, smem);
   if (e == cudaSuccess && P > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -474,22 +471,20 @@ template <typename F, int D, int P, int W, int NI> cudaError_t evict_p(Args a, c
   at.val.clusterDim = {(unsigned)P, 1, 1};
   cfg.attrs = &at;
   cfg.numAttrs = P > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W, NI>, a);
+  return cudaLaunchKernelEx(&cfg, evict_kernel<F, D, P, W>, a);
 }
 
 template <typename F, int D> cudaError_t evict_t(const Args &a, cudaStream_t st) {
   // Up to 16 CTAs share a head while the clusters all fit the device (two CTAs an SM; of 16, whose CTAs have to find
   // room in one GPC, 14 clusters fit) and each has a thousand entries.  8 heads of 131,072 entries: 58 us with 16, 76
-  // with 8, 150 with 4, all with one item a round.  Large clusters then take both items of a block a round: half the
-  // barriers and two independent chains a warp, 53 us; a CTA of its own would lose a third of its warps to the
-  // registers that takes.
+  // with 8, 150 with 4 (with rounds of one item a warp; 53 with 16 now).
   const int heads = a.c.B * a.c.H;
   auto shared = [&](int p) { return heads * p <= a.c.sms * 15 / 8 && a.c.cap / p >= 1024; };
-  if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8, 2>(a, st);
-  if (shared(8)) return evict_p<F, D, 8, 8, 2>(a, st);
-  if (shared(4)) return evict_p<F, D, 4, 8, 1>(a, st);
-  if (shared(2)) return evict_p<F, D, 2, 8, 1>(a, st);
-  return evict_p<F, D, 1, 8, 1>(a, st);
+  if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8>(a, st);
+  if (shared(8)) return evict_p<F, D, 8, 8>(a, st);
+  if (shared(4)) return evict_p<F, D, 4, 8>(a, st);
+  if (shared(2)) return evict_p<F, D, 2, 8>(a, st);
+  return evict_p<F, D, 1, 8>(a, st);
 }
 
 }  // namespace
