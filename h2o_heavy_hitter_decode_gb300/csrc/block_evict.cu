@@ -28,7 +28,7 @@
 //
 // Bound by memory in the move (1024 heads, 8,448 -> 1,690 entries: 142 us, 92 %
 // of the copy rate) and by the first digit's atomics in the selection (60 us
-// alone, part of it under other heads' moves: 185 us in all); on few heads by
+// alone, part of it under other heads' moves: 173 to 185 us in all); on few heads by
 // latency (8 heads, 131,072 -> 26,214: 53 us, of it 22 us selection).
 #include <cooperative_groups.h>
 
