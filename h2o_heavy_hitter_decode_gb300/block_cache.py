@@ -200,9 +200,10 @@ class H2OBlockCache:
         with ``score_mode`` 1 by score / (position - pos)); entries at positions
         below ``n_sink`` rank first.  Returns the new lengths (int32 [B]).  See
         h2o_bcache_evict."""
+        lens = self._lengths(lengths, "lengths")
         if new_lengths is None:
-            new_lengths = torch.empty(self.B, dtype=torch.int32, device=self.device)
-        args = (self._lengths(lengths, "lengths"), int(k_heavy), int(k_local), int(n_sink), int(score_mode),
+            new_lengths = torch.empty_like(lengths)
+        args = (lens, int(k_heavy), int(k_local), int(n_sink), int(score_mode),
                 self._dense(position, I32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
         self._use_stream()
         _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")

@@ -582,6 +582,40 @@ def test_other_stream(cap):
     same_state(c, r)
 
 
+def test_two_caches_on_two_streams():
+    """Calls of different caches may overlap on the GPU: steps, attention with many rows and evictions of two caches on
+    two streams at once give the bits that they give one after the other."""
+    def script(c, g, lens, q1, k, v, q8, outs):
+        L = ints(lens)
+        for i in range(6):
+            outs.append(c.step(q1, k, v, L).clone())
+            L = L + 1
+            outs.append(c.attend(q8, L).clone())
+            L = c.evict(L, 700 - 40 * i, 300)
+        outs += [L] + [getattr(c, n).clone() for n in ("K", "V", "K_scale", "V_scale", "pos", "score")]
+
+    def setup(seed, kv):
+        lens = [2000, 1500, 900, 33]
+        c, _, g = filled(seed, 4, 6, 128, 2048, lens, 4, 8, kv, junk=False)
+        return c, g, lens, rows(g, 4, 24, 1, 128), rows(g, 4, 6, 1, 128), rows(g, 4, 6, 1, 128), rows(g, 4, 24, 8, 128)
+
+    want = []
+    for seed, kv in ((131, "e4m3"), (137, "int8")):
+        want.append([])
+        script(*setup(seed, kv), want[-1])
+    got, streams = [[], []], [torch.cuda.Stream(), torch.cuda.Stream()]
+    both = [setup(131, "e4m3"), setup(137, "int8")]
+    torch.cuda.synchronize()
+    for s, args, outs in zip(streams, both, got):
+        with torch.cuda.stream(s):
+            script(*args, outs)
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert len(w) == len(o)
+        for x, y in zip(w, o):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_same_call_twice_gives_the_same_bits():
     lens = [3000, 1234, 17]
     outs = []
