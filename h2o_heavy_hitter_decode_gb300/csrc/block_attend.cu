@@ -27,7 +27,7 @@
 // scratch memory; the runs' and heads' boundaries form a staircase, so
 // (worker + head) numbers the partials without gaps or collisions.
 //
-// Why mma.sync and not tcgen05: a decode step has 1 to 64 rows per cached
+// Why mma.sync and not tcgen05: a decode step has 1 to 16 rows per cached
 // head, so the step is bound by the codes' bytes (2 d per entry), and the
 // codes have to pass through registers anyway to become f16; tcgen05 would
 // read them back from shared memory, 4 more bytes of its traffic per code.
