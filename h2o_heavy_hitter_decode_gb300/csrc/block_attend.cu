@@ -218,11 +218,30 @@ struct Args {
   Rows q, out;
   float *lse;
   float2 *ml;  // [workers + B*H][max_rows]  partial reference and sum
-  float *po;   // [workers + B*H][max_rows][d]  partial output
+  float *po;   // [workers + B*H][max_rows][d]  partial output, normalised, times kPartDown
   int causal, accumulate, workers;
   int rows;  // n * group: rows of a head in this call
   int streams;  // the codes pass through L2 once: they make way first
 };
+
+// Output sums are held in a unit 2^E of the warp's: bf16 values reach 2^128
+// and weights before their division by the sum 2^15, so that plain fp32 sums
+// would pass its range (|v| from 2^121 on with one entry, 2^103 with 262,144
+// of one sign).  A block whose scale is above 2^kUnitMost units sets the unit
+// anew, so that its scale is 2^kUnitSet of them: sums stay below 2^15 (weight)
+// * 2^9 (code) * 2^70 * 2^30 (entries) = 2^124, and those of blocks whose scale
+// is 2^180 times smaller are normal numbers still.
+constexpr float kUnitMost = 0x1p70f, kUnitSet = 0x1p60f, kUnitFirst = 0x1p100f;
+// Partial outputs are weighted means (their sums of weights go along): four
+// times smaller, since a code times its scale may round up to 2^128.
+constexpr float kPartDown = 0.25f, kPartUp = 4.f;
+// 1 / x of a sum of weights (0, NaN, or 1 and more: a row's largest weight is at least its reference's), 0 of 0.  Off by
+// 2^-23 at most, once a partial and once each time partials meet.
+__device__ __forceinline__ float inverse_sum(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return x == 0.f ? 0.f : y;
+}
 
 // What a warp holds of a head while it attends: Q, and for its NR tiles of 8
 // rows the output, the reference and the sum of the weights so far.
@@ -235,12 +254,14 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
   int end[NR][2];
   uint32_t qr[QSmem ? 1 : NR][KS][2];
   int min_end, live;  // live: bit 2 n + u, the row exists
+  float vunit;        // 2^-E: units of o in a value of 1
 
   // Rows row0 .. of head h of sequence b; qs: this warp's share of shared memory for Q.
   __device__ __forceinline__ void begin(const Args &a, const Seq &s, int b, int h, int row0, uint4 *qs) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     min_end = a.causal ? s.total - s.cnt + 1 : s.total;
     live = 0;
+    vunit = kUnitFirst;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
@@ -406,6 +427,15 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
       fence_proxy_async_smem();
       __syncwarp();
     }
+    if (vs * vunit > kUnitMost) {  // rare: the first block, and one of a far larger scale than those before
+      const float unit = inverse_pow2(vs) * kUnitSet, f = unit * inverse_pow2(vunit);
+      vunit = unit;
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int j = 0; j < OT; ++j) o[n][j][0] *= f, o[n][j][1] *= f, o[n][j][2] *= f, o[n][j][3] *= f;
+    }
+    vs *= vunit;
     // O += vs (P V): a fresh product per block, added in fp32 under the block's scale
     constexpr int VW = D == 128 && NR == 1 ? 4 : 2;  // words of the lane's D/8 dimensions of an entry at a time
 #pragma unroll
@@ -449,6 +479,8 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
     }
   }
 
+  // What a sum of o is as a value.
+  __device__ __forceinline__ float unit() const { return inverse_pow2(vunit); }
   // Sum of the lane's row over the warp.
   __device__ __forceinline__ float sum(int n, int u) const {
     float l = lsum[n][u];
@@ -585,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
     if (!busy) continue;
     const bool whole = first_blk == 0 && last_blk;  // no other worker holds a part of this head
     const size_t slot = ((size_t)worker + bh) * c.max_rows;
+    const float back = tl.unit(), part = back * kPartDown;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -602,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
           uint32_t w[OT];
 #pragma unroll
           for (int j = 0; j < OT; ++j) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(tl.o[n][j][u] * inv, tl.o[n][j][2 + u] * inv);
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(tl.o[n][j][u] * inv * back, tl.o[n][j][2 + u] * inv * back);
             w[j] = *(const uint32_t *)&b2;
           }
 #pragma unroll
@@ -610,10 +643,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
           if (a.lse && g == 0)
             a.lse[((size_t)ab * c.H * c.group + hq) * a.l.n + tok] = any ? (tl.m[n][u] + log2f(l)) * kLn2 : -INFINITY;
         } else {
+          const float inv = inverse_sum(l);
           float *dst = a.po + (slot + r) * D + g * (D / 8);
 #pragma unroll
           for (int j = 0; j < OT; j += 2)
-            *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u], tl.o[n][j][2 + u], tl.o[n][j + 1][u], tl.o[n][j + 1][2 + u]);
+            *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u] * inv * part, tl.o[n][j][2 + u] * inv * part,
+                                                   tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
         }
       }
   }
@@ -715,15 +750,18 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
   }
   __syncthreads();  // every warp is done with its ring: the partial outputs go there
   float *po = (float *)smem;  // [W][8][D]
+  const float part = tl.unit() * kPartDown;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float l = tl.sum(0, u);
     const int r = 2 * t + u;
     if (g == 0) part_ml[warp][r] = make_float2(tl.m[0][u], l);
+    const float inv = inverse_sum(l);
     float *dst = po + (warp * 8 + r) * D + g * (D / 8);
 #pragma unroll
     for (int j = 0; j < OT; j += 2)
-      *(float4 *)(dst + 2 * j) = make_float4(tl.o[0][j][u], tl.o[0][j][2 + u], tl.o[0][j + 1][u], tl.o[0][j + 1][2 + u]);
+      *(float4 *)(dst + 2 * j) = make_float4(tl.o[0][j][u] * inv * part, tl.o[0][j][2 + u] * inv * part,
+                                             tl.o[0][j + 1][u] * inv * part, tl.o[0][j + 1][2 + u] * inv * part);
   }
   __syncthreads();
   const int rows = s.cnt * c.group;
@@ -733,17 +771,23 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) m = fmaxf(m, part_ml[w][r].x);
+    float z[W];  // the parts' sums of weights, under the row's maximum
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float2 p = part_ml[w][r];
-      const float z = p.x == -INFINITY ? 0.f : ex2(p.x - m);
-      l += p.x == -INFINITY ? p.y : p.y * z;
-      const float4 e = *(const float4 *)(po + (w * 8 + r) * D + d0);
-      o.x = fmaf(e.x, z, o.x), o.y = fmaf(e.y, z, o.y), o.z = fmaf(e.z, z, o.z), o.w = fmaf(e.w, z, o.w);
+      z[w] = p.x == -INFINITY ? p.y : p.y * ex2(p.x - m);
+      l += z[w];
     }
     const bool any = l > 0.f || l != l;
     const float inv = any ? 1.f / l : 0.f;
-    const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float4 e = *(const float4 *)(po + (w * 8 + r) * D + d0);
+      const float x = z[w] * inv;
+      o.x = fmaf(e.x, x, o.x), o.y = fmaf(e.y, x, o.y), o.z = fmaf(e.z, x, o.z), o.w = fmaf(e.w, x, o.w);
+    }
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * kPartUp, o.y * kPartUp),
+                         p1 = __floats2bfloat162_rn(o.z * kPartUp, o.w * kPartUp);
     *(uint2 *)(const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0) =
         make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
     if (d0 == 0) {
@@ -853,7 +897,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       if (w0 == w1) continue;  // written by its worker
       const float2 *ml = a.ml + (size_t)bh * c.max_rows + r;
       const float *po = a.po + ((size_t)bh * c.max_rows + r) * D + d0;
-      // Each group weighs its partials by its own maximum, then the groups meet.
+      // Each group weighs its partials by its own maximum, then the groups meet; o is the weighted mean so far.
       constexpr int kBatch = Deep ? 8 : 4;  // partials on their way at once
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -872,19 +916,28 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
           if (wb + i * kGroups > w1) p[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           mn = fmaxf(mn, p[i].x);
         }
-        const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        const float own = m == -INFINITY ? l : l * ex2(m - mn);
         m = mn;
+        l = own;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const float z = p[i].x == -INFINITY ? 0.f : ex2(p[i].x - m);
-          l += p[i].x == -INFINITY ? p[i].y : p[i].y * z;
+          if (p[i].x != -INFINITY) p[i].y *= ex2(p[i].x - m);
+          l += p[i].y;
+        }
+        const float inv = inverse_sum(l), f = own * inv;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float z = p[i].y * inv;
           o.x = fmaf(v[i].x, z, o.x), o.y = fmaf(v[i].y, z, o.y), o.z = fmaf(v[i].z, z, o.z), o.w = fmaf(v[i].w, z, o.w);
         }
       }
       auto meet = [&](float om, float ol, float4 oo) {
-        const float mn = fmaxf(m, om), f = m == -INFINITY ? 0.f : ex2(m - mn), z = om == -INFINITY ? 0.f : ex2(om - mn);
-        l = (m == -INFINITY ? l : l * f) + (om == -INFINITY ? ol : ol * z);
+        const float mn = fmaxf(m, om);
+        float f = m == -INFINITY ? l : l * ex2(m - mn), z = om == -INFINITY ? ol : ol * ex2(om - mn);
+        l = f + z;
+        const float inv = inverse_sum(l);
+        f *= inv, z *= inv;
         o.x = o.x * f + oo.x * z, o.y = o.y * f + oo.y * z, o.z = o.z * f + oo.z * z, o.w = o.w * f + oo.w * z;
         m = mn;
       };
@@ -904,9 +957,9 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
         __syncthreads();
       }
       const bool any = l > 0.f || l != l;
-      const float inv = any ? 1.f / l : 0.f;
       if (writes) {
-        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), p1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * kPartUp, o.y * kPartUp),
+                             p1 = __floats2bfloat162_rn(o.z * kPartUp, o.w * kPartUp);
         *(uint2 *)dst = make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
         if (lse && lane == 0) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }

@@ -214,6 +214,67 @@ def test_attend_query_sizes(size):
     assert abs(float((c.score[:, :, :100].double().cpu().sum() - r.score[:, :, :100].sum()))) <= 1e-3
 
 
+LARGE = [  # B, H, G, n, d, kv, cap, longest: a CTA a head, parts of heads joined, whole heads, many rows
+    (1, 2, 1, 1, 128, "e4m3", 64, 50),
+    (2, 2, 4, 2, 64, "int8", 512, 512),
+    (3, 2, 2, 1, 128, "int8", 1024, 1000),
+    (40, 8, 1, 1, 64, "e4m3", 544, 540),
+    (8, 4, 2, 8, 128, "e4m3", 544, 540),
+    (700, 4, 1, 1, 64, "e4m3", 64, 64),
+    (3, 2, 8, 4, 128, "e4m3", 320, 300),
+    (1, 1, 16, 16, 128, "int8", 96, 70),
+    (1, 1, 1, 1, 64, "int8", 65536, 65500),
+]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=str)
+def test_attend_large_values(case):
+    """Values up to 2^126, all of one sign: the sums before the division by the weights' sum lie beyond fp32, the
+    outputs do not."""
+    B, H, G, n, d, kv, cap, longest = case
+    lens = [max(1, longest - 37 * b % longest) for b in range(B)]
+    c, r, g = filled(139, B, H, d, cap, lens, G, n, kv, junk=False)
+    if kv == "e4m3":
+        c.V.view(torch.uint8).bitwise_and_(0x7F)
+    else:
+        c.V.abs_()
+    c.V_scale.mul_(2.0 ** 123)
+    load(r, c)
+    q = rows(g, B, H * G, n, d)
+    lse = torch.zeros(B, H * G, n, device=DEV)
+    out = c.attend(q, ints(lens), lse=lse)
+    assert torch.isfinite(out).all()
+    want, want_lse, tol, lse_tol = r.attend(q, lens)
+    close(out, want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    same_state(c, r)
+    out2 = c.attend(-q, ints(lens), accumulate=False)
+    want, _, tol, _ = r.attend(-q, lens, accumulate=False)
+    close(out2, want, tol, "out")
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("cap,d", [(256, 64), (8192, 128)])
+@pytest.mark.parametrize("low,high", [(2.0 ** -100, 2.0 ** 60), (2.0 ** -60, 2.0 ** 117), (2.0 ** -3, 2.0 ** 117)])
+def test_attend_large_values_without_weight(kv, cap, d, low, high):
+    """Blocks of values up to 2^177 times larger, before and after the one whose first entry takes all the weight: the
+    others' weights are below 2^-280, so that 2^13 entries of at most 2^126 add less than 2^-140 to its row."""
+    g = torch.Generator(DEV).manual_seed(149)
+    c = H2OBlockCache(1, 2, d, cap, kv=kv)
+    K = torch.zeros(1, 2, cap, d, device=DEV)
+    at = cap // 2
+    K[:, :, at, 0] = 64.0
+    c.append(K.bfloat16(), rows(g, 1, 2, cap, d), ints([0]))
+    c.V_scale.fill_(high)
+    c.V_scale[:, :, at // BLOCK] = low
+    q = torch.zeros(1, 2, 1, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 200 * math.log(2) * d ** 0.5 / 64 * 1.5
+    out = c.attend(q, ints([cap])).double()
+    want = c.V[:, :, at].double()[:, :, None] * low
+    # the entry's weight is one: half a step of f16 for it, of bf16 for the output
+    assert ((out - want).abs() <= (2.0 ** -11 + 2.0 ** -8) * want.abs() * (1 + 2.0 ** -7) + 2.0 ** -140).all()
+
+
 def test_attend_many_splits_long():
     """One head long enough that every worker of the device holds a part of it."""
     n = 70000
