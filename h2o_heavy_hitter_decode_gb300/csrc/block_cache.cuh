@@ -5,9 +5,8 @@
 
 #include <cuda.h>
 
-#include <atomic>
-
 #include "common.cuh"
+#include "smem_limit.h"
 
 #include "../../include/h2o.h"
 
@@ -213,22 +212,6 @@ __device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows
 // what it reads of this one's results it reads after its own wait.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// A kernel's limit of dynamic shared memory, raised once for each device (the
-// call costs a microsecond).
-struct SmemLimit {
-  std::atomic<int> bytes[64] = {};
-  cudaError_t raise(const void *kernel, int want) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::atomic<int> &have = bytes[dev & 63];
-    if (dev < 64 && have.load(std::memory_order_relaxed) >= want) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
-    if (e == cudaSuccess && dev < 64) have.store(want, std::memory_order_relaxed);
-    return e;
-  }
-};
 
 // Launchers (each on the device that is current; arguments checked before).
 cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
