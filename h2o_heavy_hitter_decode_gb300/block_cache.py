@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 import torch
 
@@ -33,7 +34,8 @@ class H2OBlockCache:
     the entries' positions and accumulated attention weights: views of the
     workspace, one torch uint8 tensor owned by this object.  Calls enqueue on
     torch's current CUDA stream of the cache's device; calls of one cache must
-    not overlap on the GPU."""
+    not overlap on the GPU (host threads may share a cache: each call passes
+    its own arguments and its own stream, one thread at a time)."""
 
     BLOCK = 32
 
@@ -62,7 +64,9 @@ class H2OBlockCache:
                    "h2o_bcache_create")
         self._h, self._set_stream = h, None
         self._heads, self._per_seq = H * group, (B,)
-        # h2o_rows of q, k, v and out, filled in by each call
+        # h2o_rows of q, k, v and out, filled in by each call; the lock covers them and the handle's stream until the call
+        # is enqueued
+        self._lock = threading.Lock()
         self._slots = [(C.c_int64 * 4)() for _ in range(4)]
         self._slot_at = [C.addressof(s) for s in self._slots]
         at = [C.c_void_p() for _ in range(6)]
@@ -147,12 +151,13 @@ class H2OBlockCache:
         a prompt's column sums; default 0).  See h2o_bcache_append."""
         n = self._tokens(k, "k")
         shape = self._shape(self.H, n)
-        args = (self._rows(1, k, shape, "k"), self._rows(2, v, shape, "v"), self._lengths(lengths, "lengths"),
-                self._dense(counts, I32, self._per_seq, "counts"),
-                self._dense(position, I32, self._per_seq, "position"),
-                self._dense(score, F32, shape[:3], "score"))
-        self._use_stream()
-        _check(self._lib.h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
+        with self._lock:
+            args = (self._rows(1, k, shape, "k"), self._rows(2, v, shape, "v"), self._lengths(lengths, "lengths"),
+                    self._dense(counts, I32, self._per_seq, "counts"),
+                    self._dense(position, I32, self._per_seq, "position"),
+                    self._dense(score, F32, shape[:3], "score"))
+            self._use_stream()
+            _check(self._lib.h2o_bcache_append(self._h, n, *args), "h2o_bcache_append")
 
     def attend(self, q, lengths, counts=None, causal=True, accumulate=True, out=None, lse=None):
         """Attention of q [B, H * group, n, d] over the ``lengths[b]`` entries
@@ -162,14 +167,15 @@ class H2OBlockCache:
         the log-sum-exps.  See h2o_bcache_attend."""
         n = self._tokens(q, "q")
         shape = self._shape(self._heads, n)
-        qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
-        cnt = self._dense(counts, I32, self._per_seq, "counts")
-        if out is None:
-            out = self._new_out(shape, counts)
-        args = (qr, lens, cnt, 1 if causal else 0, 1 if accumulate else 0, self._rows(3, out, shape, "out"),
-                self._dense(lse, F32, shape[:3], "lse"))
-        self._use_stream()
-        _check(self._lib.h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
+        with self._lock:
+            qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
+            cnt = self._dense(counts, I32, self._per_seq, "counts")
+            if out is None:
+                out = self._new_out(shape, counts)
+            args = (qr, lens, cnt, 1 if causal else 0, 1 if accumulate else 0, self._rows(3, out, shape, "out"),
+                    self._dense(lse, F32, shape[:3], "lse"))
+            self._use_stream()
+            _check(self._lib.h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
         return out
 
     def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None):
@@ -178,14 +184,15 @@ class H2OBlockCache:
         counts (or n) to ``lengths`` afterwards.  See h2o_bcache_step."""
         n = self._tokens(q, "q")
         shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
-        rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
-        lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
-        if out is None:
-            out = self._new_out(shape, counts)
-        args = rows + (lens, cnt, self._dense(position, I32, self._per_seq, "position"), 1 if accumulate else 0,
-                       self._rows(3, out, shape, "out"), self._dense(lse, F32, shape[:3], "lse"))
-        self._use_stream()
-        _check(self._lib.h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
+        with self._lock:
+            rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
+            lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
+            if out is None:
+                out = self._new_out(shape, counts)
+            args = rows + (lens, cnt, self._dense(position, I32, self._per_seq, "position"), 1 if accumulate else 0,
+                           self._rows(3, out, shape, "out"), self._dense(lse, F32, shape[:3], "lse"))
+            self._use_stream()
+            _check(self._lib.h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
         return out
 
     def _new_out(self, shape, counts):
@@ -205,15 +212,17 @@ class H2OBlockCache:
             new_lengths = torch.empty_like(lengths)
         args = (lens, int(k_heavy), int(k_local), int(n_sink), int(score_mode),
                 self._dense(position, I32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
-        self._use_stream()
-        _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
+        with self._lock:
+            self._use_stream()
+            _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
         return new_lengths
 
     def error_bits(self) -> int:
         """The sticky error flag (H2O_BERR_* bits; 0 = none); synchronises."""
-        self._use_stream()
         bits = C.c_int32()
-        rc = self._lib.h2o_bcache_get_error(self._h, C.byref(bits))
+        with self._lock:
+            self._use_stream()
+            rc = self._lib.h2o_bcache_get_error(self._h, C.byref(bits))
         if rc not in (0, 5):
             _check(rc, "h2o_bcache_get_error")
         return bits.value

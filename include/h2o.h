@@ -303,7 +303,8 @@ h2o_status h2o_get_error(h2o_cache_t cache);
  * overlap.  The other conventions at the top of this file hold, and:
  * calls of one cache must not overlap on the GPU (they share its scratch
  * memory); they may be captured into graphs, and the graphs then share it
- * too.  Work goes to the cache's device whatever device is current. */
+ * too.  A handle is used by one host thread at a time (its stream is part of
+ * it); different handles may be used by different threads at once.  Work goes to the cache's device whatever device is current. */
 #define H2O_BLOCK 32
 #define H2O_BLOCK_MAX_ROWS 256 /* group * max_queries is at most this */
 typedef enum { H2O_KV_E4M3 = 0, H2O_KV_INT8 = 1 } h2o_kv8;

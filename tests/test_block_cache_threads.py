@@ -1,0 +1,93 @@
+"""H2OBlockCache shared by host threads: each call passes its own rows and
+stream (CPU, with a stand-in for the library)."""
+from __future__ import annotations
+
+import ctypes as C
+import threading
+
+import pytest
+import torch
+
+from h2o_heavy_hitter_decode_gb300 import H2OBlockCache
+from h2o_heavy_hitter_decode_gb300 import block_cache
+
+B, H, D, N = 1, 1, 64, 2
+
+
+class Library:
+    """Calls that look at their arguments only once the other thread had the time to begin its own."""
+
+    def __init__(self):
+        self.stream, self.seen, self.inside = None, [], threading.Barrier(2)
+
+    def h2o_bcache_set_stream(self, handle, stream):
+        self.stream = stream.value
+        return 0
+
+    def _call(self, kind, *rows):
+        try:
+            self.inside.wait(0.3)
+        except threading.BrokenBarrierError:
+            pass
+        self.seen.append((kind, self.stream) + tuple((C.c_int64 * 4).from_address(r)[0] for r in rows))
+        return 0
+
+    def h2o_bcache_append(self, handle, n, k, v, lengths, counts, position, score):
+        return self._call("append", k, v)
+
+    def h2o_bcache_attend(self, handle, n, q, lengths, counts, causal, accumulate, out, lse):
+        return self._call("attend", q, out)
+
+    def h2o_bcache_step(self, handle, n, q, k, v, lengths, counts, position, accumulate, out, lse):
+        return self._call("step", q, k, v, out)
+
+    def h2o_bcache_evict(self, handle, *args):
+        return self._call("evict")
+
+
+def cache_on_the_host(monkeypatch):
+    """A cache object without a device: its tensors are CPU tensors (device index -1)."""
+    lib = Library()
+    monkeypatch.setattr(block_cache, "lib", lambda: lib)
+    c = H2OBlockCache.__new__(H2OBlockCache)
+    c._lib, c._h, c._set_stream, c._index, c.device = lib, None, None, -1, torch.device("cpu")
+    c.B, c.H, c.d, c.capacity, c.group, c.max_queries = B, H, D, 32, 1, N
+    c._heads, c._per_seq = H, (B,)
+    c._lock = threading.Lock()
+    c._slots = [(C.c_int64 * 4)() for _ in range(4)]
+    c._slot_at = [C.addressof(s) for s in c._slots]
+    here = threading.local()
+    c._stream = lambda: here.stream
+    return c, lib, here
+
+
+@pytest.mark.parametrize("call", ["append", "attend", "step", "evict"])
+def test_two_threads_pass_their_own_rows_and_streams(monkeypatch, call):
+    c, lib, here = cache_on_the_host(monkeypatch)
+    want, errors = [], []
+
+    def work(stream):
+        try:
+            here.stream = stream
+            q, k, v, out = (torch.zeros(B, H, N, D, dtype=torch.bfloat16) for _ in range(4))
+            L = torch.zeros(B, dtype=torch.int32)
+            args = {"append": (k, v), "attend": (q, out), "step": (q, k, v, out), "evict": ()}[call]
+            want.append((call, stream) + tuple(t.data_ptr() for t in args))
+            if call == "append":
+                c.append(k, v, L)
+            elif call == "attend":
+                c.attend(q, L, out=out)
+            elif call == "step":
+                c.step(q, k, v, L, out=out)
+            else:
+                c.evict(L, 4, 4)
+        except Exception as e:  # noqa: BLE001  (reported by the test)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert sorted(lib.seen) == sorted(want)
