@@ -35,7 +35,9 @@ class H2OBlockCache:
     workspace, one torch uint8 tensor owned by this object.  Calls enqueue on
     torch's current CUDA stream of the cache's device; calls of one cache must
     not overlap on the GPU (host threads may share a cache: each call passes
-    its own arguments and its own stream, one thread at a time)."""
+    its own arguments and its own stream, one thread at a time).  A cache may
+    be dropped with calls still running on any stream; one that a captured
+    graph uses is kept for as long as the graph is replayed."""
 
     BLOCK = 32
 
@@ -60,9 +62,11 @@ class H2OBlockCache:
                 raise H2OError(1, f"h2o_bcache_workspace_bytes{shape}")
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             h = C.c_void_p()
-            _check(L.h2o_bcache_create(*shape, _ptr(self.workspace), C.c_void_p(self._stream()), C.byref(h)),
+            stream = self._stream()
+            _check(L.h2o_bcache_create(*shape, _ptr(self.workspace), C.c_void_p(stream), C.byref(h)),
                    "h2o_bcache_create")
-        self._h, self._set_stream = h, None
+        self._h, self._set_stream = h, stream
+        self._recorded = {stream}  # streams that the workspace's allocation knows of
         self._heads, self._per_seq = H * group, (B,)
         # h2o_rows of q, k, v and out, filled in by each call; the lock covers them and the handle's stream until the call
         # is enqueued
@@ -96,6 +100,10 @@ class H2OBlockCache:
     def _use_stream(self):
         s = self._stream()
         if s != self._set_stream:
+            if s not in self._recorded:
+                # a cache that is dropped while this stream still runs its kernels keeps its memory until they are done
+                self.workspace.record_stream(torch.cuda.current_stream(self.device))
+                self._recorded.add(s)
             _check(self._lib.h2o_bcache_set_stream(self._h, C.c_void_p(s)), "h2o_bcache_set_stream")
             self._set_stream = s
 

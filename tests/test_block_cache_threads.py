@@ -1,5 +1,6 @@
-"""H2OBlockCache shared by host threads: each call passes its own rows and
-stream (CPU, with a stand-in for the library)."""
+"""H2OBlockCache shared by host threads, and used on several streams: each
+call passes its own rows and stream, and the workspace's allocation knows of
+every stream (CPU, with a stand-in for the library)."""
 from __future__ import annotations
 
 import ctypes as C
@@ -52,7 +53,7 @@ def cache_on_the_host(monkeypatch):
     c = H2OBlockCache.__new__(H2OBlockCache)
     c._lib, c._h, c._set_stream, c._index, c.device = lib, None, None, -1, torch.device("cpu")
     c.B, c.H, c.d, c.capacity, c.group, c.max_queries = B, H, D, 32, 1, N
-    c._heads, c._per_seq = H, (B,)
+    c._heads, c._per_seq, c._recorded = H, (B,), {1, 2}
     c._lock = threading.Lock()
     c._slots = [(C.c_int64 * 4)() for _ in range(4)]
     c._slot_at = [C.addressof(s) for s in c._slots]
@@ -91,3 +92,24 @@ def test_two_threads_pass_their_own_rows_and_streams(monkeypatch, call):
         t.join()
     assert not errors
     assert sorted(lib.seen) == sorted(want)
+
+
+def test_the_workspace_knows_its_streams(monkeypatch):
+    """Each stream but the one that the workspace was allocated on is recorded with it, before the first call there."""
+    c, lib, here = cache_on_the_host(monkeypatch)
+    seen = []
+
+    class Workspace:
+        def record_stream(self, stream):
+            assert lib.stream != stream
+            seen.append(stream)
+
+    c.workspace, c._recorded, c._set_stream = Workspace(), {1}, 1
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here.stream)
+    lib.inside.abort()
+    L = torch.zeros(B, dtype=torch.int32)
+    for s in (1, 2, 1, 3, 2, 3):
+        here.stream = s
+        c.evict(L, 4, 4)
+    assert seen == [2, 3]
+    assert [x[1] for x in lib.seen] == [None, 2, 1, 3, 2, 3]

@@ -643,6 +643,29 @@ def test_other_stream(cap):
     same_state(c, r)
 
 
+def test_dropped_while_another_stream_runs_its_call():
+    """The workspace of a cache that is dropped with a call still to run on another stream is not given out again."""
+    cap = 65536
+    c, r, g = filled(151, 1, 2, 64, cap, [500], 2, 1, "int8", junk=False)
+    q, k, v = rows(g, 1, 4, 1, 64), rows(g, 1, 2, 1, 64), rows(g, 1, 2, 1, 64)
+    L, s = ints([500]), torch.cuda.Stream()
+    other_cache = filled(151, 1, 2, 64, cap, [500], 2, 1, "int8", junk=False)[0]
+    torch.cuda._sleep(1)
+    other_cache.step(q, k, v, L)  # the kernels are loaded: a first launch may wait for the device
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1_000_000_000)  # about half a second
+        out = c.step(q, k, v, L)
+    at, size = c.workspace.data_ptr(), c.workspace.numel()
+    del c
+    other = torch.empty(size, dtype=torch.uint8, device=DEV)
+    assert not s.query() and not at <= other.data_ptr() < at + size
+    other.fill_(0x7F)
+    s.synchronize()
+    want, _, tol, _ = r.step(q, k, v, [500])
+    close(out, want, tol, "out")
+
+
 def test_two_caches_on_two_streams():
     """Calls of different caches may overlap on the GPU: steps, attention with many rows and evictions of two caches on
     two streams at once give the bits that they give one after the other."""
