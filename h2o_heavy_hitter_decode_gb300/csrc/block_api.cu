@@ -55,7 +55,7 @@ bool shape_ok(int B, int H, int d, int64_t capacity, int group, int max_queries,
 bool d_supported(int d) { return d == 64 || d == 128; }
 
 struct Layout {
-  size_t K, V, Ksc, Vsc, pos, score, logits, part, err, total;
+  size_t K, V, Ksc, Vsc, pos, score, low, logits, part, err, total;
 };
 Layout layout(int B, int H, int d, int64_t cap, int rows, int sms) {
   const size_t nh = (size_t)B * H, entries = nh * (size_t)cap, scales = entries / H2O_BLOCK * sizeof(float);
@@ -67,6 +67,7 @@ Layout layout(int B, int H, int d, int64_t cap, int rows, int sms) {
   l.Vsc = o;     o = align_up(o + scales);
   l.pos = o;     o = align_up(o + entries * sizeof(int32_t));
   l.score = o;   o = align_up(o + entries * sizeof(float));
+  l.low = o;     o = align_up(o + entries * sizeof(float));
   l.logits = o;  o = align_up(o + entries * rows * sizeof(float));
   l.part = o;    o = align_up(o + blk::attend_scratch_bytes(B, H, d, rows, sms));
   l.err = o;     o = align_up(o + sizeof(int));
@@ -160,6 +161,7 @@ h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, i
   v.K = (uint8_t *)w + l.K; v.V = (uint8_t *)w + l.V;
   v.Ksc = (float *)(w + l.Ksc); v.Vsc = (float *)(w + l.Vsc);
   v.pos = (int32_t *)(w + l.pos); v.score = (float *)(w + l.score);
+  v.low = (float *)(w + l.low);
   v.logits = (float *)(w + l.logits); v.kept = (int32_t *)(w + l.logits);
   v.part = (float *)(w + l.part);
   v.err = (int *)(w + l.err);
@@ -172,7 +174,7 @@ h2o_status h2o_bcache_create(int B, int H, int d, int64_t capacity, int group, i
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&v.l2_bytes, cudaDevAttrL2CacheSize, c->device);
   if (e == cudaSuccess) e = cudaMemsetAsync(w + l.K, 0, l.pos - l.K, c->stream);  // codes and scales
   if (e == cudaSuccess) e = cudaMemsetAsync(v.pos, 0xff, l.score - l.pos, c->stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(v.score, 0, l.logits - l.score, c->stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(v.score, 0, l.logits - l.score, c->stream);  // and what they lose
   if (e == cudaSuccess) e = cudaMemsetAsync(v.err, 0, sizeof(int), c->stream);
   if (e != cudaSuccess) {
     delete c;

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const View c, co
     const size_t at = (size_t)bh * c.cap + t;
     c.pos[at] = (position ? position[b] : s.len) + (t - s.len);
     c.score[at] = score ? score[(size_t)bh * l.n + (t - s.len)] : 0.f;
+    c.low[at] = 0.f;
   }
 }
 
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
     const size_t at = (size_t)bh * c.cap + s.len + lane;
     c.pos[at] = (position ? position[b] : s.len) + lane;
     c.score[at] = 0.f;
+    c.low[at] = 0.f;
   }
 }
 

@@ -707,6 +707,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
       if (j >= lo && j < hi) {
         c.pos[(size_t)bh * c.cap + j] = (position ? position[b] : s.len) + (j - s.len);
         c.score[(size_t)bh * c.cap + j] = 0.f;
+        c.low[(size_t)bh * c.cap + j] = 0.f;
       }
       // the codes are read back by the copy below
       __threadfence();
@@ -798,11 +799,13 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
   }
   if (!a.accumulate) return;
   __syncthreads();
-  float *sc = c.score + (size_t)bh * c.cap;
+  float *sc = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   for (int j = threadIdx.x; j < s.total; j += W * 32) {
-    float w = 0.f;
+    const float old = sc[j];
+    float lost = low[j], w = 0.f;
     for (int r = 0; r < rows; ++r) w += ex2(logits[r * c.cap + j] - row_lse[r]);
-    sc[j] += w;
+    sc[j] = add_score(old, lost, w);
+    low[j] = lost;
   }
 }
 
@@ -969,8 +972,8 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
     constexpr int kRows = 8 / V;  // rows whose logits are on their way at once
     const int j_last = max(0, s.total - 1) & ~3;
     const float *lg = c.logits + (size_t)bh * c.max_rows * c.cap;
-    float *sc = c.score + (size_t)bh * c.cap;
-    float4 w[V], old[V], v[kRows][V];
+    float *sc = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
+    float4 w[V], old[V], lost[V], v[kRows][V];
     auto load = [&](int r0) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
@@ -1027,6 +1030,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       __syncwarp();
     }
     if (V > 1) first();
+    else lost[0] = *(const float4 *)(low + min(j0, j_last));
     for (int r0 = 0; r0 < rows; r0 += kRows) {
       if (V > 1 || r0 > 0) load(r0);
 #pragma unroll
@@ -1040,15 +1044,21 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
         }
       }
     }
+    if (V > 1)  // no registers for them before (72 bytes of spills)
+#pragma unroll
+      for (int y = 0; y < V; ++y) lost[y] = *(const float4 *)(low + min(j0 + y * 128, j_last));
 #pragma unroll
     for (int y = 0; y < V; ++y) {
       const int j = j0 + y * 128;
+      const float4 sum = make_float4(add_score(old[y].x, lost[y].x, w[y].x), add_score(old[y].y, lost[y].y, w[y].y),
+                                     add_score(old[y].z, lost[y].z, w[y].z), add_score(old[y].w, lost[y].w, w[y].w));
       if (j + 4 <= s.total) {
-        *(float4 *)(sc + j) = make_float4(old[y].x + w[y].x, old[y].y + w[y].y, old[y].z + w[y].z, old[y].w + w[y].w);
+        *(float4 *)(sc + j) = sum;
+        *(float4 *)(low + j) = lost[y];
       } else {  // entries behind the last one keep their score
-        if (j < s.total) sc[j] = old[y].x + w[y].x;
-        if (j + 1 < s.total) sc[j + 1] = old[y].y + w[y].y;
-        if (j + 2 < s.total) sc[j + 2] = old[y].z + w[y].z;
+        if (j < s.total) sc[j] = sum.x, low[j] = lost[y].x;
+        if (j + 1 < s.total) sc[j + 1] = sum.y, low[j + 1] = lost[y].y;
+        if (j + 2 < s.total) sc[j + 2] = sum.z, low[j + 2] = lost[y].z;
       }
     }
     __syncwarp();  // before the next item's row_lse (W = 8: the barriers above keep it back)

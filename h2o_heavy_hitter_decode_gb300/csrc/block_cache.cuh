@@ -23,6 +23,7 @@ struct View {
   float *Ksc, *Vsc;                   // [B*H][cap / kBlock]
   int32_t *pos;                       // [B*H][cap]
   float *score;                       // [B*H][cap]
+  float *low;                         // [B*H][cap] what the scores' fp32 sums have lost (add_score)
   float *logits;                      // [B*H][max_rows][cap] scratch, base-2 logits
   float *part;                        // scratch, split partials
   int32_t *kept;                      // [B*H][cap] scratch of an eviction (shares the logits' memory)
@@ -57,6 +58,20 @@ __device__ __forceinline__ Seq seq_of(const Lens &l, int b) {
   if (!s.ok) s.len = s.cnt = 0;
   s.total = s.cnt == 0 ? 0 : s.len + (l.appends ? s.cnt : 0);
   return s;
+}
+
+// score + w in fp32; low keeps what the sum loses, and is taken into the next
+// one: thousands of weights below half a step of a large score (an entry that
+// starts with its prompt's column sum) add up all the same, where plain sums
+// stay where they are.  The loss of a sum is exact (D. E. Knuth, The Art of
+// Computer Programming, vol. 2, 4.2.2, theorem B).  It is at most half a step of the score:
+// one that is larger belongs to a score that the caller has replaced.
+__device__ __forceinline__ float add_score(float score, float &low, float w) {
+  const float half_step = __uint_as_float(__float_as_uint(score) & 0x7f800000u) * 0x1p-24f;
+  const float y = __fadd_rn(w, fabsf(low) <= half_step ? low : 0.f);
+  const float sum = __fadd_rn(score, y), z = __fsub_rn(sum, score);
+  low = __fadd_rn(__fsub_rn(score, __fsub_rn(sum, z)), __fsub_rn(y, z));
+  return sum;
 }
 
 // ------------------------------------------------------------------ formats

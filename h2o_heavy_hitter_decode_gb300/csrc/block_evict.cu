@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
   if (!ok || len <= k) return;  // the whole cluster
   const int nc = len - a.kl;    // candidates 0 .. nc-1
   int32_t *pos = c.pos + (size_t)bh * c.cap;
-  float *score = c.score + (size_t)bh * c.cap;
+  float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   int32_t *kept = c.kept + (size_t)bh * c.cap;
 
   if (kh > 0) {
@@ -333,14 +333,14 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
   // The lane's entry of an item, and what travels with it.
   struct Entry {
     int pos;
-    float scale, score;
+    float scale, score, low;
   };
   auto source = [&](int q) {  // 0 behind the last entry
     const int i = (q >> 1) * kBlock + lane;
     return q >= items || i >= k ? 0 : i < kh ? min(max(kept[i], 0), len - 1) : i - kh + nc;
   };
   auto fetch = [&](int q, int slot, int src) {  // an item's rows into its buffer
-    Entry x{0, 0.f, 0.f};
+    Entry x{0, 0.f, 0.f, 0.f};
     if (q < items) {
       const bool is_v = q & 1;
       const int base = (q >> 1) * kBlock;
@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
         if (!is_v) {
           x.pos = pos[src];
           x.score = score[src];
+          x.low = low[src];
         }
       }
     }
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
     }
     const int pos_own = __shfl_sync(0xffffffffu, next[0].pos, lane);
     const float score_own = __shfl_sync(0xffffffffu, next[0].score, lane);
+    const float low_own = __shfl_sync(0xffffffffu, next[0].low, lane);
     rounds.wait();  // everyone has read the round before
     rounds.arrive(lane);
     fetch_round(q + stride, src);
@@ -442,6 +444,7 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
       if (base + lane < k) {
         pos[base + lane] = pos_own;
         score[base + lane] = score_own;
+        low[base + lane] = low_own;
       }
     }
   }

@@ -317,7 +317,7 @@ typedef struct {
 /* Bytes of device workspace (0 for invalid shapes, or without a device).
  * B, H >= 1, B * H <= 2^24; d in {64, 128}; capacity a multiple of H2O_BLOCK,
  * at most 2^30, B * H * capacity < 2^31; group, max_queries >= 1, group *
- * max_queries <= H2O_BLOCK_MAX_ROWS.  Besides the cache's arrays (2 d + 8 bytes
+ * max_queries <= H2O_BLOCK_MAX_ROWS.  Besides the cache's arrays (2 d + 12 bytes
  * an entry and the scales) the workspace holds 4 * group * max_queries bytes of
  * scratch an entry and the partial results of attention. */
 size_t h2o_bcache_workspace_bytes(int B, int H, int d, int64_t capacity, int group, int max_queries, h2o_kv8 kv);
@@ -334,7 +334,10 @@ h2o_status h2o_bcache_set_stream(h2o_bcache_t cache, void *cuda_stream);
  * [B][H][capacity][d], scales [B][H][capacity / H2O_BLOCK] fp32, pos
  * [B][H][capacity] int32, score [B][H][capacity] fp32.  The caller may read
  * and, between calls, write them; scales must stay powers of two of at least
- * 2^-100 in blocks that hold entries, and e4m3 codes must not be NaN. */
+ * 2^-100 in blocks that hold entries, and e4m3 codes must not be NaN.  Scores
+ * are sums in fp32; what their roundings lose is kept beside them (not one of
+ * these arrays), so that small weights add up on large scores.  A score that
+ * the caller writes counts as written, to half a unit in its last place. */
 h2o_status h2o_bcache_arrays(h2o_bcache_t cache, void **K, void **V, float **K_scale, float **V_scale,
                              int32_t **pos, float **score);
 

@@ -332,6 +332,67 @@ def test_attend_forms_of_the_finishing_launch(H, G, n, cap, kv):
     assert c.error_bits() == 0
 
 
+# ---------------------------------------------------------- scores over time
+
+@pytest.mark.parametrize("B,H,G,n,cap,kv", [(1, 2, 1, 1, 256, "e4m3"), (1, 2, 4, 2, 704, "int8"), (20, 8, 1, 1, 640, "e4m3"),
+                                            (1, 20, 1, 1, 65536, "e4m3"), (1, 48, 8, 2, 28672, "int8"), (1, 10, 8, 5, 5120, "e4m3")])
+def test_scores_of_many_small_weights(B, H, G, n, cap, kv):
+    """500 calls whose weights are each below a quarter of the half step of an entry's score add up: the score is off by
+    a step of its own at most, and the weights by 2^-18 of them (2^-21 for each of the exponential, its argument's
+    difference and the sum), not by a step a call."""
+    calls, d, total = 500, 64, cap - 5
+    g = torch.Generator(DEV).manual_seed(157)
+    c = H2OBlockCache(B, H, d, cap, group=G, max_queries=n, kv=kv)
+    w = G * n / total  # equal keys
+    start = 2.0 ** (math.floor(math.log2(w)) + 27)  # half a step: 4 to 8 times w
+    x = torch.ones(B, H, cap, d, dtype=torch.bfloat16, device=DEV)
+    c.append(x, x, ints([0] * B), score=torch.full((B, H, cap), start, device=DEV))
+    q, L = rows(g, B, H * G, n, d), ints([total] * B)
+    out = torch.empty_like(q)
+    for _ in range(calls):
+        c.attend(q, L, causal=False, out=out)
+    want = start + calls * w
+    got = c.score[:, :, :total].double()
+    assert ((got - want).abs() <= start * 2.0 ** -23 + calls * w * 2.0 ** -18).all()
+    assert (c.score[:, :, total:] == start).all()
+    # a score that the caller writes counts as written
+    fresh = H2OBlockCache(B, H, d, cap, group=G, max_queries=n, kv=kv)
+    fresh.append(x, x, ints([0] * B))
+    c.score.zero_()
+    for cache in (c, fresh):
+        cache.attend(q, L, causal=False, out=out)
+    assert torch.equal(c.score[:, :, :total], fresh.score[:, :, :total])
+    assert c.error_bits() == 0
+
+
+@pytest.mark.parametrize("B,H,cap,every", [(1, 2, 256, 2), (1, 2, 704, 5), (1, 400, 704, 5), (3, 24, 2048, 9)])
+def test_small_weights_across_evictions(B, H, cap, every):
+    """The same with an eviction of one entry after every few calls, fewer than their weights take to reach half a step:
+    what the sums lost moves with the entries.  Every second entry takes all the weight, the others' is below 2^-57."""
+    d, evictions = 64, 150
+    c = H2OBlockCache(B, H, d, cap, kv="int8")
+    k = torch.zeros(B, H, cap, d, device=DEV)
+    k[:, :, ::2, 0], k[:, :, 1::2, 0] = -8.0, 8.0
+    start = 2.0 ** 20 + 64.0 * torch.arange(cap, device=DEV)  # entry 0 goes first
+    c.append(k.bfloat16(), k.bfloat16(), ints([0] * B), score=start.expand(B, H, cap).contiguous())
+    q = torch.zeros(B, H, 1, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 20.0
+    n, want = cap, start.double()
+    for _ in range(evictions):
+        odd = torch.arange(cap - n, cap, device=DEV) % 2 == 1
+        assert every / int(odd.sum()) < 2.0 ** -4  # half a step of 2^20
+        for _ in range(every):
+            c.attend(q, ints([n] * B))
+        want[cap - n :] += odd * (every / int(odd.sum()))
+        c.evict(ints([n] * B), n - 1, 0)
+        n -= 1
+    got = c.score[:, :, :n].double()
+    moved = want[cap - n :]
+    assert float((moved - start[cap - n :]).max()) > 1  # eight steps of 2^-3 at least
+    assert ((got - moved).abs() <= 2.0 ** -3 + (moved - start[cap - n :]) * 2.0 ** -18).all()
+    assert torch.equal(c.pos[0, 0, :n].long(), torch.arange(cap - n, cap, device=DEV))
+
+
 def test_attend_many_sequences():
     """More sequences than a warp looks over at once, most of them short, some empty."""
     B = 700
