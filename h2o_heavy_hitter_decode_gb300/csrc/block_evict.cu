@@ -48,6 +48,11 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int kDigits = 2048;  // bins of the first digit
+// Shared memory of a CTA where two share an SM (228 KB, 1 KB of it a CTA's own), and the kernel's static part of it.
+constexpr int kSmemOfCta = 228 * 1024 / 2 - 1024;
+template <int P> constexpr int kStatic = kDigits * 4 * (P > 1 ? 2 : 1) + (P > 1 ? kDigits / P * 8 : 0) + 256;
+
 struct Args {
   View c;
   const int32_t *lengths, *position;
@@ -126,7 +131,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
 template <typename F, int D, int P, int W>
 __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
   constexpr int kThreads = W * 32;
-  constexpr int kDigits = 2048, kOwn = kDigits / kThreads;
+  constexpr int kOwn = kDigits / kThreads;
   extern __shared__ __align__(16) uint32_t dyn[];  // the keys, then the warps' row buffers
   __shared__ __align__(16) unsigned hist[P > 1 ? 2 : 1][kDigits];  // this CTA's counts, in a cluster by pass parity
   __shared__ __align__(16) unsigned totals[P > 1 ? 2 : 1][P > 1 ? kDigits / P : 4];  // the cluster's counts of a slice
@@ -135,6 +140,8 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
   __shared__ unsigned s_sum[W];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ int s_count[2];  // this CTA's entries above and at the threshold
+  static_assert(sizeof(hist) + sizeof(totals) + sizeof(s_warp) + sizeof(s_sum) + 64 <= kStatic<P>,
+                "the room for keys leaves this out");
   cg::cluster_group cluster = cg::this_cluster();
   const View &c = a.c;
   const int rank = P > 1 ? (int)cluster.block_rank() : 0;
@@ -455,7 +462,11 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
 
 template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStream_t st) {
   constexpr int kRing = W * 2 * kBlock * D;
-  const int share = ((a.c.cap + P - 1) / P + 3) & ~3, most = 110 * 1024 / 4;  // keys: two CTAs still fit an SM
+  // Keys, as many as leave room for two CTAs an SM (the clusters of evict_t count on both).  Against 110 KB of them,
+  // where the larger caches had one: 300 heads of 32,768 entries 265 -> 242 us, 64 of 131,072 276 -> 239, 16 of 262,144
+  // 207 -> 156; 300 of 65,536, more of whose keys are read again, 730 -> 765.
+  constexpr int most = (kSmemOfCta - kStatic<P>) / 4 & ~3;
+  const int share = ((a.c.cap + P - 1) / P + 3) & ~3;
   const int keys = share < most ? share : most;
   const int smem = keys * 4 > kRing ? keys * 4 : kRing;
   a.held = smem / 4;

@@ -574,6 +574,39 @@ def test_evict_shared_heads(B, H, cap, lens, kv, mode):
     assert c.error_bits() == 0
 
 
+@pytest.mark.parametrize("H,cap", [(80, 49152), (40, 98304), (16, 229376), (3, 425984)])
+@pytest.mark.parametrize("mode", [0, 1])
+def test_evict_more_candidates_than_a_cluster_holds(H, cap, mode):
+    """Clusters of 2, 4, 8 and 16 CTAs whose share of the candidates is more than they keep in shared memory."""
+    d, n, kh, kl = 64, cap - 13, cap // 9, 1001
+    g = torch.Generator(DEV).manual_seed(163)
+    c = H2OBlockCache(1, H, d, cap, kv="int8")
+    for j in range(0, cap, cap // 8):
+        c.append(rows(g, 1, H, cap // 8, d), rows(g, 1, H, cap // 8, d), ints([j]))
+    c.score.copy_(torch.rand(1, H, cap, generator=g, device=DEV).mul_(500).round_())  # many equal ones
+    score = c.score.clone()
+    i = torch.arange(cap, device=DEV)
+    key = score / (cap - i).clamp(min=1).float() if mode else score
+    key = torch.where((i >= n - kl) | (i < 4), math.inf, key)
+    order = key[..., :n].sort(dim=-1, stable=True).indices
+    gone = torch.zeros(1, H, n, dtype=torch.bool, device=DEV).scatter_(2, order, (i[:n] < n - (kh + kl)).expand(1, H, n))
+    want = i[:n].expand(1, H, n)[~gone].view(1, H, -1)
+    rows_of = {}
+    for name in ("K", "V"):
+        scales = getattr(c, name + "_scale").double().repeat_interleave(BLOCK, 2)
+        rows_of[name] = (getattr(c, name)[:, -1].double() * scales[:, -1, :, None])[0][want[0, -1]]
+    assert c.evict(ints([n]), kh, kl, n_sink=4, score_mode=mode, position=ints([cap])).tolist() == [kh + kl]
+    assert torch.equal(c.pos[:, :, : kh + kl].long(), want)
+    assert torch.equal(c.score[:, :, : kh + kl], score.gather(2, want))
+    r = RefCache(1, 1, d, cap, 1, "int8")
+    for name in ("K", "V"):  # the last head's rows, quantised anew
+        r._quantise(getattr(r, name)[0, 0], getattr(r, name + "_scale")[0, 0], rows_of[name].cpu(), 0, kh + kl)
+        assert torch.equal(getattr(c, name)[0, -1, : kh + kl].cpu().double(), getattr(r, name)[0, 0, : kh + kl])
+        used = (kh + kl + BLOCK - 1) // BLOCK
+        assert torch.equal(getattr(c, name + "_scale")[0, -1, :used].cpu().double(), getattr(r, name + "_scale")[0, 0, :used])
+    assert c.error_bits() == 0
+
+
 @pytest.mark.parametrize("H,cap", [(3, 20480), (240, 4096)])
 @pytest.mark.parametrize("every", [8, 16, 20, 40, 80])
 def test_evict_scores_with_a_period(H, cap, every):
