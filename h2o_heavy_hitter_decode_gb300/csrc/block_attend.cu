@@ -243,6 +243,14 @@ __device__ __forceinline__ float inverse_sum(float x) {
   return x == 0.f ? 0.f : y;
 }
 
+// What a row's base-2 logits are taken off to give its weights, from its reference and sum of weights.  Nothing seen: every
+// weight is 0.  NaN or infinite logits (a NaN or infinite query): the sum is NaN, and the reference in its place gives
+// NaN on the entries that the row sees and 0 on those that it does not, whose logit is -infinity.
+__device__ __forceinline__ float weight_base(float m, float l) {
+  if (l != l) return m == -INFINITY ? 0.f : m;
+  return l > 0.f ? m + log2f(l) : INFINITY;
+}
+
 // What a warp holds of a head while it attends: Q, and for its NR tiles of 8
 // rows the output, the reference and the sum of the weights so far.
 template <typename F, int D, int NR, bool QSmem> struct Tile {
@@ -792,9 +800,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
     *(uint2 *)(const_cast<__nv_bfloat16 *>(a.out.at(b, hq, tok)) + d0) =
         make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
     if (d0 == 0) {
-      const float e = m + log2f(l);
-      row_lse[r] = any ? e : INFINITY;
-      if (a.lse) a.lse[((size_t)b * c.H * c.group + hq) * a.l.n + tok] = any ? e * kLn2 : -INFINITY;
+      row_lse[r] = weight_base(m, l);
+      if (a.lse) a.lse[((size_t)b * c.H * c.group + hq) * a.l.n + tok] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
   }
   if (!a.accumulate) return;
@@ -1013,7 +1020,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
         join(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
       if (lane < 8 && r < rows) {
         if constexpr (W == 1)
-          row_lse[warp][r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;  // nothing seen: every weight 0
+          row_lse[warp][r] = weight_base(m, l);
         else
           part_ml[turn][r] = make_float2(m, l);
       }
@@ -1023,7 +1030,7 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       for (int r = threadIdx.x; r < rows; r += kFinWarps * 32) {
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < sharing; ++i) join(m, l, part_ml[i][r].x, part_ml[i][r].y);
-        row_lse[0][r] = l > 0.f || l != l ? m + log2f(l) : INFINITY;
+        row_lse[0][r] = weight_base(m, l);
       }
       __syncthreads();
     } else {

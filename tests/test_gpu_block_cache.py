@@ -214,6 +214,33 @@ def test_attend_query_sizes(size):
     assert abs(float((c.score[:, :, :100].double().cpu().sum() - r.score[:, :, :100].sum()))) <= 1e-3
 
 
+@pytest.mark.parametrize("B,H,G,n,cap,kv", [(2, 2, 2, 3, 256, "e4m3"), (1, 2, 4, 2, 704, "int8"), (20, 8, 1, 2, 640, "e4m3"),
+                                            (1, 20, 1, 2, 65536, "e4m3"), (1, 48, 8, 2, 28672, "int8"), (1, 10, 8, 5, 5120, "e4m3")])
+def test_nan_query_leaves_what_it_does_not_see(B, H, G, n, cap, kv):
+    """A NaN in the first of several query tokens makes its output and the scores of the entries that it sees NaN.  The
+    tokens behind it and the scores of the entries behind those are within the reference's tolerances (the rows of a
+    head share the moves of their weights' reference), other heads have the bits of a run with a zero in its place."""
+    d, total = 64, cap - 3
+    a, _, g = filled(167, B, H, d, cap, [total] * B, G, n, kv, junk=False)
+    z, r = H2OBlockCache(B, H, d, cap, group=G, max_queries=n, kv=kv), RefCache(1, 1, d, cap, G, kv)
+    for name in ("K", "V", "K_scale", "V_scale", "pos", "score"):
+        getattr(z, name).copy_(getattr(a, name))
+        getattr(r, name).copy_(getattr(a, name)[:1, :1].cpu())
+    q = rows(g, B, H * G, n, d)
+    q[0, 0, 0, 5] = math.nan
+    out = a.attend(q, ints([total] * B))
+    want, _, tol, _ = r.attend(q[:1, :G], [total])
+    assert out[0, 0, 0].isnan().all() and not out[0, :G].flatten(0, 1)[1:].isnan().any()
+    close(out[:1, :G], want, tol, "out")
+    seen = total - n + 1
+    assert a.score[0, 0, :seen].isnan().all() and not a.score[0, 0, seen:].isnan().any()
+    close(a.score[:1, :1, seen:], r.score[:, :, seen:], r.score_tol[:, :, seen:], "score")
+    q[0, 0, 0, 5] = 0.0
+    want = z.attend(q, ints([total] * B))
+    out[0, :G] = want[0, :G] = a.score[0, 0] = z.score[0, 0] = 0.0
+    assert torch.equal(out, want) and torch.equal(a.score, z.score) and a.error_bits() == 0
+
+
 LARGE = [  # B, H, G, n, d, kv, cap, longest: a CTA a head, parts of heads joined, whole heads, many rows
     (1, 2, 1, 1, 128, "e4m3", 64, 50),
     (2, 2, 4, 2, 64, "int8", 512, 512),
