@@ -45,6 +45,8 @@
 // TFLOP/s.
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "block_cache.cuh"
 #include "sm100.cuh"
 
@@ -372,7 +374,8 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
     uint32_t p[NR][4];  // P^T as B: entries 8 e + 2 t and + 1 of row g
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const float f0 = crow[n][0] * ks, f1 = crow[n][1] * ks;
+      // finite: an infinite factor (a huge query on a huge scale) would turn the products that are 0 into NaN
+      const float f0 = fminf(crow[n][0] * ks, FLT_MAX), f1 = fminf(crow[n][1] * ks, FLT_MAX);
 #pragma unroll
       for (int x = 0; x < 2; ++x) s[n][x][0] *= f0, s[n][x][1] *= f1, s[n][x][2] *= f0, s[n][x][3] *= f1;
       if (edge) {

@@ -214,6 +214,30 @@ def test_attend_query_sizes(size):
     assert abs(float((c.score[:, :, :100].double().cpu().sum() - r.score[:, :, :100].sum()))) <= 1e-3
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("cap", [96, 1024])
+def test_attend_huge_query_and_key(kv, cap):
+    """A query of 2^70 and one key of -2^90 along it, the others across: its logit is below fp32's range and its weight 0,
+    those of the entries beside it in its block are 0 and their weights equal."""
+    d = 128
+    c = H2OBlockCache(1, 1, d, cap, kv=kv)
+    k, v = torch.zeros(1, 1, cap, d), torch.ones(1, 1, cap, d)
+    k[0, 0, 40, 0], v[0, 0, 40] = -2.0 ** 90, 64.0
+    c.append(k.bfloat16().to(DEV), v.bfloat16().to(DEV), ints([0]))
+    q = torch.zeros(1, 1, 1, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 2.0 ** 70
+    lse = torch.zeros(1, 1, 1, device=DEV)
+    out = c.attend(q, ints([cap]), lse=lse)
+    # all weights but one equal and of value 1: f16 and fp32 roundings of them (2^-11) and of the output (2^-8)
+    assert ((out.float() - 1).abs() <= 2.0 ** -8 + 2.0 ** -11).all()
+    # 2^-20: the logarithm's and its factors' roundings, at most 2^-22 each of log2(1023) < 10
+    assert abs(float(lse) - math.log(cap - 1)) <= 2.0 ** -20 * 10
+    score = c.score[0, 0].double()
+    assert score[40] == 0
+    score[40] = 1 / (cap - 1)
+    assert ((score * (cap - 1) - 1).abs() <= 2.0 ** -18).all()
+
+
 @pytest.mark.parametrize("B,H,G,n,cap,kv", [(2, 2, 2, 3, 256, "e4m3"), (1, 2, 4, 2, 704, "int8"), (20, 8, 1, 2, 640, "e4m3"),
                                             (1, 20, 1, 2, 65536, "e4m3"), (1, 48, 8, 2, 28672, "int8"), (1, 10, 8, 5, 5120, "e4m3")])
 def test_nan_query_leaves_what_it_does_not_see(B, H, G, n, cap, kv):
