@@ -15,9 +15,6 @@ BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 KV = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(device).cuda_stream without its objects
-
-
 class H2OBlockCache:
     """Per (sequence, cached head) up to ``capacity`` entries in the order of
     their positions; ``group`` query heads share a cached head, and a call
@@ -55,6 +52,8 @@ class H2OBlockCache:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
+        # torch.cuda.current_stream(device).cuda_stream without its objects; a torch without CUDA has no such function
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         shape = (B, H, d, capacity, group, max_queries, code)
         with torch.cuda.device(self.device):
             nbytes = L.h2o_bcache_workspace_bytes(*shape)
@@ -95,7 +94,7 @@ class H2OBlockCache:
         return self.workspace[at : at + n].view(dtype).view(shape)
 
     def _stream(self) -> int:
-        return _raw_stream(self._index)
+        return self._raw_stream(self._index)
 
     def _use_stream(self):
         s = self._stream()

@@ -2,6 +2,8 @@
 from __future__ import annotations
 
 import ctypes as C
+import subprocess
+import sys
 
 import pytest
 
@@ -63,3 +65,13 @@ def test_binding_refuses_before_the_device():
         h2o.H2OBlockCache(1, 1, 64, 32, kv="fp4", device="cuda:0")
     with pytest.raises(ValueError):
         h2o.H2OBlockCache(1, 1, 64, 32, device="cpu")
+
+
+def test_import_with_a_torch_without_cuda():
+    """The package, its header's functions and its refusals are there on a host whose torch has no CUDA functions."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_getCurrent')]: delattr(torch._C, n)\n"
+            "import h2o_heavy_hitter_decode_gb300 as h2o\n"
+            "assert 'h2o_bcache_step' in h2o.declared_functions()\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=hbuild.ROOT)
+    assert r.returncode == 0, r.stderr
