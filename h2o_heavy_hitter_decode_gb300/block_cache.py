@@ -15,6 +15,14 @@ BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 KV = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
 
 
+def _whole(x, name, bits=31):
+    """x as an integer that the library's type holds (ctypes would drop the bits above)."""
+    n = int(x)
+    if not -(1 << bits) <= n < 1 << bits:
+        raise ValueError(f"{name} is out of range: {n}")
+    return n
+
+
 class H2OBlockCache:
     """Per (sequence, cached head) up to ``capacity`` entries in the order of
     their positions; ``group`` query heads share a cached head, and a call
@@ -44,6 +52,9 @@ class H2OBlockCache:
         if kv not in KV:
             raise ValueError(f"kv must be one of {sorted(KV)}, got {kv!r}")
         code, store = KV[kv]
+        B, H, d, group, max_queries = (_whole(x, n) for x, n in ((B, "B"), (H, "H"), (d, "d"), (group, "group"),
+                                                                 (max_queries, "max_queries")))
+        capacity = _whole(capacity, "capacity", 63)
         self.B, self.H, self.d, self.capacity, self.group, self.max_queries = B, H, d, capacity, group, max_queries
         self.kv = kv
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
@@ -217,7 +228,8 @@ class H2OBlockCache:
         lens = self._lengths(lengths, "lengths")
         if new_lengths is None:
             new_lengths = torch.empty_like(lengths)
-        args = (lens, int(k_heavy), int(k_local), int(n_sink), int(score_mode),
+        args = (lens, _whole(k_heavy, "k_heavy"), _whole(k_local, "k_local"), _whole(n_sink, "n_sink"),
+                _whole(score_mode, "score_mode"),
                 self._dense(position, I32, self._per_seq, "position"), self._lengths(new_lengths, "new_lengths"))
         with self._lock:
             self._use_stream()

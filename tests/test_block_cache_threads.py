@@ -1,6 +1,7 @@
 """H2OBlockCache shared by host threads, and used on several streams: each
-call passes its own rows and stream, and the workspace's allocation knows of
-every stream (CPU, with a stand-in for the library)."""
+call passes its own rows and stream, the workspace's allocation knows of
+every stream, and numbers arrive whole (CPU, with a stand-in for the
+library)."""
 from __future__ import annotations
 
 import ctypes as C
@@ -113,3 +114,23 @@ def test_the_workspace_knows_its_streams(monkeypatch):
         c.evict(L, 4, 4)
     assert seen == [2, 3]
     assert [x[1] for x in lib.seen] == [None, 2, 1, 3, 2, 3]
+
+
+@pytest.mark.parametrize("name", ["k_heavy", "k_local", "n_sink", "score_mode"])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 4, 2 ** 64 + 4, -2 ** 32 + 4])
+def test_numbers_beyond_32_bits_are_refused(monkeypatch, name, value):
+    """2^32 + 4 is not 4."""
+    c, lib, here = cache_on_the_host(monkeypatch)
+    lib.inside.abort()
+    here.stream = 1
+    with pytest.raises(ValueError):
+        c.evict(torch.zeros(B, dtype=torch.int32), **{"k_heavy": 4, "k_local": 4, name: value})
+    assert not lib.seen
+
+
+@pytest.mark.parametrize("at", range(6))
+def test_shapes_beyond_the_types_are_refused(at):
+    shape = [1, 1, 64, 32, 1, 1]
+    shape[at] += 2 ** 64 if at == 3 else 2 ** 32
+    with pytest.raises(ValueError):
+        H2OBlockCache(*shape[:4], group=shape[4], max_queries=shape[5], device="cuda:0")
