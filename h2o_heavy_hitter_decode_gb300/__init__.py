@@ -15,8 +15,8 @@ queries, 8-bit codes with one scale per block of entries, eviction in bulk.
 
     cache = H2OBlockCache(B, H, d, capacity, group=G)
     cache.append(K, V, lengths, score=colsum)        # the prompt: [B,H,n,d]
-    out = cache.step(q, k, v, lengths)               # q [B,H*G,1,d], k, v [B,H,1,d]
-    lengths = cache.evict(lengths, k_heavy, k_local)
+    out = cache.step(q, k, v, lengths, position=position)  # q [B,H*G,1,d], k, v [B,H,1,d]
+    lengths = cache.evict(lengths, k_heavy, k_local)       # position (int32 [B]) counts on
 """
 from __future__ import annotations
 

@@ -33,6 +33,9 @@ class H2OBlockCache:
     caches of all layers and captured graphs read its current values.
     ``counts`` (int32 [B], optional) are the real rows of a padded batch.
 
+    Draft tokens are taken back by passing the smaller length; the scales that
+    they made grow, and what their queries added to scores, stay.
+
     K, V [B, H, capacity, d] are the codes (torch.float8_e4m3fn or torch.int8),
     K_scale, V_scale [B, H, capacity / 32] the scales of blocks of 32 entries
     (powers of two; an entry is code * scale), pos and score [B, H, capacity]
@@ -182,7 +185,8 @@ class H2OBlockCache:
         each sequence holds; returns out (shaped like q).  ``causal``: the last
         entries are the queries' own tokens; ``accumulate``: the weights are
         added to the entries' scores; ``lse`` (fp32 [B, H * group, n]) receives
-        the log-sum-exps.  See h2o_bcache_attend."""
+        the log-sum-exps.  Rows of a sequence whose length or count is out of
+        range are not written (error_bits).  See h2o_bcache_attend."""
         n = self._tokens(q, "q")
         shape = self._shape(self._heads, n)
         with self._lock:
@@ -199,7 +203,9 @@ class H2OBlockCache:
     def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None):
         """Append k, v [B, H, n, d] behind ``lengths[b]`` entries, then attend
         causally with q [B, H * group, n, d]; returns out.  The caller adds the
-        counts (or n) to ``lengths`` afterwards.  See h2o_bcache_step."""
+        counts (or n) to ``lengths`` afterwards, and to ``position``, which is
+        needed from the first eviction on (the default are the lengths).  See
+        h2o_bcache_step."""
         n = self._tokens(q, "q")
         shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
         with self._lock:

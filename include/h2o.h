@@ -290,7 +290,11 @@ h2o_status h2o_get_error(h2o_cache_t cache);
  * The entries a sequence holds are not kept in the cache: every call takes
  * `lengths`, device int32 [B], so that one array serves the caches of every
  * layer, a captured graph reads the current values, and draft tokens are
- * taken back by passing the smaller length.  `counts` (device int32 [B] or
+ * taken back by passing the smaller length.  What the call did to earlier
+ * entries stays: a scale that the rejected rows made grow, to which the
+ * block's other codes were rounded anew (an int8 block that a value 2^3 times
+ * larger joined has three bits less for the entries that remain), and the
+ * weights that rejected queries added to scores.  `counts` (device int32 [B] or
  * NULL = n for every sequence) says how many of the call's n rows per
  * sequence are real, 0 <= counts[b] <= n; rows behind them are not read and
  * their outputs are left as they were.  A sequence whose length or count is
@@ -341,7 +345,8 @@ h2o_status h2o_bcache_set_stream(h2o_bcache_t cache, void *cuda_stream);
 h2o_status h2o_bcache_arrays(h2o_bcache_t cache, void **K, void **V, float **K_scale, float **V_scale,
                              int32_t **pos, float **score);
 
-/* Append n >= 1 rows per sequence: k, v (B, H, n, d) quantised into entries
+/* Append n rows (1 to capacity, also where counts say less) per sequence: k, v
+ * (B, H, n, d) quantised into entries
  * lengths[b] .. lengths[b] + counts[b] - 1.  Entry lengths[b] + t gets
  * position position[b] + t (position: device int32 [B], or NULL =
  * lengths) and score score[b][h][t] (device fp32 [B][H][n], for example the
@@ -358,13 +363,18 @@ h2o_status h2o_bcache_append(h2o_bcache_t cache, int n, const h2o_rows *k, const
  * softmax weights, summed over the head's group and the counts[b] queries,
  * are added to its score.  lse: device fp32 [B][H * group][n], natural-log
  * log-sum-exp of the scaled logits, or NULL.  A query that sees no entry gets
- * output 0 and lse -infinity. */
+ * output 0 and lse -infinity; one that holds a NaN or infinity, or whose
+ * logits pass fp32's range upwards, gets NaN and makes scores of entries that
+ * it sees NaN.  Outputs are sums of the weights in fp32 with each weight
+ * rounded to 16 bits (f16: 2^-11 of sum w |v|), then rounded to bf16. */
 h2o_status h2o_bcache_attend(h2o_bcache_t cache, int n, const h2o_rows *q, const int32_t *lengths,
                              const int32_t *counts, int causal, int accumulate, const h2o_rows *out, float *lse);
 
 /* h2o_bcache_append (new scores 0) followed by the causal h2o_bcache_attend
  * over lengths[b] + counts[b] entries, with the same results.  `lengths` are
- * those before the call; the caller adds the counts afterwards. */
+ * those before the call; the caller adds the counts afterwards.  Without
+ * `position` new entries get their indices as positions: right until the first
+ * eviction, behind which the caller has to count positions on its own. */
 h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h2o_rows *k, const h2o_rows *v,
                            const int32_t *lengths, const int32_t *counts, const int32_t *position,
                            int accumulate, const h2o_rows *out, float *lse);
@@ -374,7 +384,7 @@ h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h
  * plus the k_heavy others that rank highest, by score or (score_mode 1) by
  * score / (position[b] - pos), both in fp32 with the divisor at least 1;
  * entries whose pos is below n_sink (0 <= n_sink <= k_heavy) rank above all;
- * a NaN ranks below all; among equals the lowest index goes first.  The kept
+ * a NaN ranks as -infinity; among equals the lowest index goes first.  The kept
  * entries move to indices 0 .. k-1 in their order with their positions and
  * scores, and every block of them is quantised anew from the values its
  * entries stood for (a fresh block in the sense above).  Codes, positions and
@@ -389,7 +399,7 @@ h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_he
  * H2O_EDEVICE with its bits in *bits (may be NULL). */
 #define H2O_BERR_RANGE 1     /* a length or count out of range: that sequence was left alone */
 #define H2O_BERR_NONFINITE 2 /* a NaN or infinity was appended */
-#define H2O_BERR_INTERNAL 4  /* a kernel gave up a wait, or found a count that does not add up */
+#define H2O_BERR_INTERNAL 4  /* a kernel gave up a wait: the results of that call are not to be used */
 h2o_status h2o_bcache_get_error(h2o_bcache_t cache, int *bits);
 
 /* Human-readable name of a status; the last CUDA error code seen by the

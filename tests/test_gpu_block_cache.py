@@ -719,6 +719,36 @@ def test_serving_run():
     assert c.error_bits() == 0
 
 
+@pytest.mark.parametrize("mode", [0, 1])
+def test_positions_count_on_behind_evictions(mode):
+    """Prompts, steps and evictions with lengths and positions kept apart: the positions of a head's entries increase
+    throughout, end with the last token's, and rank by mean weight as the reference does."""
+    B, H, G, d, cap = 3, 2, 2, 64, 96
+    g = torch.Generator(DEV).manual_seed(173)
+    c, r = H2OBlockCache(B, H, d, cap, group=G, kv="int8"), RefCache(B, H, d, cap, G, "int8")
+    prompts, lengths = ints([40, 7, 61]), ints([0] * B)
+    k, v = rows(g, B, H, 61, d), rows(g, B, H, 61, d)
+    c.append(k, v, lengths, counts=prompts)
+    r.append(k, v, [0] * B, [40, 7, 61])
+    lengths = lengths + prompts
+    position = lengths.clone()
+    for t in range(60):
+        q, k, v = rows(g, B, H * G, 1, d, scale=2.0), rows(g, B, H, 1, d), rows(g, B, H, 1, d)
+        out = c.step(q, k, v, lengths, position=position)
+        want, _, tol, _ = r.step(q, k, v, lengths.tolist(), position=position.tolist())
+        close(out, want, tol, f"step {t}")
+        lengths += 1
+        position += 1
+        if t % 20 == 19:
+            load(r, c)
+            new = c.evict(lengths, 20, 12, score_mode=mode, position=position)
+            assert new.tolist() == r.evict(lengths.tolist(), 20, 12, 0, mode, position.tolist())
+            lengths = new
+        for b, n in enumerate(lengths.tolist()):
+            assert (c.pos[b, :, 1:n] > c.pos[b, :, : n - 1]).all() and (c.pos[b, :, n - 1] == position[b] - 1).all()
+        same_state(c, r)
+
+
 def test_prefill_then_block_cache():
     """The prompt through H2OCache.prefill (its column sums are the scores), then the block cache."""
     from h2o_heavy_hitter_decode_gb300 import H2OCache
