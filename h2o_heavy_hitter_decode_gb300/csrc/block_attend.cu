@@ -39,10 +39,12 @@
 // head_kernel: few and short heads, a CTA each, in one launch.
 //
 // Bound by memory up to about 16 rows: 8 heads of 262,000 entries, 537 MB of
-// codes, 86 us without scores, 92 % of the copy rate; with the logits of 8 rows
-// 107 us, and 17 us of the finishing launch.  Above, by the products'
-// instructions: 32 heads of 16,384 entries, d = 128, 256 rows 379 us, 181
-// TFLOP/s.
+// codes, 85 us without scores, 93 % of the copy rate; with the logits of 8 rows
+// 104 us, and about 20 us of the finishing launch.  Above, by the products'
+// instructions: 32 heads of 16,384 entries, d = 128, 256 rows 364 us, 189
+// TFLOP/s; each warp of a worker converts the block for itself, and above 64
+// rows the codes are read once for every 64.  With scores the logits' 8 bytes a
+// row and entry come on top: 64 rows 96 us without, 154 us with them.
 #include <cuda.h>
 
 #include <cfloat>
@@ -199,8 +201,9 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
 // warps that share the worker's ring.  8 to 16 warps and 96 to 192 KB of ring
 // to an SM; Q is in registers where a worker is one warp.  At d = 128 twelve
 // warps of 168 registers, at d = 64 also sixteen of 128, measured faster than
-// the other: 32 heads of 16,384 entries, d = 128, 32 rows 64 / 80 us, 64 rows
-// 101 / 121 us; d = 64, 64 rows 62 / 60 us.
+// the other: 32 heads of 16,384 entries, d = 128, 32 rows 60 / 89 us, 64 rows
+// 96 / 139 us; d = 64, 32 rows 37 / 38 us, 64 rows (sixteen) 60 / 60 us.  From
+// 17 rows on at d = 128 the 168 registers spill about 140 bytes.
 template <int D, int NR, int MT> struct Cfg {
   static constexpr int kTeams = MT == 2 ? 6 : MT == 4 && D == 128 ? 3 : 4;  // workers of a CTA, mostly of 12 warps in all
   static constexpr int kWarps = kTeams * MT;
@@ -427,7 +430,8 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
                     e3 = ex2(s[n][x][3] - mu1);
         lsum[n][0] += e0 + e2;
         lsum[n][1] += e1 + e3;
-        // 16 bits for the product with V: f16's 2^-11 per weight, an eighth of the output's own rounding
+        // 16 bits for the product with V: f16's 2^-11 of each weight, so 2^-11 of sum w |v|: an eighth of the output's own
+        // rounding where the values do not cancel
         const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
         p[n][2 * x] = transpose8(*(const uint32_t *)&a0);
         p[n][2 * x + 1] = transpose8(*(const uint32_t *)&a1);
@@ -675,10 +679,10 @@ constexpr int kHeadCap = 512;  // entries
 
 // A head of at most kHeadCap entries and 8 rows in one CTA, and with it the
 // append of a step, where the heads fit the device at once: one launch instead
-// of three that depend on each other.  Measured, us a step as a graph, this
-// form / the other: 32 heads of 256 entries 6.4 / 7.9, of 512 8.1 / 8.9, of
-// 1024 11.7 / 9.2; 128 cached heads x 4, 300 entries 8.5 / 12.1; 256 heads of
-// 512 12.8 / 14.1; 1024 heads of 512 47.7 / 35.1.  Each warp takes every W-th block through two stages of its
+// of three that depend on each other.  Measured, us a step of 50 in a graph, this
+// form / the other: 32 heads of 256 entries 6.3 / 8.5, of 512 7.9 / 9.4, of
+// 1024 11.6 / 9.0; 128 cached heads x 4, 300 entries 8.6 / 11.8; 256 heads of
+// 512 12.5 / 14.9; 1024 heads of 512 47.3 / 31.0.  Each warp takes every W-th block through two stages of its
 // own; the warp of a block that receives new rows quantises them first.  The
 // logits stay in shared memory; when every warp is done the CTA joins the
 // rows' outputs and adds the weights to the scores.
@@ -999,8 +1003,8 @@ __global__ void __launch_bounds__(kFinWarps * 32, 3) finish_kernel(const Args a)
       }
       if (V == 1) load(0);
     };
-    // One four a lane (many rows): its first loads are on their way while the LSE is gathered (draft tokens 47 -> 39 us
-    // a step); four of them would not fit the registers beside that (long text 122 -> 128 us).
+    // One four a lane (many rows): its first loads are on their way while the LSE is gathered (draft tokens, a step of 50
+    // in a graph: 44.5 us without, 37.8 us with it); four of them would not fit the registers beside that.
     if (V == 1) first();
     // Eight rows to a warp, a lane of each group of eight for one; the four groups, and the warps that have the same
     // rows, take the parts in turn.
@@ -1159,7 +1163,8 @@ Args args_of(const View &c, const Lens &l, const Rows &q, int causal, int accumu
   a.workers = 0;
   a.rows = l.n * c.group;
   // Codes of more than L2's size evict each other before the next call reads them; the logits, which are read again
-  // in this one, then stay.  56 heads, 1.3 GB of codes: 239 us without the hint.
+  // in this one, then stay.  8 heads of 262,000 entries: 129 us a step, 134 without the hint; 56 heads, 1.3 GB of codes:
+  // 246 both.
   a.streams = 2 * (int64_t)c.B * c.H * c.cap * c.d > (int64_t)c.l2_bytes;
   a.po = nullptr;
   a.ml = nullptr;

@@ -26,10 +26,11 @@
 // Every destination block gets a fresh scale from the values it receives; rows
 // whose scale it shares go over unchanged.
 //
-// Bound by memory in the move (1024 heads, 8,448 -> 1,690 entries: 142 us, 92 %
-// of the copy rate) and by the first digit's atomics in the selection (60 us
-// alone, part of it under other heads' moves: 173 to 185 us in all); on few heads by
-// latency (8 heads, 131,072 -> 26,214: 53 us, of it 22 us selection).
+// Bound by memory in the move and by the first digit's atomics in the selection
+// (1024 heads, 8,448 -> 1,690 entries: 174 us in all, 80 % of the copy rate; a
+// selection alone takes 60 us, and part of it lies under other heads' moves); on
+// few heads by latency (8 heads, 131,072 -> 26,214: 57 us, of it about 20 us
+// selection).
 #include <cooperative_groups.h>
 
 #include "block_cache.cuh"
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(W * 32, 2) evict_kernel(const Args a) {
     return x;
   };
   // A round has two items, K and V of a block, for each warp: two independent chains of work, and half the barriers of
-  // one (1024 heads 189 -> 185 us, 8 long ones 60 -> 53 us).  The next round's are on their way meanwhile.
+  // one (1024 heads 4 us less of 174, 8 long ones 7 us less of 57).  The next round's are on their way meanwhile.
   const int stride = P * W * 2;
   int q = (rank * W + warp) * 2;
   Entry next[2];
@@ -490,8 +491,8 @@ template <typename F, int D, int P, int W> cudaError_t evict_p(Args a, cudaStrea
 
 template <typename F, int D> cudaError_t evict_t(const Args &a, cudaStream_t st) {
   // Up to 16 CTAs share a head while the clusters all fit the device (two CTAs an SM; of 16, whose CTAs have to find
-  // room in one GPC, 14 clusters fit) and each has a thousand entries.  8 heads of 131,072 entries: 58 us with 16, 76
-  // with 8, 150 with 4 (with rounds of one item a warp; 53 with 16 now).
+  // room in one GPC, 14 clusters fit) and each has a thousand entries.  8 heads of 131,072 entries: 57 us with 16, 64
+  // with 8, 149 with 4.
   const int heads = a.c.B * a.c.H;
   auto shared = [&](int p) { return heads * p <= a.c.sms * 15 / 8 && a.c.cap / p >= 1024; };
   if (heads * 32 <= a.c.sms * 3 && a.c.cap >= 16384) return evict_p<F, D, 16, 8>(a, st);
