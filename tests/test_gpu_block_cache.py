@@ -875,6 +875,47 @@ def test_two_caches_on_two_streams():
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+def test_two_host_threads_with_caches_of_their_own():
+    """Caches of other capacities, so of other amounts of shared memory, from two host threads on streams of their own:
+    the same bits as one after the other."""
+    import threading
+
+    def work(seed, cap, outs):
+        c, _, g = filled(seed, 2, 3, 64, cap, [cap - 40, 9], 4, 2, "int8", junk=False)
+        q, k, v = rows(g, 2, 12, 2, 64), rows(g, 2, 3, 2, 64), rows(g, 2, 3, 2, 64)
+        L = ints([cap - 40, 9])
+        for i in range(12):
+            outs.append(c.step(q, k, v, L).clone())
+            L = c.evict(L + 2, cap // 2 - i, 10)
+        outs += [L] + [getattr(c, n).clone() for n in ("K", "V", "K_scale", "V_scale", "pos", "score")]
+        assert c.error_bits() == 0
+
+    shapes = [(179, 512), (181, 96), (191, 20480), (193, 6144)]
+    want = [[] for _ in shapes]
+    for (seed, cap), outs in zip(shapes, want):
+        work(seed, cap, outs)
+    got, errors = [[] for _ in shapes], []
+
+    def in_thread(seed, cap, outs):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                work(seed, cap, outs)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001  (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=in_thread, args=(*s, o)) for s, o in zip(shapes, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for w, o in zip(want, got):
+        assert len(w) == len(o)
+        for x, y in zip(w, o):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_same_call_twice_gives_the_same_bits():
     lens = [3000, 1234, 17]
     outs = []
