@@ -17,6 +17,11 @@ queries, 8-bit codes with one scale per block of entries, eviction in bulk.
     cache.append(K, V, lengths, score=colsum)        # the prompt: [B,H,n,d]
     out = cache.step(q, k, v, lengths, position=position)  # q [B,H*G,1,d], k, v [B,H,1,d]
     lengths = cache.evict(lengths, k_heavy, k_local)       # position (int32 [B]) counts on
+
+``H2ORotary`` norms and rotates queries and keys before they meet a cache.
+
+    rotary = H2ORotary(d, eps=1e-6, q_weight=wq, k_weight=wk)
+    q, k = rotary.apply(q, k, position)
 """
 from __future__ import annotations
 
@@ -26,7 +31,7 @@ import re
 
 import torch
 
-__all__ = ["H2OCache", "H2OBlockCache", "H2OError", "lib", "LIB_PATH", "HEADER_PATH", "declared_functions", "kernel_arch", "probe_read_gbs"]
+__all__ = ["H2OCache", "H2OBlockCache", "H2ORotary", "H2OError", "lib", "LIB_PATH", "HEADER_PATH", "declared_functions", "kernel_arch", "probe_read_gbs"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libh2o.so")
@@ -110,6 +115,7 @@ def lib():
         L.h2o_bcache_step.argtypes = [vp, i32, rows, rows, rows, vp, vp, vp, i32, rows, vp]
         L.h2o_bcache_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
         L.h2o_bcache_get_error.argtypes = [vp, C.POINTER(i32)]
+        L.h2o_rotate.argtypes = [vp] + [i32] * 5 + [rows, rows, vp, i32, vp, rows, rows, vp]
         for f in ("h2o_cache_create", "h2o_cache_destroy", "h2o_set_stream", "h2o_prefill", "h2o_prefill_rows",
                   "h2o_decode_step",
                   "h2o_decode_steps", "h2o_cache_export", "h2o_cache_import", "h2o_cache_info",
@@ -118,7 +124,7 @@ def lib():
                   "h2o_cache_export_scales", "h2o_cache_import_scales",
                   "h2o_bcache_create", "h2o_bcache_destroy", "h2o_bcache_set_stream", "h2o_bcache_arrays",
                   "h2o_bcache_append", "h2o_bcache_attend", "h2o_bcache_step", "h2o_bcache_evict",
-                  "h2o_bcache_get_error"):
+                  "h2o_bcache_get_error", "h2o_rotate"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -385,3 +391,4 @@ class H2OCache:
 
 
 from .block_cache import H2OBlockCache  # noqa: E402  (uses the names above)
+from .rotary import H2ORotary  # noqa: E402

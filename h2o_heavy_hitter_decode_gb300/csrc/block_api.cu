@@ -6,6 +6,7 @@
 #include <new>
 
 #include "block_cache.cuh"
+#include "rows.h"
 
 using namespace h2o;
 
@@ -75,33 +76,7 @@ Layout layout(int B, int H, int d, int64_t cap, int rows, int sms) {
   return l;
 }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// Reads of a row start at 16-byte boundaries.
-bool rows_ok(const h2o_rows *r) {
-  if (!r || !r->data || !aligned(r->data, 16)) return false;
-  return r->stride_b >= 0 && r->stride_h >= 0 && r->stride_t >= 0 && r->stride_b % 8 == 0 && r->stride_h % 8 == 0 &&
-         r->stride_t % 8 == 0;
-}
-// No two rows of an output share memory: in the order of their strides, each
-// dimension steps over everything the smaller ones span.
-bool rows_apart(const h2o_rows *r, int B, int H, int n, int d) {
-  int64_t size[3] = {B, H, n}, step[3] = {r->stride_b, r->stride_h, r->stride_t};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (step[j] < step[i]) {
-        const int64_t s = step[i], z = size[i];
-        step[i] = step[j], size[i] = size[j];
-        step[j] = s, size[j] = z;
-      }
-  int64_t span = d;
-  for (int i = 0; i < 3; ++i) {
-    if (size[i] == 1) continue;
-    if (step[i] < span) return false;
-    span = step[i] * (size[i] - 1) + span;
-  }
-  return true;
-}
+bool rows_ok(const h2o_rows *r) { return rows_fit(r, 8); }
 blk::Rows rows_of(const h2o_rows *r) {
   return blk::Rows{(const __nv_bfloat16 *)r->data, r->stride_b, r->stride_h, r->stride_t};
 }

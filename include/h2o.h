@@ -402,6 +402,49 @@ h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_he
 #define H2O_BERR_INTERNAL 4  /* a kernel gave up a wait: the results of that call are not to be used */
 h2o_status h2o_bcache_get_error(h2o_bcache_t cache, int *bits);
 
+/* ---------------------------------------------------------------------------
+ * Norm and rotation of queries and keys, before they meet a cache.
+ *
+ * Row x of d elements (head h, token t of sequence b) becomes
+ *   y = x / sqrt(mean x^2 + eps) * w      where norm is set, w the queries' or
+ *                                         the keys' weight; else y = x,
+ * and then pair i of its first 2 * pairs dimensions is turned by the angle
+ *   2 pi * position * turns[i] / 2^64:
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),
+ * with (a, b) = (i, i + pairs), or (2 i, 2 i + 1) where interleaved is set.
+ * The product of a position and a frequency is taken in 64-bit integers that
+ * wrap at whole turns, so angles of far positions lose nothing; all else is
+ * fp32, rounded once at the end.  Mean squares are fp32 sums: a row whose sum of
+ * squares passes fp32's range becomes 0.
+ *
+ * position: int32 [B], token t being at position[b] + t on every axis, or with
+ * per_token set int32 [axes][B][n]; pair i takes that of axis[i] (the last axis
+ * for a number that is too large).  */
+typedef struct {
+  int d;           /* 64 or 128 */
+  int pairs;       /* a multiple of 8, 2 * pairs <= d; 0: no rotation */
+  int interleaved;
+  int axes;        /* >= 1 */
+  int norm;
+  float eps;               /* >= 0 */
+  const uint64_t *turns;   /* device [pairs]: 2^64 times the fraction of a turn that a position is */
+  const uint8_t *axis;     /* device [pairs], or NULL: all on axis 0 */
+  const float *q_weight;   /* device [d], 16-byte aligned, or NULL: ones */
+  const float *k_weight;   /* the same */
+} h2o_rotary;
+
+/* q (B, q_heads, n, d) -> q_out, k (B, k_heads, n, d) -> k_out in one launch on
+ * cuda_stream of the current device; dtype H2O_F32 or H2O_BF16, the rows'
+ * element type.  Rows start at 16-byte boundaries (strides are multiples of 8
+ * elements for bf16, of 4 for fp32).  Either may be left out (0 heads, NULLs).
+ * An output may be the input's own rows (the same address and strides); else it
+ * must not overlap any argument.  counts: device int32 [B], or NULL = n: rows
+ * behind them are not read and their outputs are left as they were; a count
+ * outside 0 .. n is taken as the nearer of the two. */
+h2o_status h2o_rotate(const h2o_rotary *rotary, h2o_dtype dtype, int B, int n, int q_heads, int k_heads,
+                      const h2o_rows *q, const h2o_rows *k, const int32_t *position, int per_token,
+                      const int32_t *counts, const h2o_rows *q_out, const h2o_rows *k_out, void *cuda_stream);
+
 /* Human-readable name of a status; the last CUDA error code seen by the
  * library (0 = none). */
 const char *h2o_status_str(h2o_status s);
