@@ -115,6 +115,12 @@ def lib():
         L.h2o_bcache_step.argtypes = [vp, i32, rows, rows, rows, vp, vp, vp, i32, rows, vp]
         L.h2o_bcache_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
         L.h2o_bcache_get_error.argtypes = [vp, C.POINTER(i32)]
+        L.h2o_bcache_bounds_bytes.argtypes = [vp]
+        L.h2o_bcache_bounds_bytes.restype = sz
+        L.h2o_bcache_set_bounds.argtypes = [vp, vp]
+        L.h2o_bcache_bound.argtypes = [vp, vp]
+        L.h2o_bcache_attend_sparse.argtypes = [vp, i32, rows, vp, vp, i32, i32, i32, i32, i32, rows, vp, vp]
+        L.h2o_bcache_step_sparse.argtypes = [vp, i32, rows, rows, rows, vp, vp, vp, i32, i32, i32, i32, rows, vp, vp]
         L.h2o_rotate.argtypes = [vp] + [i32] * 5 + [rows, rows, vp, i32, vp, rows, rows, vp]
         for f in ("h2o_cache_create", "h2o_cache_destroy", "h2o_set_stream", "h2o_prefill", "h2o_prefill_rows",
                   "h2o_decode_step",
@@ -124,7 +130,8 @@ def lib():
                   "h2o_cache_export_scales", "h2o_cache_import_scales",
                   "h2o_bcache_create", "h2o_bcache_destroy", "h2o_bcache_set_stream", "h2o_bcache_arrays",
                   "h2o_bcache_append", "h2o_bcache_attend", "h2o_bcache_step", "h2o_bcache_evict",
-                  "h2o_bcache_get_error", "h2o_rotate"):
+                  "h2o_bcache_get_error", "h2o_bcache_set_bounds", "h2o_bcache_bound", "h2o_bcache_attend_sparse",
+                  "h2o_bcache_step_sparse", "h2o_rotate"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib

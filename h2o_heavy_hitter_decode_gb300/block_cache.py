@@ -40,7 +40,10 @@ class H2OBlockCache:
     K_scale, V_scale [B, H, capacity / 32] the scales of blocks of 32 entries
     (powers of two; an entry is code * scale), pos and score [B, H, capacity]
     the entries' positions and accumulated attention weights: views of the
-    workspace, one torch uint8 tensor owned by this object.  Calls enqueue on
+    workspace, one torch uint8 tensor owned by this object.  With ``bounds`` the
+    cache keeps, for ``step_sparse`` and ``attend_sparse``, bounds [B, H,
+    capacity / 32, 2, d] (torch.int8): the least and largest code of each
+    dimension of a block's keys (in units of 4 for e4m3).  Calls enqueue on
     torch's current CUDA stream of the cache's device; calls of one cache must
     not overlap on the GPU (host threads may share a cache: each call passes
     its own arguments and its own stream, one thread at a time).  A cache may
@@ -50,7 +53,7 @@ class H2OBlockCache:
     BLOCK = 32
 
     def __init__(self, B: int, H: int, d: int, capacity: int, group: int = 1, max_queries: int = 1, kv: str = "e4m3",
-                 device=None):
+                 device=None, bounds: bool = False):
         L = self._lib = lib()
         if kv not in KV:
             raise ValueError(f"kv must be one of {sorted(KV)}, got {kv!r}")
@@ -92,6 +95,12 @@ class H2OBlockCache:
         self.K, self.V = self._view(at[0], store, rows + (d,)), self._view(at[1], store, rows + (d,))
         self.K_scale, self.V_scale = self._view(at[2], torch.float32, blocks), self._view(at[3], torch.float32, blocks)
         self.pos, self.score = self._view(at[4], torch.int32, rows), self._view(at[5], torch.float32, rows)
+        self.bounds = None
+        if bounds:
+            with torch.cuda.device(self.device):
+                self.bounds = torch.zeros(blocks + (2, d), dtype=torch.int8, device=self.device)
+            assert self.bounds.nbytes == L.h2o_bcache_bounds_bytes(h)
+            _check(L.h2o_bcache_set_bounds(h, _ptr(self.bounds)), "h2o_bcache_set_bounds")
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -115,7 +124,9 @@ class H2OBlockCache:
         if s != self._set_stream:
             if s not in self._recorded:
                 # a cache that is dropped while this stream still runs its kernels keeps its memory until they are done
-                self.workspace.record_stream(torch.cuda.current_stream(self.device))
+                for t in (self.workspace, self.bounds):
+                    if t is not None:
+                        t.record_stream(torch.cuda.current_stream(self.device))
                 self._recorded.add(s)
             _check(self._lib.h2o_bcache_set_stream(self._h, C.c_void_p(s)), "h2o_bcache_set_stream")
             self._set_stream = s
@@ -218,6 +229,65 @@ class H2OBlockCache:
             self._use_stream()
             _check(self._lib.h2o_bcache_step(self._h, n, *args), "h2o_bcache_step")
         return out
+
+    def attend_sparse(self, q, lengths, n_blocks: int, n_first: int = 1, n_last: int = 2, counts=None, causal=True,
+                      accumulate=True, out=None, lse=None, blocks=None):
+        """``attend`` over ``n_blocks`` blocks of 32 entries for each query
+        token and cached head: the first ``n_first``, the last ``n_last`` and
+        those with the highest bound on the group's logits between them (all,
+        where there are no more).  ``blocks`` (int32 [B, H, n, n_blocks])
+        receives their indices, -1 behind them.  Needs a cache with ``bounds``.
+        See h2o_bcache_attend_sparse."""
+        n = self._tokens(q, "q")
+        shape, choice = self._shape(self._heads, n), self._choice(n_blocks, n_first, n_last)
+        with self._lock:
+            qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
+            cnt = self._dense(counts, I32, self._per_seq, "counts")
+            if out is None:
+                out = self._new_out(shape, counts)
+            args = (qr, lens, cnt, 1 if causal else 0, 1 if accumulate else 0, *choice, self._rows(3, out, shape, "out"),
+                    self._dense(lse, F32, shape[:3], "lse"), self._blocks(blocks, n, choice[0]))
+            self._use_stream()
+            _check(self._lib.h2o_bcache_attend_sparse(self._h, n, *args), "h2o_bcache_attend_sparse")
+        return out
+
+    def step_sparse(self, q, k, v, lengths, n_blocks: int, n_first: int = 1, n_last: int = 2, counts=None, position=None,
+                    accumulate=True, out=None, lse=None, blocks=None):
+        """``step`` whose queries attend to ``n_blocks`` chosen blocks each
+        (``attend_sparse``).  See h2o_bcache_step_sparse."""
+        n = self._tokens(q, "q")
+        shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
+        choice = self._choice(n_blocks, n_first, n_last)
+        with self._lock:
+            rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
+            lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
+            if out is None:
+                out = self._new_out(shape, counts)
+            args = rows + (lens, cnt, self._dense(position, I32, self._per_seq, "position"), 1 if accumulate else 0,
+                           *choice, self._rows(3, out, shape, "out"), self._dense(lse, F32, shape[:3], "lse"),
+                           self._blocks(blocks, n, choice[0]))
+            self._use_stream()
+            _check(self._lib.h2o_bcache_step_sparse(self._h, n, *args), "h2o_bcache_step_sparse")
+        return out
+
+    def bound(self, lengths):
+        """Make ``bounds`` anew for ``lengths`` entries a sequence: after K or
+        K_scale have been written other than by this object's calls."""
+        lens = self._lengths(lengths, "lengths")
+        with self._lock:
+            self._use_stream()
+            _check(self._lib.h2o_bcache_bound(self._h, lens), "h2o_bcache_bound")
+
+    @staticmethod
+    def _choice(n_blocks, n_first, n_last):
+        return _whole(n_blocks, "n_blocks"), _whole(n_first, "n_first"), _whole(n_last, "n_last")
+
+    def _blocks(self, t, n, n_blocks):
+        """Address of the chosen blocks' indices: the kernels hand them on through it, so it is always there."""
+        shape = (self.B, self.H, n, n_blocks)
+        if t is None and n_blocks > 0:
+            t = torch.empty(shape, dtype=I32, device=self.device)
+        return self._dense(t, I32, shape, "blocks")
 
     def _new_out(self, shape, counts):
         # rows behind a sequence's count are not written

@@ -99,6 +99,12 @@ bool code_map(CUtensorMap *m, const void *base, int d, int64_t entries) {
 
 bool ints_ok(const int32_t *p, bool may_be_null) { return p ? aligned(p, 4) : may_be_null; }
 
+// A choice of blocks holds the last one, whose bounds need not be current.
+bool choice_ok(const h2o_bcache *c, int n, int n_blocks, int n_first, int n_last, const int32_t *blocks) {
+  if (n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_blocks || !ints_ok(blocks, false)) return false;
+  return (int64_t)c->view.B * c->view.H * n * 8 <= 0x7fffffffLL;  // a grid of clusters
+}
+
 bool overlap(const int32_t *x, const int32_t *y, int n) {
   const uintptr_t a = (uintptr_t)x, z = (uintptr_t)y, bytes = (uintptr_t)n * sizeof(int32_t);
   return a < z + bytes && z < a + bytes;
@@ -190,7 +196,8 @@ h2o_status h2o_bcache_append(h2o_bcache_t c, int n, const h2o_rows *k, const h2o
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
-  const cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, score, c->stream);
+  cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, score, c->stream);
+  if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -224,13 +231,15 @@ h2o_status h2o_bcache_step(h2o_bcache_t c, int n, const h2o_rows *q, const h2o_r
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
   if (blk::head_fits(c->view, n)) {
     const blk::Rows kr = rows_of(k), vr = rows_of(v);
-    const cudaError_t e = blk::launch_head(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, rows_of(out),
-                                           lse, c->kmap, c->vmap, c->stream);
+    cudaError_t e = blk::launch_head(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, rows_of(out), lse,
+                                     c->kmap, c->vmap, c->stream);
+    if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
     return e == cudaSuccess ? H2O_OK : fail(e);
   }
   cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
   if (e == cudaSuccess)
     e = blk::launch_attend(c->view, l, rows_of(q), 1, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);
+  if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -245,8 +254,67 @@ h2o_status h2o_bcache_evict(h2o_bcache_t c, const int32_t *lengths, int k_heavy,
     return H2O_EINVAL;
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
-  const cudaError_t e = blk::launch_evict(c->view, lengths, k_heavy, k_local, n_sink, score_mode, position,
-                                          new_lengths, c->stream);
+  cudaError_t e = blk::launch_evict(c->view, lengths, k_heavy, k_local, n_sink, score_mode, position, new_lengths,
+                                    c->stream);
+  if (e == cudaSuccess && c->view.bounds)
+    e = blk::launch_bound(c->view, blk::Lens{new_lengths, nullptr, 1, 0, c->view.cap}, 1, c->stream);
+  return e == cudaSuccess ? H2O_OK : fail(e);
+}
+
+size_t h2o_bcache_bounds_bytes(h2o_bcache_t c) {
+  return c ? (size_t)c->view.B * c->view.H * (c->view.cap / H2O_BLOCK) * 2 * c->view.d : 0;
+}
+
+h2o_status h2o_bcache_set_bounds(h2o_bcache_t c, void *bounds) {
+  if (!c || !aligned(bounds, 16)) return H2O_EINVAL;
+  c->view.bounds = (int8_t *)bounds;
+  return H2O_OK;
+}
+
+h2o_status h2o_bcache_bound(h2o_bcache_t c, const int32_t *lengths) {
+  if (!c || !ints_ok(lengths, false)) return H2O_EINVAL;
+  if (!c->view.bounds) return H2O_ESTATE;
+  OnDevice on(c->device);
+  if (on.err != cudaSuccess) return fail(on.err);
+  const cudaError_t e = blk::launch_bound(c->view, blk::Lens{lengths, nullptr, 1, 0, c->view.cap}, 1, c->stream);
+  return e == cudaSuccess ? H2O_OK : fail(e);
+}
+
+h2o_status h2o_bcache_attend_sparse(h2o_bcache_t c, int n, const h2o_rows *q, const int32_t *lengths,
+                                    const int32_t *counts, int causal, int accumulate, int n_blocks, int n_first,
+                                    int n_last, const h2o_rows *out, float *lse, int32_t *blocks) {
+  if (!c || n < 1 || n > c->max_queries || !rows_ok(q) || !rows_ok(out)) return H2O_EINVAL;
+  if (!ints_ok(lengths, false) || !ints_ok(counts, true) || !aligned(lse, 4)) return H2O_EINVAL;
+  if (!rows_apart(out, c->view.B, c->view.H * c->view.group, n, c->view.d)) return H2O_EINVAL;
+  if (!choice_ok(c, n, n_blocks, n_first, n_last, blocks)) return H2O_EINVAL;
+  if (!c->view.bounds) return H2O_ESTATE;
+  OnDevice on(c->device);
+  if (on.err != cudaSuccess) return fail(on.err);
+  const blk::Lens l{lengths, counts, n, 0, c->view.cap};
+  const cudaError_t e = blk::launch_sparse(c->view, l, rows_of(q), causal != 0, accumulate != 0, n_blocks, n_first, n_last,
+                                           rows_of(out), lse, blocks, c->kmap, c->vmap, c->stream);
+  return e == cudaSuccess ? H2O_OK : fail(e);
+}
+
+h2o_status h2o_bcache_step_sparse(h2o_bcache_t c, int n, const h2o_rows *q, const h2o_rows *k, const h2o_rows *v,
+                                  const int32_t *lengths, const int32_t *counts, const int32_t *position,
+                                  int accumulate, int n_blocks, int n_first, int n_last, const h2o_rows *out, float *lse,
+                                  int32_t *blocks) {
+  if (!c || n < 1 || n > c->max_queries || n > c->view.cap) return H2O_EINVAL;
+  if (!rows_ok(q) || !rows_ok(k) || !rows_ok(v) || !rows_ok(out)) return H2O_EINVAL;
+  if (!ints_ok(lengths, false) || !ints_ok(counts, true) || !ints_ok(position, true) || !aligned(lse, 4))
+    return H2O_EINVAL;
+  if (!rows_apart(out, c->view.B, c->view.H * c->view.group, n, c->view.d)) return H2O_EINVAL;
+  if (!choice_ok(c, n, n_blocks, n_first, n_last, blocks)) return H2O_EINVAL;
+  if (!c->view.bounds) return H2O_ESTATE;
+  OnDevice on(c->device);
+  if (on.err != cudaSuccess) return fail(on.err);
+  const blk::Lens l{lengths, counts, n, 1, c->view.cap};
+  cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
+  if (e == cudaSuccess) e = blk::launch_bound(c->view, l, 0, c->stream);
+  if (e == cudaSuccess)
+    e = blk::launch_sparse(c->view, l, rows_of(q), 1, accumulate != 0, n_blocks, n_first, n_last, rows_of(out), lse, blocks,
+                           c->kmap, c->vmap, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 

@@ -23,6 +23,7 @@ struct View {
   float *Ksc, *Vsc;                   // [B*H][cap / kBlock]
   int32_t *pos;                       // [B*H][cap]
   float *score;                       // [B*H][cap]
+  int8_t *bounds;                     // [B*H][cap / kBlock][2][d] least and largest key codes of blocks, or null
   float *low;                         // [B*H][cap] what the scores' fp32 sums have lost (add_score)
   float *logits;                      // [B*H][max_rows][cap] scratch, base-2 logits
   float *part;                        // scratch, split partials
@@ -244,6 +245,12 @@ cudaError_t launch_head(const View &c, const Lens &l, const Rows &q, const Rows 
 size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms);
 cudaError_t launch_evict(const View &c, const int32_t *lengths, int k_heavy, int k_local, int n_sink, int score_mode,
                          const int32_t *position, int32_t *new_lengths, cudaStream_t st);
+// Bounds of the blocks that the call's rows went to (l.appends), or with `whole` of all that hold l.lengths entries.
+cudaError_t launch_bound(const View &c, const Lens &l, int whole, cudaStream_t st);
+// Attention over n_blocks chosen blocks a token; blocks [B*H][n][n_blocks] receives their indices.
+cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, int n_blocks,
+                          int n_first, int n_last, const Rows &out, float *lse, int32_t *blocks, const CUtensorMap &kmap,
+                          const CUtensorMap &vmap, cudaStream_t st);
 
 }  // namespace blk
 }  // namespace h2o

@@ -395,6 +395,49 @@ h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h
 h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_heavy, int k_local, int n_sink,
                             int score_mode, const int32_t *position, int32_t *new_lengths);
 
+/* Sparse attention: of a long cache each query token reads the blocks of
+ * H2O_BLOCK entries that may matter to it, and the cache keeps the others (an
+ * eviction would not).
+ *
+ * What a block may matter is bounded by the least and largest code of each
+ * dimension of its keys, kept beside the cache in a buffer of the caller's:
+ * int8 [B][H][capacity / H2O_BLOCK][2][d], 16-byte aligned, least first, in
+ * codes for int8 and in units of 4 (rounded outwards) for e4m3.  With
+ * h2o_bcache_set_bounds the cache has them kept current by every call that
+ * changes entries (NULL: no longer).  h2o_bcache_bound makes them anew for
+ * lengths[b] entries of each sequence: for a cache that held entries before, and
+ * after the caller has written K or K_scale itself. */
+size_t h2o_bcache_bounds_bytes(h2o_bcache_t cache);
+h2o_status h2o_bcache_set_bounds(h2o_bcache_t cache, void *bounds);
+h2o_status h2o_bcache_bound(h2o_bcache_t cache, const int32_t *lengths);
+
+/* h2o_bcache_attend over n_blocks chosen blocks.  The choice is made for each
+ * token t and cached head.  Of the nb blocks that hold the entries the token
+ * sees (all, if nb <= n_blocks) it keeps the first n_first, the last n_last, and
+ * of the others those with the highest keys, the lowest index first among
+ * equals:
+ *   x_gi = q_gi / 2^e to nearest even, e >= -100 the least with |q| <= 127 * 2^e
+ *          for the finite elements of the token's `group` rows (a NaN counts 0,
+ *          an infinity 127);
+ *   key_j = K_scale_j * max_g sum_i (x_gi > 0 ? x_gi hi_ji : x_gi lo_ji).
+ * n_first >= 0, n_last >= 1, n_first + n_last <= n_blocks.  Keys are exact, so
+ * the choice is the same everywhere.  Outputs, lse and the weights added to
+ * scores are those of attention over the chosen blocks' entries alone (a NaN
+ * query makes scores of its chosen entries NaN).  blocks: device int32 [B][H][n][n_blocks],
+ * receives each token's blocks in ascending order, -1 behind them; must not
+ * overlap any argument.  H2O_ESTATE without bounds. */
+h2o_status h2o_bcache_attend_sparse(h2o_bcache_t cache, int n, const h2o_rows *q, const int32_t *lengths,
+                                    const int32_t *counts, int causal, int accumulate, int n_blocks, int n_first,
+                                    int n_last, const h2o_rows *out, float *lse, int32_t *blocks);
+
+/* h2o_bcache_append (new scores 0) followed by the causal
+ * h2o_bcache_attend_sparse over lengths[b] + counts[b] entries, with the same
+ * results; lengths and position as in h2o_bcache_step. */
+h2o_status h2o_bcache_step_sparse(h2o_bcache_t cache, int n, const h2o_rows *q, const h2o_rows *k, const h2o_rows *v,
+                                  const int32_t *lengths, const int32_t *counts, const int32_t *position,
+                                  int accumulate, int n_blocks, int n_first, int n_last, const h2o_rows *out, float *lse,
+                                  int32_t *blocks);
+
 /* Synchronises the stream and reads the sticky error flag: H2O_OK, or
  * H2O_EDEVICE with its bits in *bits (may be NULL). */
 #define H2O_BERR_RANGE 1     /* a length or count out of range: that sequence was left alone */
