@@ -115,6 +115,7 @@ def lib():
         L.h2o_bcache_step.argtypes = [vp, i32, rows, rows, rows, vp, vp, vp, i32, rows, vp]
         L.h2o_bcache_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
         L.h2o_bcache_get_error.argtypes = [vp, C.POINTER(i32)]
+        L.h2o_bcache_copy.argtypes = [vp] * 6
         L.h2o_bcache_bounds_bytes.argtypes = [vp]
         L.h2o_bcache_bounds_bytes.restype = sz
         L.h2o_bcache_set_bounds.argtypes = [vp, vp]
@@ -130,7 +131,7 @@ def lib():
                   "h2o_cache_export_scales", "h2o_cache_import_scales",
                   "h2o_bcache_create", "h2o_bcache_destroy", "h2o_bcache_set_stream", "h2o_bcache_arrays",
                   "h2o_bcache_append", "h2o_bcache_attend", "h2o_bcache_step", "h2o_bcache_evict",
-                  "h2o_bcache_get_error", "h2o_bcache_set_bounds", "h2o_bcache_bound", "h2o_bcache_attend_sparse",
+                  "h2o_bcache_get_error", "h2o_bcache_copy", "h2o_bcache_set_bounds", "h2o_bcache_bound", "h2o_bcache_attend_sparse",
                   "h2o_bcache_step_sparse", "h2o_rotate"):
             getattr(L, f).restype = i32
         _lib = L

@@ -51,6 +51,7 @@ class H2OBlockCache:
     graph uses is kept for as long as the graph is replayed."""
 
     BLOCK = 32
+    bounds = None
 
     def __init__(self, B: int, H: int, d: int, capacity: int, group: int = 1, max_queries: int = 1, kv: str = "e4m3",
                  device=None, bounds: bool = False):
@@ -95,7 +96,6 @@ class H2OBlockCache:
         self.K, self.V = self._view(at[0], store, rows + (d,)), self._view(at[1], store, rows + (d,))
         self.K_scale, self.V_scale = self._view(at[2], torch.float32, blocks), self._view(at[3], torch.float32, blocks)
         self.pos, self.score = self._view(at[4], torch.int32, rows), self._view(at[5], torch.float32, rows)
-        self.bounds = None
         if bounds:
             with torch.cuda.device(self.device):
                 self.bounds = torch.zeros(blocks + (2, d), dtype=torch.int8, device=self.device)
@@ -122,14 +122,18 @@ class H2OBlockCache:
     def _use_stream(self):
         s = self._stream()
         if s != self._set_stream:
-            if s not in self._recorded:
-                # a cache that is dropped while this stream still runs its kernels keeps its memory until they are done
-                for t in (self.workspace, self.bounds):
-                    if t is not None:
-                        t.record_stream(torch.cuda.current_stream(self.device))
-                self._recorded.add(s)
+            self._record(s)
             _check(self._lib.h2o_bcache_set_stream(self._h, C.c_void_p(s)), "h2o_bcache_set_stream")
             self._set_stream = s
+
+    def _record(self, s):
+        """The current stream, s, runs kernels on this cache's memory: a cache that is dropped meanwhile keeps it until
+        they are done."""
+        if s not in self._recorded:
+            for t in (self.workspace, self.bounds):
+                if t is not None:
+                    t.record_stream(torch.cuda.current_stream(self.device))
+            self._recorded.add(s)
 
     def _dense(self, t, dtype, shape, name):
         """Address of a contiguous tensor, None for None."""
@@ -310,6 +314,36 @@ class H2OBlockCache:
         with self._lock:
             self._use_stream()
             _check(self._lib.h2o_bcache_evict(self._h, *args), "h2o_bcache_evict")
+        return new_lengths
+
+    def copy(self, parent, lengths, source=None, source_lengths=None, new_lengths=None):
+        """Row b receives the sequence of row ``parent[b]`` (int32 [B]; -1: it
+        stays), in place with any map, or out of the H2OBlockCache ``source``
+        that holds ``source_lengths``: beams reordered, prompts forked,
+        sequences moved up or taken into a running batch.  Returns the new
+        lengths (int32 [B]); what else the caller keeps for a row (positions)
+        is the caller's to reorder.  See h2o_bcache_copy."""
+        par, lens = self._dense(parent, I32, self._per_seq, "parent"), self._lengths(lengths, "lengths")
+        if par is None:
+            raise TypeError("parent must be a tensor")
+        if source is self:
+            source = None
+        if source is None:
+            if source_lengths is not None:
+                raise ValueError("source_lengths belong to another cache: pass it as source")
+            other, src = None, None
+        else:
+            if not isinstance(source, H2OBlockCache):
+                raise TypeError("source must be an H2OBlockCache")
+            other, src = source._h, source._lengths(source_lengths, "source_lengths")
+        if new_lengths is None:
+            new_lengths = torch.empty_like(lengths)
+        args = (other, par, src, lens, self._lengths(new_lengths, "new_lengths"))
+        with self._lock:
+            self._use_stream()
+            if source is not None:
+                source._record(self._set_stream)
+            _check(self._lib.h2o_bcache_copy(self._h, *args), "h2o_bcache_copy")
         return new_lengths
 
     def error_bits(self) -> int:

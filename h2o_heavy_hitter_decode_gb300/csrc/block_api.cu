@@ -105,9 +105,9 @@ bool choice_ok(const h2o_bcache *c, int n, int n_blocks, int n_first, int n_last
   return (int64_t)c->view.B * c->view.H * n * 8 <= 0x7fffffffLL;  // a grid of clusters
 }
 
-bool overlap(const int32_t *x, const int32_t *y, int n) {
-  const uintptr_t a = (uintptr_t)x, z = (uintptr_t)y, bytes = (uintptr_t)n * sizeof(int32_t);
-  return a < z + bytes && z < a + bytes;
+bool overlap(const int32_t *x, int nx, const int32_t *y, int ny) {
+  const uintptr_t a = (uintptr_t)x, z = (uintptr_t)y;
+  return a < z + (uintptr_t)ny * sizeof(int32_t) && z < a + (uintptr_t)nx * sizeof(int32_t);
 }
 
 }  // namespace
@@ -250,14 +250,36 @@ h2o_status h2o_bcache_evict(h2o_bcache_t c, const int32_t *lengths, int k_heavy,
   if (n_sink < 0 || n_sink > k_heavy || (score_mode != 0 && score_mode != 1)) return H2O_EINVAL;
   if (!ints_ok(lengths, false) || !ints_ok(new_lengths, false) || !ints_ok(position, true)) return H2O_EINVAL;
   // heads still read the lengths and positions when the first ones write the new lengths
-  if (overlap(lengths, new_lengths, c->view.B) || (position && overlap(position, new_lengths, c->view.B)))
+  if (overlap(lengths, c->view.B, new_lengths, c->view.B) ||
+      (position && overlap(position, c->view.B, new_lengths, c->view.B)))
     return H2O_EINVAL;
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   cudaError_t e = blk::launch_evict(c->view, lengths, k_heavy, k_local, n_sink, score_mode, position, new_lengths,
                                     c->stream);
   if (e == cudaSuccess && c->view.bounds)
-    e = blk::launch_bound(c->view, blk::Lens{new_lengths, nullptr, 1, 0, c->view.cap}, 1, c->stream);
+    e = blk::launch_bound(c->view, blk::Lens{new_lengths, nullptr, 1, 0, c->view.cap}, 2, c->stream);
+  return e == cudaSuccess ? H2O_OK : fail(e);
+}
+
+h2o_status h2o_bcache_copy(h2o_bcache_t c, h2o_bcache_t source, const int32_t *parent, const int32_t *source_lengths,
+                           const int32_t *lengths, int32_t *new_lengths) {
+  if (!c || !ints_ok(parent, false) || !ints_ok(lengths, false) || !ints_ok(new_lengths, false)) return H2O_EINVAL;
+  const bool same = !source || source == c;
+  if (same) source = c;
+  if (same ? source_lengths != nullptr : !ints_ok(source_lengths, false)) return H2O_EINVAL;
+  const blk::View &to = c->view, &from = source->view;
+  if (source->device != c->device || to.H != from.H || to.d != from.d || to.kv != from.kv) return H2O_EINVAL;
+  // rows still read the lengths when the first ones write the new lengths
+  if (overlap(lengths, to.B, new_lengths, to.B) || overlap(parent, to.B, new_lengths, to.B) ||
+      (!same && overlap(source_lengths, from.B, new_lengths, to.B)))
+    return H2O_EINVAL;
+  if (to.B > blk::kCopyRows || from.B > blk::kCopyRows) return H2O_EUNSUPPORTED;
+  OnDevice on(c->device);
+  if (on.err != cudaSuccess) return fail(on.err);
+  cudaError_t e = blk::launch_copy(to, from, parent, same ? lengths : source_lengths, lengths, new_lengths, c->stream);
+  if (e == cudaSuccess && to.bounds && !from.bounds)
+    e = blk::launch_bound(to, blk::Lens{new_lengths, nullptr, 1, 0, to.cap}, 2, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 

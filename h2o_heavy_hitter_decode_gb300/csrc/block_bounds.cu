@@ -19,7 +19,8 @@ constexpr int kWarps = 4;
 template <typename F> constexpr float kPerUnit = 1.f;
 template <> constexpr float kPerUnit<E4M3> = 0.25f;
 
-// Blocks of a call: those that its rows went to, or (whole) all that hold entries.
+// Blocks of a call: those that its rows went to, or (whole) all that hold entries; whole = 2
+// passes over lengths out of range, which the call before has reported.
 template <typename F, int D>
 __global__ void __launch_bounds__(kWarps * 32) bound_kernel(const View c, const Lens l, int whole, int blocks) {
   using T = ToF16<F>;
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(kWarps * 32) bound_kernel(const View c, const 
   if (whole) {
     first = 0, total = l.lengths[b];
     if (total < 0 || total > c.cap) {
-      if (lane == 0 && j == 0 && h == 0) atomicOr(c.err, H2O_BERR_RANGE);
+      if (whole == 1 && lane == 0 && j == 0 && h == 0) atomicOr(c.err, H2O_BERR_RANGE);
       return;
     }
   } else {

@@ -245,7 +245,12 @@ cudaError_t launch_head(const View &c, const Lens &l, const Rows &q, const Rows 
 size_t attend_scratch_bytes(int B, int H, int d, int max_rows, int sms);
 cudaError_t launch_evict(const View &c, const int32_t *lengths, int k_heavy, int k_local, int n_sink, int score_mode,
                          const int32_t *position, int32_t *new_lengths, cudaStream_t st);
-// Bounds of the blocks that the call's rows went to (l.appends), or with `whole` of all that hold l.lengths entries.
+// Row b of `to` receives row parent[b] of `from` (the same cache or another of its kind); at most kCopyRows rows each.
+constexpr int kCopyRows = 4096;
+cudaError_t launch_copy(const View &to, const View &from, const int32_t *parent, const int32_t *from_lengths,
+                        const int32_t *lengths, int32_t *new_lengths, cudaStream_t st);
+// Bounds of the blocks that the call's rows went to (l.appends), or with `whole` of all that hold l.lengths
+// entries (1 reports lengths out of range, 2 does not).
 cudaError_t launch_bound(const View &c, const Lens &l, int whole, cudaStream_t st);
 // Attention over n_blocks chosen blocks a token; blocks [B*H][n][n_blocks] receives their indices.
 cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, int n_blocks,

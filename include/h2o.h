@@ -395,6 +395,25 @@ h2o_status h2o_bcache_step(h2o_bcache_t cache, int n, const h2o_rows *q, const h
 h2o_status h2o_bcache_evict(h2o_bcache_t cache, const int32_t *lengths, int k_heavy, int k_local, int n_sink,
                             int score_mode, const int32_t *position, int32_t *new_lengths);
 
+/* Copy sequences: row b of the cache receives what row parent[b] of `source`
+ * holds (the same cache, also given as NULL, or another one of the same H, d,
+ * kind and device): beams reordered after a search step, a prompt forked, rows
+ * of finished sequences filled from others, a prefilled sequence taken into a
+ * running batch.  parent: device int32 [B], -1 = the row stays.  In place any map
+ * is fine.  All blocks that hold entries are copied whole (codes and scores behind
+ * the last entry of the last one too), with their scales, positions, scores and
+ * bounds; blocks behind them are left as they were.
+ * source_lengths: device int32 [source's B], NULL where the source is the cache
+ * itself; lengths: device int32 [B], before the call; new_lengths: device int32
+ * [B], receives source_lengths[parent[b]] (lengths[parent[b]]), or lengths[b]
+ * where the row stays; must not overlap the others.  A row whose parent is out of
+ * range, or whose source's length is or passes the cache's capacity, stays and
+ * raises bit H2O_BERR_RANGE.  On the cache's stream; no other call of the source
+ * may overlap that changes it.  H2O_EUNSUPPORTED for more than 4096 rows in
+ * either. */
+h2o_status h2o_bcache_copy(h2o_bcache_t cache, h2o_bcache_t source, const int32_t *parent,
+                           const int32_t *source_lengths, const int32_t *lengths, int32_t *new_lengths);
+
 /* Sparse attention: of a long cache each query token reads the blocks of
  * H2O_BLOCK entries that may matter to it, and the cache keeps the others (an
  * eviction would not).

@@ -75,3 +75,13 @@ def test_import_with_a_torch_without_cuda():
             "assert 'h2o_bcache_step' in h2o.declared_functions()\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=hbuild.ROOT)
     assert r.returncode == 0, r.stderr
+
+
+def test_null_handle_of_sparse_and_copy(L):
+    r, p = C.byref(h2o.Rows(256, 64, 64, 64)), C.c_void_p(256)
+    assert L.h2o_bcache_bounds_bytes(None) == 0
+    assert L.h2o_bcache_set_bounds(None, p) == 1
+    assert L.h2o_bcache_bound(None, p) == 1
+    assert L.h2o_bcache_attend_sparse(None, 1, r, p, None, 1, 1, 3, 1, 2, r, None, p) == 1
+    assert L.h2o_bcache_step_sparse(None, 1, r, r, r, p, None, None, 1, 3, 1, 2, r, None, p) == 1
+    assert L.h2o_bcache_copy(None, None, p, None, C.c_void_p(512), C.c_void_p(768)) == 1
