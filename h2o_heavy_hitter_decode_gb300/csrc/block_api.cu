@@ -102,7 +102,7 @@ bool ints_ok(const int32_t *p, bool may_be_null) { return p ? aligned(p, 4) : ma
 // A choice of blocks holds the last one, whose bounds need not be current.
 bool choice_ok(const h2o_bcache *c, int n, int n_blocks, int n_first, int n_last, const int32_t *blocks) {
   if (n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_blocks || !ints_ok(blocks, false)) return false;
-  return (int64_t)c->view.B * c->view.H * n * 8 <= 0x7fffffffLL;  // a grid of clusters
+  return (int64_t)c->view.B * c->view.H * n <= 0x7fffffffLL;  // a grid
 }
 
 bool overlap(const int32_t *x, int nx, const int32_t *y, int ny) {
@@ -196,8 +196,7 @@ h2o_status h2o_bcache_append(h2o_bcache_t c, int n, const h2o_rows *k, const h2o
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
-  cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, score, c->stream);
-  if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
+  const cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, score, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -231,15 +230,13 @@ h2o_status h2o_bcache_step(h2o_bcache_t c, int n, const h2o_rows *q, const h2o_r
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
   if (blk::head_fits(c->view, n)) {
     const blk::Rows kr = rows_of(k), vr = rows_of(v);
-    cudaError_t e = blk::launch_head(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, rows_of(out), lse,
-                                     c->kmap, c->vmap, c->stream);
-    if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
+    const cudaError_t e = blk::launch_head(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, rows_of(out),
+                                           lse, c->kmap, c->vmap, c->stream);
     return e == cudaSuccess ? H2O_OK : fail(e);
   }
   cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
   if (e == cudaSuccess)
     e = blk::launch_attend(c->view, l, rows_of(q), 1, accumulate != 0, rows_of(out), lse, c->kmap, c->vmap, c->stream);
-  if (e == cudaSuccess && c->view.bounds) e = blk::launch_bound(c->view, l, 0, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -313,8 +310,9 @@ h2o_status h2o_bcache_attend_sparse(h2o_bcache_t c, int n, const h2o_rows *q, co
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 0, c->view.cap};
-  const cudaError_t e = blk::launch_sparse(c->view, l, rows_of(q), causal != 0, accumulate != 0, n_blocks, n_first, n_last,
-                                           rows_of(out), lse, blocks, c->kmap, c->vmap, c->stream);
+  const cudaError_t e =
+      blk::launch_sparse(c->view, l, rows_of(q), nullptr, nullptr, nullptr, causal != 0, accumulate != 0, n_blocks, n_first,
+                         n_last, rows_of(out), lse, blocks, c->kmap, c->vmap, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 
@@ -332,11 +330,10 @@ h2o_status h2o_bcache_step_sparse(h2o_bcache_t c, int n, const h2o_rows *q, cons
   OnDevice on(c->device);
   if (on.err != cudaSuccess) return fail(on.err);
   const blk::Lens l{lengths, counts, n, 1, c->view.cap};
-  cudaError_t e = blk::launch_append(c->view, l, rows_of(k), rows_of(v), position, nullptr, c->stream);
-  if (e == cudaSuccess) e = blk::launch_bound(c->view, l, 0, c->stream);
-  if (e == cudaSuccess)
-    e = blk::launch_sparse(c->view, l, rows_of(q), 1, accumulate != 0, n_blocks, n_first, n_last, rows_of(out), lse, blocks,
-                           c->kmap, c->vmap, c->stream);
+  const blk::Rows kr = rows_of(k), vr = rows_of(v);
+  const cudaError_t e =
+      blk::launch_sparse(c->view, l, rows_of(q), &kr, &vr, position, 1, accumulate != 0, n_blocks, n_first, n_last,
+                         rows_of(out), lse, blocks, c->kmap, c->vmap, c->stream);
   return e == cudaSuccess ? H2O_OK : fail(e);
 }
 

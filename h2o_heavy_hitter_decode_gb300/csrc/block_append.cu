@@ -13,8 +13,8 @@
 // 98 % of the copy rate, with four CTAs (128 registers) an SM; three (168): 568.
 // append_few_kernel: one warp per (head, K or V) for the rows of a decode
 // step, taken one at a time; the block's earlier codes are read only where its
-// scale grows.
-#include "block_cache.cuh"
+// scale grows, or for the bounds of its keys where the cache keeps them.
+#include "block_tile.cuh"
 
 namespace h2o {
 namespace blk {
@@ -135,6 +135,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_few_kernel(const View c, c
   for (int lo = s.len, end = s.len + s.cnt; lo < end;) {
     const int hi = min(end, (lo / kBlock + 1) * kBlock);
     append_rows<F, D>(c, is_v, is_v ? v : k, b, h, s.len, lo, hi);
+    if (!is_v && c.bounds) {
+      __syncwarp();  // the codes are there
+      bound_block<F, D>(c, bh, lo / kBlock, s.len + s.cnt);
+    }
     lo = hi;
   }
   if (!is_v && lane < s.cnt) {
@@ -157,7 +161,8 @@ cudaError_t append_t(const View &c, const Lens &l, const Rows &k, const Rows &v,
   const int64_t warps = (int64_t)c.B * c.H * blocks * 2;
   append_kernel<F, D><<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(c, l, k, v, position, score,
                                                                                         blocks);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess && c.bounds ? launch_bound(c, l, 0, st) : e;
 }
 
 }  // namespace

@@ -364,6 +364,10 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
       const int lo = max(s.len, base), hi = min(s.total, base + kBlock);
       append_rows<F, D>(c, false, k, b, h, s.len, lo, hi);
       append_rows<F, D>(c, true, v, b, h, s.len, lo, hi);
+      if (c.bounds) {
+        __syncwarp();  // the codes are there
+        bound_block<F, D>(c, bh, blk, s.total);
+      }
       const int j = base + lane;
       if (j >= lo && j < hi) {
         c.pos[(size_t)bh * c.cap + j] = (position ? position[b] : s.len) + (j - s.len);

@@ -229,7 +229,7 @@ __device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Launchers (each on the device that is current; arguments checked before).
+// Launchers (each on the device that is current; arguments checked before).  An append keeps the bounds, if there are any.
 cudaError_t launch_append(const View &c, const Lens &l, const Rows &k, const Rows &v, const int32_t *position,
                           const float *score, cudaStream_t st);
 // kmap, vmap: the codes as rows of d bytes, boxes of kBlock rows (code_map).
@@ -252,10 +252,12 @@ cudaError_t launch_copy(const View &to, const View &from, const int32_t *parent,
 // Bounds of the blocks that the call's rows went to (l.appends), or with `whole` of all that hold l.lengths
 // entries (1 reports lengths out of range, 2 does not).
 cudaError_t launch_bound(const View &c, const Lens &l, int whole, cudaStream_t st);
-// Attention over n_blocks chosen blocks a token; blocks [B*H][n][n_blocks] receives their indices.
-cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, int n_blocks,
-                          int n_first, int n_last, const Rows &out, float *lse, int32_t *blocks, const CUtensorMap &kmap,
-                          const CUtensorMap &vmap, cudaStream_t st);
+// Attention over n_blocks chosen blocks a token, behind the append of k, v (null: none; position as in launch_append);
+// blocks [B*H][n][n_blocks] receives their indices.
+cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, const Rows *k, const Rows *v,
+                          const int32_t *position, int causal, int accumulate, int n_blocks, int n_first, int n_last,
+                          const Rows &out, float *lse, int32_t *blocks, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                          cudaStream_t st);
 
 }  // namespace blk
 }  // namespace h2o

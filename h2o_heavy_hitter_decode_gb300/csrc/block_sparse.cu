@@ -7,21 +7,32 @@
 //   rest those with the highest keys, lowest index first among equals; then as
 //   in block_attend.cu over the chosen blocks' entries.
 //
-// The sums are whole numbers below 2^24 and the scales powers of two, so keys
-// are exact and the choice does not depend on the order of any sum.
+// The sums are whole numbers below 2^22, exact in the fp32 sums of mma.sync on
+// f16, and the scales powers of two: keys are exact and the choice does not
+// depend on the order of any sum.
 //
 // A cluster of P CTAs takes a token's rows of a cached head from the choice to
-// the output.  Keys: each CTA a run of the candidates.  Choice: radix select
-// over the keys' bits, 8 at a time, the digits' counts of the cluster met over
-// distributed shared memory.  Attention: the chosen blocks in turn over the
-// cluster's warps, each with its own ring of TMA loads and its own partial
-// output; the CTA's and then the cluster's parts meet in shared memory.  With
-// one token a sequence the weights go to the scores in the same launch (each
-// CTA those of its own blocks); several tokens may choose the same block, so
-// theirs are added by scores_kernel, in the tokens' order.
+// the output.
+// Keys: a warp takes 16 blocks as the rows of m16n8k16 (their bounds are 2 d
+// bytes, straight from memory in 16-byte loads, the next 16 blocks' on their
+// way) and 8 query rows as its columns: x's negative part against lo, the
+// positive one against hi.
+// Choice: of up to kLocal candidates each CTA makes all keys for itself and each
+// warp finds the threshold for itself, keys in registers, a bit at a time from
+// the first one that differs, so nothing but the keys crosses a barrier.  More
+// candidates are shared by the cluster: radix select, 8 bits at a time, the
+// digits' counts met over distributed shared memory, and the list through
+// memory.
+// Attention: the chosen blocks in turn over the cluster's CTAs and their warps,
+// each with its own ring of TMA loads and its own partial output; the CTA's and
+// then the cluster's parts meet in shared memory.
+// With one token a sequence the new row is appended, and the weights are added
+// to the scores, in the same launch (each CTA those of its own blocks); several
+// tokens may choose the same block, so theirs are added by scores_kernel, in
+// the tokens' order.
 #include <cooperative_groups.h>
 
-#include <climits>
+#include <algorithm>
 
 #include "block_tile.cuh"
 
@@ -31,11 +42,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kW = 4;         // warps of a CTA
-constexpr int kThreads = kW * 32;
 constexpr int kStages = 2;    // blocks of a warp on their way
 constexpr int kBins = 256;
+constexpr int kLocal = 512;      // candidates of which each CTA makes all keys
 constexpr int kHeldMost = 4096;  // keys of a CTA that stay in shared memory
+constexpr int kOwnMost = 1024;   // chosen blocks of a CTA whose list does
+constexpr int kLogitsMost = 4096;  // logits of a CTA that do
+constexpr int kCodesMost = 64;     // query rows of a token whose codes do
 
 struct Args {
   View c;
@@ -44,15 +57,18 @@ struct Args {
   float *lse;
   int32_t *blocks;  // [B*H][n][n_blocks]
   int causal, accumulate, n_blocks, n_first, n_last;
-  int held;  // keys a CTA has room for
+  int fused;  // the launch appends the sequences' one new row: k, v, position
+  Rows k, v;
+  const int32_t *position;
+  int held, own, logits;  // keys, chosen blocks and logits a CTA has room for
 };
 
 // What token t of a sequence sees: `end` entries in nb blocks, S of them chosen.
-struct View1 {
+struct Sight {
   int end, nb, S;
 };
-__device__ __forceinline__ View1 view_of(const Args &a, const Seq &s, int t) {
-  View1 v;
+__device__ __forceinline__ Sight sight_of(const Args &a, const Seq &s, int t) {
+  Sight v;
   v.end = max(0, a.causal ? s.total - s.cnt + t + 1 : s.total);
   v.nb = ceil_div(v.end, kBlock);
   v.S = min(v.nb, a.n_blocks);
@@ -80,122 +96,299 @@ template <int P, typename T> __device__ __forceinline__ T *peer(T *p, int rank) 
     return p;
 }
 
-// Shared memory of a CTA, in order.
-template <int D> struct Room {
-  static constexpr int kRing = kW * kStages * 2 * kBlock * D;
-  static constexpr int kOut = 16 * D * 4;  // the CTA's partial output
-  __host__ __device__ static int codes(int group) { return 2 * group * D; }
-  __host__ __device__ static int bytes(int group, int held) { return 1024 + kRing + kOut + codes(group) + held * 4; }
+// ------------------------------------------------------------------- keys
+// Bounds of blocks x0 + g and x0 + 8 + g of a run of n: the lane's chunks t,
+// t + 4 .. of lo and of hi.
+template <int D> struct Bounds {
+  static constexpr int C = D / 64;
+  uint4 w[2][2][C];
+  float ks[2];
+  __device__ __forceinline__ void load(const int8_t *bounds, const float *scales, int x0, int n) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int x = min(x0 + 8 * r + g, n - 1);
+      const int8_t *p = bounds + (size_t)x * 2 * D + t * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < C; ++i) w[r][h][i] = *(const uint4 *)(p + h * D + i * 64);
+      ks[r] = scales[x];
+    }
+  }
 };
 
-template <typename F, int D, int NR, int P>
-__global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap,
-                                                          const __grid_constant__ CUtensorMap vmap) {
-  constexpr int OT = D / 16, kStage = 2 * kBlock * D, kRows = 8 * NR;
+// Codes of 8 query rows as the B operand, in the order of the bounds' words.
+template <int D> struct Codes {
+  static constexpr int C = D / 64;
+  uint32_t b[2][C][4][2];  // [lo, hi][chunk][word]
+  // f: the lane's C chunks of 16 elements of row g.
+  __device__ __forceinline__ void set(const float (&f)[C][16], float inv) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y = f[i][4 * e + j] * inv;
+          x[j] = y != y ? 0.f : rintf(fminf(fmaxf(y, -127.f), 127.f));
+        }
+        static_assert(!ToF16<I8>::kAdjacent, "pairs of a word's codes: 0 and 2, 1 and 3");
+        const __half2 l0 = __floats2half2_rn(fminf(x[0], 0.f), fminf(x[2], 0.f));
+        const __half2 l1 = __floats2half2_rn(fminf(x[1], 0.f), fminf(x[3], 0.f));
+        const __half2 h0 = __floats2half2_rn(fmaxf(x[0], 0.f), fmaxf(x[2], 0.f));
+        const __half2 h1 = __floats2half2_rn(fmaxf(x[1], 0.f), fmaxf(x[3], 0.f));
+        b[0][i][e][0] = *(const uint32_t *)&l0, b[0][i][e][1] = *(const uint32_t *)&l1;
+        b[1][i][e][0] = *(const uint32_t *)&h0, b[1][i][e][1] = *(const uint32_t *)&h1;
+      }
+  }
+};
+// The lane's chunks of a query row, and the largest finite magnitude among them as bits of a bf16.
+template <int D> __device__ __forceinline__ unsigned query_row(const __nv_bfloat16 *p, float (&f)[D / 64][16]) {
+  const int t = threadIdx.x & 3;
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint4 w = ld_nc16(p + (t + 4 * i) * 16 + u * 8);
+      Unpack<__nv_bfloat16>::run(w, f[i] + u * 8);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = (&w.x)[e], y = x & 0x7fffu, z = (x >> 16) & 0x7fffu;
+        top = max(top, max(y < 0x7f80u ? y : 0u, z < 0x7f80u ? z : 0u));
+      }
+    }
+  return top;
+}
+
+// Largest sum of the two blocks over the 8 rows; all lanes of a quad get them.
+template <int D> __device__ __forceinline__ float2 block_sums(const Bounds<D> &bd, const Codes<D> &q) {
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t a[4];
+        ToF16<I8>::run((&bd.w[0][h][i].x)[e], a[0], a[2]);
+        ToF16<I8>::run((&bd.w[1][h][i].x)[e], a[1], a[3]);
+        mma16816(c, a, q.b[h][i][e][0], q.b[h][i][e][1]);
+      }
+  float2 m = make_float2(fmaxf(c[0], c[1]), fmaxf(c[2], c[3]));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+    m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+  }
+  return m;
+}
+// Ordered like the keys.  2^-20: a key of the largest scale stays in fp32's range, one of the least a normal number.
+__device__ __forceinline__ uint32_t key_bits(float m, float ks) {
+  const uint32_t u = __float_as_uint(m * 0x1p-20f * ks + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Shared memory of a CTA, in order: the warps' rings (later their partial
+// outputs), the CTA's partial output, query codes of groups above 8, keys, the
+// own blocks, logits.
+template <int D, int NR, int W> struct Room {
+  static constexpr int kStage = 2 * kBlock * D;
+  static constexpr int kRing = W * kStages * kStage;
+  static constexpr int kOut = 8 * NR * D * 4;
+  static constexpr int kTile = sizeof(Codes<D>) * 32;  // codes of 8 rows
+  __host__ __device__ static int codes(int group) { return NR == 1 || group > kCodesMost ? 0 : (group + 7) / 8 * kTile; }
+  __host__ __device__ static int bytes(int group, int held, int own, int logits) {
+    return 1024 + kRing + kOut + codes(group) + held * 4 + own * 4 + logits * 4;
+  }
+};
+
+template <typename F, int D, int NR, int P, int W>
+__global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
+    sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using R = Room<D, NR, W>;
+  constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kRows = 8 * NR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
-  float *cta_o = (float *)(smem + Room<D>::kRing);            // [kRows][D]
-  int8_t *xs = (int8_t *)(cta_o + 16 * D);                    // [group][2][D] query codes: the positive ones, the negative ones
-  __shared__ __align__(8) uint64_t full[kW][kStages];
+  float *cta_o = (float *)(smem + R::kRing);                  // [kRows][D]
+  const int group = a.c.group;
+  Codes<D> *codes = (Codes<D> *)(smem + R::kRing + R::kOut);  // [tile][lane], groups above 8
+  uint32_t *held = (uint32_t *)((uint8_t *)codes + R::codes(group));
+  int *own = (int *)(held + a.held);
+  float *held_logits = (float *)(own + a.own);
+  __shared__ __align__(8) uint64_t full[W][kStages];
   __shared__ unsigned hist[2][kBins];
-  __shared__ unsigned s_sum[kW], s_digit, s_want, s_top;
-  __shared__ int s_scan[2][kW], s_count[2];
-  __shared__ float2 part_ml[kW][kRows], cta_ml[kRows];
+  __shared__ unsigned s_sum[W], s_digit, s_want, s_have, s_top;
+  __shared__ int s_scan[2][W], s_count[2];
+  __shared__ float2 part_ml[W][kRows], cta_ml[kRows];
   __shared__ float row_base[H2O_BLOCK_MAX_ROWS];
   const View &c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int rank = P > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int64_t item = blockIdx.x / P;
   const int bh = (int)(item / a.l.n), t = (int)(item - (int64_t)bh * a.l.n), b = bh / c.H, h = bh - b * c.H;
-  const int group = c.group;
   const Seq s = seq_of(a.l, b);
   if (!s.ok && h == 0 && t == 0 && rank == 0 && tid == 0) atomicOr(c.err, H2O_BERR_RANGE);
   if (t >= s.cnt) return;  // the whole cluster
-  const View1 v = view_of(a, s, t);
+  const Sight v = sight_of(a, s, t);
   const Rows q{a.q.p + t * a.q.st, a.q.sb, a.q.sh, a.q.st};  // the token's rows alone
   const Seq one{s.len, 1, v.end, true};
   int32_t *list = list_of(a, bh, t);
   const size_t scales = (size_t)bh * (c.cap / kBlock);
+  const bool all = v.nb <= a.n_blocks;
+  const int nc = all ? 0 : v.nb - a.n_first - a.n_last;  // candidates n_first .. n_first + nc - 1
+  const bool shared = P > 1 && (nc > kLocal || ceil_div(v.S, P) > a.own);  // the cluster shares the choice
+  const bool local = !all && !shared && nc <= kLocal && ceil_div(v.S, P) <= a.own;
+  const int share = shared ? ceil_div(nc, P) : nc;
+  const int lo = a.n_first + (shared ? min(nc, rank * share) : 0);
+  const int n = min(a.n_first + nc, lo + share) - lo;  // this CTA's candidates lo .. lo + n - 1
+  unsigned want = all ? 0u : (unsigned)(a.n_blocks - a.n_first - a.n_last);
+  const int steps = want > 0 ? ceil_div(n, 16) : 0;
+  const int8_t *bounds = c.bounds + (scales + lo) * 2 * D;
+  const float *ksc = c.Ksc + scales + lo;
 
-  if (warp < kW && lane == 0) {
+  grid_dependency_wait();
+  Bounds<D> bd;
+  if (warp < steps) bd.load(bounds, ksc, warp * 16, n);
+  if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
-  if (tid == 0) s_top = 0;
-  __syncthreads();
+  // The new row: its block is the last one of the list, and no other CTA touches it.
+  if (a.fused && rank == (v.S - 1) % P && warp < 2) {
+    append_rows<F, D>(c, warp == 1, warp ? a.v : a.k, b, h, s.len, s.len, s.len + 1);
+    if (warp == 0) {
+      __syncwarp();
+      bound_block<F, D>(c, bh, s.len / kBlock, s.total);
+      if (lane == 0) {
+        const size_t at = (size_t)bh * c.cap + s.len;
+        c.pos[at] = a.position ? a.position[b] : s.len;
+        c.score[at] = 0.f;
+        c.low[at] = 0.f;
+      }
+    }
+    __threadfence();  // the codes are read back by a copy
+    asm volatile("fence.proxy.async;" ::: "memory");
+  }
 
   // ------------------------------------------------------------- the choice
-  if (rank == 0)
-    for (int i = v.S + tid; i < a.n_blocks; i += kThreads) list[i] = -1;
-  if (v.nb <= a.n_blocks) {
-    for (int i = rank * kThreads + tid; i < v.nb; i += P * kThreads) list[i] = i;
-  } else {
-    if (rank == 0) {
-      for (int i = tid; i < a.n_first; i += kThreads) list[i] = i;
-      for (int i = tid; i < a.n_last; i += kThreads) list[a.n_blocks - a.n_last + i] = v.nb - a.n_last + i;
+  if (want > 0) {
+    uint32_t *keys = n <= a.held ? held : (uint32_t *)logits_of(a, bh, t, 0) + (shared ? rank * share : 0);  // read before any logit is written
+    Codes<D> qc;
+    float inv;
+    if constexpr (NR == 1) {  // every warp for itself; columns behind the last row repeat it
+      float f[D / 64][16];
+      const unsigned top = query_row<D>(q.at(b, h * group + min(g, group - 1), 0), f);
+      inv = inverse_pow2(block_scale<I8>(__uint_as_float(__reduce_max_sync(0xffffffffu, top) << 16)));
+      qc.set(f, inv);
+    } else {
+      if (tid == 0) s_top = 0;
+      __syncthreads();
+      const int tiles = ceil_div(group, 8);
+      for (int x = warp; x < tiles; x += W) {
+        float f[D / 64][16];
+        const unsigned top = __reduce_max_sync(0xffffffffu, query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), f));
+        if (lane == 0) atomicMax(&s_top, top);
+      }
+      __syncthreads();
+      inv = inverse_pow2(block_scale<I8>(__uint_as_float(s_top << 16)));
+      if (group <= kCodesMost) {
+        for (int x = warp; x < tiles; x += W) {
+          float f[D / 64][16];
+          query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), f);
+          qc.set(f, inv);
+          codes[x * 32 + lane] = qc;
+        }
+        __syncthreads();
+      }
     }
-    const int nc = v.nb - a.n_first - a.n_last;
-    unsigned want = (unsigned)(a.n_blocks - a.n_first - a.n_last);
-    const int share = ceil_div(nc, P), lo = a.n_first + min(nc, rank * share);
-    const int n = min(a.n_first + nc, lo + share) - lo;  // this CTA's candidates lo .. lo + n - 1
-    uint32_t *keys = share <= a.held ? (uint32_t *)(xs + Room<D>::codes(group))
-                                     : (uint32_t *)logits_of(a, bh, t, 0) + rank * share;  // read before any logit is written
-    if (want > 0) {
-      // query codes
-      for (int x = tid; x < group * (D / 8); x += kThreads) {
-        const uint4 w = *(const uint4 *)(q.at(b, h * group + x / (D / 8), 0) + x % (D / 8) * 8);
-        unsigned top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = (&w.x)[e], y = u & 0x7fffu, z = (u >> 16) & 0x7fffu;
-          top = max(top, max(y < 0x7f80u ? y : 0u, z < 0x7f80u ? z : 0u));
-        }
-        atomicMax(&s_top, top);
-      }
-      __syncthreads();
-      const float inv = inverse_pow2(block_scale<I8>(__uint_as_float(s_top << 16)));
-      for (int x = tid; x < group * (D / 8); x += kThreads) {
-        float f[8];
-        Unpack<__nv_bfloat16>::run(*(const uint4 *)(q.at(b, h * group + x / (D / 8), 0) + x % (D / 8) * 8), f);
-        int8_t *dst = xs + x / (D / 8) * 2 * D + x % (D / 8) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float y = f[e] * inv;
-          y = y != y ? 0.f : fminf(fmaxf(y, -127.f), 127.f);
-          const int k = __float2int_rn(y);
-          dst[e] = (int8_t)max(k, 0);
-          dst[D + e] = (int8_t)min(k, 0);
+    for (int x = warp; x < steps; x += W) {
+      Bounds<D> now = bd;
+      if (x + W < steps) bd.load(bounds, ksc, (x + W) * 16, n);
+      float2 m;
+      if constexpr (NR == 1) {
+        m = block_sums<D>(now, qc);
+      } else {
+        m = make_float2(-INFINITY, -INFINITY);
+        for (int y = 0; y < ceil_div(group, 8); ++y) {
+          if (group <= kCodesMost) {
+            qc = codes[y * 32 + lane];
+          } else {  // made anew for each 16 blocks
+            float f[D / 64][16];
+            query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), f);
+            qc.set(f, inv);
+          }
+          const float2 z = block_sums<D>(now, qc);
+          m = make_float2(fmaxf(m.x, z.x), fmaxf(m.y, z.y));
         }
       }
-      __syncthreads();
-      // keys: D / 16 lanes to a block
-      constexpr int L = D / 16;
-      for (int x0 = 0; x0 < n; x0 += kThreads / L) {
-        const int x = x0 + tid / L, sub = tid % L;
-        const int8_t *bd = c.bounds + (scales + lo + min(x, n - 1)) * 2 * D + sub * 16;
-        const int4 low = *(const int4 *)bd, high = *(const int4 *)(bd + D);
-        int m = INT_MIN;
-        for (int r = 0; r < group; ++r) {
-          const int4 up = *(const int4 *)(xs + r * 2 * D + sub * 16), dn = *(const int4 *)(xs + r * 2 * D + D + sub * 16);
-          int k = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) k = __dp4a((&dn.x)[e], (&low.x)[e], __dp4a((&up.x)[e], (&high.x)[e], k));
-#pragma unroll
-          for (int o = 1; o < L; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
-          m = max(m, k);
-        }
-        // 2^-20: a key of the largest scale stays in fp32's range, one of the least scale a normal number
-        const float key = (float)m * 0x1p-20f * c.Ksc[scales + lo + min(x, n - 1)];
-        const uint32_t u = __float_as_uint(key);
-        if (sub == 0 && x < n) keys[x] = u & 0x80000000u ? ~u : u | 0x80000000u;
+      if (t4 < 2) {
+        const int j = x * 16 + t4 * 8 + g;
+        if (j < n) keys[j] = t4 ? key_bits(m.y, now.ks[1]) : key_bits(m.x, now.ks[0]);
       }
-      __syncthreads();
     }
-    uint32_t prefix = 0, pmask = 0;
-    if (want > 0) {
+    __syncthreads();
+    if (local) {
+      // threshold: the largest T with count(key >= T) >= want
+      uint32_t k[kLocal / 32], high = 0, same = 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < kLocal / 32; ++i) {
+        k[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0u;  // no key is 0
+        high = max(high, k[i]);
+      }
+      high = __reduce_max_sync(0xffffffffu, high);
+#pragma unroll
+      for (int i = 0; i < kLocal / 32; ++i)
+        if (i * 32 + lane < n) same &= ~(k[i] ^ high);
+      same = __reduce_and_sync(0xffffffffu, same);
+      const int first_bit = 31 - __clz(~same);  // -1: all equal
+      uint32_t T = first_bit < 0 ? high : high & ~((2u << first_bit) - 1u);
+      unsigned ge = (unsigned)n;
+      for (int bit = first_bit; bit >= 0 && ge != want; --bit) {
+        const uint32_t at = T | 1u << bit;
+        unsigned cnt = 0;
+#pragma unroll
+        for (int i = 0; i < kLocal / 32; ++i) cnt += k[i] >= at;
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (cnt >= want) T = at, ge = cnt;
+      }
+      // kept: above T all, equal to it (at T's bits: all that are left if ge == want) the first ones
+      const bool exact = ge == want;
+      unsigned above = 0;
+      if (!exact) {
+#pragma unroll
+        for (int i = 0; i < kLocal / 32; ++i) above += k[i] > T;
+        above = __reduce_add_sync(0xffffffffu, above);
+      }
+      const int ties = (int)(want - above);
+      int taken = 0, equal = 0;
+      const unsigned below = (1u << lane) - 1;
+#pragma unroll
+      for (int i = 0; i < kLocal / 32; ++i) {
+        if (i * 32 >= n) break;
+        bool keep = exact ? k[i] >= T : k[i] > T;
+        if (!exact) {
+          const unsigned eq = __ballot_sync(0xffffffffu, k[i] == T);
+          keep |= k[i] == T && equal + __popc(eq & below) < ties;
+          equal += __popc(eq);
+        }
+        if (i * 32 + lane >= n) keep = false;
+        const unsigned kept = __ballot_sync(0xffffffffu, keep);
+        const int slot = a.n_first + taken + __popc(kept & below);
+        if (keep && slot % P == rank) {
+          const int mine = slot / P;
+          if (mine % W == warp) own[mine] = lo + i * 32 + lane, list[slot] = lo + i * 32 + lane;
+        }
+        taken += __popc(kept);
+      }
+    } else {
+      uint32_t prefix = 0, pmask = 0;
       constexpr int kOwn = kBins / kThreads;
+      unsigned have = 0;
 #pragma unroll 1
-      for (int pass = 0; pass < 4; ++pass) {
+      for (int pass = 0; pass < 4 && have != want; ++pass) {
         const int shift = 24 - 8 * pass;
         unsigned *mine = hist[pass & 1];
         for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
@@ -206,14 +399,18 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
         }
         team_sync<P>();
         // thread i sums its digits over the cluster, the highest ones first
-        unsigned own[kOwn], sum = 0;
+        unsigned mine_of[kOwn], sum = 0;
         const int top = kBins - kOwn * (tid + 1);
 #pragma unroll
         for (int e = 0; e < kOwn; ++e) {
-          own[e] = 0;
+          mine_of[e] = 0;
+          if (P == 1 || !shared) {
+            mine_of[e] = mine[top + e];
+          } else {
 #pragma unroll
-          for (int i = 0; i < P; ++i) own[e] += *peer<P>(mine + top + e, i);
-          sum += own[e];
+            for (int i = 0; i < P; ++i) mine_of[e] += *peer<P>(mine + top + e, i);
+          }
+          sum += mine_of[e];
         }
         unsigned run = sum;
 #pragma unroll
@@ -228,19 +425,21 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
         if (cum < want && want <= run) {
 #pragma unroll
           for (int e = kOwn - 1; e >= 0; --e) {
-            if (cum < want && want <= cum + own[e]) s_digit = (unsigned)(top + e), s_want = want - cum;
-            cum += own[e];
+            if (cum < want && want <= cum + mine_of[e])
+              s_digit = (unsigned)(top + e), s_want = want - cum, s_have = mine_of[e];
+            cum += mine_of[e];
           }
         }
         __syncthreads();
         prefix |= s_digit << shift;
         pmask |= 255u << shift;
         want = s_want;
+        have = s_have;  // as many as are wanted: the digits so far decide
       }
       // each thread scans a run of consecutive candidates
       const int run = ceil_div(n, kThreads), x0 = min(n, tid * run), x1 = min(n, x0 + run);
       int above = 0, equal = 0;
-      for (int x = x0; x < x1; ++x) above += keys[x] > prefix, equal += keys[x] == prefix;
+      for (int x = x0; x < x1; ++x) above += (keys[x] & pmask) > prefix, equal += (keys[x] & pmask) == prefix;
       int ia = above, ie = equal;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -257,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
         for (int i = 0; i < rank; ++i) before_a += *peer<P>(&s_count[0], i), before_e += *peer<P>(&s_count[1], i);
       }
       for (int x = x0; x < x1; ++x) {
-        const uint32_t u = keys[x];
+        const uint32_t u = keys[x] & pmask;
         const int slot = before_a + min(before_e, (int)want);  // the first of the equal ones stay
         const bool keep = u > prefix || (u == prefix && before_e < (int)want);
         before_a += u > prefix;
@@ -266,10 +465,29 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
       }
     }
   }
-  team_sync<P>();  // the list is whole; every key and count has been read
+  // the list's ends, and what is behind it
+  const int first = all ? v.S : a.n_first, last = all ? v.S : v.S - a.n_last;
+  if (rank == 0) {
+    for (int i = tid; i < first; i += kThreads) list[i] = i;
+    for (int i = last + tid; i < v.S; i += kThreads) list[i] = v.nb - v.S + i;
+    for (int i = v.S + tid; i < a.n_blocks; i += kThreads) list[i] = -1;
+  }
+  if (all || local)
+    __syncthreads();  // the new row is there, every key has been read
+  else
+    team_sync<P>();  // the list is whole too
+  auto block_of = [&](int slot) {
+    if (slot < first) return slot;
+    if (slot >= last) return v.nb - v.S + slot;
+    return local ? own[slot / P] : list[slot];
+  };
 
   // ----------------------------------------------------------- the attention
-  // Slot rank + P (warp + kW i) of the list is the i-th block of a warp.
+  // Slot rank + P (warp + W i) of the list is the i-th block of a warp.  Logits: by own blocks in shared memory, or by slots in memory.
+  const bool near = a.l.n == 1 && group * ceil_div(v.S, P) * kBlock <= a.logits;
+  const int64_t row_step = near ? ceil_div(v.S, P) * kBlock : c.cap;
+  float *logits = near ? held_logits : logits_of(a, bh, t, 0);
+  auto place = [&](int slot) { return (near ? slot / P : slot) * kBlock; };
   uint8_t *ring = smem + warp * kStages * kStage;
   const uint64_t policy = l2_policy(false);
   const int first_slot = rank + P * warp;
@@ -277,12 +495,12 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
   uint32_t phases = 0;
   for (int row0 = 0; row0 < group; row0 += kRows) {
     auto fetch = [&](int i) {
-      const int slot = first_slot + i * P * kW;
+      const int slot = first_slot + i * P * W;
       if (slot >= v.S || lane != 0 || lost) return;
       asm volatile("fence.proxy.async;" ::: "memory");
       uint8_t *dst = ring + i % kStages * kStage;
       uint64_t *bar = &full[warp][i % kStages];
-      const int row = bh * c.cap + list[slot] * kBlock;
+      const int row = bh * c.cap + block_of(slot) * kBlock;
       mbar_expect_tx(bar, kStage);
       tma_load_2d(dst, &kmap, bar, 0, row, policy);
       tma_load_2d(dst + kBlock * D, &vmap, bar, 0, row, policy);
@@ -290,8 +508,8 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
     for (int i = 0; i < kStages; ++i) fetch(i);
     Tile<F, D, NR, false> tl;
     tl.begin(q, group, 0, one, b, h, row0, nullptr);
-    for (int i = 0; first_slot + i * P * kW < v.S; ++i) {
-      const int slot = first_slot + i * P * kW, blk = list[slot];
+    for (int i = 0; first_slot + i * P * W < v.S; ++i) {
+      const int slot = first_slot + i * P * W, blk = block_of(slot);
       const float ks = c.Ksc[scales + blk], vs = c.Vsc[scales + blk];
       const int st = i % kStages;
       if (!lost && !mbar_wait(&full[warp][st], phases >> st & 1)) lost = true;
@@ -301,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
       tl.block(kt, kt + kBlock * D, ks, vs, blk, v.end - blk * kBlock, nullptr,
                [&](int r, int j, float s0, float s1, float s2, float s3) {
                  if (!a.accumulate) return;
-                 float *lg = logits_of(a, bh, t, row0 + r) + slot * kBlock + (j - blk * kBlock);
+                 float *lg = logits + (row0 + r) * row_step + place(slot) + (j - blk * kBlock);
                  lg[0] = s0, lg[8] = s1, lg[16] = s2, lg[24] = s3;
                });
       __syncwarp();  // this warp has read the stage
@@ -312,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
       for (int i = 0; i < kStages; ++i) mbar_wait(&full[warp][i], 0), mbar_wait(&full[warp][i], 1);
     }
     __syncthreads();  // every warp is done with its ring: the partial outputs go there
-    float *po = (float *)smem;  // [kW][kRows][D]
+    float *po = (float *)smem;  // [W][kRows][D]
     const float part = tl.unit() * kPartDown;
 #pragma unroll
     for (int n = 0; n < NR; ++n)
@@ -351,7 +569,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
       const int r = x / (D / 4), d0 = x % (D / 4) * 4;
       float m, l;
       float4 o;
-      meet(kW, [&](int i) { return part_ml[i][r]; }, [&](int i) { return *(const float4 *)(po + (i * kRows + r) * D + d0); },
+      meet(W, [&](int i) { return part_ml[i][r]; }, [&](int i) { return *(const float4 *)(po + (i * kRows + r) * D + d0); },
            m, l, o);
       *(float4 *)(cta_o + r * D + d0) = o;
       if (d0 == 0) cta_ml[r] = make_float2(m, l);
@@ -383,97 +601,128 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const Args a, const __
       row_base[row0 + tid] = weight_base(m, l);
     }
     fence_proxy_async_smem();  // the next rows' copies land where the parts were
-    team_sync<P>();            // the parts have been read
+    if (row0 + kRows < group) team_sync<P>();  // the parts have been read
   }
+  __syncwarp();
+  if (P > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // and the last ones too
 
   // -------------------------------------------------------------- the scores
-  if (a.l.n > 1 || !a.accumulate) return;
-  float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
-  const float *lg = logits_of(a, bh, t, 0);
-  for (int x = tid; rank + x / kBlock * P < v.S; x += kThreads) {
-    const int slot = rank + x / kBlock * P, j = list[slot] * kBlock + x % kBlock;
-    if (j >= v.end) continue;
-    const float old = score[j];
-    float lost_part = low[j], w = 0.f;
-    for (int r = 0; r < group; ++r) w += ex2(lg[(size_t)r * c.cap + slot * kBlock + x % kBlock] - row_base[r]);
-    score[j] = add_score(old, lost_part, w);
-    low[j] = lost_part;
+  if (a.l.n == 1 && a.accumulate) {
+    __syncthreads();
+    float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
+    for (int x = tid; rank + x / kBlock * P < v.S; x += kThreads) {
+      const int slot = rank + x / kBlock * P, j = block_of(slot) * kBlock + x % kBlock;
+      if (j >= v.end) continue;
+      const float old = score[j];
+      float lost_part = low[j], w = 0.f;
+      const float *lg = logits + place(slot) + x % kBlock;
+      for (int r = 0; r < group; ++r) w += ex2(lg[r * row_step] - row_base[r]);
+      score[j] = add_score(old, lost_part, w);
+      low[j] = lost_part;
+    }
   }
+  __syncwarp();
+  if (P > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // a peer may still read this CTA's parts
 }
 
 // The weights of several tokens' rows, added in the tokens' order: a CTA has a
-// run of a head's blocks, and finds in each token's list those of them that it
-// holds.
-__global__ void __launch_bounds__(256) scores_kernel(const Args a, int slices) {
+// run of a head's blocks, and counts in each token's list, a warp a token, where
+// they begin and end.
+constexpr int kScoreThreads = 256;
+__global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int slices) {
   const View &c = a.c;
   const int bh = blockIdx.x / slices, slice = blockIdx.x - bh * slices, b = bh / c.H, group = c.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Seq s = seq_of(a.l, b);
   const int nblk = ceil_div(s.total, kBlock);
   const int j0 = (int)((int64_t)slice * nblk / slices), j1 = (int)((int64_t)(slice + 1) * nblk / slices);
   __shared__ float base[H2O_BLOCK_MAX_ROWS];
+  __shared__ int from[H2O_BLOCK_MAX_ROWS], to[H2O_BLOCK_MAX_ROWS];
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
-  for (int t = 0; t < s.cnt; ++t) {
-    const View1 v = view_of(a, s, t);
+  grid_dependency_wait();
+  for (int r = threadIdx.x; r < s.cnt * group; r += kScoreThreads) base[r] = c.part[(size_t)bh * c.max_rows + r];
+  for (int t = warp; t < s.cnt; t += kScoreThreads / 32) {
+    const Sight v = sight_of(a, s, t);
     const int32_t *list = list_of(a, bh, t);
-    auto first = [&](int j) {  // the first slot whose block is j or later
-      int lo = 0, hi = v.S;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (list[mid] < j)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      return lo;
-    };
-    const int s0 = first(j0), s1 = first(j1);
-    __syncthreads();  // the token before is done
-    for (int r = threadIdx.x; r < group; r += 256) base[r] = c.part[(size_t)bh * c.max_rows + t * group + r];
-    __syncthreads();
+    int before = 0, within = 0;
+#pragma unroll 4
+    for (int i = lane; i < v.S; i += 32) {
+      const int j = list[i];
+      before += j < j0, within += j < j1;
+    }
+    before = __reduce_add_sync(0xffffffffu, before), within = __reduce_add_sync(0xffffffffu, within);
+    if (lane == 0) from[t] = before, to[t] = within;
+  }
+  __syncthreads();
+  for (int t = 0; t < s.cnt; ++t) {
+    const Sight v = sight_of(a, s, t);
+    const int32_t *list = list_of(a, bh, t);
     const float *lg = logits_of(a, bh, t, 0);
-    for (int x = s0 * kBlock + threadIdx.x; x < s1 * kBlock; x += 256) {
+    for (int x = from[t] * kBlock + threadIdx.x; x < to[t] * kBlock; x += kScoreThreads) {
       const int j = list[x / kBlock] * kBlock + x % kBlock;
       if (j >= v.end) continue;
       const float old = score[j];
       float lost = low[j], w = 0.f;
-      for (int r = 0; r < group; ++r) w += ex2(lg[(size_t)r * c.cap + x] - base[r]);
+      for (int r = 0; r < group; ++r) w += ex2(lg[(size_t)r * c.cap + x] - base[t * group + r]);
       score[j] = add_score(old, lost, w);
       low[j] = lost;
     }
+    __syncthreads();  // the next token may have chosen the same blocks
   }
 }
 
-template <typename F, int D, int NR, int P>
-cudaError_t sparse_p(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-  const int most = (a.c.cap / kBlock + P - 1) / P;
-  a.held = most < kHeldMost ? most : kHeldMost;
-  const int smem = Room<D>::bytes(a.c.group, a.held);
-  static SmemLimit limit;
-  const void *kernel = (const void *)sparse_kernel<F, D, NR, P>;
-  cudaError_t e = limit.raise(kernel, smem);
-  if (e != cudaSuccess) return e;
+template <typename... X>
+cudaError_t launch_with(void (*kernel)(X...), unsigned ctas, int threads, int smem, int cluster, bool after,
+                        cudaStream_t st, X... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.c.B * a.c.H * a.l.n * P));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {(unsigned)P, 1, 1};
-  cfg.attrs = &at;
-  cfg.numAttrs = P > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, sparse_kernel<F, D, NR, P>, a, kmap, vmap);
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n++].val.clusterDim = {(unsigned)cluster, 1, 1};
+  }
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename F, int D, int NR, int P, int W>
+cudaError_t sparse_p(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+  const int blocks = a.c.cap / kBlock, own = (std::min(blocks, a.n_blocks) + P - 1) / P;
+  const int share = std::min(blocks, std::max(kLocal, (blocks + P - 1) / P));
+  a.held = (std::min(share, kHeldMost) + 3) & ~3;
+  a.own = (std::min(own, kOwnMost) + 3) & ~3;
+  const int64_t logits = (int64_t)a.c.group * own * kBlock;
+  a.logits = a.accumulate && a.l.n == 1 && logits <= kLogitsMost ? (int)logits : 0;
+  const int smem = Room<D, NR, W>::bytes(a.c.group, a.held, a.own, a.logits);
+  static SmemLimit limit;
+  const auto kernel = sparse_kernel<F, D, NR, P, W>;
+  cudaError_t e = limit.raise((const void *)kernel, smem);
+  if (e == cudaSuccess && P > 8)
+    e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * P;
+  return launch_with(kernel, (unsigned)ctas, W * 32, smem, P, a.l.appends && !a.fused, st, a, kmap, vmap);
 }
 
 template <typename F, int D, int NR>
 cudaError_t sparse_n(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   const int64_t items = (int64_t)a.c.B * a.c.H * a.l.n;
   const int blocks = a.c.cap / kBlock;
-  auto fits = [&](int p) { return items * p <= 2 * a.c.sms && blocks >= 8 * p; };
-  if (fits(8)) return sparse_p<F, D, NR, 8>(a, kmap, vmap, st);
-  if (fits(4)) return sparse_p<F, D, NR, 4>(a, kmap, vmap, st);
-  if (fits(2)) return sparse_p<F, D, NR, 2>(a, kmap, vmap, st);
-  return sparse_p<F, D, NR, 1>(a, kmap, vmap, st);
+  auto fits = [&](int p, int per_sm) { return items * p <= (int64_t)per_sm * a.c.sms && blocks >= 8 * p; };
+  if (items * 16 <= a.c.sms && blocks >= 2048) return sparse_p<F, D, NR, 16, 8>(a, kmap, vmap, st);
+  if (fits(8, 1)) return sparse_p<F, D, NR, 8, 8>(a, kmap, vmap, st);
+  if (fits(4, 2)) return sparse_p<F, D, NR, 4, 4>(a, kmap, vmap, st);
+  if (fits(2, 2)) return sparse_p<F, D, NR, 2, 4>(a, kmap, vmap, st);
+  return sparse_p<F, D, NR, 1, 4>(a, kmap, vmap, st);
 }
 
 template <typename F, int D>
@@ -483,16 +732,23 @@ cudaError_t sparse_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &
   const int64_t heads = (int64_t)a.c.B * a.c.H;
   int64_t slices = (2 * a.c.sms + heads - 1) / heads;
   if (slices > a.c.cap / kBlock) slices = a.c.cap / kBlock;
-  scores_kernel<<<(unsigned)(heads * slices), 256, 0, st>>>(a, (int)slices);
-  return cudaGetLastError();
+  return launch_with(scores_kernel, (unsigned)(heads * slices), kScoreThreads, 0, 1, true, st, a, (int)slices);
 }
 
 }  // namespace
 
-cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, int causal, int accumulate, int n_blocks,
-                          int n_first, int n_last, const Rows &out, float *lse, int32_t *blocks, const CUtensorMap &kmap,
-                          const CUtensorMap &vmap, cudaStream_t st) {
-  const Args a{c, l, q, out, lse, blocks, causal, accumulate, n_blocks, n_first, n_last, 0};
+cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, const Rows *k, const Rows *v,
+                          const int32_t *position, int causal, int accumulate, int n_blocks, int n_first, int n_last,
+                          const Rows &out, float *lse, int32_t *blocks, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                          cudaStream_t st) {
+  const Rows none{};
+  const bool fused = k && l.n == 1;
+  if (k && !fused) {
+    cudaError_t e = launch_append(c, l, *k, *v, position, nullptr, st);
+    if (e != cudaSuccess) return e;
+  }
+  const Args a{c, l, q, out, lse, blocks, causal, accumulate, n_blocks, n_first, n_last,
+               fused, k ? *k : none, v ? *v : none, position, 0, 0, 0};
   if (c.kv == H2O_KV_E4M3)
     return c.d == 128 ? sparse_d<E4M3, 128>(a, kmap, vmap, st) : sparse_d<E4M3, 64>(a, kmap, vmap, st);
   return c.d == 128 ? sparse_d<I8, 128>(a, kmap, vmap, st) : sparse_d<I8, 64>(a, kmap, vmap, st);

@@ -85,6 +85,60 @@ template <int D> __device__ __forceinline__ int chunk_at(int row, int chunk) {
   return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
 }
 
+// ------------------------------------------------------------------- bounds
+template <typename F> constexpr float kPerUnit = 1.f;
+template <> constexpr float kPerUnit<E4M3> = 0.25f;
+
+// Least and largest key code of each dimension of a block of head bh, in units of 1 (int8) or 4 (e4m3) rounded outwards,
+// over its entries below `total`.  One warp: the block's rows in 16-byte loads, all on their way together, as f16 (exact);
+// two dimensions at a time.
+template <typename F, int D> __device__ __forceinline__ void bound_block(const View &c, int64_t bh, int blk, int total) {
+  using T = ToF16<F>;
+  constexpr int LPR = D / 16;       // lanes per row, 16 codes each
+  constexpr int RPI = 32 / LPR;     // rows per load of the warp
+  constexpr int IT = kBlock / RPI;  // loads
+  const int lane = threadIdx.x & 31, sub = lane % LPR, row0 = lane / LPR, rest = total - blk * kBlock;
+  const uint8_t *codes = c.K + ((size_t)bh * c.cap + (size_t)blk * kBlock) * D + sub * 16;
+  uint4 w[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int r = i * RPI + row0;
+    w[i] = *(const uint4 *)(codes + (size_t)(r < rest ? r : 0) * D);  // row 0 again in the place of none
+  }
+  __half2 lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t a, z;
+      T::run((&w[i].x)[e], a, z);
+      const __half2 x = *(const __half2 *)&a, y = *(const __half2 *)&z;
+      lo[2 * e] = i == 0 ? x : __hmin2(lo[2 * e], x), hi[2 * e] = i == 0 ? x : __hmax2(hi[2 * e], x);
+      lo[2 * e + 1] = i == 0 ? y : __hmin2(lo[2 * e + 1], y), hi[2 * e + 1] = i == 0 ? y : __hmax2(hi[2 * e + 1], y);
+    }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+      hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+    }
+  if (row0 > 1) return;
+  const bool high = row0 == 1;  // the second group of lanes writes the largest
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 unit = __float2half2_rn(kPerUnit<F>);
+    const __half2 x = __hmul2(high ? hi[2 * e] : lo[2 * e], unit), y = __hmul2(high ? hi[2 * e + 1] : lo[2 * e + 1], unit);
+    const __half2 p = high ? h2ceil(x) : h2floor(x), q = high ? h2ceil(y) : h2floor(y);
+    const uint32_t p0 = __half2int_rn(__low2half(p)) & 0xff, p1 = __half2int_rn(__high2half(p)) & 0xff;
+    const uint32_t q0 = __half2int_rn(__low2half(q)) & 0xff, q1 = __half2int_rn(__high2half(q)) & 0xff;
+    out[e] = T::kAdjacent ? p0 | p1 << 8 | q0 << 16 | q1 << 24 : p0 | q0 << 8 | p1 << 16 | q1 << 24;
+  }
+  int8_t *dst = c.bounds + ((size_t)bh * (c.cap / kBlock) + blk) * 2 * D + (high ? D : 0) + sub * 16;
+  *(uint4 *)dst = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // Output sums are held in a unit 2^E of the warp's: bf16 values reach 2^128
 // and weights before their division by the sum 2^15, so that plain fp32 sums
 // would pass its range (|v| from 2^121 on with one entry, 2^103 with 262,144

@@ -428,3 +428,83 @@ def test_refusals():
     with pytest.raises(H2OError):
         c.attend_sparse(torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device=DEV), lens, 3)
     assert c.bounds.shape == (2, 2, 2, 2, 64) and plain.bounds is None
+
+
+@pytest.mark.parametrize("cap", [2048, 32768])
+def test_keys_one_apart(cap):
+    """Sums next to 2^21 that differ by 1, in an order of their own: few candidates, and more than a CTA takes."""
+    g = torch.Generator(DEV).manual_seed(14)
+    n = cap // 32
+    c = H2OBlockCache(1, 1, 128, cap, kv="int8", bounds=True)
+    c.K.fill_(127)
+    step = torch.randperm(n, generator=g, device=DEV)
+    low = (step % 128).to(torch.int8)          # times a query code of 1
+    high = (step // 128).to(torch.int8)        # times a query code of 127, with 127 - low beside it
+    c.K[0, 0, :, 126] = low.repeat_interleave(32)
+    c.K[0, 0, :, 127] = high.repeat_interleave(32)
+    c.K_scale.fill_(1.0)
+    c.V_scale.fill_(1.0)
+    c.bound(ints([cap]))
+    q = torch.full((1, 1, 1, 128), 127.0, device=DEV).bfloat16()
+    q[..., 126] = 1.0
+    blocks = torch.zeros(1, 1, 1, 40, dtype=torch.int32, device=DEV)
+    c.attend_sparse(q, ints([cap]), 40, 0, 1, accumulate=False, blocks=blocks)
+    m = low.long() + 127 * high.long()
+    best = (-m[: n - 1]).sort(stable=True).indices[:39].sort().values
+    assert blocks[0, 0, 0, :39].tolist() == best.tolist()
+
+
+@pytest.mark.parametrize("B,H,n,cap,len_", [(1, 8, 1, 131072, 130001), (1, 1, 1, 65536, 65536), (2, 4, 2, 65536, 65001),
+                                            (40, 4, 1, 20000 // 32 * 32, 19900), (16, 2, 1, 32768, 32768)])
+def test_forms_of_many_candidates(B, H, n, cap, len_):
+    """Clusters of 16, 8, 4, 2 and one CTA, each with more candidates than a CTA takes: the choice on the device."""
+    g = torch.Generator(DEV).manual_seed(15)
+    c = H2OBlockCache(B, H, 64, cap, group=3, max_queries=n, kv="int8", bounds=True)
+    c.K.copy_(torch.randint(-30, 31, c.K.shape, generator=g, device=DEV, dtype=torch.int8))
+    c.V.copy_(torch.randint(-127, 128, c.V.shape, generator=g, device=DEV, dtype=torch.int8))
+    c.K_scale.fill_(2.0 ** -5)
+    c.V_scale.fill_(2.0 ** -6)
+    lens = [len_ - 977 * b for b in range(B)]
+    c.bound(ints(lens))
+    q = rows(g, B, 3 * H, n, 64)
+    blocks = torch.zeros(B, H, n, 30, dtype=torch.int32, device=DEV)
+    lse = torch.zeros(B, 3 * H, n, device=DEV)
+    out = c.attend_sparse(q, ints(lens), 30, 1, 2, lse=lse, blocks=blocks)
+    for b in range(B):
+        if lens[b] < 0:  # refused
+            continue
+        K = c.K[b].view(H, -1, 32, 64)
+        lo, hi = K.amin(2).double(), K.amax(2).double()
+        for t in range(n):
+            end = lens[b] - n + t + 1
+            nb = -(-end // 32)
+            qt = q[b, :, t].double().view(H, 3, 64)
+            e = torch.ceil(torch.log2(qt.abs().amax((1, 2)) / 127))
+            x = torch.round(qt / torch.exp2(e)[:, None, None])
+            m = (x.clamp(min=0) @ hi.transpose(1, 2) + x.clamp(max=0) @ lo.transpose(1, 2)).amax(1)[:, :nb]
+            if nb > 30:
+                best = (-m[:, 1 : nb - 2]).sort(dim=-1, stable=True).indices[:, :27] + 1
+                ends = torch.tensor([0, nb - 2, nb - 1], device=DEV).expand(H, -1)
+                mine = torch.cat([best, ends], 1).sort(-1).values
+            else:  # all of them
+                mine = torch.arange(nb, device=DEV).expand(H, -1)
+            assert torch.equal(blocks[b, :, t, : mine.shape[1]].long(), mine), b
+            assert bool((blocks[b, :, t, mine.shape[1] :] == -1).all())
+            if nb == 0:
+                assert bool((out[b, :, t] == 0).all()) and bool((lse[b, :, t] == -math.inf).all())
+                continue
+            at = (mine[:, :, None] * 32 + torch.arange(32, device=DEV)).flatten(1)
+            h = torch.arange(H, device=DEV)[:, None]
+            k, v = c.K[b][h, at].double() * 2.0 ** -5, c.V[b][h, at].double() * 2.0 ** -6
+            s = (qt @ k.transpose(1, 2) / 8).masked_fill((at >= end)[:, None], -math.inf)
+            w = torch.softmax(s, -1)
+            e_w = 2 * 2.0 ** -23 * 68 * float((qt.abs() @ k.abs().transpose(1, 2)).max()) / 8 + 2.0 ** -21 * 98
+            want, mass = (w @ v).flatten(0, 1), (w @ v.abs()).flatten(0, 1)
+            tol = 2.0 ** -8 * want.abs() + (e_w + 2.0 ** -11) * mass * (1 + 2.0 ** -7) + 1e-6
+            assert bool(((out[b, :, t].double() - want).abs() <= tol).all())
+            L = torch.logsumexp(s, -1).flatten()
+            assert bool(((lse[b, :, t].double() - L).abs() <= e_w + 2.0 ** -21 * (1 + L.abs())).all())
+    # every row's weights add up to 1, within e_w and the fp32 sums of scores
+    seen = sum(a - n + t + 1 > 0 for a in lens for t in range(n)) * H * 3
+    assert abs(float(c.score.double().sum()) - seen) <= seen * (e_w + 2.0 ** -20)
+    assert c.error_bits() == (1 if min(lens) < 0 else 0)
