@@ -101,7 +101,8 @@ bool ints_ok(const int32_t *p, bool may_be_null) { return p ? aligned(p, 4) : ma
 
 // A choice of blocks holds the last one, whose bounds need not be current.
 bool choice_ok(const h2o_bcache *c, int n, int n_blocks, int n_first, int n_last, const int32_t *blocks) {
-  if (n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_blocks || !ints_ok(blocks, false)) return false;
+  if (n_first < 0 || n_last < 1 || (int64_t)n_first + n_last > n_blocks || n_blocks > H2O_SPARSE_MAX_BLOCKS) return false;
+  if (!ints_ok(blocks, false)) return false;
   return (int64_t)c->view.B * c->view.H * n <= 0x7fffffffLL;  // a grid
 }
 

@@ -42,7 +42,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kStages = 2;    // blocks of a warp on their way
 constexpr int kBins = 256;
 constexpr int kLocal = 512;      // candidates of which each CTA makes all keys
 constexpr int kHeldMost = 4096;  // keys of a CTA that stay in shared memory
@@ -94,6 +93,21 @@ template <int P, typename T> __device__ __forceinline__ T *peer(T *p, int rank) 
     return cg::this_cluster().map_shared_rank(p, rank);
   else
     return p;
+}
+
+// Four entries' scores with weights w added; entries from `left` on keep theirs.
+__device__ __forceinline__ void store_scores(float *score, float *low, int left, const float4 &old, float4 less,
+                                             const float4 &w) {
+  const float4 sum = make_float4(add_score(old.x, less.x, w.x), add_score(old.y, less.y, w.y),
+                                 add_score(old.z, less.z, w.z), add_score(old.w, less.w, w.w));
+  if (left >= 4) {
+    *(float4 *)score = sum;
+    *(float4 *)low = less;
+  } else {
+    if (left > 0) score[0] = sum.x, low[0] = less.x;
+    if (left > 1) score[1] = sum.y, low[1] = less.y;
+    if (left > 2) score[2] = sum.z, low[2] = less.z;
+  }
 }
 
 // ------------------------------------------------------------------- keys
@@ -191,11 +205,79 @@ __device__ __forceinline__ uint32_t key_bits(float m, float ks) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The `want` highest of n <= 32 N keys, the first ones among equals, found by a
+// warp alone: the largest T with count(key >= T) >= want, two bits at a time
+// from the first one in which keys differ.  Those that are the warp's go to own
+// and to the list.
+template <int N, int P, int W>
+__device__ __forceinline__ void choose(const Args &a, const uint32_t *keys, int n, unsigned want, int lo, int rank,
+                                       int warp, int *own, int32_t *list) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k[N], high = 0, low = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool is = i * 32 + lane < n;
+    k[i] = is ? keys[i * 32 + lane] : 0u;  // no key is 0
+    high = max(high, k[i]);
+    if (is) low = min(low, k[i]);
+  }
+  high = __reduce_max_sync(0xffffffffu, high);
+  low = __reduce_min_sync(0xffffffffu, low);
+  const int differ = 32 - __clz(high ^ low);  // bits below which keys differ
+  int bit = (differ + 1) & ~1;                 // T is right in its bits from `bit` up
+  uint32_t T = bit >= 32 ? 0u : high >> bit << bit;
+  unsigned ge = (unsigned)n;
+  while (bit > 0 && ge != want) {
+    bit -= 2;
+    const uint32_t at1 = T | 1u << bit, at2 = T | 2u << bit, at3 = T | 3u << bit;
+    unsigned c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c1 += k[i] >= at1, c2 += k[i] >= at2, c3 += k[i] >= at3;
+    const unsigned sum = __reduce_add_sync(0xffffffffu, c1 | c2 << 10 | c3 << 20);  // at most 512 each
+    c1 = sum & 1023u, c2 = sum >> 10 & 1023u, c3 = sum >> 20;
+    if (c3 >= want)
+      T = at3, ge = c3;
+    else if (c2 >= want)
+      T = at2, ge = c2;
+    else if (c1 >= want)
+      T = at1, ge = c1;
+  }
+  const bool exact = ge == want;  // else T is a key itself, and only the first of its equals stay
+  unsigned above = 0;
+  if (!exact) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) above += k[i] > T;
+    above = __reduce_add_sync(0xffffffffu, above);
+  }
+  const int ties = (int)(want - above);
+  int taken = 0, equal = 0;
+  const unsigned below = (1u << lane) - 1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i * 32 >= n) break;
+    bool keep = exact ? k[i] >= T : k[i] > T;
+    if (!exact) {
+      const unsigned eq = __ballot_sync(0xffffffffu, k[i] == T);
+      keep |= k[i] == T && equal + __popc(eq & below) < ties;
+      equal += __popc(eq);
+    }
+    if (i * 32 + lane >= n) keep = false;
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    const int slot = a.n_first + taken + __popc(kept & below);
+    if (keep && slot % P == rank) {
+      const int mine = slot / P;
+      if (mine % W == warp) own[mine] = lo + i * 32 + lane, list[slot] = lo + i * 32 + lane;
+    }
+    taken += __popc(kept);
+  }
+}
+
 // Shared memory of a CTA, in order: the warps' rings (later their partial
 // outputs), the CTA's partial output, query codes of groups above 8, keys, the
 // own blocks, logits.
 template <int D, int NR, int W> struct Room {
   static constexpr int kStage = 2 * kBlock * D;
+  static constexpr int kStages = D == 64 ? 4 : 2;  // blocks of a warp on their way
   static constexpr int kRing = W * kStages * kStage;
   static constexpr int kOut = 8 * NR * D * 4;
   static constexpr int kTile = sizeof(Codes<D>) * 32;  // codes of 8 rows
@@ -206,10 +288,10 @@ template <int D, int NR, int W> struct Room {
 };
 
 template <typename F, int D, int NR, int P, int W>
-__global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
+__global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
     sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using R = Room<D, NR, W>;
-  constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kRows = 8 * NR;
+  constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kStages = R::kStages, kRows = 8 * NR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
   float *cta_o = (float *)(smem + R::kRing);                  // [kRows][D]
@@ -220,12 +302,17 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
   float *held_logits = (float *)(own + a.own);
   __shared__ __align__(8) uint64_t full[W][kStages];
   __shared__ unsigned hist[2][kBins];
-  __shared__ unsigned s_sum[W], s_digit, s_want, s_have, s_top;
-  __shared__ int s_scan[2][W], s_count[2];
+  __shared__ unsigned s_sum[W + 1], s_digit, s_want, s_have, s_top;
+  __shared__ int s_scan[2][W + 1], s_count[2];
   __shared__ float2 part_ml[W][kRows], cta_ml[kRows];
   __shared__ float row_base[H2O_BLOCK_MAX_ROWS];
   const View &c = a.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  // W warps work; one more, where the launch appends, has the new row and then only meets the barriers: its tid is behind
+  // every loop's end (2^25 blocks and list places of at most 2^26)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  const bool works = warp < W;
+  constexpr int kNone = 1 << 26;
+  const int tid = works ? (int)threadIdx.x : kNone;
   const int rank = P > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int64_t item = blockIdx.x / P;
   const int bh = (int)(item / a.l.n), t = (int)(item - (int64_t)bh * a.l.n), b = bh / c.H, h = bh - b * c.H;
@@ -251,24 +338,23 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
 
   grid_dependency_wait();
   Bounds<D> bd;
-  if (warp < steps) bd.load(bounds, ksc, warp * 16, n);
-  if (lane == 0) {
+  if (works && warp < steps) bd.load(bounds, ksc, warp * 16, n);
+  if (works && lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
   // The new row: its block is the last one of the list, and no other CTA touches it.
-  if (a.fused && rank == (v.S - 1) % P && warp < 2) {
-    append_rows<F, D>(c, warp == 1, warp ? a.v : a.k, b, h, s.len, s.len, s.len + 1);
-    if (warp == 0) {
-      __syncwarp();
-      bound_block<F, D>(c, bh, s.len / kBlock, s.total);
-      if (lane == 0) {
-        const size_t at = (size_t)bh * c.cap + s.len;
-        c.pos[at] = a.position ? a.position[b] : s.len;
-        c.score[at] = 0.f;
-        c.low[at] = 0.f;
-      }
+  if (!works && rank == (v.S - 1) % P) {
+    append_rows<F, D>(c, false, a.k, b, h, s.len, s.len, s.len + 1);
+    append_rows<F, D>(c, true, a.v, b, h, s.len, s.len, s.len + 1);
+    if (lane == 0) {
+      const size_t at = (size_t)bh * c.cap + s.len;
+      c.pos[at] = a.position ? a.position[b] : s.len;
+      c.score[at] = 0.f;
+      c.low[at] = 0.f;
     }
+    __syncwarp();
+    bound_block<F, D>(c, bh, s.len / kBlock, s.total);
     __threadfence();  // the codes are read back by a copy
     asm volatile("fence.proxy.async;" ::: "memory");
   }
@@ -286,7 +372,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
     } else {
       if (tid == 0) s_top = 0;
       __syncthreads();
-      const int tiles = ceil_div(group, 8);
+      const int tiles = works ? ceil_div(group, 8) : 0;
       for (int x = warp; x < tiles; x += W) {
         float f[D / 64][16];
         const unsigned top = __reduce_max_sync(0xffffffffu, query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), f));
@@ -304,7 +390,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
         __syncthreads();
       }
     }
-    for (int x = warp; x < steps; x += W) {
+    for (int x = works ? warp : steps; x < steps; x += W) {
       Bounds<D> now = bd;
       if (x + W < steps) bd.load(bounds, ksc, (x + W) * 16, n);
       float2 m;
@@ -331,57 +417,11 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
     }
     __syncthreads();
     if (local) {
-      // threshold: the largest T with count(key >= T) >= want
-      uint32_t k[kLocal / 32], high = 0, same = 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < kLocal / 32; ++i) {
-        k[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0u;  // no key is 0
-        high = max(high, k[i]);
-      }
-      high = __reduce_max_sync(0xffffffffu, high);
-#pragma unroll
-      for (int i = 0; i < kLocal / 32; ++i)
-        if (i * 32 + lane < n) same &= ~(k[i] ^ high);
-      same = __reduce_and_sync(0xffffffffu, same);
-      const int first_bit = 31 - __clz(~same);  // -1: all equal
-      uint32_t T = first_bit < 0 ? high : high & ~((2u << first_bit) - 1u);
-      unsigned ge = (unsigned)n;
-      for (int bit = first_bit; bit >= 0 && ge != want; --bit) {
-        const uint32_t at = T | 1u << bit;
-        unsigned cnt = 0;
-#pragma unroll
-        for (int i = 0; i < kLocal / 32; ++i) cnt += k[i] >= at;
-        cnt = __reduce_add_sync(0xffffffffu, cnt);
-        if (cnt >= want) T = at, ge = cnt;
-      }
-      // kept: above T all, equal to it (at T's bits: all that are left if ge == want) the first ones
-      const bool exact = ge == want;
-      unsigned above = 0;
-      if (!exact) {
-#pragma unroll
-        for (int i = 0; i < kLocal / 32; ++i) above += k[i] > T;
-        above = __reduce_add_sync(0xffffffffu, above);
-      }
-      const int ties = (int)(want - above);
-      int taken = 0, equal = 0;
-      const unsigned below = (1u << lane) - 1;
-#pragma unroll
-      for (int i = 0; i < kLocal / 32; ++i) {
-        if (i * 32 >= n) break;
-        bool keep = exact ? k[i] >= T : k[i] > T;
-        if (!exact) {
-          const unsigned eq = __ballot_sync(0xffffffffu, k[i] == T);
-          keep |= k[i] == T && equal + __popc(eq & below) < ties;
-          equal += __popc(eq);
-        }
-        if (i * 32 + lane >= n) keep = false;
-        const unsigned kept = __ballot_sync(0xffffffffu, keep);
-        const int slot = a.n_first + taken + __popc(kept & below);
-        if (keep && slot % P == rank) {
-          const int mine = slot / P;
-          if (mine % W == warp) own[mine] = lo + i * 32 + lane, list[slot] = lo + i * 32 + lane;
-        }
-        taken += __popc(kept);
+      if (works) {
+        if (n <= 128)
+          choose<4, P, W>(a, keys, n, want, lo, rank, warp, own, list);
+        else
+          choose<kLocal / 32, P, W>(a, keys, n, want, lo, rank, warp, own, list);
       }
     } else {
       uint32_t prefix = 0, pmask = 0;
@@ -400,13 +440,11 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
         team_sync<P>();
         // thread i sums its digits over the cluster, the highest ones first
         unsigned mine_of[kOwn], sum = 0;
-        const int top = kBins - kOwn * (tid + 1);
+        const int top = works ? kBins - kOwn * (tid + 1) : 0;
 #pragma unroll
         for (int e = 0; e < kOwn; ++e) {
           mine_of[e] = 0;
-          if (P == 1 || !shared) {
-            mine_of[e] = mine[top + e];
-          } else {
+          if (works) {
 #pragma unroll
             for (int i = 0; i < P; ++i) mine_of[e] += *peer<P>(mine + top + e, i);
           }
@@ -437,7 +475,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
         have = s_have;  // as many as are wanted: the digits so far decide
       }
       // each thread scans a run of consecutive candidates
-      const int run = ceil_div(n, kThreads), x0 = min(n, tid * run), x1 = min(n, x0 + run);
+      const int run = ceil_div(n, kThreads), x0 = works ? min(n, tid * run) : n, x1 = min(n, x0 + run);
       int above = 0, equal = 0;
       for (int x = x0; x < x1; ++x) above += (keys[x] & pmask) > prefix, equal += (keys[x] & pmask) == prefix;
       int ia = above, ie = equal;
@@ -493,10 +531,22 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
   const int first_slot = rank + P * warp;
   bool lost = false;
   uint32_t phases = 0;
+  // Scores: 8 threads to an own block, four entries each; kAhead of a thread's are on their way at once.
+  constexpr int kAhead = 4;
+  float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
+  float4 old[kAhead], less[kAhead];
+  auto entry_of = [&](int y) {  // the first of the thread's y-th four, -1 behind the last
+    const int slot = rank + (tid / 8 + y * (kThreads / 8)) * P;
+    return works && slot < v.S ? block_of(slot) * kBlock + tid % 8 * 4 : -1;
+  };
+  auto load_scores = [&](int y, int at) {
+    const int j = entry_of(y);
+    if (j >= 0) old[at] = *(const float4 *)(score + j), less[at] = *(const float4 *)(low + j);
+  };
   for (int row0 = 0; row0 < group; row0 += kRows) {
     auto fetch = [&](int i) {
       const int slot = first_slot + i * P * W;
-      if (slot >= v.S || lane != 0 || lost) return;
+      if (!works || slot >= v.S || lane != 0 || lost) return;
       asm volatile("fence.proxy.async;" ::: "memory");
       uint8_t *dst = ring + i % kStages * kStage;
       uint64_t *bar = &full[warp][i % kStages];
@@ -507,8 +557,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
     };
     for (int i = 0; i < kStages; ++i) fetch(i);
     Tile<F, D, NR, false> tl;
-    tl.begin(q, group, 0, one, b, h, row0, nullptr);
-    for (int i = 0; first_slot + i * P * W < v.S; ++i) {
+    if (works) tl.begin(q, group, 0, one, b, h, row0, nullptr);
+    for (int i = 0; works && first_slot + i * P * W < v.S; ++i) {
       const int slot = first_slot + i * P * W, blk = block_of(slot);
       const float ks = c.Ksc[scales + blk], vs = c.Vsc[scales + blk];
       const int st = i % kStages;
@@ -525,27 +575,34 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
       __syncwarp();  // this warp has read the stage
       fetch(i + kStages);
     }
-    if (lost) {  // a copy never arrived: report, and wait for the other one before the memory goes
+    if (lost) {  // a copy never arrived: report, and wait for the others before the memory goes
       if (lane == 0) atomicOr(c.err, H2O_BERR_INTERNAL);
       for (int i = 0; i < kStages; ++i) mbar_wait(&full[warp][i], 0), mbar_wait(&full[warp][i], 1);
     }
     __syncthreads();  // every warp is done with its ring: the partial outputs go there
     float *po = (float *)smem;  // [W][kRows][D]
-    const float part = tl.unit() * kPartDown;
+    if (works) {
+      const float part = tl.unit() * kPartDown;
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float l = tl.sum(n, u);
-        const int r = 8 * n + 2 * t4 + u;
-        if (g == 0) part_ml[warp][r] = make_float2(tl.m[n][u], l);
-        const float inv = inverse_sum(l);
-        float *dst = po + (warp * kRows + r) * D + g * (D / 8);
+        for (int u = 0; u < 2; ++u) {
+          const float l = tl.sum(n, u);
+          const int r = 8 * n + 2 * t4 + u;
+          if (g == 0) part_ml[warp][r] = make_float2(tl.m[n][u], l);
+          const float inv = inverse_sum(l);
+          float *dst = po + (warp * kRows + r) * D + g * (D / 8);
 #pragma unroll
-        for (int j = 0; j < OT; j += 2)
-          *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u] * inv * part, tl.o[n][j][2 + u] * inv * part,
-                                                 tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
-      }
+          for (int j = 0; j < OT; j += 2)
+            *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u] * inv * part, tl.o[n][j][2 + u] * inv * part,
+                                                   tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
+        }
+    }
+    // the own entries' scores are on their way while the parts meet
+    if (row0 == 0 && a.l.n == 1 && a.accumulate) {
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) load_scores(y, y);
+    }
     __syncthreads();
     // the CTA's warps, then the cluster's CTAs: weighted means of weighted means
     auto meet = [&](int parts, auto ml_of, auto o_of, float &m, float &l, float4 &o) {
@@ -609,65 +666,87 @@ __global__ void __launch_bounds__(W * 32, W == 4 && NR == 1 ? 3 : 1)
   // -------------------------------------------------------------- the scores
   if (a.l.n == 1 && a.accumulate) {
     __syncthreads();
-    float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
-    for (int x = tid; rank + x / kBlock * P < v.S; x += kThreads) {
-      const int slot = rank + x / kBlock * P, j = block_of(slot) * kBlock + x % kBlock;
-      if (j >= v.end) continue;
-      const float old = score[j];
-      float lost_part = low[j], w = 0.f;
-      const float *lg = logits + place(slot) + x % kBlock;
-      for (int r = 0; r < group; ++r) w += ex2(lg[r * row_step] - row_base[r]);
-      score[j] = add_score(old, lost_part, w);
-      low[j] = lost_part;
+    for (int y0 = 0; entry_of(y0) >= 0; y0 += kAhead) {
+      if (y0 > 0) {
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) load_scores(y0 + y, y);
+      }
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) {
+        const int j = entry_of(y0 + y);
+        if (j < 0) break;
+        const float *lg = logits + place(rank + (tid / 8 + (y0 + y) * (kThreads / 8)) * P) + tid % 8 * 4;
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < group; ++r) {
+          const float4 x = *(const float4 *)(lg + r * row_step);
+          const float e = row_base[r];
+          w.x += ex2(x.x - e), w.y += ex2(x.y - e), w.z += ex2(x.z - e), w.w += ex2(x.w - e);
+        }
+        store_scores(score + j, low + j, v.end - j, old[y], less[y], w);
+      }
     }
   }
   __syncwarp();
   if (P > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // a peer may still read this CTA's parts
 }
 
-// The weights of several tokens' rows, added in the tokens' order: a CTA has a
-// run of a head's blocks, and counts in each token's list, a warp a token, where
-// they begin and end.
-constexpr int kScoreThreads = 256;
+// The weights of several tokens' rows, added in the tokens' order: a CTA has
+// kSlice blocks of a head, four entries a thread, and finds each token's slots
+// of them first (a warp a token).
+constexpr int kSlice = 32, kScoreThreads = kSlice * 8;
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int slices) {
+  extern __shared__ int slot_of[];  // [n][kSlice], -1: not chosen
   const View &c = a.c;
-  const int bh = blockIdx.x / slices, slice = blockIdx.x - bh * slices, b = bh / c.H, group = c.group;
+  const int bh = blockIdx.x / slices, j0 = (blockIdx.x - bh * slices) * kSlice, b = bh / c.H, group = c.group;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Seq s = seq_of(a.l, b);
-  const int nblk = ceil_div(s.total, kBlock);
-  const int j0 = (int)((int64_t)slice * nblk / slices), j1 = (int)((int64_t)(slice + 1) * nblk / slices);
+  if (s.cnt == 0 || j0 * kBlock >= s.total) return;
   __shared__ float base[H2O_BLOCK_MAX_ROWS];
-  __shared__ int from[H2O_BLOCK_MAX_ROWS], to[H2O_BLOCK_MAX_ROWS];
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
+  const int mine = threadIdx.x / 8, j = (j0 + mine) * kBlock + threadIdx.x % 8 * 4;
   grid_dependency_wait();
+  const bool in = j < s.total;
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f), less = old;
+  if (in) old = *(const float4 *)(score + j), less = *(const float4 *)(low + j);
   for (int r = threadIdx.x; r < s.cnt * group; r += kScoreThreads) base[r] = c.part[(size_t)bh * c.max_rows + r];
   for (int t = warp; t < s.cnt; t += kScoreThreads / 32) {
     const Sight v = sight_of(a, s, t);
     const int32_t *list = list_of(a, bh, t);
-    int before = 0, within = 0;
+    slot_of[t * kSlice + lane] = -1;
+    __syncwarp();
 #pragma unroll 4
     for (int i = lane; i < v.S; i += 32) {
-      const int j = list[i];
-      before += j < j0, within += j < j1;
+      const int x = list[i] - j0;
+      if (x >= 0 && x < kSlice) slot_of[t * kSlice + x] = i;
     }
-    before = __reduce_add_sync(0xffffffffu, before), within = __reduce_add_sync(0xffffffffu, within);
-    if (lane == 0) from[t] = before, to[t] = within;
   }
   __syncthreads();
+  if (!in) return;
+  bool any = false;
   for (int t = 0; t < s.cnt; ++t) {
-    const Sight v = sight_of(a, s, t);
-    const int32_t *list = list_of(a, bh, t);
-    const float *lg = logits_of(a, bh, t, 0);
-    for (int x = from[t] * kBlock + threadIdx.x; x < to[t] * kBlock; x += kScoreThreads) {
-      const int j = list[x / kBlock] * kBlock + x % kBlock;
-      if (j >= v.end) continue;
-      const float old = score[j];
-      float lost = low[j], w = 0.f;
-      for (int r = 0; r < group; ++r) w += ex2(lg[(size_t)r * c.cap + x] - base[t * group + r]);
-      score[j] = add_score(old, lost, w);
-      low[j] = lost;
+    const int slot = slot_of[t * kSlice + mine];
+    if (slot < 0) continue;
+    const float *lg = logits_of(a, bh, t, 0) + slot * kBlock + threadIdx.x % 8 * 4;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int r = 0; r < group; ++r) {
+      const float4 x = *(const float4 *)(lg + (size_t)r * c.cap);
+      const float e = base[t * group + r];
+      w.x += ex2(x.x - e), w.y += ex2(x.y - e), w.z += ex2(x.z - e), w.w += ex2(x.w - e);
     }
-    __syncthreads();  // the next token may have chosen the same blocks
+    old.x = add_score(old.x, less.x, w.x), old.y = add_score(old.y, less.y, w.y);
+    old.z = add_score(old.z, less.z, w.z), old.w = add_score(old.w, less.w, w.w);
+    any = true;
+  }
+  if (!any) return;
+  if (j + 4 <= s.total) {
+    *(float4 *)(score + j) = old;
+    *(float4 *)(low + j) = less;
+  } else {  // entries behind the last one keep their score
+    score[j] = old.x, low[j] = less.x;
+    if (j + 1 < s.total) score[j + 1] = old.y, low[j + 1] = less.y;
+    if (j + 2 < s.total) score[j + 2] = old.z, low[j + 2] = less.z;
   }
 }
 
@@ -710,7 +789,7 @@ cudaError_t sparse_p(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
     e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * P;
-  return launch_with(kernel, (unsigned)ctas, W * 32, smem, P, a.l.appends && !a.fused, st, a, kmap, vmap);
+  return launch_with(kernel, (unsigned)ctas, (W + a.fused) * 32, smem, P, a.l.appends && !a.fused, st, a, kmap, vmap);
 }
 
 template <typename F, int D, int NR>
@@ -730,9 +809,8 @@ cudaError_t sparse_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &
   cudaError_t e = a.c.group <= 8 ? sparse_n<F, D, 1>(a, kmap, vmap, st) : sparse_n<F, D, 2>(a, kmap, vmap, st);
   if (e != cudaSuccess || !a.accumulate || a.l.n == 1) return e;
   const int64_t heads = (int64_t)a.c.B * a.c.H;
-  int64_t slices = (2 * a.c.sms + heads - 1) / heads;
-  if (slices > a.c.cap / kBlock) slices = a.c.cap / kBlock;
-  return launch_with(scores_kernel, (unsigned)(heads * slices), kScoreThreads, 0, 1, true, st, a, (int)slices);
+  const int slices = (a.c.cap / kBlock + kSlice - 1) / kSlice;
+  return launch_with(scores_kernel, (unsigned)(heads * slices), kScoreThreads, a.l.n * kSlice * 4, 1, true, st, a, slices);
 }
 
 }  // namespace

@@ -439,12 +439,13 @@ h2o_status h2o_bcache_bound(h2o_bcache_t cache, const int32_t *lengths);
  *          for the finite elements of the token's `group` rows (a NaN counts 0,
  *          an infinity 127);
  *   key_j = K_scale_j * max_g sum_i (x_gi > 0 ? x_gi hi_ji : x_gi lo_ji).
- * n_first >= 0, n_last >= 1, n_first + n_last <= n_blocks.  Keys are exact, so
+ * n_first >= 0, n_last >= 1, n_first + n_last <= n_blocks <= H2O_SPARSE_MAX_BLOCKS.  Keys are exact, so
  * the choice is the same everywhere.  Outputs, lse and the weights added to
  * scores are those of attention over the chosen blocks' entries alone (a NaN
  * query makes scores of its chosen entries NaN).  blocks: device int32 [B][H][n][n_blocks],
  * receives each token's blocks in ascending order, -1 behind them; must not
  * overlap any argument.  H2O_ESTATE without bounds. */
+#define H2O_SPARSE_MAX_BLOCKS (1 << 26)
 h2o_status h2o_bcache_attend_sparse(h2o_bcache_t cache, int n, const h2o_rows *q, const int32_t *lengths,
                                     const int32_t *counts, int causal, int accumulate, int n_blocks, int n_first,
                                     int n_last, const h2o_rows *out, float *lse, int32_t *blocks);

@@ -328,6 +328,35 @@ def test_steps(case, layout):
     assert c.error_bits() == 0
 
 
+@pytest.mark.parametrize("B,H,cap,length", [(1, 8, 131072, 130000), (2, 8, 32768, 32000), (8, 8, 8192, 8000), (16, 8, 40000 // 32 * 32, 39000),
+                                            (16, 8, 4096, 4000), (40, 12, 2048, 2000), (3, 1, 64, 33)])
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_one_launch_is_append_and_attend(B, H, cap, length, kv):
+    """A step of one token in every size of cluster, few and many candidates: the bits of the two calls."""
+    twins = []
+    for i in range(2):
+        g = torch.Generator(DEV).manual_seed(16)
+        c = H2OBlockCache(B, H, 64, cap, group=2, kv=kv, bounds=True)
+        k, v = rows(g, B, H, cap, 64), rows(g, B, H, cap, 64)
+        lens = ints([max(0, length - 31 * b) for b in range(B)])
+        c.append(k, v, ints([0] * B), counts=lens)
+        q, k, v = rows(g, B, 2 * H, 1, 64), rows(g, B, H, 1, 64, "tokens", 3.0), rows(g, B, H, 1, 64)
+        out, lse = torch.zeros_like(q), torch.zeros(B, 2 * H, 1, device=DEV)
+        blocks = torch.zeros(B, H, 1, 20, dtype=torch.int32, device=DEV)
+        where = lens + 5
+        for _ in range(2):
+            if i == 0:
+                c.step_sparse(q, k, v, lens, 20, position=where, out=out, lse=lse, blocks=blocks)
+            else:
+                c.append(k, v, lens, position=where)
+                c.attend_sparse(q, lens + 1, 20, out=out, lse=lse, blocks=blocks)
+            lens, where = lens + 1, where + 1
+        assert c.error_bits() == 0
+        twins.append([x.view(torch.uint8) for x in (out, lse, blocks, c.K, c.V, c.K_scale, c.V_scale, c.pos, c.score, c.bounds)])
+    for a, z in zip(*twins):
+        assert torch.equal(a, z)
+
+
 def test_rejected_draft_tokens():
     """The smaller length takes tokens back, across the end of a block too; the next step's choice is the reference's."""
     c, r, g = filled(9, 2, 2, 64, 512, [300, 318], 2, 6)
@@ -409,6 +438,9 @@ def test_refusals():
             c.attend_sparse(q, lens, *choice)
         with pytest.raises((H2OError, ValueError)):
             c.step_sparse(q, k, k, lens, *choice)
+    with pytest.raises(H2OError) as e:  # 2^26 + 1 places a token
+        H2OBlockCache(1, 1, 64, 32, bounds=True).attend_sparse(q[:1, :1], lens[:1], 2 ** 26 + 1)
+    assert e.value.status == 1
     for choice in ((2 ** 31, 0, 1), (3, 2 ** 40, 1)):
         with pytest.raises(ValueError):
             c.attend_sparse(q, lens, *choice)
