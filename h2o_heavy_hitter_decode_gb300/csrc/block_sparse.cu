@@ -12,20 +12,19 @@
 // depend on the order of any sum.
 //
 // A cluster of P CTAs takes a token's rows of a cached head from the choice to
-// the output.
+// the output, each CTA a run of the list's places (slots).
 // Keys: a warp takes 16 blocks as the rows of m16n8k16 (their bounds are 2 d
 // bytes, straight from memory in 16-byte loads, the next 16 blocks' on their
 // way) and 8 query rows as its columns: x's negative part against lo, the
 // positive one against hi.
-// Choice: of up to kLocal candidates each CTA makes all keys for itself and each
-// warp finds the threshold for itself, keys in registers, a bit at a time from
-// the first one that differs, so nothing but the keys crosses a barrier.  More
-// candidates are shared by the cluster: radix select, 8 bits at a time, the
-// digits' counts met over distributed shared memory, and the list through
-// memory.
-// Attention: the chosen blocks in turn over the cluster's CTAs and their warps,
-// each with its own ring of TMA loads and its own partial output; the CTA's and
-// then the cluster's parts meet in shared memory.
+// Choice: of up to kAloneKeys candidates each CTA makes all keys and finds the
+// threshold for itself (up to kWarpKeys each warp: keys in registers, two bits
+// at a time from the first one that differs); of more it makes a share, and the
+// cluster finds the threshold together, counting keys in bins that meet over
+// distributed shared memory.
+// Attention: each warp takes every W-th slot of its CTA through its own ring of
+// TMA loads; the warps' and then the CTAs' parts meet in shared memory, each CTA
+// joining a slice of the output that the others have handed to it.
 // With one token a sequence the new row is appended, and the weights are added
 // to the scores, in the same launch (each CTA those of its own blocks); several
 // tokens may choose the same block, so theirs are added by scores_kernel, in
@@ -42,11 +41,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kBins = 256;
-constexpr int kLocal = 512;      // candidates of which each CTA makes all keys
-constexpr int kHeldMost = 4096;  // keys of a CTA that stay in shared memory
-constexpr int kOwnMost = 1024;   // chosen blocks of a CTA whose list does
-constexpr int kLogitsMost = 4096;  // logits of a CTA that do
+constexpr int kMostCtas = 8;      // of a cluster
+constexpr int kWarpKeys = 128, kAloneKeys = 512;
+constexpr int kHeldKeys = 4096;    // of a CTA, in shared memory
+constexpr int kOwnMost = 1024;    // chosen blocks of a CTA whose list stays in shared memory
+constexpr int kLogitsMost = 512;  // logits of a CTA that do
 constexpr int kCodesMost = 64;     // query rows of a token whose codes do
 
 struct Args {
@@ -59,7 +58,8 @@ struct Args {
   int fused;  // the launch appends the sequences' one new row: k, v, position
   Rows k, v;
   const int32_t *position;
-  int held, own, logits;  // keys, chosen blocks and logits a CTA has room for
+  int P;           // CTAs of a cluster
+  int own, logits;  // chosen blocks and logits a CTA has room for
 };
 
 // What token t of a sequence sees: `end` entries in nb blocks, S of them chosen.
@@ -81,18 +81,23 @@ __device__ __forceinline__ float *logits_of(const Args &a, int bh, int t, int r)
   return a.c.logits + ((size_t)bh * a.c.max_rows + t * a.c.group + r) * a.c.cap;
 }
 
-template <int P> __device__ __forceinline__ void team_sync() {
-  if constexpr (P > 1)
-    cg::this_cluster().sync();
-  else
-    __syncthreads();
+// The cluster's barrier in two halves: what a thread wrote before its arrival, also to other CTAs' shared memory, is
+// there for all behind the wait.
+__device__ __forceinline__ void team_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void team_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void team_sync() {
+  team_arrive();
+  team_wait();
 }
 // `p` of this CTA's shared memory in CTA `rank` of the cluster.
-template <int P, typename T> __device__ __forceinline__ T *peer(T *p, int rank) {
-  if constexpr (P > 1)
-    return cg::this_cluster().map_shared_rank(p, rank);
-  else
-    return p;
+template <typename T> __device__ __forceinline__ T *peer(T *p, int rank) {
+  return cg::this_cluster().map_shared_rank(p, rank);
 }
 
 // Four entries' scores with weights w added; entries from `left` on keep theirs.
@@ -205,13 +210,34 @@ __device__ __forceinline__ uint32_t key_bits(float m, float ks) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The `want` highest of n <= 32 N keys, the first ones among equals, found by a
-// warp alone: the largest T with count(key >= T) >= want, two bits at a time
-// from the first one in which keys differ.  Those that are the warp's go to own
-// and to the list.
-template <int N, int P, int W>
-__device__ __forceinline__ void choose(const Args &a, const uint32_t *keys, int n, unsigned want, int lo, int rank,
-                                       int warp, int *own, int32_t *list) {
+// A threshold among keys that some threads hold: the largest T with count(key
+// >= T) >= want, or, where a T has exactly `want` keys from it on, that one.
+struct Cut {
+  uint32_t T;
+  unsigned want;
+  bool exact;  // else T is a key itself, and of its equals only the first ones stay
+};
+// count(c): c[0..2] over all keys for thresholds at[0..2].
+template <typename Count>
+__device__ __forceinline__ Cut find_cut(uint32_t high, uint32_t low, unsigned n, unsigned want, Count count) {
+  const int differ = 32 - __clz(high ^ low);  // bits below which keys differ
+  int bit = (differ + 1) & ~1;                // T is right in its bits from `bit` up
+  Cut c{bit >= 32 ? 0u : high >> bit << bit, want, n == want};
+  while (bit > 0 && !c.exact) {
+    bit -= 2;
+    const uint32_t at[3] = {c.T | 1u << bit, c.T | 2u << bit, c.T | 3u << bit};
+    unsigned cnt[3];
+    count(at, cnt);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (cnt[i] >= want) c.T = at[i], c.exact = cnt[i] == want;
+  }
+  return c;
+}
+
+// Keys of n <= 32 N candidates chosen by a warp alone; emit(slot among the chosen, candidate) in order.
+template <int N, typename Emit>
+__device__ __forceinline__ void choose_warp(const uint32_t *keys, int n, unsigned want, Emit emit) {
   const int lane = threadIdx.x & 31;
   uint32_t k[N], high = 0, low = 0xffffffffu;
 #pragma unroll
@@ -223,30 +249,18 @@ __device__ __forceinline__ void choose(const Args &a, const uint32_t *keys, int 
   }
   high = __reduce_max_sync(0xffffffffu, high);
   low = __reduce_min_sync(0xffffffffu, low);
-  const int differ = 32 - __clz(high ^ low);  // bits below which keys differ
-  int bit = (differ + 1) & ~1;                 // T is right in its bits from `bit` up
-  uint32_t T = bit >= 32 ? 0u : high >> bit << bit;
-  unsigned ge = (unsigned)n;
-  while (bit > 0 && ge != want) {
-    bit -= 2;
-    const uint32_t at1 = T | 1u << bit, at2 = T | 2u << bit, at3 = T | 3u << bit;
-    unsigned c1 = 0, c2 = 0, c3 = 0;
+  const Cut c = find_cut(high, low, (unsigned)n, want, [&](const uint32_t (&at)[3], unsigned (&cnt)[3]) {
+    unsigned c0 = 0, c1 = 0, c2 = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) c1 += k[i] >= at1, c2 += k[i] >= at2, c3 += k[i] >= at3;
-    const unsigned sum = __reduce_add_sync(0xffffffffu, c1 | c2 << 10 | c3 << 20);  // at most 512 each
-    c1 = sum & 1023u, c2 = sum >> 10 & 1023u, c3 = sum >> 20;
-    if (c3 >= want)
-      T = at3, ge = c3;
-    else if (c2 >= want)
-      T = at2, ge = c2;
-    else if (c1 >= want)
-      T = at1, ge = c1;
-  }
-  const bool exact = ge == want;  // else T is a key itself, and only the first of its equals stay
+    for (int i = 0; i < N; ++i) c0 += k[i] >= at[0], c1 += k[i] >= at[1], c2 += k[i] >= at[2];
+    static_assert(32 * N < 1024, "three counts to a word");
+    const unsigned sum = __reduce_add_sync(0xffffffffu, c0 | c1 << 10 | c2 << 20);
+    cnt[0] = sum & 1023u, cnt[1] = sum >> 10 & 1023u, cnt[2] = sum >> 20;
+  });
   unsigned above = 0;
-  if (!exact) {
+  if (!c.exact) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) above += k[i] > T;
+    for (int i = 0; i < N; ++i) above += k[i] > c.T;
     above = __reduce_add_sync(0xffffffffu, above);
   }
   const int ties = (int)(want - above);
@@ -255,142 +269,301 @@ __device__ __forceinline__ void choose(const Args &a, const uint32_t *keys, int 
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (i * 32 >= n) break;
-    bool keep = exact ? k[i] >= T : k[i] > T;
-    if (!exact) {
-      const unsigned eq = __ballot_sync(0xffffffffu, k[i] == T);
-      keep |= k[i] == T && equal + __popc(eq & below) < ties;
+    bool keep = c.exact ? k[i] >= c.T : k[i] > c.T;
+    if (!c.exact) {
+      const unsigned eq = __ballot_sync(0xffffffffu, k[i] == c.T);
+      keep |= k[i] == c.T && equal + __popc(eq & below) < ties;
       equal += __popc(eq);
     }
     if (i * 32 + lane >= n) keep = false;
     const unsigned kept = __ballot_sync(0xffffffffu, keep);
-    const int slot = a.n_first + taken + __popc(kept & below);
-    if (keep && slot % P == rank) {
-      const int mine = slot / P;
-      if (mine % W == warp) own[mine] = lo + i * 32 + lane, list[slot] = lo + i * 32 + lane;
-    }
+    if (keep) emit(taken + __popc(kept & below), i * 32 + lane);
     taken += __popc(kept);
   }
 }
 
-// Shared memory of a CTA, in order: the warps' rings (later their partial
-// outputs), the CTA's partial output, query codes of groups above 8, keys, the
-// own blocks, logits.
+// The same by a team of P CTAs, each of W warps, each CTA with n keys of its own
+// (P = 1: by a CTA alone): counts in 2^8 bins between the team's least and
+// largest key, then in as many of the bin that holds the threshold, until the
+// keys above it and in it are as many as are wanted, or it is one key.  The bins
+// are summed over the team by every CTA, which tells it also how many chosen
+// keys the CTAs before it have.
+constexpr int kBins = 256;
+template <int W> struct ChooseRoom {
+  uint32_t high[W], low[W];
+  uint32_t team_high[kMostCtas], team_low[kMostCtas];
+  unsigned sum[W], bin, want, have;
+  unsigned before[2][W];
+  int scan[2][W];
+};
+template <int W, typename Emit>
+__device__ __forceinline__ void choose_team(const uint32_t *keys, int n, unsigned want, int P, int rank,
+                                            unsigned (*bins)[kBins], ChooseRoom<W> &room, Emit emit) {
+  constexpr int kThreads = W * 32, kOwn = kBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (n + kThreads - 1) / kThreads * 32, x0 = warp * run + lane, x1 = min(n, (warp + 1) * run);  // the warp's keys
+  auto meet = [&]() {
+    if (P > 1)
+      team_sync();
+    else
+      __syncthreads();
+  };
+  uint32_t high = 0, low = 0xffffffffu;
+#pragma unroll 4
+  for (int x = x0; x < x1; x += 32) {
+    const uint32_t k = keys[x];
+    high = max(high, k), low = min(low, k);
+  }
+  high = __reduce_max_sync(0xffffffffu, high);
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) room.high[warp] = high, room.low[warp] = low;
+  for (int i = tid; i < kBins; i += kThreads) bins[0][i] = 0, bins[1][i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) high = max(high, room.high[w]), low = min(low, room.low[w]);
+  if (P > 1) {
+    if (tid < P) *peer(&room.team_high[rank], tid) = high, *peer(&room.team_low[rank], tid) = low;
+    team_sync();
+    for (int i = 0; i < P; ++i) high = max(high, room.team_high[i]), low = min(low, room.team_low[i]);
+  }
+  // keys low .. low + span are counted; want of them, the highest, are kept with all above
+  uint32_t span = high - low;
+  int shift = max(0, 32 - __clz(span) - 8);
+  bool exact = false;
+  unsigned taken_before = 0, equal_before = 0;  // a thread's part of what the CTAs before this one have above the bin, and in it
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    unsigned *mine = bins[pass & 1];
+#pragma unroll 4
+    for (int x = x0; x < x1; x += 32) {
+      const uint32_t k = keys[x] - low;
+      if (k <= span) atomicAdd(&mine[k >> shift], 1u);
+    }
+    meet();
+    // thread i sums its bins over the team, the highest ones first
+    unsigned own[kOwn], before[kOwn], sum = 0;
+    const int top = kBins - kOwn * (tid + 1);
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      own[e] = before[e] = 0;
+#pragma unroll 4
+      for (int i = 0; i < P; ++i) {
+        const unsigned u = P > 1 ? *peer(mine + top + e, i) : mine[top + e];
+        own[e] += u;
+        if (i < rank) before[e] += u;
+      }
+      sum += own[e];
+    }
+    unsigned cum = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, cum, o);
+      if (lane >= o) cum += x;
+    }
+    if (lane == 31) room.sum[warp] = cum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) cum += room.sum[w];
+    const unsigned upto = cum;
+    cum -= sum;
+    if (cum < want && want <= upto) {
+#pragma unroll
+      for (int e = kOwn - 1; e >= 0; --e) {
+        if (cum < want && want <= cum + own[e]) room.bin = (unsigned)(top + e), room.want = want - cum, room.have = own[e];
+        cum += own[e];
+      }
+    }
+    __syncthreads();
+    const int bin = (int)room.bin;
+    equal_before = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      if (top + e > bin) taken_before += before[e];
+      if (top + e == bin) equal_before = before[e];
+    }
+    low += (uint32_t)bin << shift;
+    want = room.want;
+    exact = room.have == want;
+    if (exact || shift == 0) break;
+    span = (1u << shift) - 1u;
+    shift = max(0, shift - 8);
+    // read by others in the pass before the last one: its barrier is behind them
+    if (pass > 0)
+      for (int i = tid; i < kBins; i += kThreads) bins[(pass + 1) & 1][i] = 0;
+    __syncthreads();
+  }
+  // kept: the keys from low on if exact, else those above it and the first `want` that equal it
+  int above = 0, equal = 0;
+#pragma unroll 4
+  for (int x = x0; x < x1; x += 32) {
+    const uint32_t k = keys[x];
+    above += k > low || (exact && k == low);
+    equal += !exact && k == low;
+  }
+  above = (int)__reduce_add_sync(0xffffffffu, (unsigned)above);
+  equal = (int)__reduce_add_sync(0xffffffffu, (unsigned)equal);
+  taken_before = __reduce_add_sync(0xffffffffu, taken_before);
+  equal_before = __reduce_add_sync(0xffffffffu, equal_before);
+  if (lane == 0) {
+    room.scan[0][warp] = above, room.scan[1][warp] = equal;
+    room.before[0][warp] = taken_before, room.before[1][warp] = equal_before;
+  }
+  __syncthreads();
+  int taken = 0, seen = 0;  // by the CTAs and warps before; exact: what is in the bin is all kept
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    taken += room.before[0][w] + (exact ? room.before[1][w] : 0u), seen += exact ? 0u : room.before[1][w];
+    if (w < warp) taken += room.scan[0][w], seen += room.scan[1][w];
+  }
+  taken += min(seen, (int)want);
+  const unsigned below = (1u << lane) - 1;
+#pragma unroll 1
+  for (int x = x0; x - lane < x1; x += 32) {
+    const uint32_t k = x < x1 ? keys[x] : 0u;  // no key is 0
+    const unsigned eq = exact ? 0u : __ballot_sync(0xffffffffu, k == low && x < x1);
+    const bool keep = x < x1 && (k > low || (k == low && (exact || seen + __popc(eq & below) < (int)want)));
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) emit(taken + __popc(kept & below), x);
+    seen += __popc(eq);
+    taken += __popc(kept);
+  }
+}
+
+// Shared memory of a CTA, in order: the warps' rings (before them the keys,
+// after them the warps' partial outputs), the parts that the cluster's CTAs hand
+// over, query codes of groups above 8, the own blocks, logits.
 template <int D, int NR, int W> struct Room {
+  static constexpr int kRows = 8 * NR;
   static constexpr int kStage = 2 * kBlock * D;
   static constexpr int kStages = D == 64 ? 4 : 2;  // blocks of a warp on their way
   static constexpr int kRing = W * kStages * kStage;
-  static constexpr int kOut = 8 * NR * D * 4;
+  static constexpr int kParts = (kRows * D / 4 + kMostCtas) * 16;
   static constexpr int kTile = sizeof(Codes<D>) * 32;  // codes of 8 rows
+  static_assert(kRing >= kHeldKeys * 4 + 2 * kBins * 4, "the keys and their bins share the rings' memory");
   __host__ __device__ static int codes(int group) { return NR == 1 || group > kCodesMost ? 0 : (group + 7) / 8 * kTile; }
-  __host__ __device__ static int bytes(int group, int held, int own, int logits) {
-    return 1024 + kRing + kOut + codes(group) + held * 4 + own * 4 + logits * 4;
+  __host__ __device__ static int bytes(int group, int own, int logits) {
+    return 1024 + kRing + kParts + codes(group) + own * 4 + logits * 4;
   }
 };
 
-template <typename F, int D, int NR, int P, int W>
-__global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
+// Weights of the N parts of a row under their maximum: z[i] of each part's mean, and the whole's reference and sum.
+template <int N> __device__ __forceinline__ float2 weigh(const float2 *ml, int step, float (&z)[N]) {
+  float2 p[N];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = ml[i * step], m = fmaxf(m, p[i].x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    z[i] = p[i].x == -INFINITY ? p[i].y : p[i].y * ex2(p[i].x - m);
+    l += z[i];
+  }
+  const float inv = inverse_sum(l);
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] *= inv;
+  return make_float2(m, l);
+}
+
+template <typename F, int D, int NR, int W>
+__global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
     sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using R = Room<D, NR, W>;
-  constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kStages = R::kStages, kRows = 8 * NR;
+  constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kStages = R::kStages, kRows = R::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // swizzled tiles start at multiples of 1024
-  float *cta_o = (float *)(smem + R::kRing);                  // [kRows][D]
-  const int group = a.c.group;
-  Codes<D> *codes = (Codes<D> *)(smem + R::kRing + R::kOut);  // [tile][lane], groups above 8
-  uint32_t *held = (uint32_t *)((uint8_t *)codes + R::codes(group));
-  int *own = (int *)(held + a.held);
+  const int group = a.c.group, P = a.P;
+  uint32_t *keys = (uint32_t *)smem;
+  unsigned(*bins)[kBins] = (unsigned(*)[kBins])(keys + kHeldKeys);
+  float *parts = (float *)(smem + R::kRing);                     // [P][float4s of this CTA's slice]
+  Codes<D> *codes = (Codes<D> *)(smem + R::kRing + R::kParts);  // [tile][lane], groups above 8
+  int *own = (int *)((uint8_t *)codes + R::codes(group));
   float *held_logits = (float *)(own + a.own);
   __shared__ __align__(8) uint64_t full[W][kStages];
-  __shared__ unsigned hist[2][kBins];
-  __shared__ unsigned s_sum[W + 1], s_digit, s_want, s_have, s_top;
-  __shared__ int s_scan[2][W + 1], s_count[2];
-  __shared__ float2 part_ml[W][kRows], cta_ml[kRows];
-  __shared__ float row_base[H2O_BLOCK_MAX_ROWS];
+  __shared__ unsigned s_top;
+  __shared__ ChooseRoom<W> choose_room;
+  __shared__ float2 part_ml[W][kRows], team_ml[kMostCtas][kRows];
+  __shared__ float row_z[kRows][kMostCtas], row_base[H2O_BLOCK_MAX_ROWS];
   const View &c = a.c;
-  // W warps work; one more, where the launch appends, has the new row and then only meets the barriers: its tid is behind
-  // every loop's end (2^25 blocks and list places of at most 2^26)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-  const bool works = warp < W;
-  constexpr int kNone = 1 << 26;
-  const int tid = works ? (int)threadIdx.x : kNone;
-  const int rank = P > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int64_t item = blockIdx.x / P;
+  const int rank = blockIdx.x - (int)item * P;
   const int bh = (int)(item / a.l.n), t = (int)(item - (int64_t)bh * a.l.n), b = bh / c.H, h = bh - b * c.H;
   const Seq s = seq_of(a.l, b);
   if (!s.ok && h == 0 && t == 0 && rank == 0 && tid == 0) atomicOr(c.err, H2O_BERR_RANGE);
   if (t >= s.cnt) return;  // the whole cluster
+  if (a.l.n > 1) grid_launch_dependents();  // scores_kernel
   const Sight v = sight_of(a, s, t);
   const Rows q{a.q.p + t * a.q.st, a.q.sb, a.q.sh, a.q.st};  // the token's rows alone
   const Seq one{s.len, 1, v.end, true};
   int32_t *list = list_of(a, bh, t);
   const size_t scales = (size_t)bh * (c.cap / kBlock);
+  const int per = ceil_div(v.S, P), slot0 = min(v.S, rank * per), slot1 = min(v.S, slot0 + per);  // this CTA's slots
   const bool all = v.nb <= a.n_blocks;
   const int nc = all ? 0 : v.nb - a.n_first - a.n_last;  // candidates n_first .. n_first + nc - 1
-  const bool shared = P > 1 && (nc > kLocal || ceil_div(v.S, P) > a.own);  // the cluster shares the choice
-  const bool local = !all && !shared && nc <= kLocal && ceil_div(v.S, P) <= a.own;
-  const int share = shared ? ceil_div(nc, P) : nc;
-  const int lo = a.n_first + (shared ? min(nc, rank * share) : 0);
-  const int n = min(a.n_first + nc, lo + share) - lo;  // this CTA's candidates lo .. lo + n - 1
-  unsigned want = all ? 0u : (unsigned)(a.n_blocks - a.n_first - a.n_last);
-  const int steps = want > 0 ? ceil_div(n, 16) : 0;
-  const int8_t *bounds = c.bounds + (scales + lo) * 2 * D;
-  const float *ksc = c.Ksc + scales + lo;
+  const unsigned wanted = all ? 0u : (unsigned)(a.n_blocks - a.n_first - a.n_last);
+  const bool near_list = per <= a.own;
+  const bool shared = P > 1 && nc > kAloneKeys;  // each CTA has a share of the keys to make
+  const int share = shared ? (ceil_div(nc, P) + 3) & ~3 : nc;
+  const int lo = shared ? min(nc, rank * share) : 0;
+  const int n = min(nc, lo + share) - lo;  // this CTA's candidates n_first + lo ..
+  const int steps = wanted > 0 ? ceil_div(n, 16) : 0;
+  const int8_t *bounds = c.bounds + (scales + a.n_first + lo) * 2 * D;
+  const float *ksc = c.Ksc + scales + a.n_first + lo;
+  const bool new_row = a.fused && v.S - 1 >= slot0 && v.S - 1 < slot1;  // the last slot's block
 
   grid_dependency_wait();
+  // every CTA has begun before another one writes to its memory
+  if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   Bounds<D> bd;
-  if (works && warp < steps) bd.load(bounds, ksc, warp * 16, n);
-  if (works && lane == 0) {
+  if (warp < steps) bd.load(bounds, ksc, warp * 16, n);
+  Codes<D> qc;
+  float qf[D / 64][16];
+  unsigned top = 0;
+  // every warp for itself; columns behind the last row repeat it
+  if (NR == 1 && steps > 0) top = query_row<D>(q.at(b, h * group + min(g, group - 1), 0), qf);
+  if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
   }
-  // The new row: its block is the last one of the list, and no other CTA touches it.
-  if (!works && rank == (v.S - 1) % P) {
-    append_rows<F, D>(c, false, a.k, b, h, s.len, s.len, s.len + 1);
-    append_rows<F, D>(c, true, a.v, b, h, s.len, s.len, s.len + 1);
-    if (lane == 0) {
+  // The new row, while those loads are on their way; no other CTA touches its block.
+  if (new_row && warp >= W - 2) {
+    const bool is_v = warp == W - 2;
+    append_rows<F, D>(c, is_v, is_v ? a.v : a.k, b, h, s.len, s.len, s.len + 1);
+    if (!is_v && lane == 0) {
       const size_t at = (size_t)bh * c.cap + s.len;
       c.pos[at] = a.position ? a.position[b] : s.len;
       c.score[at] = 0.f;
       c.low[at] = 0.f;
     }
-    __syncwarp();
-    bound_block<F, D>(c, bh, s.len / kBlock, s.total);
     __threadfence();  // the codes are read back by a copy
     asm volatile("fence.proxy.async;" ::: "memory");
   }
 
   // ------------------------------------------------------------- the choice
-  if (want > 0) {
-    uint32_t *keys = n <= a.held ? held : (uint32_t *)logits_of(a, bh, t, 0) + (shared ? rank * share : 0);  // read before any logit is written
-    Codes<D> qc;
+  if (wanted > 0) {
     float inv;
-    if constexpr (NR == 1) {  // every warp for itself; columns behind the last row repeat it
-      float f[D / 64][16];
-      const unsigned top = query_row<D>(q.at(b, h * group + min(g, group - 1), 0), f);
+    if constexpr (NR == 1) {
       inv = inverse_pow2(block_scale<I8>(__uint_as_float(__reduce_max_sync(0xffffffffu, top) << 16)));
-      qc.set(f, inv);
+      if (steps > 0) qc.set(qf, inv);
     } else {
       if (tid == 0) s_top = 0;
       __syncthreads();
-      const int tiles = works ? ceil_div(group, 8) : 0;
+      const int tiles = ceil_div(group, 8);
       for (int x = warp; x < tiles; x += W) {
-        float f[D / 64][16];
-        const unsigned top = __reduce_max_sync(0xffffffffu, query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), f));
+        top = __reduce_max_sync(0xffffffffu, query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), qf));
         if (lane == 0) atomicMax(&s_top, top);
       }
       __syncthreads();
       inv = inverse_pow2(block_scale<I8>(__uint_as_float(s_top << 16)));
       if (group <= kCodesMost) {
         for (int x = warp; x < tiles; x += W) {
-          float f[D / 64][16];
-          query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), f);
-          qc.set(f, inv);
+          query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), qf);
+          qc.set(qf, inv);
           codes[x * 32 + lane] = qc;
         }
         __syncthreads();
       }
     }
-    for (int x = works ? warp : steps; x < steps; x += W) {
+    if (n > kHeldKeys) keys = (uint32_t *)logits_of(a, bh, t, 0) + lo;  // read before any logit is written
+    for (int x = warp; x < steps; x += W) {
       Bounds<D> now = bd;
       if (x + W < steps) bd.load(bounds, ksc, (x + W) * 16, n);
       float2 m;
@@ -402,106 +575,45 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
           if (group <= kCodesMost) {
             qc = codes[y * 32 + lane];
           } else {  // made anew for each 16 blocks
-            float f[D / 64][16];
-            query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), f);
-            qc.set(f, inv);
+            query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), qf);
+            qc.set(qf, inv);
           }
           const float2 z = block_sums<D>(now, qc);
           m = make_float2(fmaxf(m.x, z.x), fmaxf(m.y, z.y));
         }
       }
-      if (t4 < 2) {
-        const int j = x * 16 + t4 * 8 + g;
-        if (j < n) keys[j] = t4 ? key_bits(m.y, now.ks[1]) : key_bits(m.x, now.ks[0]);
-      }
+      // keys of a quad's two blocks are known to its four lanes
+      const int j = x * 16 + (t4 & 1) * 8 + g;
+      const uint32_t key = t4 & 1 ? key_bits(m.y, now.ks[1]) : key_bits(m.x, now.ks[0]);
+      if (t4 < 2 && j < n) keys[j] = key;
     }
     __syncthreads();
-    if (local) {
-      if (works) {
-        if (n <= 128)
-          choose<4, P, W>(a, keys, n, want, lo, rank, warp, own, list);
-        else
-          choose<kLocal / 32, P, W>(a, keys, n, want, lo, rank, warp, own, list);
-      }
+    if (P > 1) team_wait();
+    // Each slot's block, to the list and to the CTA that attends to it.
+    if (shared) {
+      choose_team<W>(keys, n, wanted, P, rank, bins, choose_room, [&](int slot, int x) {
+        slot += a.n_first;
+        const int to = slot / per;
+        list[slot] = a.n_first + lo + x;
+        if (near_list) peer(own, to)[slot - to * per] = a.n_first + lo + x;
+      });
+      team_sync();
     } else {
-      uint32_t prefix = 0, pmask = 0;
-      constexpr int kOwn = kBins / kThreads;
-      unsigned have = 0;
-#pragma unroll 1
-      for (int pass = 0; pass < 4 && have != want; ++pass) {
-        const int shift = 24 - 8 * pass;
-        unsigned *mine = hist[pass & 1];
-        for (int i = tid; i < kBins; i += kThreads) mine[i] = 0;
-        __syncthreads();
-        for (int x = tid; x < n; x += kThreads) {
-          const uint32_t u = keys[x];
-          if ((u & pmask) == prefix) atomicAdd(&mine[(u >> shift) & 255u], 1u);
-        }
-        team_sync<P>();
-        // thread i sums its digits over the cluster, the highest ones first
-        unsigned mine_of[kOwn], sum = 0;
-        const int top = works ? kBins - kOwn * (tid + 1) : 0;
-#pragma unroll
-        for (int e = 0; e < kOwn; ++e) {
-          mine_of[e] = 0;
-          if (works) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) mine_of[e] += *peer<P>(mine + top + e, i);
-          }
-          sum += mine_of[e];
-        }
-        unsigned run = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += x;
-        }
-        if (lane == 31) s_sum[warp] = run;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) run += s_sum[w];
-        unsigned cum = run - sum;
-        if (cum < want && want <= run) {
-#pragma unroll
-          for (int e = kOwn - 1; e >= 0; --e) {
-            if (cum < want && want <= cum + mine_of[e])
-              s_digit = (unsigned)(top + e), s_want = want - cum, s_have = mine_of[e];
-            cum += mine_of[e];
-          }
-        }
-        __syncthreads();
-        prefix |= s_digit << shift;
-        pmask |= 255u << shift;
-        want = s_want;
-        have = s_have;  // as many as are wanted: the digits so far decide
-      }
-      // each thread scans a run of consecutive candidates
-      const int run = ceil_div(n, kThreads), x0 = works ? min(n, tid * run) : n, x1 = min(n, x0 + run);
-      int above = 0, equal = 0;
-      for (int x = x0; x < x1; ++x) above += (keys[x] & pmask) > prefix, equal += (keys[x] & pmask) == prefix;
-      int ia = above, ie = equal;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ie, o);
-        if (lane >= o) ia += x, ie += y;
-      }
-      if (lane == 31) s_scan[0][warp] = ia, s_scan[1][warp] = ie;
-      __syncthreads();
-      int before_a = ia - above, before_e = ie - equal;
-      for (int w = 0; w < warp; ++w) before_a += s_scan[0][w], before_e += s_scan[1][w];
-      if (P > 1) {
-        if (tid == kThreads - 1) s_count[0] = before_a + above, s_count[1] = before_e + equal;
-        team_sync<P>();
-        for (int i = 0; i < rank; ++i) before_a += *peer<P>(&s_count[0], i), before_e += *peer<P>(&s_count[1], i);
-      }
-      for (int x = x0; x < x1; ++x) {
-        const uint32_t u = keys[x] & pmask;
-        const int slot = before_a + min(before_e, (int)want);  // the first of the equal ones stay
-        const bool keep = u > prefix || (u == prefix && before_e < (int)want);
-        before_a += u > prefix;
-        before_e += u == prefix;
-        if (keep) list[a.n_first + slot] = lo + x;
-      }
+      auto mine = [&](int slot, int x) {
+        slot += a.n_first;
+        if (slot < slot0 || slot >= slot1) return;
+        list[slot] = a.n_first + x;
+        if (near_list) own[slot - slot0] = a.n_first + x;
+      };
+      if (nc <= kWarpKeys)  // every warp for itself, and its own slots alone
+        choose_warp<kWarpKeys / 32>(keys, nc, wanted, [&](int slot, int x) {
+          if ((slot + a.n_first - slot0) % W == warp) mine(slot, x);
+        });
+      else
+        choose_team<W>(keys, nc, wanted, 1, 0, bins, choose_room, mine);
     }
+  } else if (P > 1) {
+    team_wait();
   }
   // the list's ends, and what is behind it
   const int first = all ? v.S : a.n_first, last = all ? v.S : v.S - a.n_last;
@@ -510,44 +622,47 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
     for (int i = last + tid; i < v.S; i += kThreads) list[i] = v.nb - v.S + i;
     for (int i = v.S + tid; i < a.n_blocks; i += kThreads) list[i] = -1;
   }
-  if (all || local)
-    __syncthreads();  // the new row is there, every key has been read
-  else
-    team_sync<P>();  // the list is whole too
+  fence_proxy_async_smem();  // copies land where the keys were
+  __syncthreads();           // the new row is there, every key has been read
+  if (new_row && lane == 0) asm volatile("fence.proxy.async;" ::: "memory");
   auto block_of = [&](int slot) {
     if (slot < first) return slot;
     if (slot >= last) return v.nb - v.S + slot;
-    return local ? own[slot / P] : list[slot];
+    return near_list ? own[slot - slot0] : list[slot];
   };
 
   // ----------------------------------------------------------- the attention
-  // Slot rank + P (warp + W i) of the list is the i-th block of a warp.  Logits: by own blocks in shared memory, or by slots in memory.
-  const bool near = a.l.n == 1 && group * ceil_div(v.S, P) * kBlock <= a.logits;
-  const int64_t row_step = near ? ceil_div(v.S, P) * kBlock : c.cap;
-  float *logits = near ? held_logits : logits_of(a, bh, t, 0);
-  auto place = [&](int slot) { return (near ? slot / P : slot) * kBlock; };
+  // Logits: by own blocks in shared memory, or by slots in memory.
+  const bool near = group * per * kBlock <= a.logits;
+  const int64_t row_step = near ? per * kBlock : c.cap;
+  float *logits = near ? held_logits : logits_of(a, bh, t, 0) + slot0 * kBlock;
   uint8_t *ring = smem + warp * kStages * kStage;
   const uint64_t policy = l2_policy(false);
-  const int first_slot = rank + P * warp;
   bool lost = false;
   uint32_t phases = 0;
   // Scores: 8 threads to an own block, four entries each; kAhead of a thread's are on their way at once.
   constexpr int kAhead = 4;
+  const bool weights = a.l.n == 1 && a.accumulate;
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   float4 old[kAhead], less[kAhead];
   auto entry_of = [&](int y) {  // the first of the thread's y-th four, -1 behind the last
-    const int slot = rank + (tid / 8 + y * (kThreads / 8)) * P;
-    return works && slot < v.S ? block_of(slot) * kBlock + tid % 8 * 4 : -1;
+    const int slot = slot0 + tid / 8 + y * (kThreads / 8);
+    return slot < slot1 ? block_of(slot) * kBlock + tid % 8 * 4 : -1;
   };
   auto load_scores = [&](int y, int at) {
     const int j = entry_of(y);
     if (j >= 0) old[at] = *(const float4 *)(score + j), less[at] = *(const float4 *)(low + j);
   };
   for (int row0 = 0; row0 < group; row0 += kRows) {
+    float ks, vs;  // the next block's scales, a block ahead
+    auto scales_of = [&](int slot) {
+      if (slot >= slot1) return;
+      const size_t at = scales + block_of(slot);
+      ks = c.Ksc[at], vs = c.Vsc[at];
+    };
     auto fetch = [&](int i) {
-      const int slot = first_slot + i * P * W;
-      if (!works || slot >= v.S || lane != 0 || lost) return;
-      asm volatile("fence.proxy.async;" ::: "memory");
+      const int slot = slot0 + warp + i * W;
+      if (slot >= slot1 || lane != 0 || lost) return;
       uint8_t *dst = ring + i % kStages * kStage;
       uint64_t *bar = &full[warp][i % kStages];
       const int row = bh * c.cap + block_of(slot) * kBlock;
@@ -556,20 +671,22 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
       tma_load_2d(dst + kBlock * D, &vmap, bar, 0, row, policy);
     };
     for (int i = 0; i < kStages; ++i) fetch(i);
+    scales_of(slot0 + warp);
     Tile<F, D, NR, false> tl;
-    if (works) tl.begin(q, group, 0, one, b, h, row0, nullptr);
-    for (int i = 0; works && first_slot + i * P * W < v.S; ++i) {
-      const int slot = first_slot + i * P * W, blk = block_of(slot);
-      const float ks = c.Ksc[scales + blk], vs = c.Vsc[scales + blk];
+    tl.begin(q, group, 0, one, b, h, row0, nullptr);
+    for (int i = 0; slot0 + warp + i * W < slot1; ++i) {
+      const int slot = slot0 + warp + i * W, blk = block_of(slot);
+      const float ks_now = ks, vs_now = vs;
+      scales_of(slot + W);
       const int st = i % kStages;
       if (!lost && !mbar_wait(&full[warp][st], phases >> st & 1)) lost = true;
       if (lost) break;
       phases ^= 1u << st;
       uint8_t *kt = ring + st * kStage;
-      tl.block(kt, kt + kBlock * D, ks, vs, blk, v.end - blk * kBlock, nullptr,
+      tl.block(kt, kt + kBlock * D, ks_now, vs_now, blk, v.end - blk * kBlock, nullptr,
                [&](int r, int j, float s0, float s1, float s2, float s3) {
                  if (!a.accumulate) return;
-                 float *lg = logits + (row0 + r) * row_step + place(slot) + (j - blk * kBlock);
+                 float *lg = logits + (row0 + r) * row_step + (slot - slot0) * kBlock + (j - blk * kBlock);
                  lg[0] = s0, lg[8] = s1, lg[16] = s2, lg[24] = s3;
                });
       __syncwarp();  // this warp has read the stage
@@ -581,91 +698,91 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
     }
     __syncthreads();  // every warp is done with its ring: the partial outputs go there
     float *po = (float *)smem;  // [W][kRows][D]
-    if (works) {
-      const float part = tl.unit() * kPartDown;
+    const float part = tl.unit() * kPartDown;
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float l = tl.sum(n, u);
-          const int r = 8 * n + 2 * t4 + u;
-          if (g == 0) part_ml[warp][r] = make_float2(tl.m[n][u], l);
-          const float inv = inverse_sum(l);
-          float *dst = po + (warp * kRows + r) * D + g * (D / 8);
+      for (int u = 0; u < 2; ++u) {
+        const float l = tl.sum(n, u);
+        const int r = 8 * n + 2 * t4 + u;
+        if (g == 0) part_ml[warp][r] = make_float2(tl.m[n][u], l);
+        const float inv = inverse_sum(l);
+        float *dst = po + (warp * kRows + r) * D + g * (D / 8);
 #pragma unroll
-          for (int j = 0; j < OT; j += 2)
-            *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u] * inv * part, tl.o[n][j][2 + u] * inv * part,
-                                                   tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
-        }
-    }
+        for (int j = 0; j < OT; j += 2)
+          *(float4 *)(dst + 2 * j) = make_float4(tl.o[n][j][u] * inv * part, tl.o[n][j][2 + u] * inv * part,
+                                                 tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
+      }
     // the own entries' scores are on their way while the parts meet
-    if (row0 == 0 && a.l.n == 1 && a.accumulate) {
+    if (row0 == 0 && weights) {
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) load_scores(y, y);
     }
     __syncthreads();
-    // the CTA's warps, then the cluster's CTAs: weighted means of weighted means
-    auto meet = [&](int parts, auto ml_of, auto o_of, float &m, float &l, float4 &o) {
-      m = -INFINITY, l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < parts; ++i) m = fmaxf(m, ml_of(i).x);
-      for (int i = 0; i < parts; ++i) {
-        const float2 p = ml_of(i);
-        l += p.x == -INFINITY ? p.y : p.y * ex2(p.x - m);
+    // The CTA's parts become one, and go to the CTA that joins their slice: four dimensions of a row to a thread.
+    const int rows = min(group - row0, kRows), fours = rows * (D / 4), slice = ceil_div(fours, P);
+    for (int x = tid; x < fours; x += kThreads) {
+      const int r = x / (D / 4), d0 = x % (D / 4) * 4;
+      float z[W];
+      const float2 ml = weigh<W>(&part_ml[0][r], kRows, z);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float4 e = *(const float4 *)(po + (i * kRows + r) * D + d0);
+        o.x = fmaf(e.x, z[i], o.x), o.y = fmaf(e.y, z[i], o.y), o.z = fmaf(e.z, z[i], o.z), o.w = fmaf(e.w, z[i], o.w);
       }
+      const int to = x / slice;
+      *(float4 *)peer(parts + (rank * slice + x - to * slice) * 4, to) = o;
+      if (d0 < P * 4)  // (m, l) to every CTA, by as many threads
+        for (int i = d0 / 4; i < P; i += D / 4) *peer(&team_ml[rank][r], i) = ml;
+    }
+    team_sync();
+    // A row's parts, kMostCtas lanes to a row: their weights, the row's sum.
+    for (int x = tid; x < kRows * kMostCtas; x += kThreads) {
+      const int r = x / kMostCtas, i = x % kMostCtas;
+      const float2 p = i < P && r < rows ? team_ml[i][r] : make_float2(-INFINITY, 0.f);
+      float m = p.x;
+#pragma unroll
+      for (int o = 1; o < kMostCtas; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float z = p.x == -INFINITY ? p.y : p.y * ex2(p.x - m);
+      float l = z;
+#pragma unroll
+      for (int o = 1; o < kMostCtas; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       const bool any = l > 0.f || l != l;
-      const float inv = any ? 1.f / l : 0.f;
-      for (int i = 0; i < parts; ++i) {
-        const float2 p = ml_of(i);
-        const float z = (p.x == -INFINITY ? p.y : p.y * ex2(p.x - m)) * inv;
-        const float4 e = o_of(i);
+      row_z[r][i] = any ? z / l : 0.f;
+      if (i == 0 && r < rows) {
+        const float base = weight_base(m, l);
+        const int hq = h * group + row0 + r;
+        row_base[row0 + r] = base;
+        if (rank == 0) {
+          if (a.lse) a.lse[((size_t)b * c.H * group + hq) * a.l.n + t] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (a.l.n > 1) c.part[(size_t)bh * c.max_rows + t * group + row0 + r] = base;
+        }
+      }
+    }
+    __syncthreads();
+    for (int y = tid; y < slice && rank * slice + y < fours; y += kThreads) {
+      const int x = rank * slice + y, r = x / (D / 4), d0 = x % (D / 4) * 4, hq = h * group + row0 + r;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < P; ++i) {
+        const float4 e = *(const float4 *)(parts + (i * slice + y) * 4);
+        const float z = row_z[r][i];
         o.x = fmaf(e.x, z, o.x), o.y = fmaf(e.y, z, o.y), o.z = fmaf(e.z, z, o.z), o.w = fmaf(e.w, z, o.w);
       }
-    };
-    const int rows = min(group - row0, kRows);
-    for (int x = tid; x < rows * (D / 4); x += kThreads) {
-      const int r = x / (D / 4), d0 = x % (D / 4) * 4;
-      float m, l;
-      float4 o;
-      meet(W, [&](int i) { return part_ml[i][r]; }, [&](int i) { return *(const float4 *)(po + (i * kRows + r) * D + d0); },
-           m, l, o);
-      *(float4 *)(cta_o + r * D + d0) = o;
-      if (d0 == 0) cta_ml[r] = make_float2(m, l);
-    }
-    team_sync<P>();
-    for (int x = rank * kThreads + tid; x < rows * (D / 4); x += P * kThreads) {
-      const int r = x / (D / 4), d0 = x % (D / 4) * 4, hq = h * group + row0 + r;
-      float m, l;
-      float4 o;
-      meet(P, [&](int i) { return *peer<P>(&cta_ml[r], i); },
-           [&](int i) { return *(const float4 *)peer<P>(cta_o + r * D + d0, i); }, m, l, o);
       const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * kPartUp, o.y * kPartUp),
                            p1 = __floats2bfloat162_rn(o.z * kPartUp, o.w * kPartUp);
       *(uint2 *)(const_cast<__nv_bfloat16 *>(a.out.at(b, hq, t)) + d0) =
           make_uint2(*(const uint32_t *)&p0, *(const uint32_t *)&p1);
-      if (d0 == 0) {
-        const bool any = l > 0.f || l != l;
-        if (a.lse) a.lse[((size_t)b * c.H * group + hq) * a.l.n + t] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
-        if (a.l.n > 1) c.part[(size_t)bh * c.max_rows + t * group + row0 + r] = weight_base(m, l);
-      }
     }
-    if (a.l.n == 1 && a.accumulate && tid < rows) {
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < P; ++i) m = fmaxf(m, peer<P>(&cta_ml[tid], i)->x);
-      for (int i = 0; i < P; ++i) {
-        const float2 p = *peer<P>(&cta_ml[tid], i);
-        l += p.x == -INFINITY ? p.y : p.y * ex2(p.x - m);
-      }
-      row_base[row0 + tid] = weight_base(m, l);
+    if (row0 + kRows < group) {
+      fence_proxy_async_smem();  // the next rows' copies land where the parts were
+      team_sync();               // and every part has been read
     }
-    fence_proxy_async_smem();  // the next rows' copies land where the parts were
-    if (row0 + kRows < group) team_sync<P>();  // the parts have been read
   }
-  __syncwarp();
-  if (P > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // and the last ones too
 
   // -------------------------------------------------------------- the scores
-  if (a.l.n == 1 && a.accumulate) {
-    __syncthreads();
+  if (weights) {
     for (int y0 = 0; entry_of(y0) >= 0; y0 += kAhead) {
       if (y0 > 0) {
 #pragma unroll
@@ -675,7 +792,7 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
       for (int y = 0; y < kAhead; ++y) {
         const int j = entry_of(y0 + y);
         if (j < 0) break;
-        const float *lg = logits + place(rank + (tid / 8 + (y0 + y) * (kThreads / 8)) * P) + tid % 8 * 4;
+        const float *lg = logits + (tid / 8 + (y0 + y) * (kThreads / 8)) * kBlock + tid % 8 * 4;
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int r = 0; r < group; ++r) {
@@ -687,8 +804,7 @@ __global__ void __launch_bounds__(W * 32 + 32, W == 4 && NR == 1 ? 2 : 1)
       }
     }
   }
-  __syncwarp();
-  if (P > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // a peer may still read this CTA's parts
+  if (new_row && warp == W - 1) bound_block<F, D>(c, bh, s.len / kBlock, s.total);  // for the calls to come
 }
 
 // The weights of several tokens' rows, added in the tokens' order: a CTA has
@@ -773,39 +889,47 @@ cudaError_t launch_with(void (*kernel)(X...), unsigned ctas, int threads, int sm
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename F, int D, int NR, int P, int W>
-cudaError_t sparse_p(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-  const int blocks = a.c.cap / kBlock, own = (std::min(blocks, a.n_blocks) + P - 1) / P;
-  const int share = std::min(blocks, std::max(kLocal, (blocks + P - 1) / P));
-  a.held = (std::min(share, kHeldMost) + 3) & ~3;
+template <typename F, int D, int NR, int W>
+cudaError_t sparse_w(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+  const int own = (std::min(a.c.cap / kBlock, a.n_blocks) + a.P - 1) / a.P;
   a.own = (std::min(own, kOwnMost) + 3) & ~3;
   const int64_t logits = (int64_t)a.c.group * own * kBlock;
   a.logits = a.accumulate && a.l.n == 1 && logits <= kLogitsMost ? (int)logits : 0;
-  const int smem = Room<D, NR, W>::bytes(a.c.group, a.held, a.own, a.logits);
+  const int smem = Room<D, NR, W>::bytes(a.c.group, a.own, a.logits);
   static SmemLimit limit;
-  const auto kernel = sparse_kernel<F, D, NR, P, W>;
-  cudaError_t e = limit.raise((const void *)kernel, smem);
-  if (e == cudaSuccess && P > 8)
-    e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const auto kernel = sparse_kernel<F, D, NR, W>;
+  const cudaError_t e = limit.raise((const void *)kernel, smem);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * P;
-  return launch_with(kernel, (unsigned)ctas, (W + a.fused) * 32, smem, P, a.l.appends && !a.fused, st, a, kmap, vmap);
+  const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * a.P;
+  return launch_with(kernel, (unsigned)ctas, W * 32, smem, a.P, a.l.appends && !a.fused, st, a, kmap, vmap);
 }
 
+// CTAs of 8 warps, one an SM, while they all fit at once, as many to a token as
+// do; more tokens than SMs: CTAs of 4 warps, three an SM; more than those hold:
+// of 2 warps, six an SM, since the way from lengths to outputs is then hidden by
+// other tokens and not by more warps.  Measured, us a call (2 / 4 / 8 warps, the
+// best P of each): 8 heads of 8,000 entries 25 (P = 16, 15) / 13.8; 128 of
+// 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512 90 / 107 /
+// 104; 3,584 of 700 to 2,047 145 / 163 / 284.
 template <typename F, int D, int NR>
-cudaError_t sparse_n(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
-  const int64_t items = (int64_t)a.c.B * a.c.H * a.l.n;
-  const int blocks = a.c.cap / kBlock;
-  auto fits = [&](int p, int per_sm) { return items * p <= (int64_t)per_sm * a.c.sms && blocks >= 8 * p; };
-  if (items * 16 <= a.c.sms && blocks >= 2048) return sparse_p<F, D, NR, 16, 8>(a, kmap, vmap, st);
-  if (fits(8, 1)) return sparse_p<F, D, NR, 8, 8>(a, kmap, vmap, st);
-  if (fits(4, 2)) return sparse_p<F, D, NR, 4, 4>(a, kmap, vmap, st);
-  if (fits(2, 2)) return sparse_p<F, D, NR, 2, 4>(a, kmap, vmap, st);
-  return sparse_p<F, D, NR, 1, 4>(a, kmap, vmap, st);
+cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+  // counts leave tokens out: half of those behind the first, on the average
+  const int64_t heads = (int64_t)a.c.B * a.c.H;
+  const int64_t items = a.l.counts ? heads * (a.l.n + 1) / 2 : heads * a.l.n;
+  const int blocks = a.c.cap / kBlock, sms = a.c.sms;
+  a.P = 1;
+  if (items <= sms) {
+    for (int p : {2, 3, 4, 6, 8})
+      if (items * p <= sms && blocks >= 8 * p) a.P = p;
+    return sparse_w<F, D, NR, 8>(a, kmap, vmap, st);
+  }
+  if (2 * items <= 3 * sms && blocks >= 16) a.P = 2;
+  if (NR == 1 && items > 3 * sms) return sparse_w<F, D, 1, 2>(a, kmap, vmap, st);
+  return sparse_w<F, D, NR, 4>(a, kmap, vmap, st);
 }
 
 template <typename F, int D>
-cudaError_t sparse_d(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+cudaError_t sparse_d(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   cudaError_t e = a.c.group <= 8 ? sparse_n<F, D, 1>(a, kmap, vmap, st) : sparse_n<F, D, 2>(a, kmap, vmap, st);
   if (e != cudaSuccess || !a.accumulate || a.l.n == 1) return e;
   const int64_t heads = (int64_t)a.c.B * a.c.H;
@@ -825,8 +949,8 @@ cudaError_t launch_sparse(const View &c, const Lens &l, const Rows &q, const Row
     cudaError_t e = launch_append(c, l, *k, *v, position, nullptr, st);
     if (e != cudaSuccess) return e;
   }
-  const Args a{c, l, q, out, lse, blocks, causal, accumulate, n_blocks, n_first, n_last,
-               fused, k ? *k : none, v ? *v : none, position, 0, 0, 0};
+  Args a{c, l, q, out, lse, blocks, causal, accumulate, n_blocks, n_first, n_last,
+               fused, k ? *k : none, v ? *v : none, position, 1, 0, 0};
   if (c.kv == H2O_KV_E4M3)
     return c.d == 128 ? sparse_d<E4M3, 128>(a, kmap, vmap, st) : sparse_d<E4M3, 64>(a, kmap, vmap, st);
   return c.d == 128 ? sparse_d<I8, 128>(a, kmap, vmap, st) : sparse_d<I8, 64>(a, kmap, vmap, st);
