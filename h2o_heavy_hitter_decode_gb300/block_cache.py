@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes as C
+import struct
 import threading
 
 import torch
@@ -12,6 +13,7 @@ from . import H2OError, _check, _ptr, lib
 __all__ = ["H2OBlockCache"]
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+PACK = struct.Struct("4q").pack_into  # an h2o_rows
 KV = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
 
 
@@ -166,8 +168,7 @@ class H2OBlockCache:
             if one != 1 or (sb | sh | st) & 7 or p & 15:
                 raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
                                  f"{t.stride()} at address {p:#x}")
-        r = self._slots[slot]
-        r[0], r[1], r[2], r[3] = p, sb, sh, st
+        PACK(self._slots[slot], 0, p, sb, sh, st)
         return self._slot_at[slot]
 
     @staticmethod
@@ -284,6 +285,8 @@ class H2OBlockCache:
 
     @staticmethod
     def _choice(n_blocks, n_first, n_last):
+        if type(n_blocks) is type(n_first) is type(n_last) is int and 0 <= n_first <= n_blocks < 1 << 31 > n_last >= 0:
+            return n_blocks, n_first, n_last
         return _whole(n_blocks, "n_blocks"), _whole(n_first, "n_first"), _whole(n_last, "n_last")
 
     def _blocks(self, t, n, n_blocks):

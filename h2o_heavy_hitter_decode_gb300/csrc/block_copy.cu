@@ -125,8 +125,9 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
     int x = 0;
     int64_t i = item;
     while (i >= items_of[x]) i -= items_of[x++];
-    const int h = (int)(i % a.H);
-    const int64_t at = i / a.H * chunk;  // the chunk's first byte of a row's
+    const int64_t pieces = items_of[x] / a.H;  // neighbours in a row to neighbouring CTAs
+    const int h = (int)(i / pieces);
+    const int64_t at = (i - h * pieces) * chunk;  // the chunk's first byte of a row's
     auto bytes_of = [&](int p) {
       const int64_t left = (int64_t)blocks[p] * a.per_block[x] - at;
       return (int)(left < 0 ? 0 : left < chunk ? left : chunk);

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const Args a) {
   constexpr int L = D / 16;       // lanes of a row
   constexpr int kAtOnce = 32 / L;  // heads
   constexpr int N = 8 / VecN<T>::N;
+  constexpr int kAhead = 4 / N;
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int all = a.chunks[0] + a.chunks[1];
@@ -104,41 +105,49 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const Args a) {
   const T *in = (const T *)a.in[which] + b * a.sin[which][0] + t * a.sin[which][2];
   T *out = (T *)a.out[which] + b * a.sout[which][0] + t * a.sout[which][2];
   const int end = min(a.heads[which], (chunk + 1) * a.per);
-  for (int h = chunk * a.per + lane / L; h - lane / L < end; h += kAtOnce) {
-    const bool is = h < end;
-    const T *src = in + (int64_t)(is ? h : 0) * a.sin[which][1];  // its lanes work on head 0 behind the last one
-    uint4 u0[N], u1[N];
-    float x[16];
-    load8(src + c0 * 8, u0), load8(src + c1 * 8, u1);
-    unpack8<T>(u0, x), unpack8<T>(u1, x + 8);
-    if (r.norm) {
-      float s = 0.f;
+  // kAhead rows of a lane are on their way at once.
+  for (int h0 = chunk * a.per + lane / L; h0 - lane / L < end; h0 += kAtOnce * kAhead) {
+    uint4 u[kAhead][2][N];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
-#pragma unroll
-      for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float f = rsqrtf(s * (1.f / D) + r.eps);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= f * w[e];
+    for (int y = 0; y < kAhead; ++y) {
+      const int h = h0 + y * kAtOnce;
+      const T *src = in + (int64_t)(h < end ? h : 0) * a.sin[which][1];  // behind the last one head 0 again
+      load8(src + c0 * 8, u[y][0]), load8(src + c1 * 8, u[y][1]);
     }
-    if (turns) {
-      auto turn = [&](int e, float &p, float &q) {
-        const float p0 = p;
-        p = p0 * cs[e] - q * sn[e];
-        q = q * cs[e] + p0 * sn[e];
-      };
-      if (r.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn(e, x[2 * e], x[2 * e + 1]);
-      } else {
+    for (int y = 0; y < kAhead; ++y) {
+      const int h = h0 + y * kAtOnce;
+      float x[16];
+      unpack8<T>(u[y][0], x), unpack8<T>(u[y][1], x + 8);
+      if (r.norm) {
+        float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn(e, x[e], x[e + 8]);
+        for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float f = rsqrtf(s * (1.f / D) + r.eps);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= f * w[e];
       }
+      if (turns) {
+        auto turn = [&](int e, float &p, float &q) {
+          const float p0 = p;
+          p = p0 * cs[e] - q * sn[e];
+          q = q * cs[e] + p0 * sn[e];
+        };
+        if (r.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) turn(e, x[2 * e], x[2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) turn(e, x[e], x[e + 8]);
+        }
+      }
+      if (h >= end) continue;
+      T *dst = out + (int64_t)h * a.sout[which][1];
+      store8(dst + c0 * 8, x);
+      store8(dst + c1 * 8, x + 8);
     }
-    if (!is) continue;
-    T *dst = out + (int64_t)h * a.sout[which][1];
-    store8(dst + c0 * 8, x);
-    store8(dst + c1 * 8, x + 8);
   }
 }
 

@@ -4,6 +4,8 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import struct
+import threading
 from fractions import Fraction
 
 import torch
@@ -12,8 +14,9 @@ from . import H2O_BF16, H2O_F32, _check, lib
 
 __all__ = ["H2ORotary"]
 
-TYPES = {torch.bfloat16: (H2O_BF16, 8), torch.float32: (H2O_F32, 4)}  # and elements in 16 bytes
-I32 = torch.int32
+BF16, I32 = torch.bfloat16, torch.int32
+TYPES = {BF16: H2O_BF16, torch.float32: H2O_F32}
+PACK = struct.Struct("4q").pack_into  # an h2o_rows
 # 2 pi to 50 digits: a frequency's fraction of a turn is taken to 64 bits
 TWO_PI = Fraction("6.2831853071795864769252867665590057683943387987502")
 
@@ -96,26 +99,37 @@ class H2ORotary:
         at = [t.data_ptr() if t is not None and t.numel() else None for t in (self._turns, self._axis, *self._weights)]
         torch.cuda.current_stream(self.device).synchronize()  # the tables are there for every stream
         self._known = {self._raw_stream(self._index)}  # streams that the tables' allocations know of
+        self._lock = threading.Lock()
+        self._slots = (C.c_int64 * 16)()  # h2o_rows of q, k, q_out and k_out
+        self._slots_at = C.addressof(self._slots)
         self._desc = _Rotary(d, pairs, int(self.interleaved), self.axes, int(eps is not None),
                              0.0 if eps is None else eps, *at)
         self._desc_at = C.addressof(self._desc)
 
-    def _rows(self, t, shape, name):
-        """The h2o_rows of a tensor [B, heads, n, d] whose rows are contiguous."""
+    def _rows(self, slot, t, shape, dtype, name):
+        """Address of the h2o_rows of a tensor of that shape and type whose rows are contiguous."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor")
-        if t.shape != shape or t.dtype not in TYPES or t.get_device() != self._index:
-            raise ValueError(f"{name}: expected bfloat16 or float32 {tuple(shape)} on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        step = TYPES[t.dtype][1] - 1
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {self.device}, got {t.dtype} {tuple(t.shape)} "
+                             f"on {t.device}")
+        step = 7 if dtype is BF16 else 3
         sb, sh, st, one = t.stride()
         p = t.data_ptr()
-        # a dimension of size 1 is never stepped over: its stride may be anything
-        sb, sh, st = (s if n > 1 else 0 for s, n in zip((sb, sh, st), shape))
         if one != 1 or (sb | sh | st) & step or p & 15:
-            raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
-                             f"{t.stride()} at address {p:#x}")
-        return (C.c_int64 * 4)(p, sb, sh, st)
+            # a dimension of size 1 is never stepped over: its stride may be anything
+            sb, sh, st = (s if n > 1 else 0 for s, n in zip((sb, sh, st), shape))
+            if one != 1 or (sb | sh | st) & step or p & 15:
+                raise ValueError(f"{name}: rows must be contiguous and start at 16-byte boundaries, got strides "
+                                 f"{t.stride()} at address {p:#x}")
+        PACK(self._slots, slot, p, sb, sh, st)
+        return self._slots_at + slot
+
+    def _ints(self, t, shape, name):
+        if not isinstance(t, torch.Tensor) or t.dtype is not I32 or t.shape != shape or \
+                t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {I32} {shape} on {self.device}")
+        return t.data_ptr()
 
     def apply(self, q, k, position, counts=None, q_out=None, k_out=None):
         """Norm and rotate q [B, query heads, n, d] and k [B, key heads, n, d]
@@ -126,51 +140,59 @@ class H2ORotary:
         on every axis, or int32 [axes, B, n].  ``counts`` (int32 [B]): rows
         behind a sequence's count are not read, and left as they were in the
         outputs.  See h2o_rotate."""
-        ref = q if q is not None else k
+        ref = k if q is None else q
         if not isinstance(ref, torch.Tensor) or ref.dim() != 4:
             raise ValueError("q, k: expected [B, heads, n, d] tensors, one of them at least")
         B, _, n, d = ref.shape
-        if d != self.d:
-            raise ValueError(f"rows of {self.d} elements expected, got {d}")
-        if ref.dtype not in TYPES:
-            raise ValueError(f"q, k: expected torch.bfloat16 or torch.float32, got {ref.dtype}")
-        heads, ins, outs, given = [], [], [], []
-        for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                if y is not None:
-                    raise ValueError(f"{name}_out without {name}")
-                heads.append(0), ins.append(None), outs.append(None), given.append(None)
-                continue
-            if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.dtype is not ref.dtype:
-                raise ValueError(f"{name}: expected a {ref.dtype} [B, heads, n, d] tensor")
-            shape = (B, x.shape[1], n, d)
-            if y is None:
-                # rows behind a sequence's count are not written
-                y = (torch.empty if counts is None else torch.zeros)(shape, dtype=x.dtype, device=self.device)
-            elif not isinstance(y, torch.Tensor) or y.dtype is not x.dtype:
-                raise ValueError(f"{name}_out: expected a {x.dtype} tensor")
-            heads.append(shape[1]), ins.append(self._rows(x, shape, name)), outs.append(self._rows(y, shape, name + "_out"))
-            given.append(y)
-        per_token = isinstance(position, torch.Tensor) and position.dim() == 3
-        want = (max(self.axes, position.shape[0]), B, n) if per_token else (B,)
-        for t, shape, name in ((position, want, "position"), (counts, (B,), "counts")):
-            if t is None and (name == "counts" or self.dims == 0):
-                continue
-            if not isinstance(t, torch.Tensor) or t.dtype is not I32 or t.shape != shape or \
-                    t.get_device() != self._index or not t.is_contiguous():
-                raise ValueError(f"{name}: expected contiguous {I32} {shape} on {self.device}")
-        stream = self._raw_stream(self._index)
-        if stream not in self._known:
-            # tables that are dropped while this stream still runs keep their memory until it is done
-            for t in self._tables:
-                t.record_stream(torch.cuda.current_stream(self.device))
-            self._known.add(stream)
-        args = (self._desc_at, TYPES[ref.dtype][0], B, n, *heads, *ins, None if position is None else position.data_ptr(),
-                per_token, None if counts is None else counts.data_ptr(), *outs, stream)
-        if torch.cuda.current_device() == self._index:
-            rc = self._lib.h2o_rotate(*args)
+        dtype = ref.dtype
+        if d != self.d or dtype not in TYPES:
+            raise ValueError(f"q, k: expected rows of {self.d} torch.bfloat16 or torch.float32, got {d} {dtype}")
+        cnt = None if counts is None else self._ints(counts, (B,), "counts")
+        if position is None and self.dims == 0:
+            where, per_token = None, 0
+        elif isinstance(position, torch.Tensor) and position.dim() == 3:
+            where, per_token = self._ints(position, (max(self.axes, position.shape[0]), B, n), "position"), 1
         else:
-            with torch.cuda.device(self._index):
+            where, per_token = self._ints(position, (B,), "position"), 0
+        with self._lock:  # its rows' descriptors
+            hq = hk = 0
+            qi = ki = qo = ko = None
+            if q is not None:
+                hq = ref.shape[1]
+                shape = (B, hq, n, d)
+                qi = self._rows(0, q, shape, dtype, "q")
+                if q_out is None:
+                    q_out = self._new(shape, dtype, counts)
+                qo = self._rows(64, q_out, shape, dtype, "q_out")
+            elif q_out is not None:
+                raise ValueError("q_out without q")
+            if k is not None:
+                if not isinstance(k, torch.Tensor) or k.dim() != 4:
+                    raise ValueError("k: expected a [B, heads, n, d] tensor")
+                hk = k.shape[1]
+                shape = (B, hk, n, d)
+                ki = self._rows(32, k, shape, dtype, "k")
+                if k_out is None:
+                    k_out = self._new(shape, dtype, counts)
+                ko = self._rows(96, k_out, shape, dtype, "k_out")
+            elif k_out is not None:
+                raise ValueError("k_out without k")
+            stream = self._raw_stream(self._index)
+            if stream not in self._known:
+                # tables that are dropped while this stream still runs keep their memory until it is done
+                for t in self._tables:
+                    t.record_stream(torch.cuda.current_stream(self.device))
+                self._known.add(stream)
+            args = (self._desc_at, TYPES[dtype], B, n, hq, hk, qi, ki, where, per_token, cnt, qo, ko, stream)
+            if torch.cuda.current_device() == self._index:
                 rc = self._lib.h2o_rotate(*args)
-        _check(rc, "h2o_rotate")
-        return given[0], given[1]
+            else:
+                with torch.cuda.device(self._index):
+                    rc = self._lib.h2o_rotate(*args)
+        if rc:
+            _check(rc, "h2o_rotate")
+        return q_out, k_out
+
+    def _new(self, shape, dtype, counts):
+        # rows behind a sequence's count are not written
+        return (torch.empty if counts is None else torch.zeros)(shape, dtype=dtype, device=self.device)
