@@ -21,7 +21,6 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kBulk = 6, kArrays = 8;  // K, V, pos, score, low, bounds; then the scales
-constexpr int kMostChunk = 4096;       // bytes of a row that a CTA takes at a time, at most
 
 struct Args {
   const uint8_t *from[kArrays];
@@ -34,6 +33,7 @@ struct Args {
   int H, to_rows, from_rows, from_cap, to_cap;
   int same;    // the rows are those of one cache
   int arrays;  // kBulk, or one less without bounds
+  int chunk;   // bytes of a row that a CTA takes at a time, at most: a power of two
   int room;    // bytes for the rows' pieces
 };
 
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
   }
   const int sources = s_sources, n_moves = s_moves, most = s_most;
   if (n_moves == 0 || most == 0) return;
-  int chunk = kMostChunk;
+  int chunk = a.chunk;
   while (chunk > 16 && (int64_t)chunk * sources > a.room) chunk >>= 1;
 
   // Items: (head, array, chunk), then the scales.
@@ -201,13 +201,17 @@ cudaError_t launch_copy(const View &to, const View &from, const int32_t *parent,
   a.same = to.K == from.K;
   a.arrays = to.bounds && from.bounds ? kBulk : kBulk - 1;
   const int lists = (3 * from.B + to.B) * 4;
-  const int most = 16 * from.B > 65536 ? 16 * from.B : 65536;
-  a.room = most;
+  // Four CTAs an SM.  Large caches: several waves of them and larger pieces (64 rows of 56 heads 309 -> 306 us, prompt forks
+  // 194 -> 177; four beams of 255 entries would take 18 us for 9).  Room for fewer and larger pieces, 98 KB of two CTAs an
+  // SM, 315 and 190; the next item's reads under this one's writes, with half the pieces' size, 312 and 192 at best.
+  const bool large = 2 * (int64_t)to.B * to.H * to.cap * to.d >= 256 << 20;
+  a.chunk = large ? 8192 : 4096;
+  a.room = 16 * from.B > 49152 ? 16 * from.B : 49152;
   const int smem = a.room + lists;
   static SmemLimit limit;
   const cudaError_t e = limit.raise((const void *)copy_kernel, smem);
   if (e != cudaSuccess) return e;
-  copy_kernel<<<to.sms * 3, kThreads, smem, st>>>(a);
+  copy_kernel<<<to.sms * (large ? 16 : 4), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
