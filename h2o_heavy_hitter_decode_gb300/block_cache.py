@@ -181,13 +181,17 @@ class H2OBlockCache:
         return (self.B, heads, n, self.d)
 
     # ---------------------------------------------------------------- calls
-    def append(self, k, v, lengths, counts=None, position=None, score=None):
+    def append(self, k, v, lengths, counts=None, position=None, score=None, rotary=None):
         """Quantise rows k, v [B, H, n, d] (bf16) into entries ``lengths[b]``
         .. of each sequence, with positions from ``position`` (int32 [B],
         default ``lengths``) and scores ``score`` (fp32 [B, H, n], for example
-        a prompt's column sums; default 0).  See h2o_bcache_append."""
+        a prompt's column sums; default 0).  With an H2ORotary ``rotary`` the
+        keys are normed and rotated by those positions first.  See
+        h2o_bcache_append."""
         n = self._tokens(k, "k")
         shape = self._shape(self.H, n)
+        if rotary is not None:
+            k = self._turned(rotary, None, k, lengths, counts, position)[1]
         with self._lock:
             args = (self._rows(1, k, shape, "k"), self._rows(2, v, shape, "v"), self._lengths(lengths, "lengths"),
                     self._dense(counts, I32, self._per_seq, "counts"),
@@ -216,14 +220,18 @@ class H2OBlockCache:
             _check(self._lib.h2o_bcache_attend(self._h, n, *args), "h2o_bcache_attend")
         return out
 
-    def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None):
+    def step(self, q, k, v, lengths, counts=None, position=None, accumulate=True, out=None, lse=None, rotary=None):
         """Append k, v [B, H, n, d] behind ``lengths[b]`` entries, then attend
         causally with q [B, H * group, n, d]; returns out.  The caller adds the
         counts (or n) to ``lengths`` afterwards, and to ``position``, which is
-        needed from the first eviction on (the default are the lengths).  See
+        needed from the first eviction on (the default are the lengths).  With
+        an H2ORotary ``rotary``, q and k are normed and rotated by those
+        positions first (q and k themselves stay as they are).  See
         h2o_bcache_step."""
         n = self._tokens(q, "q")
         shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
+        if rotary is not None:
+            q, k = self._turned(rotary, q, k, lengths, counts, position)
         with self._lock:
             rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
             lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
@@ -257,11 +265,13 @@ class H2OBlockCache:
         return out
 
     def step_sparse(self, q, k, v, lengths, n_blocks: int, n_first: int = 1, n_last: int = 2, counts=None, position=None,
-                    accumulate=True, out=None, lse=None, blocks=None):
+                    accumulate=True, out=None, lse=None, blocks=None, rotary=None):
         """``step`` whose queries attend to ``n_blocks`` chosen blocks each
         (``attend_sparse``).  See h2o_bcache_step_sparse."""
         n = self._tokens(q, "q")
         shape, kv_shape = self._shape(self._heads, n), self._shape(self.H, n)
+        if rotary is not None:
+            q, k = self._turned(rotary, q, k, lengths, counts, position)
         choice = self._choice(n_blocks, n_first, n_last)
         with self._lock:
             rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
@@ -295,6 +305,12 @@ class H2OBlockCache:
         if t is None and n_blocks > 0:
             t = torch.empty(shape, dtype=I32, device=self.device)
         return self._dense(t, I32, shape, "blocks")
+
+    def _turned(self, rotary, q, k, lengths, counts, position):
+        """q and k normed and rotated by their positions, in rows of their own (those behind a count hold anything: no
+        call reads them)."""
+        outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=self.device) for t in (q, k)]
+        return rotary.apply(q, k, lengths if position is None else position, counts, *outs)
 
     def _new_out(self, shape, counts):
         # rows behind a sequence's count are not written

@@ -43,12 +43,13 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
 }
 
 // Shared memory: the pieces; slot_of [from_rows] (a read row's place among the
-// pieces, -1); blocks [from_rows]; and the list of moves.
+// pieces, -1); blocks [from_rows] (their lengths first); the read rows and the
+// rows that receive something, in order; parent [to_rows].
 __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   int *slot_of = (int *)(smem + a.room), *blocks = slot_of + a.from_rows;
   int *source = blocks + a.from_rows;  // of a piece
-  int *dest = source + a.from_rows;    // rows that receive something, in order
+  int *dest = source + a.from_rows, *parent = dest + a.to_rows;
   __shared__ __align__(8) uint64_t bar;
   __shared__ int s_sources, s_moves, s_most, s_warp[kThreads / 32], s_lost;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -57,24 +58,17 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
     mbar_init(&bar, 1);
     fence_mbar_init();
   }
-  for (int p = tid; p < a.from_rows; p += kThreads) slot_of[p] = -1;
+  for (int p = tid; p < a.from_rows; p += kThreads) slot_of[p] = -1, blocks[p] = a.from_lengths[p];
+  for (int b = tid; b < a.to_rows; b += kThreads) parent[b] = a.parent[b];
   __syncthreads();
-  // What moves: a row in place stays, one whose source or length is out of range too.
-  auto moves = [&](int b, int &p) {
-    p = a.parent[b];
-    if (p == -1) return false;
-    if (p < -1 || p >= a.from_rows) return false;
-    const int len = a.from_lengths[p];
-    return len >= 0 && len <= a.from_cap && len <= a.to_cap && !(a.same && p == b);
-  };
   for (int b0 = 0; b0 < a.to_rows; b0 += kThreads) {
     const int b = b0 + tid;
-    int p = -1;
-    const bool is = b < a.to_rows && moves(b, p);
+    const int p = b < a.to_rows ? parent[b] : -1;
+    const bool known = p >= 0 && p < a.from_rows;
+    const int len = known ? blocks[p] : 0;
+    const bool fits = known && len >= 0 && len <= a.from_cap && len <= a.to_cap;
+    const bool is = fits && !(a.same && p == b);  // it moves
     if (b < a.to_rows && blockIdx.x == 0) {
-      const bool known = p >= 0 && p < a.from_rows;
-      const int len = known ? a.from_lengths[p] : 0;
-      const bool fits = known && len >= 0 && len <= a.from_cap && len <= a.to_cap;
       if (p != -1 && !fits) atomicOr(a.err, H2O_BERR_RANGE);
       a.new_lengths[b] = fits ? len : a.lengths[b];
     }
@@ -100,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
     for (int w = 0; w < warp; ++w) at += s_warp[w];
     if (is) {
       slot_of[p] = at, source[at] = p;
-      blocks[p] = (a.from_lengths[p] + kBlock - 1) / kBlock;
+      blocks[p] = (blocks[p] + kBlock - 1) / kBlock;
       atomicMax(&s_most, blocks[p]);
     }
     __syncthreads();
@@ -157,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
         }
         phase ^= 1;
         for (int m = lane; m < n_moves; m += 32) {
-          const int b = dest[m], p = a.parent[b], n = bytes_of(p);
+          const int b = dest[m], p = parent[b], n = bytes_of(p);
           if (n) bulk_store(to + b * to_row, smem + slot_of[p] * chunk, n);
         }
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -175,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
     }
     __syncthreads();
     for (int z = tid; z < n_moves * words; z += kThreads) {
-      const int b = dest[z / words], w = z % words, p = a.parent[b];
+      const int b = dest[z / words], w = z % words, p = parent[b];
       if (w * 4 < bytes_of(p)) *(float *)(to + b * to_row + w * 4) = ((const float *)smem)[slot_of[p] * words + w];
     }
     __syncthreads();
@@ -200,7 +194,7 @@ cudaError_t launch_copy(const View &to, const View &from, const int32_t *parent,
   a.H = to.H, a.to_rows = to.B, a.from_rows = from.B, a.from_cap = from.cap, a.to_cap = to.cap;
   a.same = to.K == from.K;
   a.arrays = to.bounds && from.bounds ? kBulk : kBulk - 1;
-  const int lists = (3 * from.B + to.B) * 4;
+  const int lists = (3 * from.B + 2 * to.B) * 4;
   // Four CTAs an SM.  Large caches: several waves of them and larger pieces (64 rows of 56 heads 309 -> 306 us, prompt forks
   // 194 -> 177; four beams of 255 entries would take 18 us for 9).  Room for fewer and larger pieces, 98 KB of two CTAs an
   // SM, 315 and 190; the next item's reads under this one's writes, with half the pieces' size, 312 and 192 at best.
