@@ -512,8 +512,11 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   grid_dependency_wait();
   // every CTA has begun before another one writes to its memory
   if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  Bounds<D> bd;
-  if (warp < steps) bd.load(bounds, ksc, warp * 16, n);
+  constexpr int kDeep = W > 4 ? 3 : 2;  // a warp's sixteens of blocks on their way at once
+  Bounds<D> bd[kDeep];
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i)
+    if (warp + i * W < steps) bd[i].load(bounds, ksc, (warp + i * W) * 16, n);
   Codes<D> qc;
   float qf[D / 64][16];
   unsigned top = 0;
@@ -563,29 +566,33 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
       }
     }
     if (n > kHeldKeys) keys = (uint32_t *)logits_of(a, bh, t, 0) + lo;  // read before any logit is written
-    for (int x = warp; x < steps; x += W) {
-      Bounds<D> now = bd;
-      if (x + W < steps) bd.load(bounds, ksc, (x + W) * 16, n);
-      float2 m;
-      if constexpr (NR == 1) {
-        m = block_sums<D>(now, qc);
-      } else {
-        m = make_float2(-INFINITY, -INFINITY);
-        for (int y = 0; y < ceil_div(group, 8); ++y) {
-          if (group <= kCodesMost) {
-            qc = codes[y * 32 + lane];
-          } else {  // made anew for each 16 blocks
-            query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), qf);
-            qc.set(qf, inv);
+    for (int x0 = warp; x0 < steps; x0 += W * kDeep) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int x = x0 + i * W;
+        if (x >= steps) break;
+        float2 m;
+        if constexpr (NR == 1) {
+          m = block_sums<D>(bd[i], qc);
+        } else {
+          m = make_float2(-INFINITY, -INFINITY);
+          for (int y = 0; y < ceil_div(group, 8); ++y) {
+            if (group <= kCodesMost) {
+              qc = codes[y * 32 + lane];
+            } else {  // made anew for each 16 blocks
+              query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), qf);
+              qc.set(qf, inv);
+            }
+            const float2 z = block_sums<D>(bd[i], qc);
+            m = make_float2(fmaxf(m.x, z.x), fmaxf(m.y, z.y));
           }
-          const float2 z = block_sums<D>(now, qc);
-          m = make_float2(fmaxf(m.x, z.x), fmaxf(m.y, z.y));
         }
+        // keys of a quad's two blocks are known to its four lanes
+        const int j = x * 16 + (t4 & 1) * 8 + g;
+        const uint32_t key = t4 & 1 ? key_bits(m.y, bd[i].ks[1]) : key_bits(m.x, bd[i].ks[0]);
+        if (t4 < 2 && j < n) keys[j] = key;
+        if (x + W * kDeep < steps) bd[i].load(bounds, ksc, (x + W * kDeep) * 16, n);
       }
-      // keys of a quad's two blocks are known to its four lanes
-      const int j = x * 16 + (t4 & 1) * 8 + g;
-      const uint32_t key = t4 & 1 ? key_bits(m.y, now.ks[1]) : key_bits(m.x, now.ks[0]);
-      if (t4 < 2 && j < n) keys[j] = key;
     }
     __syncthreads();
     if (P > 1) team_wait();
@@ -794,7 +801,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
         if (j < 0) break;
         const float *lg = logits + (tid / 8 + (y0 + y) * (kThreads / 8)) * kBlock + tid % 8 * 4;
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int r = 0; r < group; ++r) {
           const float4 x = *(const float4 *)(lg + r * row_step);
           const float e = row_base[r];

@@ -28,6 +28,7 @@ struct Args {
   const int32_t *position, *counts;
   int per_token;
   int chunks[2];  // warps that share a token's query heads, and its key heads
+  int both;       // or one warp has all of them
   int per;        // heads of a warp
 };
 
@@ -55,19 +56,19 @@ __device__ __forceinline__ void store8(float *p, const float *x) {
 }
 
 template <typename T, int D, int kAhead>
-__global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const Args a) {
+__global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
   constexpr int L = D / 16;       // lanes of a row
   constexpr int kAtOnce = 32 / L;  // heads
   constexpr int N = 8 / VecN<T>::N;
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int all = a.chunks[0] + a.chunks[1];
+  const int all = a.both ? 1 : a.chunks[0] + a.chunks[1];
   const int64_t token = item / all;
   int chunk = (int)(item - token * all);
   const int b = (int)(token / a.n), t = (int)(token - (int64_t)b * a.n);
   if (b >= a.B) return;
   if (a.counts && t >= a.counts[b]) return;
-  const int which = chunk >= a.chunks[0];
+  int which = chunk >= a.chunks[0];
   if (which) chunk -= a.chunks[0];
 
   // The lane's two runs of 8 elements: c0 and c1.  Pair e of them: elements e
@@ -97,56 +98,60 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(const Args a) {
       sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[e], &cs[e]);
     }
   }
-  const float *weight = which ? r.k_weight : r.q_weight;
+  for (;;) {
+    const float *weight = which ? r.k_weight : r.q_weight;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = r.norm && weight ? weight[(e < 8 ? c0 : c1) * 8 + (e & 7)] : 1.f;
+    for (int e = 0; e < 16; ++e) w[e] = r.norm && weight ? weight[(e < 8 ? c0 : c1) * 8 + (e & 7)] : 1.f;
 
-  const T *in = (const T *)a.in[which] + b * a.sin[which][0] + t * a.sin[which][2];
-  T *out = (T *)a.out[which] + b * a.sout[which][0] + t * a.sout[which][2];
-  const int end = min(a.heads[which], (chunk + 1) * a.per);
-  // kAhead rows of a lane are on their way at once.
-  for (int h0 = chunk * a.per + lane / L; h0 - lane / L < end; h0 += kAtOnce * kAhead) {
-    uint4 u[kAhead][2][N];
+    const T *in = (const T *)a.in[which] + b * a.sin[which][0] + t * a.sin[which][2];
+    T *out = (T *)a.out[which] + b * a.sout[which][0] + t * a.sout[which][2];
+    const int end = min(a.heads[which], (chunk + 1) * a.per);
+    // kAhead rows of a lane are on their way at once.
+    for (int h0 = chunk * a.per + lane / L; h0 - lane / L < end; h0 += kAtOnce * kAhead) {
+      uint4 u[kAhead][2][N];
 #pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const int h = h0 + y * kAtOnce;
-      const T *src = in + (int64_t)(h < end ? h : 0) * a.sin[which][1];  // behind the last one head 0 again
-      load8(src + c0 * 8, u[y][0]), load8(src + c1 * 8, u[y][1]);
-    }
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const int h = h0 + y * kAtOnce;
-      float x[16];
-      unpack8<T>(u[y][0], x), unpack8<T>(u[y][1], x + 8);
-      if (r.norm) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float f = rsqrtf(s * (1.f / D) + r.eps);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= f * w[e];
+      for (int y = 0; y < kAhead; ++y) {
+        const int h = h0 + y * kAtOnce;
+        const T *src = in + (int64_t)(h < end ? h : 0) * a.sin[which][1];  // behind the last one head 0 again
+        load8(src + c0 * 8, u[y][0]), load8(src + c1 * 8, u[y][1]);
       }
-      if (turns) {
-        auto turn = [&](int e, float &p, float &q) {
-          const float p0 = p;
-          p = p0 * cs[e] - q * sn[e];
-          q = q * cs[e] + p0 * sn[e];
-        };
-        if (r.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) turn(e, x[2 * e], x[2 * e + 1]);
-        } else {
+      for (int y = 0; y < kAhead; ++y) {
+        const int h = h0 + y * kAtOnce;
+        float x[16];
+        unpack8<T>(u[y][0], x), unpack8<T>(u[y][1], x + 8);
+        if (r.norm) {
+          float s = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) turn(e, x[e], x[e + 8]);
+          for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
+#pragma unroll
+          for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const float f = rsqrtf(s * (1.f / D) + r.eps);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] *= f * w[e];
         }
+        if (turns) {
+          auto turn = [&](int e, float &p, float &q) {
+            const float p0 = p;
+            p = p0 * cs[e] - q * sn[e];
+            q = q * cs[e] + p0 * sn[e];
+          };
+          if (r.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn(e, x[2 * e], x[2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn(e, x[e], x[e + 8]);
+          }
+        }
+        if (h >= end) continue;
+        T *dst = out + (int64_t)h * a.sout[which][1];
+        store8(dst + c0 * 8, x);
+        store8(dst + c1 * 8, x + 8);
       }
-      if (h >= end) continue;
-      T *dst = out + (int64_t)h * a.sout[which][1];
-      store8(dst + c0 * 8, x);
-      store8(dst + c1 * 8, x + 8);
     }
+    if (!a.both || which) break;
+    which = 1;
   }
 }
 
@@ -159,7 +164,9 @@ template <typename T, int D> cudaError_t rotate_t(Args &a, int sms, cudaStream_t
   if (share < 1) share = 1;
   a.per = (int)(((most + share - 1) / share + kAtOnce - 1) / kAtOnce) * kAtOnce;
   for (int i = 0; i < 2; ++i) a.chunks[i] = (a.heads[i] + a.per - 1) / a.per;
-  const int64_t ctas = (tokens * (a.chunks[0] + a.chunks[1]) + kWarps - 1) / kWarps;
+  // Many tokens: queries and keys by one warp, under the same sines.
+  a.both = share == 1 && a.heads[0] > 0 && a.heads[1] > 0;
+  const int64_t ctas = (tokens * (a.both ? 1 : a.chunks[0] + a.chunks[1]) + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // 64 bytes a lane on their way where a warp has rows enough (8K prompts 803 -> 708 us), else less code (one token 3.1 -> 2.3)
   if (a.per > kAtOnce)
