@@ -8,8 +8,14 @@
 // when all are there; no two CTAs share bytes.  So each row that is read is
 // read once, however many receive it, and nothing is copied twice.
 //
-// Copies in both directions are bulk ones, a few KB each; the scales, whose
-// rows may start at any multiple of 4 bytes, go through registers.
+// Copies in both directions are bulk ones, a few KB each, by one warp of a CTA;
+// the scales, whose rows may start at any multiple of 4 bytes, go through the
+// registers of the others meanwhile.
+//
+// Bound by memory: beams of 64 rows of 56 heads, 700 to 2,047 entries, 1,771
+// MB, 283 us, 92 % of the copy rate; two prompts of 8,000 tokens forked into 13
+// rows, 1,065 MB, 175 us, 90 %.  Four beams of 255 entries by latency: 7 us, the
+// maps' way through shared memory, one piece a CTA in and out.
 #include "block_cache.cuh"
 #include "sm100.cuh"
 
@@ -35,6 +41,7 @@ struct Args {
   int arrays;  // kBulk, or one less without bounds
   int chunk;   // bytes of a row that a CTA takes at a time, at most: a power of two
   int room;    // bytes for the rows' pieces
+  int words;   // and words for those of scales: a power of two
 };
 
 __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
@@ -42,19 +49,19 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
                : "memory");
 }
 
-// Shared memory: the pieces; slot_of [from_rows] (a read row's place among the
+// Shared memory: the bulk copies' pieces; slot_of [from_rows] (a read row's place among the
 // pieces, -1); blocks [from_rows] (their lengths first); the read rows and the
-// rows that receive something, in order; parent [to_rows].
+// rows that receive something, in order; parent [to_rows]; the scales' pieces.
 __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   int *slot_of = (int *)(smem + a.room), *blocks = slot_of + a.from_rows;
   int *source = blocks + a.from_rows;  // of a piece
   int *dest = source + a.from_rows, *parent = dest + a.to_rows;
   __shared__ __align__(8) uint64_t bar;
-  __shared__ int s_sources, s_moves, s_most, s_warp[kThreads / 32], s_lost;
+  __shared__ int s_sources, s_moves, s_most, s_warp[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    s_sources = s_moves = s_most = s_lost = 0;
+    s_sources = s_moves = s_most = 0;
     mbar_init(&bar, 1);
     fence_mbar_init();
   }
@@ -105,76 +112,91 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const Args a) {
   if (n_moves == 0 || most == 0) return;
   int chunk = a.chunk;
   while (chunk > 16 && (int64_t)chunk * sources > a.room) chunk >>= 1;
+  int words = a.words;  // of a row's scales
+  while (words > 1 && words * sources > a.words) words >>= 1;
 
-  // Items: (head, array, chunk), then the scales.
-  int64_t items_of[kArrays], items = 0;
+  // Items: (array, head, chunk); warp 0 has the bulk copies, the others the scales.
+  int64_t items_of[kArrays];
 #pragma unroll
   for (int x = 0; x < kArrays; ++x) {
     const bool none = x == kBulk - 1 && a.arrays < kBulk;
-    items_of[x] = none ? 0 : ((int64_t)most * a.per_block[x] + chunk - 1) / chunk * a.H;
-    items += items_of[x];
+    const int piece = x < kBulk ? chunk : words * 4;
+    items_of[x] = none ? 0 : ((int64_t)most * a.per_block[x] + piece - 1) / piece * a.H;
   }
-  uint32_t phase = 0;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    int x = 0;
-    int64_t i = item;
-    while (i >= items_of[x]) i -= items_of[x++];
-    const int64_t pieces = items_of[x] / a.H;  // neighbours in a row to neighbouring CTAs
-    const int h = (int)(i / pieces);
-    const int64_t at = (i - h * pieces) * chunk;  // the chunk's first byte of a row's
-    auto bytes_of = [&](int p) {
-      const int64_t left = (int64_t)blocks[p] * a.per_block[x] - at;
-      return (int)(left < 0 ? 0 : left < chunk ? left : chunk);
-    };
-    const uint8_t *from = a.from[x] + h * a.from_head[x] + at;
-    uint8_t *to = a.to[x] + h * a.to_head[x] + at;
-    const int64_t from_row = a.from_head[x] * a.H, to_row = a.to_head[x] * a.H;
-    if (x < kBulk) {
-      if (warp == 0 && !s_lost) {
-        // the last item's pieces have left shared memory
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-        int total = 0;
-        for (int s = lane; s < sources; s += 32) total += bytes_of(source[s]);
-        total = __reduce_add_sync(0xffffffffu, total);
-        if (lane == 0) mbar_expect_tx(&bar, total);
-        __syncwarp();
-        for (int s = lane; s < sources; s += 32) {
-          const int n = bytes_of(source[s]);
-          if (n) bulk_load(smem + s * chunk, from + source[s] * from_row, n, &bar);
-        }
-        if (!mbar_wait(&bar, phase)) {  // a copy never arrived: report, wait once more, and move nothing else
-          if (lane == 0) atomicOr(a.err, H2O_BERR_INTERNAL), s_lost = 1;
-          mbar_wait(&bar, phase);
-          __syncwarp();
-          continue;
-        }
-        phase ^= 1;
-        for (int m = lane; m < n_moves; m += 32) {
-          const int b = dest[m], p = parent[b], n = bytes_of(p);
-          if (n) bulk_store(to + b * to_row, smem + slot_of[p] * chunk, n);
-        }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  struct Item {
+    int x, h;
+    int64_t at;  // the first byte of a row's
+  };
+  auto item_at = [&](int64_t i, int x, int piece) {  // the i-th from array x on
+    Item it;
+    it.x = x;
+    while (i >= items_of[it.x]) i -= items_of[it.x++];
+    const int64_t pieces = items_of[it.x] / a.H;  // neighbours in a row to neighbouring CTAs
+    it.h = (int)(i / pieces);
+    it.at = (i - it.h * pieces) * piece;
+    return it;
+  };
+  auto bytes_of = [&](const Item &it, int p, int piece) {
+    const int64_t left = (int64_t)blocks[p] * a.per_block[it.x] - it.at;
+    return (int)(left < 0 ? 0 : left < piece ? left : piece);
+  };
+  auto from_of = [&](const Item &it, int p) {
+    return a.from[it.x] + ((int64_t)p * a.H + it.h) * a.from_head[it.x] + it.at;
+  };
+  auto to_of = [&](const Item &it, int b) {
+    return a.to[it.x] + ((int64_t)b * a.H + it.h) * a.to_head[it.x] + it.at;
+  };
+  int64_t bulk = 0;
+#pragma unroll
+  for (int x = 0; x < kBulk; ++x) bulk += items_of[x];
+  if (warp == 0) {
+    uint32_t phase = 0;
+    for (int64_t item = blockIdx.x; item < bulk; item += gridDim.x) {
+      const Item it = item_at(item, 0, chunk);
+      int total = 0;
+      for (int s = lane; s < sources; s += 32) total += bytes_of(it, source[s], chunk);
+      total = __reduce_add_sync(0xffffffffu, total);
+      if (lane == 0) mbar_expect_tx(&bar, total);
+      // the last item's pieces have left shared memory
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+      for (int s = lane; s < sources; s += 32) {
+        const int n = bytes_of(it, source[s], chunk);
+        if (n) bulk_load(smem + s * chunk, from_of(it, source[s]), n, &bar);
       }
-      continue;
+      if (!mbar_wait(&bar, phase)) {  // a copy never arrived: report, wait once more, and move nothing else
+        if (lane == 0) atomicOr(a.err, H2O_BERR_INTERNAL);
+        mbar_wait(&bar, phase);
+        break;
+      }
+      phase ^= 1;
+      for (int m = lane; m < n_moves; m += 32) {
+        const int b = dest[m], p = parent[b], n = bytes_of(it, p, chunk);
+        if (n) bulk_store(to_of(it, b), smem + slot_of[p] * chunk, n);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    // scales: words of 4 bytes
-    if (warp == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncthreads();
-    if (s_lost) continue;
-    const int words = chunk / 4;
-    for (int z = tid; z < sources * words; z += kThreads) {
-      const int s = z / words, w = z % words;
-      if (w * 4 < bytes_of(source[s])) ((float *)smem)[z] = *(const float *)(from + source[s] * from_row + w * 4);
-    }
-    __syncthreads();
-    for (int z = tid; z < n_moves * words; z += kThreads) {
-      const int b = dest[z / words], w = z % words, p = parent[b];
-      if (w * 4 < bytes_of(p)) *(float *)(to + b * to_row + w * 4) = ((const float *)smem)[slot_of[p] * words + w];
-    }
-    __syncthreads();
+    __syncwarp();
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    return;
   }
-  if (warp == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  float *held = (float *)(parent + a.to_rows);  // [sources][words]
+  auto others = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory"); };
+  // from the last CTA down: those have the fewer bulk items
+  const int64_t scales = items_of[kBulk] + items_of[kBulk + 1];
+  for (int64_t item = gridDim.x - 1 - blockIdx.x; item < scales; item += gridDim.x) {
+    const Item it = item_at(item, kBulk, words * 4);
+    for (int z = tid - 32; z < sources * words; z += kThreads - 32) {
+      const int s = z / words, w = z % words;
+      if (w * 4 < bytes_of(it, source[s], words * 4)) held[z] = *(const float *)(from_of(it, source[s]) + w * 4);
+    }
+    others();
+    for (int z = tid - 32; z < n_moves * words; z += kThreads - 32) {
+      const int b = dest[z / words], w = z % words, p = parent[b];
+      if (w * 4 < bytes_of(it, p, words * 4)) *(float *)(to_of(it, b) + w * 4) = held[slot_of[p] * words + w];
+    }
+    others();
+  }
 }
 
 }  // namespace
@@ -194,10 +216,13 @@ cudaError_t launch_copy(const View &to, const View &from, const int32_t *parent,
   a.H = to.H, a.to_rows = to.B, a.from_rows = from.B, a.from_cap = from.cap, a.to_cap = to.cap;
   a.same = to.K == from.K;
   a.arrays = to.bounds && from.bounds ? kBulk : kBulk - 1;
-  const int lists = (3 * from.B + 2 * to.B) * 4;
+  a.words = 1024;
+  while (a.words < from.B) a.words *= 2;
+  const int lists = (3 * from.B + 2 * to.B + a.words) * 4;
   // Four CTAs an SM.  Large caches: several waves of them and larger pieces (64 rows of 56 heads 309 -> 306 us, prompt forks
-  // 194 -> 177; four beams of 255 entries would take 18 us for 9).  Room for fewer and larger pieces, 98 KB of two CTAs an
-  // SM, 315 and 190; the next item's reads under this one's writes, with half the pieces' size, 312 and 192 at best.
+  // 194 -> 177 when it was measured; four beams of 255 entries would take 18 us for 9).  Fewer and larger pieces, 98 KB
+  // for two CTAs an SM, took 315 and 190; the next item's reads under this one's writes, in pieces of half the size, 312
+  // and 192 at best.
   const bool large = 2 * (int64_t)to.B * to.H * to.cap * to.d >= 256 << 20;
   a.chunk = large ? 8192 : 4096;
   a.room = 16 * from.B > 49152 ? 16 * from.B : 49152;

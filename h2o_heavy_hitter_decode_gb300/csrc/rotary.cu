@@ -9,6 +9,12 @@
 // computed once and used for all the warp's heads.  Angles: position times the
 // 64-bit fraction of a turn wraps at whole turns by itself, and its upper 32
 // bits go through sincospif.
+//
+// Bound by memory: 16 prompts of 8,192 tokens, 32 query and 32 key heads of 128
+// (4.3 GB) 643 us, 98 % of the copy rate, with five CTAs an SM (four 690, six
+// 717 with spills); 6,771 patches of 16 and 16 heads of 64 in fp32 24 us, 68 %,
+// by the way from positions to sines to stores, four and a half waves of it.
+// One token by latency, 2.4 us.
 #include <cstdint>
 
 #include "common.cuh"
