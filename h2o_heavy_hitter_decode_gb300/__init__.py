@@ -17,6 +17,11 @@ queries, 8-bit codes with one scale per block of entries, eviction in bulk.
     cache.append(K, V, lengths, score=colsum)        # the prompt: [B,H,n,d]
     out = cache.step(q, k, v, lengths, position=position)  # q [B,H*G,1,d], k, v [B,H,1,d]
     lengths = cache.evict(lengths, k_heavy, k_local)       # position (int32 [B]) counts on
+    lengths = cache.copy(parent, lengths)                  # beams, forks: row b goes on as row parent[b] was
+
+With ``bounds=True`` a step can attend to a few chosen blocks of a long cache:
+
+    out = cache.step_sparse(q, k, v, lengths, n_blocks=64)
 
 ``H2ORotary`` norms and rotates queries and keys before they meet a cache.
 
