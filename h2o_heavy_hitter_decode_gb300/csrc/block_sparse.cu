@@ -516,19 +516,20 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   const float *ksc = c.Ksc + scales + a.n_first + lo;
   const bool new_row = a.fused && v.S - 1 >= slot0 && v.S - 1 < slot1;  // the last slot's block
 
-  grid_dependency_wait();
   // every CTA has begun before another one writes to its memory
+  __syncwarp();
   if (P > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  constexpr int kDeep = W > 4 ? 3 : 2;  // a warp's sixteens of blocks on their way at once
-  Bounds<D> bd[kDeep];
-#pragma unroll
-  for (int i = 0; i < kDeep; ++i)
-    if (warp + i * W < steps) bd[i].load(bounds, ksc, (warp + i * W) * 16, n);
   Codes<D> qc;
   float qf[D / 64][16];
   unsigned top = 0;
   // every warp for itself; columns behind the last row repeat it
   if (NR == 1 && steps > 0) top = query_row<D>(q.at(b, h * group + min(g, group - 1), 0), qf);
+  grid_dependency_wait();  // an append
+  constexpr int kDeep = W > 4 ? 3 : 2;  // a warp's sixteens of blocks on their way at once
+  Bounds<D> bd[kDeep];
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i)
+    if (warp + i * W < steps) bd[i].load(bounds, ksc, (warp + i * W) * 16, n);
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   uint32_t phases = 0;
   // Scores: 8 threads to an own block, four entries each; kAhead of a thread's are on their way at once.
   constexpr int kAhead = 4;
-  const bool weights = a.l.n == 1 && a.accumulate;
+  const bool alone = a.l.n == 1;  // no other token's weights meet these
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   float4 old[kAhead], less[kAhead];
   auto entry_of = [&](int y) {  // the first of the thread's y-th four, -1 behind the last
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
                                                  tl.o[n][j + 1][u] * inv * part, tl.o[n][j + 1][2 + u] * inv * part);
       }
     // the own entries' scores are on their way while the parts meet
-    if (row0 == 0 && weights) {
+    if (row0 == 0 && alone && a.accumulate) {
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) load_scores(y, y);
     }
@@ -768,10 +769,8 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
         const float base = weight_base(m, l);
         const int hq = h * group + row0 + r;
         row_base[row0 + r] = base;
-        if (rank == 0) {
-          if (a.lse) a.lse[((size_t)b * c.H * group + hq) * a.l.n + t] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
-          if (a.l.n > 1) c.part[(size_t)bh * c.max_rows + t * group + row0 + r] = base;
-        }
+        if (rank == 0 && a.lse)
+          a.lse[((size_t)b * c.H * group + hq) * a.l.n + t] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     __syncthreads();
@@ -796,9 +795,11 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   }
 
   // -------------------------------------------------------------- the scores
-  if (weights) {
+  // Several tokens: the weights go where the first row's logits were, for scores_kernel.
+  float *sums = logits_of(a, bh, t, 0) + slot0 * kBlock;
+  if (a.accumulate) {
     for (int y0 = 0; entry_of(y0) >= 0; y0 += kAhead) {
-      if (y0 > 0) {
+      if (y0 > 0 && alone) {
 #pragma unroll
         for (int y = 0; y < kAhead; ++y) load_scores(y0 + y, y);
       }
@@ -806,15 +807,18 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
       for (int y = 0; y < kAhead; ++y) {
         const int j = entry_of(y0 + y);
         if (j < 0) break;
-        const float *lg = logits + (tid / 8 + (y0 + y) * (kThreads / 8)) * kBlock + tid % 8 * 4;
+        const int x = (tid / 8 + (y0 + y) * (kThreads / 8)) * kBlock + tid % 8 * 4;
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int r = 0; r < group; ++r) {
-          const float4 x = *(const float4 *)(lg + r * row_step);
+          const float4 u = *(const float4 *)(logits + x + r * row_step);
           const float e = row_base[r];
-          w.x += ex2(x.x - e), w.y += ex2(x.y - e), w.z += ex2(x.z - e), w.w += ex2(x.w - e);
+          w.x += ex2(u.x - e), w.y += ex2(u.y - e), w.z += ex2(u.z - e), w.w += ex2(u.w - e);
         }
-        store_scores(score + j, low + j, v.end - j, old[y], less[y], w);
+        if (alone)
+          store_scores(score + j, low + j, v.end - j, old[y], less[y], w);
+        else
+          *(float4 *)(sums + x) = w;
       }
     }
   }
@@ -823,23 +827,21 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
 
 // The weights of several tokens' rows, added in the tokens' order: a CTA has
 // kSlice blocks of a head, four entries a thread, and finds each token's slots
-// of them first (a warp a token).
+// of them first (a warp a token); the rows' weights are summed already.
 constexpr int kSlice = 32, kScoreThreads = kSlice * 8;
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int slices) {
   extern __shared__ int slot_of[];  // [n][kSlice], -1: not chosen
   const View &c = a.c;
-  const int bh = blockIdx.x / slices, j0 = (blockIdx.x - bh * slices) * kSlice, b = bh / c.H, group = c.group;
+  const int bh = blockIdx.x / slices, j0 = (blockIdx.x - bh * slices) * kSlice, b = bh / c.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Seq s = seq_of(a.l, b);
   if (s.cnt == 0 || j0 * kBlock >= s.total) return;
-  __shared__ float base[H2O_BLOCK_MAX_ROWS];
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   const int mine = threadIdx.x / 8, j = (j0 + mine) * kBlock + threadIdx.x % 8 * 4;
   grid_dependency_wait();
   const bool in = j < s.total;
   float4 old = make_float4(0.f, 0.f, 0.f, 0.f), less = old;
   if (in) old = *(const float4 *)(score + j), less = *(const float4 *)(low + j);
-  for (int r = threadIdx.x; r < s.cnt * group; r += kScoreThreads) base[r] = c.part[(size_t)bh * c.max_rows + r];
   for (int t = warp; t < s.cnt; t += kScoreThreads / 32) {
     const Sight v = sight_of(a, s, t);
     const int32_t *list = list_of(a, bh, t);
@@ -857,16 +859,12 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int
   for (int t = 0; t < s.cnt; ++t) {
     const int slot = slot_of[t * kSlice + mine];
     if (slot < 0) continue;
-    const float *lg = logits_of(a, bh, t, 0) + slot * kBlock + threadIdx.x % 8 * 4;
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int r = 0; r < group; ++r) {
-      const float4 x = *(const float4 *)(lg + (size_t)r * c.cap);
-      const float e = base[t * group + r];
-      w.x += ex2(x.x - e), w.y += ex2(x.y - e), w.z += ex2(x.z - e), w.w += ex2(x.w - e);
-    }
-    old.x = add_score(old.x, less.x, w.x), old.y = add_score(old.y, less.y, w.y);
-    old.z = add_score(old.z, less.z, w.z), old.w = add_score(old.w, less.w, w.w);
+    const float4 w = *(const float4 *)(logits_of(a, bh, t, 0) + slot * kBlock + threadIdx.x % 8 * 4);
+    const int left = sight_of(a, s, t).end - j;  // entries that the token does not see keep their score
+    if (left > 0) old.x = add_score(old.x, less.x, w.x);
+    if (left > 1) old.y = add_score(old.y, less.y, w.y);
+    if (left > 2) old.z = add_score(old.z, less.z, w.z);
+    if (left > 3) old.w = add_score(old.w, less.w, w.w);
     any = true;
   }
   if (!any) return;
@@ -908,7 +906,7 @@ cudaError_t sparse_w(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
   const int own = (std::min(a.c.cap / kBlock, a.n_blocks) + a.P - 1) / a.P;
   a.own = (std::min(own, kOwnMost) + 3) & ~3;
   const int64_t logits = (int64_t)a.c.group * own * kBlock;
-  a.logits = a.accumulate && a.l.n == 1 && logits <= kLogitsMost ? (int)logits : 0;
+  a.logits = a.accumulate && logits <= kLogitsMost ? (int)logits : 0;
   const int smem = Room<D, NR, W>::bytes(a.c.group, a.own, a.logits);
   static SmemLimit limit;
   const auto kernel = sparse_kernel<F, D, NR, W>;
