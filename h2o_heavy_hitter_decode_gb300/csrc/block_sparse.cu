@@ -39,6 +39,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "block_tile.cuh"
 
@@ -878,27 +879,29 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int
   }
 }
 
-template <typename... X>
-cudaError_t launch_with(void (*kernel)(X...), unsigned ctas, int threads, int smem, int cluster, bool after,
-                        cudaStream_t st, X... args) {
+struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cudaLaunchAttribute at[2];
-  int n = 0;
-  if (cluster > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n++].val.clusterDim = {(unsigned)cluster, 1, 1};
+  Launch(unsigned ctas, int threads, int smem, int cluster, bool after, cudaStream_t st) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    if (cluster > 1) {
+      at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      at[cfg.numAttrs++].val.clusterDim = {(unsigned)cluster, 1, 1};
+    }
+    if (after) {
+      at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
   }
-  if (after) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+};
+
+template <typename F, int D, int NR, int W> SmemLimit &limit_of() {  // one for all launches of a kernel
+  static SmemLimit limit;
+  return limit;
 }
 
 template <typename F, int D, int NR, int W>
@@ -908,12 +911,34 @@ cudaError_t sparse_w(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
   const int64_t logits = (int64_t)a.c.group * own * kBlock;
   a.logits = a.accumulate && logits <= kLogitsMost ? (int)logits : 0;
   const int smem = Room<D, NR, W>::bytes(a.c.group, a.own, a.logits);
-  static SmemLimit limit;
   const auto kernel = sparse_kernel<F, D, NR, W>;
-  const cudaError_t e = limit.raise((const void *)kernel, smem);
+  const cudaError_t e = limit_of<F, D, NR, W>().raise((const void *)kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * a.P;
-  return launch_with(kernel, (unsigned)ctas, W * 32, smem, a.P, a.l.appends && !a.fused, st, a, kmap, vmap);
+  const Launch l((unsigned)ctas, W * 32, smem, a.P, a.l.appends && !a.fused, st);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a, kmap, vmap);
+}
+
+// Clusters of P CTAs of 8 warps, one an SM, that run at once: a cluster has to
+// find its SMs in one GPC (16 of 8 CTAs do not all, on 152 SMs: 35 us, 16 of 6:
+// 21).  Asked once for each device.
+template <typename F, int D, int NR> int clusters_at_once(int P) {
+  static std::atomic<int> known[SmemLimit::kDevices][kMostCtas + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= SmemLimit::kDevices) return 0;
+  int n = known[dev][P].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const auto kernel = sparse_kernel<F, D, NR, 8>;
+    const int smem = Room<D, NR, 8>::bytes(8 * NR, kOwnMost, kLogitsMost);
+    const Launch l(P, 8 * 32, smem, P, false, nullptr);
+    if (limit_of<F, D, NR, 8>().raise((const void *)kernel, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
+      cudaGetLastError();  // no answer: no cluster
+      return 0;
+    }
+    known[dev][P].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // CTAs of 8 warps, one an SM, while they all fit at once, as many to a token as
@@ -932,7 +957,7 @@ cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, 
   a.P = 1;
   if (items <= sms) {
     for (int p : {2, 3, 4, 6, 8})
-      if (items * p <= sms && blocks >= 8 * p) a.P = p;
+      if (items * p <= sms && blocks >= 8 * p && items <= clusters_at_once<F, D, NR>(p)) a.P = p;
     return sparse_w<F, D, NR, 8>(a, kmap, vmap, st);
   }
   if (2 * items <= 3 * sms && blocks >= 16) a.P = 2;
@@ -946,7 +971,8 @@ cudaError_t sparse_d(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, 
   if (e != cudaSuccess || !a.accumulate || a.l.n == 1) return e;
   const int64_t heads = (int64_t)a.c.B * a.c.H;
   const int slices = (a.c.cap / kBlock + kSlice - 1) / kSlice;
-  return launch_with(scores_kernel, (unsigned)(heads * slices), kScoreThreads, a.l.n * kSlice * 4, 1, true, st, a, slices);
+  const Launch s((unsigned)(heads * slices), kScoreThreads, a.l.n * kSlice * 4, 1, true, st);
+  return cudaLaunchKernelEx(&s.cfg, scores_kernel, a, slices);
 }
 
 }  // namespace
