@@ -35,7 +35,7 @@
 // the choice, 2 for copy and products, 3 to join the parts, 1 for the scores);
 // larger ones by memory in two of them, the keys' (4 to 5 TB/s) and the
 // blocks' (6 TB/s of 4 KB pieces): 128 heads of 20,000 to 65,500 entries, 128
-// blocks each, 183 MB, 55 us, where memory alone would take 27.
+// blocks each, 183 MB, 56 us, where memory alone would take 27.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -49,7 +49,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMostCtas = 8;      // of a cluster
+constexpr int kMostCtas = 16;     // of a cluster
 constexpr int kWarpKeys = 128, kAloneKeys = 512;
 constexpr int kHeldKeys = 4096;    // of a CTA, in shared memory
 constexpr int kOwnMost = 1024;    // chosen blocks of a CTA whose list stays in shared memory
@@ -912,7 +912,9 @@ cudaError_t sparse_w(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
   a.logits = a.accumulate && logits <= kLogitsMost ? (int)logits : 0;
   const int smem = Room<D, NR, W>::bytes(a.c.group, a.own, a.logits);
   const auto kernel = sparse_kernel<F, D, NR, W>;
-  const cudaError_t e = limit_of<F, D, NR, W>().raise((const void *)kernel, smem);
+  cudaError_t e = limit_of<F, D, NR, W>().raise((const void *)kernel, smem);
+  if (e == cudaSuccess && a.P > 8)
+    e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)a.c.B * a.c.H * a.l.n * a.P;
   const Launch l((unsigned)ctas, W * 32, smem, a.P, a.l.appends && !a.fused, st);
@@ -920,8 +922,9 @@ cudaError_t sparse_w(Args a, const CUtensorMap &kmap, const CUtensorMap &vmap, c
 }
 
 // Clusters of P CTAs of 8 warps, one an SM, that run at once: a cluster has to
-// find its SMs in one GPC (16 of 8 CTAs do not all, on 152 SMs: 35 us, 16 of 6:
-// 21).  Asked once for each device.
+// find its SMs in one GPC (16 heads of 100,000 entries: 35 us with 8 CTAs, for
+// which not all find them on 152 SMs, 21 with 6; 8 heads of 262,000: 23 with 8,
+// 21 with 12, 37 with 16).  Asked once for each device.
 template <typename F, int D, int NR> int clusters_at_once(int P) {
   static std::atomic<int> known[SmemLimit::kDevices][kMostCtas + 1] = {};
   int dev = 0;
@@ -931,6 +934,7 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
     const auto kernel = sparse_kernel<F, D, NR, 8>;
     const int smem = Room<D, NR, 8>::bytes(8 * NR, kOwnMost, kLogitsMost);
     const Launch l(P, 8 * 32, smem, P, false, nullptr);
+    if (P > 8) cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (limit_of<F, D, NR, 8>().raise((const void *)kernel, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
       cudaGetLastError();  // no answer: no cluster
@@ -945,9 +949,9 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
 // do; more tokens than SMs: CTAs of 4 warps, three an SM; more than those hold:
 // of 2 warps, six an SM, since the way from lengths to outputs is then hidden by
 // other tokens and not by more warps.  Measured, us a call (2 / 4 / 8 warps, the
-// best P of each): 8 heads of 8,000 entries 25 (P = 16, 15) / 13.8; 128 of
-// 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512 90 / 107 /
-// 104; 3,584 of 700 to 2,047 145 / 163 / 284.
+// best P of each): 8 heads of 8,000 entries 25 / 16 / 13; 128 of 3,000 to 8,400
+// 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512 of them 84 / 107 / 104;
+// 3,584 of 700 to 2,047 142 / 163 / 284.
 template <typename F, int D, int NR>
 cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   // counts leave tokens out: half of those behind the first, on the average
@@ -956,7 +960,7 @@ cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, 
   const int blocks = a.c.cap / kBlock, sms = a.c.sms;
   a.P = 1;
   if (items <= sms) {
-    for (int p : {2, 3, 4, 6, 8})
+    for (int p : {2, 3, 4, 6, 8, 10, 12, 14, 16})
       if (items * p <= sms && blocks >= 8 * p && items <= clusters_at_once<F, D, NR>(p)) a.P = p;
     return sparse_w<F, D, NR, 8>(a, kmap, vmap, st);
   }
