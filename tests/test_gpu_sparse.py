@@ -156,6 +156,9 @@ ATTEND = [  # B, H, G, n, d, kv, cap, lens, counts, causal, (n_blocks, n_first, 
     (1, 2, 8, 1, 64, "e4m3", 16384, [16001], None, True, (501, 0, 1)),          # all
     (1, 1, 2, 1, 64, "int8", 64, [64], None, True, (1000, 400, 500)),           # more than there are
     (3, 1, 1, 5, 64, "e4m3", 96, [2, 5, 40], None, True, (1, 0, 1)),            # fewer entries than queries
+    (70, 8, 2, 1, 128, "int8", 160, [(53 * b) % 161 for b in range(70)], None, True, (3, 1, 1)),   # more heads than CTAs fit at once
+    (60, 4, 3, 3, 64, "e4m3", 128, [(29 * b) % 129 for b in range(60)], [b % 4 for b in range(60)], True, (2, 0, 1)),
+    (40, 4, 10, 1, 64, "int8", 128, [(31 * b) % 129 for b in range(40)], None, False, (2, 0, 1)),  # 10 rows a token
 ]
 
 
@@ -540,3 +543,53 @@ def test_forms_of_many_candidates(B, H, n, cap, len_):
     seen = sum(a - n + t + 1 > 0 for a in lens for t in range(n)) * H * 3
     assert abs(float(c.score.double().sum()) - seen) <= seen * (e_w + 2.0 ** -20)
     assert c.error_bits() == (1 if min(lens) < 0 else 0)
+
+
+def test_offsets_past_32_bits():
+    """A second sequence whose codes lie behind 2^31 bytes of the first's: attention to its end, and a copy of it."""
+    cap = 1 << 24
+    g = torch.Generator(DEV).manual_seed(17)
+    c = H2OBlockCache(2, 1, 128, cap, group=2, kv="int8", bounds=True)
+    c.K.random_(-30, 31, generator=g)
+    c.V.random_(-127, 128, generator=g)
+    c.K_scale.fill_(2.0 ** -5)
+    c.V_scale.fill_(2.0 ** -6)
+    lens = [1000, cap - 7]
+    c.K_scale[1, 0, -5000:] = 2.0 ** -4  # the choice lies behind
+    q, k = rows(g, 2, 2, 1, 128), rows(g, 2, 1, 1, 128)
+    c.bound(ints(lens))
+    blocks, lse = torch.zeros(2, 1, 1, 70, dtype=torch.int32, device=DEV), torch.zeros(2, 2, 1, device=DEV)
+    out = c.step_sparse(q, k, k, ints(lens), 70, 2, 3, lse=lse, blocks=blocks)
+    K = c.K[1, 0].view(-1, 32, 128)
+    x = q[1, :, 0].double()
+    x = torch.round(x / 2.0 ** math.ceil(math.log2(float(x.abs().max()) / 127)))
+    m = torch.zeros(cap // 32, dtype=torch.float64, device=DEV)
+    for a in range(0, cap // 32, 1 << 16):
+        lo, hi = K[a : a + (1 << 16)].amin(1).double(), K[a : a + (1 << 16)].amax(1).double()
+        m[a : a + (1 << 16)] = (x.clamp(min=0) @ hi.T + x.clamp(max=0) @ lo.T).amax(0)
+    m *= c.K_scale[1, 0].double()
+    nb = cap // 32
+    best = (-m[2 : nb - 3]).sort(stable=True).indices[:65] + 2
+    ends = torch.tensor([0, 1, nb - 3, nb - 2, nb - 1], device=DEV)
+    mine = torch.cat([best, ends]).sort().values
+    assert torch.equal(blocks[1, 0, 0].long(), mine) and int(mine[2]) >= nb - 5000
+    at = (mine[:, None] * 32 + torch.arange(32, device=DEV)).flatten()
+    at = at[at < lens[1] + 1]
+    key = c.K[1, 0, at].double() * c.K_scale[1, 0, at // 32, None].double()
+    v = c.V[1, 0, at].double() * c.V_scale[1, 0, at // 32, None].double()
+    s = q[1, :, 0].double() @ key.T / math.sqrt(128)
+    w = torch.softmax(s, -1)
+    size = float((q[1, :, 0].double().abs() @ key.abs().T).max()) / math.sqrt(128)
+    e_s = 2.0 ** -23 * (128 * size + 4 * float(s.abs().max()))
+    e_w = 2 * e_s + 2.0 ** -21 * 98
+    want, mass = w @ v, w @ v.abs()
+    assert bool(((out[1, :, 0].double() - want).abs() <= 2.0 ** -8 * want.abs() + (e_w + 2.0 ** -11) * mass * (1 + 2.0 ** -7) + 1e-6).all())
+    L = torch.logsumexp(s, -1)
+    assert bool(((lse[1, :, 0].double() - L).abs() <= e_s + 2.0 ** -21 * (1 + L.abs())).all())
+    assert bool(((c.score[1, 0, at].double() - w.sum(0)).abs() <= 2 * e_w * w.sum(0) + 2.0 ** -23).all())
+    got = c.copy(ints([1, -1]), ints([1001, cap - 6]))
+    assert got.tolist() == [cap - 6, cap - 6]
+    for n in ("K", "V", "K_scale", "V_scale", "pos", "score", "bounds"):
+        x = getattr(c, n)
+        assert torch.equal(x[0], x[1]), n
+    assert c.error_bits() == 0
