@@ -167,9 +167,10 @@ __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float(
 constexpr int kFewRows = 8;  // rows of a sequence that are appended one at a time
 
 // Rows lo .. hi-1 of head (b, h), all in one block, appended behind `len`
-// entries by one warp, a lane taking D/32 neighbours of a row.  The block's
-// earlier codes are read only where its scale grows.
-template <typename F, int D>
+// entries by one warp, a lane taking D/32 neighbours of a row; at most N rows,
+// all on their way together.  The block's earlier codes are read only where its
+// scale grows.
+template <typename F, int D, int N = kFewRows>
 __device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows &x, int b, int h, int len, int lo,
                                             int hi) {
   constexpr int E = D / 32;
@@ -186,19 +187,22 @@ __device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows
     }
   };
   const float before = base < len ? *scale : 0.f;
-  uint32_t top = 0, odd = 0;
-  for (int t = lo; t < hi; ++t) {
-    uint32_t u[2];
-    row(t, u);
+  uint32_t u[N][2], top = 0, odd = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    u[i][0] = u[i][1] = 0u;
+    if (lo + i < hi) row(lo + i, u[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint32_t y = (u[e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+      const uint32_t y = (u[i][e >> 1] >> (16 * (e & 1))) & 0x7fffu;
       if (y < 0x7f80u)
         top = max(top, y);
       else
         odd = 1;
     }
-  }
   top = __reduce_max_sync(0xffffffffu, top);
   if (odd) atomicOr(c.err, H2O_BERR_NONFINITE);
   const float after = fmaxf(before, block_scale<F>(__uint_as_float(top << 16)));
@@ -210,16 +214,17 @@ __device__ __forceinline__ void append_rows(const View &c, bool is_v, const Rows
       store_codes<E>(p, 0, shift.run(E == 4 ? *(const uint32_t *)p : *(const uint16_t *)p));
     }
   }
-  for (int t = lo; t < hi; ++t) {
-    uint32_t u[2], out = 0;
-    row(t, u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (lo + i >= hi) break;
+    uint32_t out = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      float y = (e & 1 ? bf16hi(u[e >> 1]) : bf16lo(u[e >> 1])) * inv;
+      float y = (e & 1 ? bf16hi(u[i][e >> 1]) : bf16lo(u[i][e >> 1])) * inv;
       y = y != y ? 0.f : fminf(fmaxf(y, -F::kMax), F::kMax);
       out |= F::code(y) << (8 * e);
     }
-    store_codes<E>(codes + (size_t)t * D, 0, out);
+    store_codes<E>(codes + (size_t)(lo + i) * D, 0, out);
   }
   if (lane == 0) *scale = after;
 }

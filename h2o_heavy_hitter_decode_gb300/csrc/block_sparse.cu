@@ -35,7 +35,7 @@
 // the choice, 2 for copy and products, 3 to join the parts, 1 for the scores);
 // larger ones by memory in two of them, the keys' (4 to 5 TB/s) and the
 // blocks' (6 TB/s of 4 KB pieces): 128 heads of 20,000 to 65,500 entries, 128
-// blocks each, 183 MB, 56 us, where memory alone would take 27.
+// blocks each, 183 MB, 57 us, where memory alone would take 27.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -149,6 +149,23 @@ template <int D> struct Bounds {
 template <int D> struct Codes {
   static constexpr int C = D / 64;
   uint32_t b[2][C][4][2];  // [lo, hi][chunk][word]
+  // In shared memory: 16 bytes of each lane beside those of the next one.
+  static constexpr int kFours = 4 * C;
+  __device__ __forceinline__ void put(uint4 *tile) const {
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) {
+      const uint32_t *w = &b[0][0][0][0] + 4 * i;
+      tile[i * 32 + (threadIdx.x & 31)] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void get(const uint4 *tile) {
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) {
+      uint32_t *w = &b[0][0][0][0] + 4 * i;
+      const uint4 u = tile[i * 32 + (threadIdx.x & 31)];
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    }
+  }
   // f: the lane's C chunks of 16 elements of row g.
   __device__ __forceinline__ void set(const float (&f)[C][16], float inv) {
 #pragma unroll
@@ -471,7 +488,7 @@ template <int N> __device__ __forceinline__ float2 weigh(const float2 *ml, int s
 }
 
 template <typename F, int D, int NR, int W>
-__global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
+__global__ void __launch_bounds__(W * 32, W < 8 ? (NR == 1 ? 12 : 8) / W : 1)
     sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using R = Room<D, NR, W>;
   constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kStages = R::kStages, kRows = R::kRows;
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   uint32_t *keys = (uint32_t *)smem;
   unsigned(*bins)[kBins] = (unsigned(*)[kBins])(keys + kHeldKeys);
   float *parts = (float *)(smem + R::kRing);                     // [P][float4s of this CTA's slice]
-  Codes<D> *codes = (Codes<D> *)(smem + R::kRing + R::kParts);  // [tile][lane], groups above 8
+  uint4 *codes = (uint4 *)(smem + R::kRing + R::kParts);         // [tile][kFours][lane], groups above 8
   int *own = (int *)((uint8_t *)codes + R::codes(group));
   float *held_logits = (float *)(own + a.own);
   __shared__ __align__(8) uint64_t full[W][kStages];
@@ -538,7 +555,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
   // The new row, while those loads are on their way; no other CTA touches its block.
   if (new_row && warp >= W - 2) {
     const bool is_v = warp == W - 2;
-    append_rows<F, D>(c, is_v, is_v ? a.v : a.k, b, h, s.len, s.len, s.len + 1);
+    append_rows<F, D, 1>(c, is_v, is_v ? a.v : a.k, b, h, s.len, s.len, s.len + 1);
     if (!is_v && lane == 0) {
       const size_t at = (size_t)bh * c.cap + s.len;
       c.pos[at] = a.position ? a.position[b] : s.len;
@@ -569,7 +586,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
         for (int x = warp; x < tiles; x += W) {
           query_row<D>(q.at(b, h * group + min(8 * x + g, group - 1), 0), qf);
           qc.set(qf, inv);
-          codes[x * 32 + lane] = qc;
+          qc.put(codes + x * Codes<D>::kFours * 32);
         }
         __syncthreads();
       }
@@ -587,7 +604,7 @@ __global__ void __launch_bounds__(W * 32, NR == 1 && W < 8 ? 12 / W : 1)
           m = make_float2(-INFINITY, -INFINITY);
           for (int y = 0; y < ceil_div(group, 8); ++y) {
             if (group <= kCodesMost) {
-              qc = codes[y * 32 + lane];
+              qc.get(codes + y * Codes<D>::kFours * 32);
             } else {  // made anew for each 16 blocks
               query_row<D>(q.at(b, h * group + min(8 * y + g, group - 1), 0), qf);
               qc.set(qf, inv);
@@ -946,8 +963,8 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
 }
 
 // CTAs of 8 warps, one an SM, while they all fit at once, as many to a token as
-// do; more tokens than SMs: CTAs of 4 warps, three an SM; more than those hold:
-// of 2 warps, six an SM, since the way from lengths to outputs is then hidden by
+// do; more tokens than SMs: CTAs of 4 warps, three an SM (two with 9 rows and
+// more); more than those hold: of 2 warps, twice as many an SM, since the way from lengths to outputs is then hidden by
 // other tokens and not by more warps.  Measured, us a call (2 / 4 / 8 warps, the
 // best P of each): 8 heads of 8,000 entries 25 / 16 / 13; 128 of 3,000 to 8,400
 // 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512 of them 84 / 107 / 104;
@@ -964,8 +981,9 @@ cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, 
       if (items * p <= sms && blocks >= 8 * p && items <= clusters_at_once<F, D, NR>(p)) a.P = p;
     return sparse_w<F, D, NR, 8>(a, kmap, vmap, st);
   }
-  if (2 * items <= 3 * sms && blocks >= 16) a.P = 2;
-  if (NR == 1 && items > 3 * sms) return sparse_w<F, D, 1, 2>(a, kmap, vmap, st);
+  constexpr int kFours = NR == 1 ? 3 : 2;  // CTAs of 4 warps on an SM
+  if (2 * items <= kFours * sms && blocks >= 16) a.P = 2;
+  if (items > kFours * sms) return sparse_w<F, D, NR, 2>(a, kmap, vmap, st);
   return sparse_w<F, D, NR, 4>(a, kmap, vmap, st);
 }
 

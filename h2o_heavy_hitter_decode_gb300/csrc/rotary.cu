@@ -3,7 +3,8 @@
 //
 //   y = x / sqrt(mean x^2 + eps) * w;  (y_a, y_b) turned by position * frequency
 //
-// A warp takes some heads of one token: a row is held by d / 16 lanes, 16
+// A warp takes some heads of one token, or of several where a token has few: a
+// row is held by d / 16 lanes, 16
 // elements each, arranged so that both halves of a pair are one lane's.  The
 // sines and cosines of a lane's 8 pairs depend on the token alone: they are
 // computed once and used for all the warp's heads.  Angles: position times the
@@ -11,7 +12,7 @@
 // bits go through sincospif.
 //
 // Bound by memory: 16 prompts of 8,192 tokens, 32 query and 32 key heads of 128
-// (4.3 GB) 643 us, 98 % of the copy rate, with five CTAs an SM (four 690, six
+// (4.3 GB) 650 us, 97 % of the copy rate, with five CTAs an SM (four 690, six
 // 717 with spills); 6,771 patches of 16 and 16 heads of 64 in fp32 24 us, 68 %,
 // by the way from positions to sines to stores, four and a half waves of it.
 // One token by latency, 2.4 us.
@@ -35,6 +36,7 @@ struct Args {
   int per_token;
   int chunks[2];  // warps that share a token's query heads, and its key heads
   int both;       // or one warp has all of them
+  int heads_at_once;
   int per;        // heads of a warp
 };
 
@@ -61,7 +63,8 @@ __device__ __forceinline__ void store8(float *p, const float *x) {
   *(float4 *)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-template <typename T, int D, int kAhead>
+// Few: a token has fewer heads than a warp takes at a time.
+template <typename T, int D, int kAhead, bool Few>
 __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
   constexpr int L = D / 16;       // lanes of a row
   constexpr int kAtOnce = 32 / L;  // heads
@@ -69,11 +72,16 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int all = a.both ? 1 : a.chunks[0] + a.chunks[1];
-  const int64_t token = item / all;
-  int chunk = (int)(item - token * all);
-  const int b = (int)(token / a.n), t = (int)(token - (int64_t)b * a.n);
-  if (b >= a.B) return;
-  if (a.counts && t >= a.counts[b]) return;
+  // kAtOnce rows at a time: heads of a token, or where it has fewer, of several tokens.
+  const int slot = lane / L, heads_at_once = Few ? a.heads_at_once : kAtOnce;
+  int chunk = (int)(item % all);
+  const int64_t token = item / all * (kAtOnce / heads_at_once) + slot / heads_at_once;
+  bool is = token < (int64_t)a.B * a.n;
+  if (!Few && !is) return;
+  const int b = is ? (int)(token / a.n) : 0, t = is ? (int)(token - (int64_t)b * a.n) : 0;
+  if (is && a.counts && t >= a.counts[b]) is = false;
+  if (!__any_sync(0xffffffffu, is)) return;
+  if (!Few) is = true;  // all lanes or none
   int which = chunk >= a.chunks[0];
   if (which) chunk -= a.chunks[0];
 
@@ -81,9 +89,9 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
   // of both, or (interleaved) neighbours in the 16 elements that they make.
   const h2o_rotary &r = a.r;
   const int turning = r.pairs / 8;  // lanes of a row that turn
-  const bool turns = sub < turning;
+  const bool turns = sub < turning && is;
   int c0, c1;
-  if (r.interleaved || !turns)
+  if (r.interleaved || sub >= turning)
     c0 = 2 * sub, c1 = c0 + 1;
   else
     c0 = sub, c1 = sub + turning;
@@ -112,18 +120,19 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
     const T *in = (const T *)a.in[which] + b * a.sin[which][0] + t * a.sin[which][2];
     T *out = (T *)a.out[which] + b * a.sout[which][0] + t * a.sout[which][2];
     const int end = min(a.heads[which], (chunk + 1) * a.per);
-    // kAhead rows of a lane are on their way at once.
-    for (int h0 = chunk * a.per + lane / L; h0 - lane / L < end; h0 += kAtOnce * kAhead) {
+    // kAhead rows of a lane are on their way at once
+    for (int first = chunk * a.per; first < end; first += heads_at_once * kAhead) {
+      const int h0 = first + slot % heads_at_once;
       uint4 u[kAhead][2][N];
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) {
-        const int h = h0 + y * kAtOnce;
+        const int h = h0 + y * heads_at_once;
         const T *src = in + (int64_t)(h < end ? h : 0) * a.sin[which][1];  // behind the last one head 0 again
-        load8(src + c0 * 8, u[y][0]), load8(src + c1 * 8, u[y][1]);
+        if (is) load8(src + c0 * 8, u[y][0]), load8(src + c1 * 8, u[y][1]);
       }
 #pragma unroll
       for (int y = 0; y < kAhead; ++y) {
-        const int h = h0 + y * kAtOnce;
+        const int h = h0 + y * heads_at_once;
         float x[16];
         unpack8<T>(u[y][0], x), unpack8<T>(u[y][1], x + 8);
         if (r.norm) {
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
             for (int e = 0; e < 8; ++e) turn(e, x[e], x[e + 8]);
           }
         }
-        if (h >= end) continue;
+        if (h >= end || !is) continue;
         T *dst = out + (int64_t)h * a.sout[which][1];
         store8(dst + c0 * 8, x);
         store8(dst + c1 * 8, x + 8);
@@ -164,21 +173,27 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
 template <typename T, int D> cudaError_t rotate_t(Args &a, int sms, cudaStream_t st) {
   constexpr int kAtOnce = 32 / (D / 16);
   const int64_t tokens = (int64_t)a.B * a.n;
-  // Few tokens: their heads go to several warps each.
   const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
+  a.heads_at_once = 1;
+  while (a.heads_at_once < kAtOnce && a.heads_at_once < most) a.heads_at_once *= 2;
+  // Few tokens: their heads go to several warps each.
   int64_t share = (int64_t)sms * 16 / tokens;
   if (share < 1) share = 1;
-  a.per = (int)(((most + share - 1) / share + kAtOnce - 1) / kAtOnce) * kAtOnce;
+  a.per = (int)(((most + share - 1) / share + a.heads_at_once - 1) / a.heads_at_once) * a.heads_at_once;
   for (int i = 0; i < 2; ++i) a.chunks[i] = (a.heads[i] + a.per - 1) / a.per;
   // Many tokens: queries and keys by one warp, under the same sines.
   a.both = share == 1 && a.heads[0] > 0 && a.heads[1] > 0;
-  const int64_t ctas = (tokens * (a.both ? 1 : a.chunks[0] + a.chunks[1]) + kWarps - 1) / kWarps;
+  const int at_once = kAtOnce / a.heads_at_once;  // tokens of a warp
+  const int64_t ctas = ((tokens + at_once - 1) / at_once * (a.both ? 1 : a.chunks[0] + a.chunks[1]) + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // 64 bytes a lane on their way where a warp has rows enough (8K prompts 803 -> 708 us), else less code (one token 3.1 -> 2.3)
-  if (a.per > kAtOnce)
-    rotate_kernel<T, D, 4 * VecN<T>::N / 8><<<(unsigned)ctas, kWarps * 32, 0, st>>>(a);
+  const dim3 grid((unsigned)ctas);
+  if (a.heads_at_once < kAtOnce)
+    rotate_kernel<T, D, 1, true><<<grid, kWarps * 32, 0, st>>>(a);
+  else if (a.per > kAtOnce)
+    rotate_kernel<T, D, 4 * VecN<T>::N / 8, false><<<grid, kWarps * 32, 0, st>>>(a);
   else
-    rotate_kernel<T, D, 1><<<(unsigned)ctas, kWarps * 32, 0, st>>>(a);
+    rotate_kernel<T, D, 1, false><<<grid, kWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -80,6 +80,9 @@ CASES = [  # B, query heads, key heads, n, d, dims, dtype, axes, interleaved, no
     (2, 4, 4, 4, 128, 0, torch.bfloat16, 1, False, True, "dense", 9),
     (700, 6, 3, 1, 64, 64, torch.bfloat16, 1, False, False, "dense", 5000),
     (1, 3, 2, 2257, 128, 128, torch.bfloat16, 3, False, True, "tokens", 64),
+    (7, 2, 1, 33, 64, 64, torch.bfloat16, 1, False, True, "tokens", 999),      # fewer heads than a warp takes at a time
+    (3, 1, 1, 5, 128, 64, torch.float32, 2, True, False, "slice", 40),
+    (9, 2, 2, 1, 128, 128, torch.bfloat16, 1, True, True, "dense", 100000),
 ]
 
 
@@ -132,10 +135,11 @@ def test_far_positions_agree_with_near_ones():
     assert float((near - far).abs().max()) <= 2 * math.pi * 524287 * 1024 * 2.0 ** -53 * 8 + 2.0 ** -20
 
 
-def test_padded_batch():
+@pytest.mark.parametrize("hq,hk", [(3, 2), (1, 1), (2, 1), (9, 20)])
+def test_padded_batch(hq, hk):
     """Rows behind the counts are neither read nor written; counts out of range are the nearest that is not."""
     g = torch.Generator(DEV).manual_seed(8)
-    q, k = rows(g, 5, 3, 4, 128, torch.bfloat16, "tokens"), rows(g, 5, 2, 4, 128, torch.bfloat16)
+    q, k = rows(g, 5, hq, 4, 128, torch.bfloat16, "tokens"), rows(g, 5, hk, 4, 128, torch.bfloat16)
     r = H2ORotary(128, eps=0.0)
     counts, real = ints([0, 1, 4, -3, 9]), [0, 1, 4, 0, 4]
     position = ints([3, 0, 9, 1, 2])
