@@ -513,7 +513,10 @@ __global__ void __launch_bounds__(W * 32, W < 8 ? (NR == 1 ? 12 : 8) / W : 1)
   const int bh = (int)(item / a.l.n), t = (int)(item - (int64_t)bh * a.l.n), b = bh / c.H, h = bh - b * c.H;
   const Seq s = seq_of(a.l, b);
   if (!s.ok && h == 0 && t == 0 && rank == 0 && tid == 0) atomicOr(c.err, H2O_BERR_RANGE);
-  if (t >= s.cnt) return;  // the whole cluster
+  if (t >= s.cnt) {  // the whole cluster; what comes behind this launch counts on the one before it too
+    grid_dependency_wait();
+    return;
+  }
   if (a.l.n > 1) grid_launch_dependents();  // scores_kernel
   const Sight v = sight_of(a, s, t);
   const Rows q{a.q.p + t * a.q.st, a.q.sb, a.q.sh, a.q.st};  // the token's rows alone
@@ -853,7 +856,10 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const Args a, int
   const int bh = blockIdx.x / slices, j0 = (blockIdx.x - bh * slices) * kSlice, b = bh / c.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Seq s = seq_of(a.l, b);
-  if (s.cnt == 0 || j0 * kBlock >= s.total) return;
+  if (s.cnt == 0 || j0 * kBlock >= s.total) {
+    grid_dependency_wait();
+    return;
+  }
   float *score = c.score + (size_t)bh * c.cap, *low = c.low + (size_t)bh * c.cap;
   const int mine = threadIdx.x / 8, j = (j0 + mine) * kBlock + threadIdx.x % 8 * 4;
   grid_dependency_wait();
@@ -957,6 +963,7 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
       cudaGetLastError();  // no answer: no cluster
       return 0;
     }
+    if (n == 0) n = -1;  // an answer too
     known[dev][P].store(n, std::memory_order_relaxed);
   }
   return n;
@@ -964,11 +971,11 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
 
 // CTAs of 8 warps, one an SM, while they all fit at once, as many to a token as
 // do; more tokens than SMs: CTAs of 4 warps, three an SM (two with 9 rows and
-// more); more than those hold: of 2 warps, twice as many an SM, since the way from lengths to outputs is then hidden by
-// other tokens and not by more warps.  Measured, us a call (2 / 4 / 8 warps, the
-// best P of each): 8 heads of 8,000 entries 25 / 16 / 13; 128 of 3,000 to 8,400
-// 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512 of them 84 / 107 / 104;
-// 3,584 of 700 to 2,047 142 / 163 / 284.
+// more); more than those hold: of 2 warps, twice as many an SM, since the way
+// from lengths to outputs is then hidden by other tokens and not by more warps.
+// Measured, us a call (2 / 4 / 8 warps, the best P of each): 8 heads of 8,000
+// entries 25 / 16 / 13; 128 of 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000
+// 48 / 36 / 49; 512 of them 84 / 107 / 104; 3,584 of 700 to 2,047 142 / 163 / 284.
 template <typename F, int D, int NR>
 cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   // counts leave tokens out: half of those behind the first, on the average

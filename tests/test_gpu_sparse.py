@@ -593,3 +593,55 @@ def test_offsets_past_32_bits():
         x = getattr(c, n)
         assert torch.equal(x[0], x[1]), n
     assert c.error_bits() == 0
+
+
+def test_batches_of_nothing():
+    """No real row, no entry, every sequence refused: the calls behind find what the ones before left."""
+    c, r, g = filled(18, 3, 2, 64, 128, [100, 5, 64], 2, 3)
+    q, k = rows(g, 3, 4, 3, 64), rows(g, 3, 2, 3, 64)
+    before = [getattr(c, n).clone().view(torch.uint8) for n in ("K", "score", "bounds", "pos")]
+    out = torch.full((3, 4, 3, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    blocks = torch.full((3, 2, 3, 3), -7, dtype=torch.int32, device=DEV)
+    c.step_sparse(q, k, k, ints([100, 5, 64]), 3, counts=ints([0, 0, 0]), out=out, blocks=blocks)
+    c.attend_sparse(q, ints([100, 5, 64]), 3, counts=ints([0, 0, 0]), out=out, blocks=blocks)
+    assert c.error_bits() == 0
+    c.step_sparse(q, k, k, ints([-1, 129, 126]), 3, out=out, blocks=blocks)
+    assert c.error_bits() == 1
+    assert bool((out == 5).all()) and bool((blocks == -7).all())
+    for a, n in zip(before, ("K", "score", "bounds", "pos")):
+        assert torch.equal(a, getattr(c, n).view(torch.uint8))
+    lse = torch.zeros(3, 4, 3, device=DEV)
+    for causal in (True, False):  # nothing to see
+        out = c.attend_sparse(q, ints([0, 0, 0]), 3, causal=causal, lse=lse, blocks=blocks)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and bool((blocks == -1).all())
+    for a, n in zip(before, ("K", "score", "bounds", "pos")):
+        assert torch.equal(a, getattr(c, n).view(torch.uint8))
+    out = c.step_sparse(q, k, k, ints([100, 5, 64]), 3, 0, 1, lse=lse, blocks=blocks)
+    compare(c, r, out, lse, blocks, r.step_sparse(q, k, k, [100, 5, 64], 3, 0, 1), 3)
+
+
+def test_two_graphs_of_one_cache():
+    """A step of one token and one of three, captured apart and replayed in turn: they share the cache and its scratch."""
+    c, r, g = filled(19, 2, 2, 128, 1024, [600, 40], 3, 3)
+    lens = ints([600, 40])
+    made = []
+    for n in (1, 3):
+        q, k, v = rows(g, 2, 6, n, 128), rows(g, 2, 2, n, 128), rows(g, 2, 2, n, 128)
+        out, lse = torch.zeros_like(q), torch.zeros(2, 6, n, device=DEV)
+        blocks = torch.zeros(2, 2, n, 5, dtype=torch.int32, device=DEV)
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            c.step_sparse(q, k, v, lens, 5, out=out, lse=lse, blocks=blocks)
+        torch.cuda.current_stream().wait_stream(side)
+        r.step_sparse(q, k, v, lens.tolist(), 5, 1, 2)
+        with torch.cuda.graph(graph):
+            c.step_sparse(q, k, v, lens, 5, out=out, lse=lse, blocks=blocks)
+        made.append((n, q, k, v, out, lse, blocks, graph))
+    for i in range(4):
+        n, q, k, v, out, lse, blocks, graph = made[i % 2]
+        q.copy_(rows(g, 2, 6, n, 128)), k.copy_(rows(g, 2, 2, n, 128)), v.copy_(rows(g, 2, 2, n, 128))
+        graph.replay()
+        compare(c, r, out, lse, blocks, r.step_sparse(q, k, v, lens.tolist(), 5, 1, 2), 5)
+        lens += n
+    assert c.error_bits() == 0
