@@ -87,7 +87,7 @@ def test_in_place(name, B, of, kv, d, cap, bounds):
     assert c.error_bits() == 0
 
 
-@pytest.mark.parametrize("B,rows", [(1, 1), (4, 1), (9, 2), (2, 70), (130, 5)])
+@pytest.mark.parametrize("B,rows", [(1, 1), (4, 1), (9, 2), (2, 70), (130, 5), (3, 4096), (4096, 1), (300, 4000)])
 def test_from_another_cache(B, rows):
     """Other batch sizes, capacities, groups and numbers of queries."""
     to, source = noise(2, B, 2, 64, 256, "int8", group=4, max_queries=3), noise(3, rows, 2, 64, 96, "int8", max_queries=2)
