@@ -81,7 +81,8 @@ class H2ORotary:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        # torch.cuda.current_stream(device).cuda_stream and current_device() without their objects and checks
+        self._raw_stream, self._current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         turns = [round(Fraction(f) / TWO_PI * 2 ** 64) % 2 ** 64 for f in frequency]
         turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]  # the same bits in an int64
 
@@ -184,7 +185,7 @@ class H2ORotary:
                     t.record_stream(torch.cuda.current_stream(self.device))
                 self._known.add(stream)
             args = (self._desc_at, TYPES[dtype], B, n, hq, hk, qi, ki, where, per_token, cnt, qo, ko, stream)
-            if torch.cuda.current_device() == self._index:
+            if self._current_device() == self._index:
                 rc = self._lib.h2o_rotate(*args)
             else:
                 with torch.cuda.device(self._index):

@@ -33,7 +33,7 @@ class Library:
         return 0
 
 
-def rotary_on_the_host(monkeypatch):
+def rotary_on_the_host():
     """A rotary object without a device: its tensors are CPU tensors (device index -1)."""
     lib, here = Library(), threading.local()
     r = H2ORotary.__new__(H2ORotary)
@@ -41,12 +41,12 @@ def rotary_on_the_host(monkeypatch):
     r._raw_stream, r._known, r._tables = (lambda index: here.stream), {1, 2}, []
     r._lock, r._slots, r._desc_at = threading.Lock(), (C.c_int64 * 16)(), 256
     r._slots_at = C.addressof(r._slots)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    r._current_device = lambda: -1
     return r, lib, here
 
 
-def test_two_threads_pass_their_own_rows_and_streams(monkeypatch):
-    r, lib, here = rotary_on_the_host(monkeypatch)
+def test_two_threads_pass_their_own_rows_and_streams():
+    r, lib, here = rotary_on_the_host()
     want, errors = [], []
 
     def work(stream):
@@ -77,7 +77,7 @@ class Memory:
 
 
 def test_tables_know_their_streams(monkeypatch):
-    r, lib, here = rotary_on_the_host(monkeypatch)
+    r, lib, here = rotary_on_the_host()
     lib.inside.abort()
     r._known, r._tables = {1}, [Memory(), Memory()]
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here.stream)
