@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, MT>::kWarps * 32, Cfg<D, NR, MT>::k
 
   const int row0 = (blockIdx.y * MT + tile) * (8 * NR);  // the warp's rows of the head
   const int nsc = c.cap / kBlock;
-  Tile<F, D, NR, G::kQSmem> tl;
+  Tile<F, D, NR, G::kQSmem, false> tl;
   int first_blk = 0;
   bool open = false, busy = true, lost = false;
   float ks, vs;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? 3 : 1)
   };
   for (int i = 0; i < S; ++i) fetch(i);
 
-  Tile<F, D, 1, false> tl;
+  Tile<F, D, 1, false, false> tl;
   tl.begin(a.q, c.group, a.causal, s, b, h, 0, nullptr);
   const size_t scales = (size_t)bh * (c.cap / kBlock);
   bool lost = false;

@@ -25,6 +25,10 @@
 // Attention: each warp takes every W-th slot of its CTA through its own ring of
 // TMA loads; the warps' and then the CTAs' parts meet in shared memory, each CTA
 // joining a slice of the output that the others have handed to it.
+// Weights meet V whole, as two f16 numbers each (Tile): products are not what
+// bounds this kernel, and 11 bits showed in one output of fifty (a step of bf16,
+// 8e-4 of the outputs' norm against 32-bit weights; now 1e-4 and less).  Second
+// products cost 2 to 7 % (one sequence 10.7 -> 10.9 us, long batch 56.9 -> 60.8).
 // With one token a sequence the new row is appended, and the weights are added
 // to the scores, in the same launch (each CTA those of its own blocks); several
 // tokens may choose the same block, so theirs are added by scores_kernel, in
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(W * 32, W < 8 ? (NR == 1 ? 12 : 8) / W : 1)
     };
     for (int i = 0; i < kStages; ++i) fetch(i);
     scales_of(slot0 + warp);
-    Tile<F, D, NR, false> tl;
+    Tile<F, D, NR, false, true> tl;
     tl.begin(q, group, 0, one, b, h, row0, nullptr);
     for (int i = 0; slot0 + warp + i * W < slot1; ++i) {
       const int slot = slot0 + warp + i * W, blk = block_of(slot);

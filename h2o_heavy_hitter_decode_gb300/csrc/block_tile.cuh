@@ -167,8 +167,10 @@ __device__ __forceinline__ float weight_base(float m, float l) {
 }
 
 // What a warp holds of a head while it attends: Q, and for its NR tiles of 8
-// rows the output, the reference and the sum of the weights so far.
-template <typename F, int D, int NR, bool QSmem> struct Tile {
+// rows the output, the reference and the sum of the weights so far.  Whole: a
+// weight meets V as two f16 numbers, its rounding and what that loses, so with
+// 22 bits, where one of them has 11.
+template <typename F, int D, int NR, bool QSmem, bool Whole> struct Tile {
   using T = ToF16<F>;
   static constexpr int KS = D / 16;  // k steps of S, words of a lane's share of a K entry
   static constexpr int OT = D / 16;  // 16-row tiles of O^T
@@ -286,6 +288,7 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
     const int j0 = blk * kBlock + g;
     const bool edge = blk * kBlock + kBlock > min_end;
     uint32_t p[NR][4];  // P^T as B: entries 8 e + 2 t and + 1 of row g
+    uint32_t rest16[Whole ? NR : 1][4];  // what its rounding to 16 bits loses
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       // finite: an infinite factor (a huge query on a huge scale) would turn the products that are 0 into NaN
@@ -342,10 +345,17 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
         lsum[n][0] += e0 + e2;
         lsum[n][1] += e1 + e3;
         // 16 bits for the product with V: f16's 2^-11 of each weight, so 2^-11 of sum w |v|: an eighth of the output's own
-        // rounding where the values do not cancel
+        // rounding where the values do not cancel.  In two parts 2^-22, and 2^-25 below f16's normal numbers, 2^-32 of
+        // the largest weight.
         const __half2 a0 = __floats2half2_rn(e0, e1), a1 = __floats2half2_rn(e2, e3);
         p[n][2 * x] = transpose8(*(const uint32_t *)&a0);
         p[n][2 * x + 1] = transpose8(*(const uint32_t *)&a1);
+        if constexpr (Whole) {
+          const float2 h0 = __half22float2(a0), h1 = __half22float2(a1);
+          const __half2 z0 = __floats2half2_rn(e0 - h0.x, e1 - h0.y), z1 = __floats2half2_rn(e2 - h1.x, e3 - h1.y);
+          rest16[n][2 * x] = transpose8(*(const uint32_t *)&z0);
+          rest16[n][2 * x + 1] = transpose8(*(const uint32_t *)&z1);
+        }
       }
     }
     if (rest < kBlock) {  // codes behind the last entry may be anything, also NaN: weight 0 needs a finite code
@@ -396,7 +406,13 @@ template <typename F, int D, int NR, bool QSmem> struct Tile {
           for (int y = 0; y < 2; ++y) {
             const int j = (part * VW + w) * 2 + y;
             float acc[4];
-            mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
+            if constexpr (Whole) {
+              mma16816_new(acc, va[y][0], rest16[n][0], rest16[n][1]);
+              mma16816(acc, va[y][1], rest16[n][2], rest16[n][3]);
+              mma16816(acc, va[y][0], p[n][0], p[n][1]);
+            } else {
+              mma16816_new(acc, va[y][0], p[n][0], p[n][1]);
+            }
             mma16816(acc, va[y][1], p[n][2], p[n][3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][j][e] = fmaf(acc[e], vs, o[n][j][e]);

@@ -442,7 +442,8 @@ h2o_status h2o_bcache_bound(h2o_bcache_t cache, const int32_t *lengths);
  * n_first >= 0, n_last >= 1, n_first + n_last <= n_blocks <= H2O_SPARSE_MAX_BLOCKS.  Keys are exact, so
  * the choice is the same everywhere.  Outputs, lse and the weights added to
  * scores are those of attention over the chosen blocks' entries alone (a NaN
- * query makes scores of its chosen entries NaN).  blocks: device int32 [B][H][n][n_blocks],
+ * query makes scores of its chosen entries NaN), the weights taken whole: with 22
+ * bits, 2^-22 of sum w |v|.  blocks: device int32 [B][H][n][n_blocks],
  * receives each token's blocks in ascending order, -1 behind them; must not
  * overlap any argument.  H2O_ESTATE without bounds. */
 #define H2O_SPARSE_MAX_BLOCKS (1 << 26)
