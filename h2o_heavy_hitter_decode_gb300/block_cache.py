@@ -253,6 +253,8 @@ class H2OBlockCache:
         See h2o_bcache_attend_sparse."""
         n = self._tokens(q, "q")
         shape, choice = self._shape(self._heads, n), self._choice(n_blocks, n_first, n_last)
+        if blocks is None:
+            blocks = self._new_blocks(n, choice[0])
         with self._lock:
             qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
             cnt = self._dense(counts, I32, self._per_seq, "counts")
@@ -273,6 +275,8 @@ class H2OBlockCache:
         if rotary is not None:
             q, k = self._turned(rotary, q, k, lengths, counts, position)
         choice = self._choice(n_blocks, n_first, n_last)
+        if blocks is None:
+            blocks = self._new_blocks(n, choice[0])
         with self._lock:
             rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
             lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
@@ -299,12 +303,13 @@ class H2OBlockCache:
             return n_blocks, n_first, n_last
         return _whole(n_blocks, "n_blocks"), _whole(n_first, "n_first"), _whole(n_last, "n_last")
 
+    def _new_blocks(self, n, n_blocks):
+        """Room for the chosen blocks' indices, which the kernels hand on through memory.  The caller holds it until its
+        call is enqueued: only work enqueued behind that may be given the memory anew."""
+        return torch.empty((self.B, self.H, n, n_blocks), dtype=I32, device=self.device) if n_blocks > 0 else None
+
     def _blocks(self, t, n, n_blocks):
-        """Address of the chosen blocks' indices: the kernels hand them on through it, so it is always there."""
-        shape = (self.B, self.H, n, n_blocks)
-        if t is None and n_blocks > 0:
-            t = torch.empty(shape, dtype=I32, device=self.device)
-        return self._dense(t, I32, shape, "blocks")
+        return self._dense(t, I32, (self.B, self.H, n, n_blocks), "blocks")
 
     def _turned(self, rotary, q, k, lengths, counts, position):
         """q and k normed and rotated by their positions, in rows of their own (those behind a count hold anything: no
