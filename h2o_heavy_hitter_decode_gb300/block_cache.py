@@ -53,6 +53,7 @@ class H2OBlockCache:
     graph uses is kept for as long as the graph is replayed."""
 
     BLOCK = 32
+    _most_blocks = 1 << 26  # H2O_SPARSE_MAX_BLOCKS
     bounds = None
 
     def __init__(self, B: int, H: int, d: int, capacity: int, group: int = 1, max_queries: int = 1, kv: str = "e4m3",
@@ -254,7 +255,7 @@ class H2OBlockCache:
         n = self._tokens(q, "q")
         shape, choice = self._shape(self._heads, n), self._choice(n_blocks, n_first, n_last)
         if blocks is None:
-            blocks = self._new_blocks(n, choice[0])
+            choice, blocks = self._new_blocks(n, *choice)
         with self._lock:
             qr, lens = self._rows(0, q, shape, "q"), self._lengths(lengths, "lengths")
             cnt = self._dense(counts, I32, self._per_seq, "counts")
@@ -276,7 +277,7 @@ class H2OBlockCache:
             q, k = self._turned(rotary, q, k, lengths, counts, position)
         choice = self._choice(n_blocks, n_first, n_last)
         if blocks is None:
-            blocks = self._new_blocks(n, choice[0])
+            choice, blocks = self._new_blocks(n, *choice)
         with self._lock:
             rows = (self._rows(0, q, shape, "q"), self._rows(1, k, kv_shape, "k"), self._rows(2, v, kv_shape, "v"))
             lens, cnt = self._lengths(lengths, "lengths"), self._dense(counts, I32, self._per_seq, "counts")
@@ -303,10 +304,15 @@ class H2OBlockCache:
             return n_blocks, n_first, n_last
         return _whole(n_blocks, "n_blocks"), _whole(n_first, "n_first"), _whole(n_last, "n_last")
 
-    def _new_blocks(self, n, n_blocks):
-        """Room for the chosen blocks' indices, which the kernels hand on through memory.  The caller holds it until its
-        call is enqueued: only work enqueued behind that may be given the memory anew."""
-        return torch.empty((self.B, self.H, n, n_blocks), dtype=I32, device=self.device) if n_blocks > 0 else None
+    def _new_blocks(self, n, n_blocks, n_first, n_last):
+        """A choice as the call makes it, and room for its list of blocks, which the kernels hand on through memory.  The
+        caller holds that until its call is enqueued: only work enqueued behind it may be given the memory anew."""
+        if not (n_first >= 0 and 1 <= n_last and n_first + n_last <= n_blocks <= self._most_blocks):
+            return (n_blocks, n_first, n_last), None  # the library refuses it
+        most = self.capacity // self.BLOCK
+        if n_blocks > most:  # every block, however they are named: no list longer than that
+            n_blocks, n_first, n_last = most, 0, 1
+        return (n_blocks, n_first, n_last), torch.empty((self.B, self.H, n, n_blocks), dtype=I32, device=self.device)
 
     def _blocks(self, t, n, n_blocks):
         return self._dense(t, I32, (self.B, self.H, n, n_blocks), "blocks")

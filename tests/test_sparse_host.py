@@ -8,6 +8,7 @@ import weakref
 import pytest
 import torch
 
+from h2o_heavy_hitter_decode_gb300 import HEADER_PATH, H2OBlockCache
 from test_block_cache_threads import B, D, H, N, Library, cache_on_the_host
 
 
@@ -23,7 +24,7 @@ class Sparse(Library):
         gc.collect()
         alive = [t() for t in self.made]
         assert all(t is not None for t in alive), "memory of a call was given back before the call"
-        assert blocks is None or any(t.data_ptr() == blocks and t.numel() >= B * H * n * n_blocks for t in alive)
+        assert blocks is None or any(t.data_ptr() == blocks and t.numel() == B * H * n * n_blocks for t in alive)
         self.calls.append((kind, n, n_blocks, n_first, n_last, blocks))
         return 0
 
@@ -68,3 +69,30 @@ def test_the_list_of_blocks_lives_until_the_call(monkeypatch, kind):
     lib.made.pop(0)
     call(c, kind, 1, 0, 1, blocks=mine)
     assert len(lib.made) == 1 and lib.calls[1][5] == mine.data_ptr()
+
+
+@pytest.mark.parametrize("kind", ["attend", "step"])
+def test_a_list_is_no_longer_than_the_cache(monkeypatch, kind):
+    """More blocks than the cache has are all of them (here one): a list of 2^26 for each token and head would not fit a
+    GPU.  A choice that is refused gets no memory at all, and reaches the library as it was given."""
+    c, lib = sparse_on_the_host(monkeypatch)
+    for choice in ((2, 1, 1), (1 << 26, 5, 1 << 25), (1 << 26, 0, 1), (1000, 0, 1000)):
+        call(c, kind, *choice)
+        assert lib.calls.pop()[:5] == (kind, N, 1, 0, 1)
+        assert lib.made.pop()() is None  # one word a token and head was enough (note), and is gone with the call
+    for bad in ((0, 0, 1), (-1, 0, 1), (1, 0, 0), (1, 1, 1), (1, -1, 2), (2 ** 26 + 1, 1, 1), (2 ** 31 - 1, 2 ** 31 - 1, 1),
+                (1 << 26, 1 << 26, 1)):
+        call(c, kind, *bad)
+        assert lib.calls.pop() == (kind, N, *bad, None) and not lib.made
+    with pytest.raises(ValueError):
+        call(c, kind, 2 ** 31, 0, 1)
+    # the caller's own list is as long as the caller says
+    mine = torch.zeros(B, H, N, 7, dtype=torch.int32)
+    lib.made.append(weakref.ref(mine))
+    call(c, kind, 7, 2, 3, blocks=mine)
+    assert lib.calls.pop() == (kind, N, 7, 2, 3, mine.data_ptr())
+
+
+def test_the_largest_list_is_the_library_s():
+    text = open(HEADER_PATH).read()
+    assert "#define H2O_SPARSE_MAX_BLOCKS (1 << 26)" in text and H2OBlockCache._most_blocks == 1 << 26
