@@ -672,8 +672,9 @@ __global__ void __launch_bounds__(W * 32, W < 8 ? (NR == 1 ? 12 : 8) / W : 1)
   };
 
   // ----------------------------------------------------------- the attention
-  // Logits: by own blocks in shared memory, or by slots in memory.
-  const bool near = group * per * kBlock <= a.logits;
+  // Logits: by own blocks in shared memory, or by slots in memory.  The host made room for all of a CTA's or for none
+  // (per <= its own), in 64 bits: 256 rows of 2^18 blocks are 2^31 logits.
+  const bool near = a.logits > 0;
   const int64_t row_step = near ? per * kBlock : c.cap;
   float *logits = near ? held_logits : logits_of(a, bh, t, 0) + slot0 * kBlock;
   uint8_t *ring = smem + warp * kStages * kStage;
