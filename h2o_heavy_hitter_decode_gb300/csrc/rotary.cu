@@ -63,6 +63,28 @@ __device__ __forceinline__ void store8(float *p, const float *x) {
   *(float4 *)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// Rows of L lanes, by whole warps.  One whose mean square plus eps is below kTiny takes the power of two that brings the
+// larger of its largest element and sqrt(eps) to 1 .. 2, which its norm takes out again; squares that are lost then are
+// 2^-126 of the mean and below.  Returns the mean square plus eps; the other rows stay as they are.  Rare.
+constexpr float kTiny = 0x1p-96f;
+template <int L> __device__ __forceinline__ float rescale(float (&x)[16], float mean, float eps) {
+  float top = sqrtf(eps);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool tiny = mean < kTiny && top > 0.f;
+  // 2^k in two factors: k is up to 149 (the least number of 32 bits is 2^-149)
+  const int k = tiny ? -ilogbf(top) : 0;
+  const float up = ldexpf(1.f, k / 2), more = ldexpf(1.f, k - k / 2);
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = x[e] * up * more, s = fmaf(x[e], x[e], s);
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return tiny ? s * (1.f / (16 * L)) + eps * up * more * up * more : mean;
+}
+
 // Few: a token has fewer heads than a warp takes at a time.
 template <typename T, int D, int kAhead, bool Few>
 __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
@@ -141,7 +163,10 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rotate_kernel(const Args a) {
           for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
 #pragma unroll
           for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const float f = rsqrtf(s * (1.f / D) + r.eps);
+          float mean = s * (1.f / D) + r.eps;
+          // squares of tiny elements leave fp32's range downwards, which shows where eps does not hide it
+          if (__any_sync(0xffffffffu, mean < kTiny)) mean = rescale<L>(x, mean, r.eps);
+          const float f = rsqrtf(mean);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] *= f * w[e];
         }

@@ -479,7 +479,9 @@ h2o_status h2o_bcache_get_error(h2o_bcache_t cache, int *bits);
  * The product of a position and a frequency is taken in 64-bit integers that
  * wrap at whole turns, so angles of far positions lose nothing; all else is
  * fp32, rounded once at the end.  Mean squares are fp32 sums: a row whose sum of
- * squares passes fp32's range becomes 0.
+ * squares passes fp32's range becomes 0; of one whose squares are lost below it
+ * (eps 0 or below 2^-96) the sum is taken in a power of two of its own, and loses
+ * nothing.  A row of zeros with eps 0 is 0 / 0: NaN.
  *
  * position: int32 [B], token t being at position[b] + t on every axis, or with
  * per_token set int32 [axes][B][n]; pair i takes that of axis[i] (the last axis
