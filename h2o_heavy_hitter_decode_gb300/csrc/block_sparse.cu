@@ -491,8 +491,15 @@ template <int N> __device__ __forceinline__ float2 weigh(const float2 *ml, int s
   return make_float2(m, l);
 }
 
+// CTAs that shared memory leaves room for on an SM (at d = 128, of 228 KB: 8 warps 140 KB and more; 4 warps 75 KB, three
+// while a CTA's list is at most 688 blocks, else two; 2 warps 42 KB; above 8 rows 85 and 56 KB), so the registers that a
+// thread may have: a partition's 512 x 32 among its warps, 168 for three of them and 255 for two.  At d = 128 the forms of
+// 168 registers spill 140 to 150 bytes a thread, those of more than 8 rows 100 to 130 at 255 and that of 8 warps 30; at
+// d = 64 it is 12 at most.
+template <int NR, int W> constexpr int kResident = W == 8 ? 1 : W == 4 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 5 : 4);
+
 template <typename F, int D, int NR, int W>
-__global__ void __launch_bounds__(W * 32, W < 8 ? (NR == 1 ? 12 : 8) / W : 1)
+__global__ void __launch_bounds__(W * 32, kResident<NR, W>)
     sparse_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using R = Room<D, NR, W>;
   constexpr int kThreads = W * 32, OT = D / 16, kStage = R::kStage, kStages = R::kStages, kRows = R::kRows;
@@ -976,11 +983,13 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
 
 // CTAs of 8 warps, one an SM, while they all fit at once, as many to a token as
 // do; more tokens than SMs: CTAs of 4 warps, three an SM (two with 9 rows and
-// more); more than those hold: of 2 warps, twice as many an SM, since the way
-// from lengths to outputs is then hidden by other tokens and not by more warps.
-// Measured, us a call (2 / 4 / 8 warps, the best P of each): 8 heads of 8,000
-// entries 25 / 16 / 13; 128 of 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000
-// 48 / 36 / 49; 512 of them 84 / 107 / 104; 3,584 of 700 to 2,047 142 / 163 / 284.
+// more, or lists above 688 blocks); more than those hold: of 2 warps, five an SM
+// (four), since the way from lengths to outputs is then hidden by other tokens
+// and not by more warps.  Measured, us a call (2 / 4 / 8 warps, the best P of
+// each), 64 blocks a token but the last (16): 8 heads of 8,000 entries 25 / 16 /
+// 13; 128 of 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512
+// of them 84 / 107 / 104; 3,584 of 700 to 2,047 142 / 163 / 284.  With the weights
+// whole the last four take 30, 38, 88 (floor 45) and 146 (floor 78).
 template <typename F, int D, int NR>
 cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   // counts leave tokens out: half of those behind the first, on the average
