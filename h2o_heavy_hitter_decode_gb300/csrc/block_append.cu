@@ -12,7 +12,8 @@
 // written once.  Bound by memory: 16 x 32 heads x 8,192 rows, 3.26 GB, 490 us,
 // 98 % of the copy rate, with four CTAs (128 registers) an SM; three (168): 568.
 // append_few_kernel: one warp per (head, K or V) for the rows of a decode
-// step, taken one at a time; the block's earlier codes are read only where its
+// step, up to kFewRows, all on their way together and under one scale a block;
+// the block's earlier codes are read only where its
 // scale grows, or for the bounds of its keys where the cache keeps them.
 #include "block_tile.cuh"
 

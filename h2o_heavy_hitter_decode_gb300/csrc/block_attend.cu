@@ -841,7 +841,7 @@ cudaError_t launch_attend(const View &c, const Lens &l, const Rows &q, int causa
 }
 
 bool head_fits(const View &c, int n) {
-  return n * c.group <= 8 && c.cap <= kHeadCap && (int64_t)c.B * c.H <= 2 * c.sms;
+  return n <= kFewRows && n * c.group <= 8 && c.cap <= kHeadCap && (int64_t)c.B * c.H <= 2 * c.sms;
 }
 
 cudaError_t launch_head(const View &c, const Lens &l, const Rows &q, const Rows *k, const Rows *v,

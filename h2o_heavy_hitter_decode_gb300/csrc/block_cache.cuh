@@ -164,7 +164,7 @@ __device__ __forceinline__ int exponent(float s) { return (int)(__float_as_uint(
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 // ------------------------------------------------------------ few new rows
-constexpr int kFewRows = 8;  // rows of a sequence that are appended one at a time
+constexpr int kFewRows = 8;  // rows of a sequence that one warp appends together, at most (append_rows holds them all)
 
 // Rows lo .. hi-1 of head (b, h), all in one block, appended behind `len`
 // entries by one warp, a lane taking D/32 neighbours of a row; at most N rows,
