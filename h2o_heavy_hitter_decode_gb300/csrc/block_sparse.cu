@@ -28,7 +28,7 @@
 // Weights meet V whole, as two f16 numbers each (Tile): products are not what
 // bounds this kernel, and 11 bits showed in one output of fifty (a step of bf16,
 // 8e-4 of the outputs' norm against 32-bit weights; now 1e-4 and less).  Second
-// products cost 2 to 7 % (one sequence 10.7 -> 10.9 us, long batch 56.9 -> 60.8).
+// products cost up to 6 % (groups of 4 28.1 -> 29.0 us, long batch 56.9 -> 60.1).
 // With one token a sequence the new row is appended, and the weights are added
 // to the scores, in the same launch (each CTA those of its own blocks); several
 // tokens may choose the same block, so theirs are added by scores_kernel, in
@@ -494,8 +494,8 @@ template <int N> __device__ __forceinline__ float2 weigh(const float2 *ml, int s
 // CTAs that shared memory leaves room for on an SM (at d = 128, of 228 KB: 8 warps 140 KB and more; 4 warps 75 KB, three
 // while a CTA's list is at most 688 blocks, else two; 2 warps 42 KB; above 8 rows 85 and 56 KB), so the registers that a
 // thread may have: a partition's 512 x 32 among its warps, 168 for three of them and 255 for two.  At d = 128 the forms of
-// 168 registers spill 140 to 150 bytes a thread, those of more than 8 rows 100 to 130 at 255 and that of 8 warps 30; at
-// d = 64 it is 12 at most.
+// 168 registers spill 80 to 140 bytes a thread, those of more than 8 rows 100 to 130 at 255 and that of 8 warps 20; at
+// d = 64 it is 8 at most.
 template <int NR, int W> constexpr int kResident = W == 8 ? 1 : W == 4 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 5 : 4);
 
 template <typename F, int D, int NR, int W>
@@ -989,7 +989,7 @@ template <typename F, int D, int NR> int clusters_at_once(int P) {
 // each), 64 blocks a token but the last (16): 8 heads of 8,000 entries 25 / 16 /
 // 13; 128 of 3,000 to 8,400 44 / 30 / 28; 192 of 4,000 to 8,000 48 / 36 / 49; 512
 // of them 84 / 107 / 104; 3,584 of 700 to 2,047 142 / 163 / 284.  With the weights
-// whole the last four take 30, 38, 88 (floor 45) and 146 (floor 78).
+// whole the last four take 29, 36, 88 (floor 45) and 146 (floor 78).
 template <typename F, int D, int NR>
 cudaError_t sparse_n(Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
   // counts leave tokens out: half of those behind the first, on the average
