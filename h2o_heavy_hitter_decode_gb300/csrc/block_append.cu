@@ -13,8 +13,9 @@
 // 98 % of the copy rate, with four CTAs (128 registers) an SM; three (168): 568.
 // append_few_kernel: one warp per (head, K or V) for the rows of a decode
 // step, up to kFewRows, all on their way together and under one scale a block;
-// the block's earlier codes are read only where its
-// scale grows, or for the bounds of its keys where the cache keeps them.
+// the block's earlier codes are read only where its scale grows, or for the
+// bounds of its keys where the cache keeps them.  Those of many rows are made by
+// a launch that reads the key codes again: 105 us more for the rows above.
 #include "block_tile.cuh"
 
 namespace h2o {

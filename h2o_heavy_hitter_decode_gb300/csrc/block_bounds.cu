@@ -7,7 +7,10 @@
 //
 // One warp per (head, block) for many rows (bound_block in block_tile.cuh).
 // Few new rows have theirs made by the warp that appends them.  Bound by
-// memory: d bytes read an entry and d / 16 written.
+// memory: d bytes read an entry and d / 16 written.  A pass of its own: 16 x 32
+// heads x 8,192 new rows 105 us more (537 MB read, 5.4 TB/s); an eviction from
+// 8,448 to 1,690 entries of 32 x 32 heads 208 -> 265 us (int8 216 -> 301), and one
+// that leaves everything as it is 7 -> 68.
 #include "block_tile.cuh"
 
 namespace h2o {

@@ -35,11 +35,11 @@
 // the tokens' order.
 //
 // Bound: short runs by latency, a dozen steps from the lengths to the scores (32
-// heads of 2,560 entries, 16 blocks each, 10.5 us, of it 3 to the keys, 1 for
+// heads of 2,560 entries, 16 blocks each, 10.6 us, of it 3 to the keys, 1 for
 // the choice, 2 for copy and products, 3 to join the parts, 1 for the scores);
 // larger ones by memory in two of them, the keys' (4 to 5 TB/s) and the
 // blocks' (6 TB/s of 4 KB pieces): 128 heads of 20,000 to 65,500 entries, 128
-// blocks each, 183 MB, 57 us, where memory alone would take 27.
+// blocks each, 183 MB, 60 us, where memory alone would take 27.
 #include <cooperative_groups.h>
 
 #include <algorithm>

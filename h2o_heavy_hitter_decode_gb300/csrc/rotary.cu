@@ -4,18 +4,18 @@
 //   y = x / sqrt(mean x^2 + eps) * w;  (y_a, y_b) turned by position * frequency
 //
 // A warp takes some heads of one token, or of several where a token has few: a
-// row is held by d / 16 lanes, 16
-// elements each, arranged so that both halves of a pair are one lane's.  The
+// row is held by d / 16 lanes, 16 elements each, arranged so that both halves of
+// a pair are one lane's.  The
 // sines and cosines of a lane's 8 pairs depend on the token alone: they are
 // computed once and used for all the warp's heads.  Angles: position times the
 // 64-bit fraction of a turn wraps at whole turns by itself, and its upper 32
 // bits go through sincospif, 24 of them as its argument.
 //
 // Bound by memory: 16 prompts of 8,192 tokens, 32 query and 32 key heads of 128
-// (4.3 GB) 650 us, 97 % of the copy rate, with five CTAs an SM (four 690, six
-// 717 with spills); 6,771 patches of 16 and 16 heads of 64 in fp32 24 us, 68 %,
-// by the way from positions to sines to stores, four and a half waves of it.
-// One token by latency, 2.4 us.
+// (4.3 GB) 649 us, 98 % of the copy rate, with five CTAs an SM (four 690, six
+// 717 with spills); 6,771 patches of 16 and 16 heads of 64 in fp32 23 us, 69 %,
+// by the way from positions to sines to stores, 2.2 waves of it (1,693 CTAs).
+// One token by latency, 2.7 us.
 #include <cstdint>
 
 #include "common.cuh"

@@ -43,7 +43,10 @@ class H2ORotary:
     norms only.
 
     The object owns small tables on its device and nothing else: layers that
-    agree in them share it, on any streams and host threads."""
+    agree in them share it, on any streams and host threads.  The weights are
+    copied into them, as fp32: a weight that is changed afterwards takes a new
+    object.  One that a captured graph uses is kept for as long as the graph is
+    replayed."""
 
     def __init__(self, d: int, dims: int | None = None, theta: float = 10000.0, frequency=None, axis=None,
                  interleaved: bool = False, eps: float | None = None, q_weight=None, k_weight=None, device=None):
